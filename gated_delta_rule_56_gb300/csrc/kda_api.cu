@@ -12,11 +12,10 @@
 #include "kda_tc.cuh"
 
 namespace kda {
+
 namespace {
-
-__device__ unsigned g_error_word;  // one per device: bits kErrBadSeqlens | kErrTimeout
-
 thread_local char g_last_error[512];
+}  // namespace
 
 kda_status fail(kda_status st, const char *fmt, ...) {
     va_list ap;
@@ -33,16 +32,6 @@ kda_status ok() {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-bool supported_head(int dk, int dv) { return dk == dv && (dk == 32 || dk == 64 || dk == 128); }
-
-kda_status check_head(int dk, int dv) {
-    if (dk <= 0 || dv <= 0) return fail(KDA_ERR_INVALID_ARG, "dk=%d dv=%d must be positive", dk, dv);
-    if (!supported_head(dk, dv))
-        return fail(KDA_ERR_UNSUPPORTED, "head sizes dk=%d dv=%d: supported dk == dv in {32, 64, 128}",
-                    dk, dv);
-    return KDA_OK;
-}
-
 kda_status check_dtype(kda_dtype dt) {
     if (dt != KDA_BF16 && dt != KDA_F32) return fail(KDA_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
     return KDA_OK;
@@ -51,6 +40,35 @@ kda_status check_dtype(kda_dtype dt) {
 kda_status check_ptr(const void *p, const char *name, bool need_align) {
     if (!p) return fail(KDA_ERR_INVALID_ARG, "%s is NULL", name);
     if (need_align && !aligned16(p)) return fail(KDA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+    return KDA_OK;
+}
+
+kda_status launched(cudaError_t e, const char *what) {
+    if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    return ok();
+}
+
+// SMs of the current device (0 when none is visible).
+int current_sms() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        sms = 0;
+    }
+    return sms;
+}
+
+namespace {
+
+__device__ unsigned g_error_word;  // one per device: bits kErrBadSeqlens | kErrTimeout
+
+bool supported_head(int dk, int dv) { return dk == dv && (dk == 32 || dk == 64 || dk == 128); }
+
+kda_status check_head(int dk, int dv) {
+    if (dk <= 0 || dv <= 0) return fail(KDA_ERR_INVALID_ARG, "dk=%d dv=%d must be positive", dk, dv);
+    if (!supported_head(dk, dv))
+        return fail(KDA_ERR_UNSUPPORTED, "head sizes dk=%d dv=%d: supported dk == dv in {32, 64, 128}",
+                    dk, dv);
     return KDA_OK;
 }
 
@@ -63,11 +81,6 @@ __global__ void wait_timeout_kernel(uint64_t limit_ns) {
         tc::fence_mbar_init();
         if (!tc::mbar_wait(&bar, 0, limit_ns)) atomicOr(&g_error_word, kErrTimeout);
     }
-}
-
-kda_status launched(cudaError_t e, const char *what) {
-    if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-    return ok();
 }
 
 // Scratch of kda_prefill_noalloc: one array per device, placed when the module loads, so that
@@ -220,16 +233,6 @@ size_t prefill_workspace_bytes_for(kda_dtype dtype, int B, int T, int H, int dk,
     size_t bytes = 0;
     segmented_plan_for(B, T, H, sms, &P, &Ls, &bytes);
     return bytes;
-}
-
-// SMs of the current device (0 when none is visible).
-int current_sms() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        (void)cudaGetLastError();
-        sms = 0;
-    }
-    return sms;
 }
 
 // The same on the current device.
@@ -602,6 +605,8 @@ kda_status kda_check_status(kda_stream_t stream) {
     if (word & kErrTimeout) return fail(KDA_ERR_TIMEOUT, "a device-side wait gave up (error word 0x%x)", word);
     if (word & kErrBadIndex)
         return fail(KDA_ERR_INVALID_ARG, "a state index is at or past the pool end (error word 0x%x)", word);
+    if (word & kErrBadPosition)
+        return fail(KDA_ERR_INVALID_ARG, "a position is outside the rotation tables (error word 0x%x)", word);
     if (word & kErrBadSeqlens)
         return fail(KDA_ERR_INVALID_ARG, "cu_seqlens is not a non-decreasing list ending at T (error word 0x%x)", word);
     return ok();

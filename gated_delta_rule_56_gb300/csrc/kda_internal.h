@@ -11,7 +11,7 @@
 namespace kda {
 
 // Bits of the per-device error word (see kda_check_status).
-enum : unsigned { kErrBadSeqlens = 1u, kErrTimeout = 2u, kErrBadIndex = 4u };
+enum : unsigned { kErrBadSeqlens = 1u, kErrTimeout = 2u, kErrBadIndex = 4u, kErrBadPosition = 8u };
 
 // Arguments of one prefill or decode launch, already validated on the host.
 struct RunParams {
@@ -43,6 +43,16 @@ struct RunParams {
     float *dump;                // non-null: plain bf16 d = 128 only
     int dump_chunks;
 };
+
+// Host-side argument checks and error reporting (kda_api.cu): the status is returned, its detail
+// kept for kda_last_error() in the calling thread.
+kda_status fail(kda_status st, const char *fmt, ...);
+kda_status ok();
+kda_status launched(cudaError_t e, const char *what);  // a launch's error, or ok()
+kda_status check_dtype(kda_dtype dt);
+kda_status check_ptr(const void *p, const char *name, bool need_align);  // not NULL; 16-byte aligned if asked
+bool aligned16(const void *p);
+int current_sms();  // SMs of the current device (0 when none is visible)
 
 // Device error word of the current device (created on first use).
 unsigned *device_error_word();

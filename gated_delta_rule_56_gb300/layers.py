@@ -1,0 +1,426 @@
+"""ctypes binding of the operators around the mixer: the short causal convolution, the selective
+state space scan and the norm of q and k with the position rotation.
+
+As in ``_lib``: argument marshalling only. Inputs named as row inputs (x, dt, z, B, C, q, k) may be
+slices of a wider projection: their innermost dimensions are dense and their rows lie at one
+uniform distance; everything else is contiguous. There is no fallback without the library.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._lib import _check, _check_indices, _DTYPES, _ptr, _raise_if, _stream, load
+
+_vp, _i, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+
+
+def _struct(name, fields):
+    return type(name, (ctypes.Structure,), {"_fields_": [("struct_size", _sz)] + fields,
+                                            "__doc__": f"{name} of include/kda.h."})
+
+
+ConvArgs = _struct("kda_conv_args", [
+    ("dtype", _i), ("B", _i), ("T", _i), ("C", _i), ("W", _i), ("activation", _i), ("x", _vp), ("x_stride", _i64),
+    ("weight", _vp), ("bias", _vp), ("cu_seqlens", _vp), ("n_seqs", _i), ("initial_state", _vp),
+    ("initial_state_indices", _vp), ("final_state_indices", _vp), ("state_pool_size", _i)])
+ScanArgs = _struct("kda_scan_args", [
+    ("dtype", _i), ("B", _i), ("T", _i), ("D", _i), ("N", _i), ("G", _i), ("dt_softplus", _i), ("x", _vp), ("dt", _vp),
+    ("Bm", _vp), ("Cm", _vp), ("z", _vp), ("x_stride", _i64), ("dt_stride", _i64), ("B_stride", _i64),
+    ("C_stride", _i64), ("z_stride", _i64), ("A", _vp), ("Dskip", _vp), ("dt_bias", _vp), ("cu_seqlens", _vp),
+    ("n_seqs", _i), ("initial_state", _vp), ("initial_state_indices", _vp), ("final_state_indices", _vp),
+    ("state_pool_size", _i)])
+ScanGrads = _struct("kda_scan_grads", [(n, _vp) for n in (
+    "dy", "d_final_state", "dx", "ddt", "dA", "dB", "dC", "dDskip", "dz", "ddt_bias", "d_initial_state")])
+RotaryArgs = _struct("kda_rotary_args", [
+    ("dtype", _i), ("rows", _i64), ("q_heads", _i), ("k_heads", _i), ("head", _i), ("half", _i), ("norm", _i),
+    ("interleaved", _i), ("eps", ctypes.c_float), ("q", _vp), ("k", _vp), ("q_stride", _i64), ("k_stride", _i64),
+    ("q_weight", _vp), ("k_weight", _vp), ("cos_table", _vp), ("sin_table", _vp), ("positions", _vp),
+    ("table_rows", _i64)])
+
+_typed = None
+
+
+def _library():
+    """The library with the argument types of these entry points set."""
+    global _typed
+    lib = load()
+    if _typed is not lib:
+        P = ctypes.POINTER
+        for name, args in (("kda_conv_prefill", [P(ConvArgs), _vp, _vp, _vp]),
+                           ("kda_conv_decode_step", [P(ConvArgs), _vp, _vp, _vp]),
+                           ("kda_conv_backward", [P(ConvArgs)] + [_vp] * 7 + [_sz, _vp]),
+                           ("kda_scan_prefill", [P(ScanArgs), _vp, _vp, _vp, _sz, _vp]),
+                           ("kda_scan_decode_step", [P(ScanArgs), _vp, _vp, _vp]),
+                           ("kda_scan_backward", [P(ScanArgs), P(ScanGrads), _vp, _sz, _vp]),
+                           ("kda_qk_norm_rotary", [P(RotaryArgs), _vp, _vp, _vp]),
+                           ("kda_qk_norm_rotary_backward", [P(RotaryArgs)] + [_vp] * 7 + [_sz, _vp])):
+            f = getattr(lib, name)
+            f.argtypes, f.restype = args, _i
+        for name, arg in (("kda_conv_backward_workspace_size", ConvArgs), ("kda_scan_prefill_workspace_size", ScanArgs),
+                          ("kda_scan_backward_workspace_size", ScanArgs),
+                          ("kda_qk_norm_rotary_backward_workspace_size", RotaryArgs)):
+            f = getattr(lib, name)
+            f.argtypes, f.restype = [P(arg)], _sz
+        _typed = lib
+    return lib
+
+
+def _device(t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("inputs must be torch tensors")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    if t.device.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    return t.device
+
+
+def _row_stride(name, t, dtype, shape, lead, device):
+    """Checks an input whose first ``lead`` dimensions are rows; returns the elements between rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    width = 1
+    if t.numel() == 0:
+        return 0
+    for d in range(t.dim() - 1, lead - 1, -1):
+        if t.shape[d] != 1 and t.stride(d) != width:
+            raise ValueError(f"{name}: the values of a row must be dense")
+        width *= t.shape[d]
+    stride, rows = None, 1
+    for d in range(lead - 1, -1, -1):
+        if t.shape[d] != 1:
+            if stride is None:
+                stride = t.stride(d)
+            elif t.stride(d) != stride * rows:
+                raise ValueError(f"{name}: rows must lie at one uniform distance")
+            rows *= t.shape[d]
+    if stride is None:
+        return width
+    if stride < width:
+        raise ValueError(f"{name}: rows must not overlap")
+    return stride
+
+
+def _sequences(cu_seqlens, batch, device):
+    if cu_seqlens is None:
+        return batch
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be a 1-D int32 tensor [N+1]")
+    _check("cu_seqlens", cu_seqlens, torch.int32, (cu_seqlens.numel(),), device)
+    if batch != 1:
+        raise ValueError("cu_seqlens needs a batch of 1 (packed rows)")
+    return cu_seqlens.numel() - 1
+
+
+def _states(initial, final, initial_indices, final_indices, n, shape, dtype, device):
+    """Checks states of one call (``shape`` is one sequence's) and returns the pool size (0: no pool)."""
+    pools = [t.shape[0] for t, i in ((initial, initial_indices), (final, final_indices)) if t is not None and i is not None]
+    if len(set(pools)) > 1:
+        raise ValueError("initial and final state pools must have the same number of slots")
+    if initial_indices is not None and initial is None:
+        raise ValueError("initial_state_indices needs initial_state (the pool)")
+    if final_indices is not None and final is None:
+        raise ValueError("final_state_indices needs final_state (the pool)")
+    pool = pools[0] if pools else 0
+    _check_indices("initial_state_indices", initial_indices, n, device)
+    _check_indices("final_state_indices", final_indices, n, device)
+    for name, t, i in (("initial_state", initial, initial_indices), ("final_state", final, final_indices)):
+        if t is not None:
+            _check(name, t, dtype, (pool if i is not None else n, *shape), device)
+    return pool
+
+
+def _output(name, t, dtype, shape, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check(name, t, dtype, shape, device)
+    return t
+
+
+def _workspace(nbytes, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+# ------------------------------------------------------------------ short convolution ---
+
+
+def _conv_args(x, weight, bias, activation, lead):
+    dev = _device(x)
+    if x.dim() != lead + 1:
+        raise ValueError(f"x must have {lead + 1} dimensions")
+    if activation not in (None, "silu"):
+        raise ValueError(f"unknown activation {activation!r}: None or 'silu'")
+    C = x.shape[-1]
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a tensor [C, W]")
+    W = weight.shape[1]
+    _check("weight", weight, x.dtype, (C, W), dev)
+    if bias is not None:
+        _check("bias", bias, x.dtype, (C,), dev)
+    stride = _row_stride("x", x, x.dtype, tuple(x.shape), lead, dev)
+    a = ConvArgs(struct_size=ctypes.sizeof(ConvArgs), dtype=_DTYPES[x.dtype], B=x.shape[0], T=x.shape[1] if lead == 2 else 1,
+                 C=C, W=W, activation=1 if activation == "silu" else 0, x=x.data_ptr(), x_stride=stride,
+                 weight=weight.data_ptr(), bias=None if bias is None else bias.data_ptr())
+    return a, dev, C, W
+
+
+def conv_prefill(x, weight, bias=None, activation="silu", cu_seqlens=None, initial_state=None, output_final_state=True,
+                 y=None, final_state=None, initial_state_indices=None, final_state_indices=None):
+    """Short causal convolution of whole sequences, one filter per channel.
+
+    x [B, T, C] (rows may be strided), weight [C, W] with W 2 to 4, bias [C] or None, bf16 or fp32:
+    y_t = act(bias + sum_j weight[:, j] x_{t-(W-1)+j}) with act SiLU or none, each sequence on its own. With
+    ``cu_seqlens`` (int32 [N+1] on the device) B must be 1 and the rows are packed sequences. The state of a
+    sequence is its last W-1 inputs [N, W-1, C] in x's dtype; ``initial_state`` None means zeros. With
+    ``initial_state_indices`` / ``final_state_indices`` (int32 [N]) the matching state is a pool, as in
+    ``prefill``. ``final_state`` may be ``initial_state``'s memory. Returns (y [B, T, C], final_state or None).
+    """
+    lib = _library()
+    a, dev, C, W = _conv_args(x, weight, bias, activation, 2)
+    n = _sequences(cu_seqlens, x.shape[0], dev)
+    pool = _states(initial_state, final_state, initial_state_indices, final_state_indices, n, (W - 1, C), x.dtype, dev)
+    y = _output("y", y, x.dtype, tuple(x.shape), dev)
+    if final_state is None and output_final_state:
+        final_state = torch.empty(n, W - 1, C, dtype=x.dtype, device=dev)
+    a.cu_seqlens, a.n_seqs, a.initial_state = _ptr(cu_seqlens), n, _ptr(initial_state)
+    a.initial_state_indices, a.final_state_indices = _ptr(initial_state_indices), _ptr(final_state_indices)
+    a.state_pool_size = pool
+    with torch.cuda.device(dev):
+        _raise_if(lib.kda_conv_prefill(ctypes.byref(a), _ptr(y), _ptr(final_state), _stream(dev)))
+    return y, final_state
+
+
+def conv_decode_step(x, weight, state, bias=None, activation="silu", state_indices=None, final_state_indices=None, y=None):
+    """One token of the convolution for N sequences: x [N, C]; ``state`` [N, W-1, C] (or a pool with
+    ``state_indices`` int32 [N], as in ``decode_step``) is shifted in place. Returns y [N, C]."""
+    lib = _library()
+    a, dev, C, W = _conv_args(x, weight, bias, activation, 1)
+    n = x.shape[0]
+    if final_state_indices is not None and state_indices is None:
+        raise ValueError("final_state_indices needs state_indices")
+    _check_indices("state_indices", state_indices, n, dev)
+    _check_indices("final_state_indices", final_state_indices, n, dev)
+    pool = state.shape[0] if state_indices is not None and state.dim() == 3 else 0
+    _check("state", state, x.dtype, (pool if state_indices is not None else n, W - 1, C), dev)
+    y = _output("y", y, x.dtype, (n, C), dev)
+    a.initial_state_indices, a.final_state_indices, a.state_pool_size = _ptr(state_indices), _ptr(final_state_indices), pool
+    with torch.cuda.device(dev):
+        _raise_if(lib.kda_conv_decode_step(ctypes.byref(a), _ptr(state), _ptr(y), _stream(dev)))
+    return y
+
+
+def conv_backward(x, weight, dy, bias=None, activation="silu", cu_seqlens=None, initial_state=None, d_final_state=None,
+                  want_d_initial_state=True):
+    """Gradients of sum(dy * y) + sum(d_final_state * final_state) through ``conv_prefill`` (no pools).
+    dy has y's layout and dtype; d_final_state fp32 [N, W-1, C] or None. Returns a dict of fp32 tensors: dx
+    [B, T, C], dweight [C, W], dbias [C] (None without a bias), d_initial_state [N, W-1, C] (or None)."""
+    lib = _library()
+    a, dev, C, W = _conv_args(x, weight, bias, activation, 2)
+    n = _sequences(cu_seqlens, x.shape[0], dev)
+    _check("dy", dy, x.dtype, tuple(x.shape), dev)
+    _states(initial_state, None, None, None, n, (W - 1, C), x.dtype, dev)
+    if d_final_state is not None:
+        _check("d_final_state", d_final_state, torch.float32, (n, W - 1, C), dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    out = dict(dx=torch.empty(tuple(x.shape), **f32), dweight=torch.empty(C, W, **f32),
+               dbias=None if bias is None else torch.empty(C, **f32),
+               d_initial_state=torch.empty(n, W - 1, C, **f32) if want_d_initial_state else None)
+    a.cu_seqlens, a.n_seqs, a.initial_state = _ptr(cu_seqlens), n, _ptr(initial_state)
+    with torch.cuda.device(dev):
+        ws_bytes = int(lib.kda_conv_backward_workspace_size(ctypes.byref(a)))
+        ws = _workspace(ws_bytes, dev)
+        _raise_if(lib.kda_conv_backward(ctypes.byref(a), _ptr(dy), _ptr(d_final_state), _ptr(out["dx"]), _ptr(out["dweight"]),
+                                        _ptr(out["dbias"]), _ptr(out["d_initial_state"]), _ptr(ws), ws_bytes, _stream(dev)))
+    return out
+
+
+# -------------------------------------------------------------- selective state space ---
+
+
+def _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, lead):
+    dev = _device(x)
+    if x.dim() != lead + 1:
+        raise ValueError(f"x must have {lead + 1} dimensions")
+    ch = x.shape[-1]
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be a tensor [D, N]")
+    N = A.shape[1]
+    if not isinstance(B, torch.Tensor) or B.dim() != lead + 2:
+        raise ValueError(f"B must have {lead + 2} dimensions")
+    G = B.shape[-2]
+    rows = tuple(x.shape[:-1])
+    strides = {}
+    for name, t, shape in (("x", x, (*rows, ch)), ("dt", dt, (*rows, ch)), ("B", B, (*rows, G, N)), ("C", C, (*rows, G, N)),
+                           ("z", z, (*rows, ch))):
+        strides[name] = 0 if name == "z" and t is None else _row_stride(name, t, x.dtype, shape, lead, dev)
+    _check("A", A, torch.float32, (ch, N), dev)
+    for name, t in (("D", D), ("dt_bias", dt_bias)):
+        if t is not None:
+            _check(name, t, torch.float32, (ch,), dev)
+    a = ScanArgs(struct_size=ctypes.sizeof(ScanArgs), dtype=_DTYPES[x.dtype], B=x.shape[0], T=x.shape[1] if lead == 2 else 1,
+                 D=ch, N=N, G=G, dt_softplus=1 if dt_softplus else 0, x=x.data_ptr(), dt=dt.data_ptr(), Bm=B.data_ptr(),
+                 Cm=C.data_ptr(), z=None if z is None else z.data_ptr(), x_stride=strides["x"], dt_stride=strides["dt"],
+                 B_stride=strides["B"], C_stride=strides["C"], z_stride=strides["z"], A=A.data_ptr(),
+                 Dskip=None if D is None else D.data_ptr(), dt_bias=None if dt_bias is None else dt_bias.data_ptr())
+    return a, dev, ch, N, G
+
+
+def scan_prefill(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, cu_seqlens=None, initial_state=None,
+                 output_final_state=True, y=None, final_state=None, initial_state_indices=None, final_state_indices=None):
+    """Selective state space scan of whole sequences.
+
+    x, dt, z [B, T, D] and B, C [B, T, G, N], bf16 or fp32, rows may be strided; A [D, N] (negative for a decay), D
+    and dt_bias [D], fp32. With dt' = softplus(dt + dt_bias) (or dt + dt_bias), per channel c of group g:
+    h_t = exp(dt'_t A) h_{t-1} + dt'_t x_t B_t,  y_t = sum_n C_t h_t + D x_t, times z_t sigmoid(z_t) with a gate.
+    ``cu_seqlens``, states (fp32 [N_seqs, D, N]) and pools as in ``prefill``. Returns (y [B, T, D], final_state or None).
+    """
+    lib = _library()
+    a, dev, ch, N, _ = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 2)
+    n = _sequences(cu_seqlens, x.shape[0], dev)
+    pool = _states(initial_state, final_state, initial_state_indices, final_state_indices, n, (ch, N), torch.float32, dev)
+    y = _output("y", y, x.dtype, tuple(x.shape), dev)
+    if final_state is None and output_final_state:
+        final_state = torch.empty(n, ch, N, dtype=torch.float32, device=dev)
+    a.cu_seqlens, a.n_seqs, a.initial_state = _ptr(cu_seqlens), n, _ptr(initial_state)
+    a.initial_state_indices, a.final_state_indices = _ptr(initial_state_indices), _ptr(final_state_indices)
+    a.state_pool_size = pool
+    with torch.cuda.device(dev):
+        ws_bytes = int(lib.kda_scan_prefill_workspace_size(ctypes.byref(a)))
+        ws = _workspace(ws_bytes, dev)
+        _raise_if(lib.kda_scan_prefill(ctypes.byref(a), _ptr(y), _ptr(final_state), _ptr(ws), ws_bytes, _stream(dev)))
+    return y, final_state
+
+
+def scan_decode_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softplus=True, state_indices=None,
+                     final_state_indices=None, y=None):
+    """One token of the scan for N sequences: x, dt, z [N, D], B, C [N, G, N_states]; ``state`` fp32
+    [N, D, N_states] (or a pool with ``state_indices`` int32 [N]) is updated in place. Returns y [N, D]."""
+    lib = _library()
+    a, dev, ch, N, _ = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 1)
+    n = x.shape[0]
+    if final_state_indices is not None and state_indices is None:
+        raise ValueError("final_state_indices needs state_indices")
+    _check_indices("state_indices", state_indices, n, dev)
+    _check_indices("final_state_indices", final_state_indices, n, dev)
+    pool = state.shape[0] if state_indices is not None and state.dim() == 3 else 0
+    _check("state", state, torch.float32, (pool if state_indices is not None else n, ch, N), dev)
+    y = _output("y", y, x.dtype, (n, ch), dev)
+    a.initial_state_indices, a.final_state_indices, a.state_pool_size = _ptr(state_indices), _ptr(final_state_indices), pool
+    with torch.cuda.device(dev):
+        _raise_if(lib.kda_scan_decode_step(ctypes.byref(a), _ptr(state), _ptr(y), _stream(dev)))
+    return y
+
+
+def scan_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_softplus=True, cu_seqlens=None, initial_state=None,
+                  d_final_state=None, want_d_initial_state=True):
+    """Gradients of sum(dy * y) + sum(d_final_state * final_state) through ``scan_prefill`` (no pools). Returns a
+    dict of fp32 tensors shaped like their inputs: dx, ddt, dA, dB, dC, dD, dz, ddt_bias (the last three None
+    without their input) and d_initial_state [N_seqs, D, N] (or None)."""
+    lib = _library()
+    a, dev, ch, N, G = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 2)
+    n = _sequences(cu_seqlens, x.shape[0], dev)
+    _check("dy", dy, x.dtype, tuple(x.shape), dev)
+    _states(initial_state, None, None, None, n, (ch, N), torch.float32, dev)
+    if d_final_state is not None:
+        _check("d_final_state", d_final_state, torch.float32, (n, ch, N), dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    rows = tuple(x.shape[:-1])
+    out = dict(dx=torch.empty(*rows, ch, **f32), ddt=torch.empty(*rows, ch, **f32), dA=torch.empty(ch, N, **f32),
+               dB=torch.empty(*rows, G, N, **f32), dC=torch.empty(*rows, G, N, **f32),
+               dD=None if D is None else torch.empty(ch, **f32), dz=None if z is None else torch.empty(*rows, ch, **f32),
+               ddt_bias=None if dt_bias is None else torch.empty(ch, **f32),
+               d_initial_state=torch.empty(n, ch, N, **f32) if want_d_initial_state else None)
+    a.cu_seqlens, a.n_seqs, a.initial_state = _ptr(cu_seqlens), n, _ptr(initial_state)
+    g = ScanGrads(struct_size=ctypes.sizeof(ScanGrads), dy=_ptr(dy), d_final_state=_ptr(d_final_state), dx=_ptr(out["dx"]),
+                  ddt=_ptr(out["ddt"]), dA=_ptr(out["dA"]), dB=_ptr(out["dB"]), dC=_ptr(out["dC"]), dDskip=_ptr(out["dD"]),
+                  dz=_ptr(out["dz"]), ddt_bias=_ptr(out["ddt_bias"]), d_initial_state=_ptr(out["d_initial_state"]))
+    with torch.cuda.device(dev):
+        ws_bytes = int(lib.kda_scan_backward_workspace_size(ctypes.byref(a)))
+        ws = _workspace(ws_bytes, dev)
+        _raise_if(lib.kda_scan_backward(ctypes.byref(a), ctypes.byref(g), _ptr(ws), ws_bytes, _stream(dev)))
+    return out
+
+
+# ------------------------------------------------------------------- norm and rotation ---
+
+
+def _rotary_args(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved):
+    dev = _device(q)
+    if q.dim() < 2 or not isinstance(k, torch.Tensor) or k.dim() != q.dim():
+        raise ValueError("q and k must be tensors [..., heads, head] with the same rows")
+    if norm not in ("rms", "l2"):
+        raise ValueError(f"unknown norm {norm!r}: 'rms' or 'l2'")
+    lead, head = q.dim() - 2, q.shape[-1]
+    rows = tuple(q.shape[:-2])
+    q_stride = _row_stride("q", q, q.dtype, (*rows, q.shape[-2], head), lead, dev)
+    k_stride = _row_stride("k", k, q.dtype, (*rows, k.shape[-2], head), lead, dev)
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None:
+            _check(name, t, q.dtype, (head,), dev)
+    count = 1
+    for r in rows:
+        count *= r
+    a = RotaryArgs(struct_size=ctypes.sizeof(RotaryArgs), dtype=_DTYPES[q.dtype], rows=count, q_heads=q.shape[-2],
+                   k_heads=k.shape[-2], head=head, norm=0 if norm == "rms" else 1, interleaved=1 if interleaved else 0,
+                   eps=float(eps), q=q.data_ptr(), k=k.data_ptr(), q_stride=q_stride, k_stride=k_stride,
+                   q_weight=None if q_weight is None else q_weight.data_ptr(),
+                   k_weight=None if k_weight is None else k_weight.data_ptr())
+    if (cos is None) != (sin is None) or (cos is None) != (positions is None):
+        raise ValueError("cos, sin and positions are given together or not at all")
+    if cos is not None:
+        if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
+            raise ValueError("cos must be a tensor [table rows, rotated pairs]")
+        _check("cos", cos, torch.float32, tuple(cos.shape), dev)
+        _check("sin", sin, torch.float32, tuple(cos.shape), dev)
+        _check("positions", positions, torch.int32, rows, dev)
+        a.half, a.table_rows = cos.shape[1], cos.shape[0]
+        a.cos_table, a.sin_table, a.positions = _ptr(cos), _ptr(sin), _ptr(positions)
+    return a, dev
+
+
+def qk_norm_rotary(q, k, cos=None, sin=None, positions=None, q_weight=None, k_weight=None, norm="rms", eps=1e-6,
+                   interleaved=False, q_out=None, k_out=None):
+    """Norm of every head's row of q and k, then the position rotation, in one pass.
+
+    q [..., Hq, d], k [..., Hk, d] (bf16 or fp32; the leading dimensions are tokens, whose rows may be strided),
+    weights [d] or None (ones). norm "rms": x weight / sqrt(mean(x^2) + eps); "l2": x weight / sqrt(sum(x^2) + eps), the
+    unit rows ``prefill`` takes. cos, sin fp32 [P, pairs]: line positions[token] (int32) turns the first 2 * pairs
+    values, paired as halves (i, pairs + i), or as (2i, 2i + 1) with ``interleaved``. Without tables there is no
+    rotation. Returns dense (q_out, k_out)."""
+    lib = _library()
+    a, dev = _rotary_args(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
+    q_out = _output("q_out", q_out, q.dtype, tuple(q.shape), dev)
+    k_out = _output("k_out", k_out, q.dtype, tuple(k.shape), dev)
+    with torch.cuda.device(dev):
+        _raise_if(lib.kda_qk_norm_rotary(ctypes.byref(a), _ptr(q_out), _ptr(k_out), _stream(dev)))
+    return q_out, k_out
+
+
+def qk_norm_rotary_backward(q, k, cos, sin, positions, dq_out, dk_out, q_weight=None, k_weight=None, norm="rms", eps=1e-6,
+                            interleaved=False):
+    """Gradients of sum(dq_out * q_out) + sum(dk_out * k_out) through ``qk_norm_rotary``: a dict of fp32 tensors dq, dk,
+    dq_weight, dk_weight (None without the weight). dq_out, dk_out have the outputs' layout and dtype."""
+    lib = _library()
+    a, dev = _rotary_args(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
+    _check("dq_out", dq_out, q.dtype, tuple(q.shape), dev)
+    _check("dk_out", dk_out, q.dtype, tuple(k.shape), dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    out = dict(dq=torch.empty(tuple(q.shape), **f32), dk=torch.empty(tuple(k.shape), **f32),
+               dq_weight=None if q_weight is None else torch.empty(q.shape[-1], **f32),
+               dk_weight=None if k_weight is None else torch.empty(q.shape[-1], **f32))
+    with torch.cuda.device(dev):
+        ws_bytes = int(lib.kda_qk_norm_rotary_backward_workspace_size(ctypes.byref(a)))
+        ws = _workspace(ws_bytes, dev)
+        _raise_if(lib.kda_qk_norm_rotary_backward(ctypes.byref(a), _ptr(dq_out), _ptr(dk_out), _ptr(out["dq"]), _ptr(out["dk"]),
+                                                  _ptr(out["dq_weight"]), _ptr(out["dk_weight"]), _ptr(ws), ws_bytes,
+                                                  _stream(dev)))
+    return out

@@ -299,9 +299,154 @@ KDA_API kda_status kda_decode_step_gated(kda_dtype dtype, int N, int H, int dk, 
                                          void *o, float gate_bound, kda_stream_t stream);
 
 /*
+ * The operators around the mixer. None of them is on the pages; they are what stands between a layer's
+ * projections and kda_prefill / kda_decode_step (a short causal convolution of q, k and v, the norm of q
+ * and k with the position rotation), and the other recurrent mixer of hybrid models (a selective
+ * state space scan). Arguments come in one struct per operator: zero it, set struct_size to its sizeof,
+ * set the fields. The library reads only the first struct_size bytes (later fields are zero).
+ *
+ * Conventions beyond those at the top: "rows" are the B * T tokens (or the T packed ones). Inputs with a
+ * *_stride field may have rows further apart than dense ones (slices of a fused projection): the stride
+ * is in elements between consecutive rows, uniform over the batch, 0 for dense rows. Alignment to
+ * the element size is enough for them; 16-byte aligned rows take the wide loads. Outputs are dense.
+ * Outputs must not overlap inputs, except states updated in place. Packed sequences and state pools as in
+ * kda_prefill and kda_options (a pool's slots have the shape of one sequence's state); a cu_seqlens that is
+ * not a non-decreasing list from 0 to T sets KDA_ERR_INVALID_ARG in the error word and leaves the outputs
+ * unspecified (nothing out of range is read or written). Gradients are fp32, and the same bits
+ * every time (no atomics).
+ */
+
+/*
+ * Short causal convolution, one filter per channel:
+ *     p_t[c] = bias[c] + sum_{j < W} weight[c, j] x_{t - (W - 1) + j}[c],   y_t = p_t or p_t sigmoid(p_t)
+ * within each sequence; the W - 1 inputs before its first come from its state (zeros without one). The state
+ * of a sequence is its last W - 1 inputs, oldest first: [N, W - 1, C] in `dtype`, copied unrounded.
+ */
+typedef struct kda_conv_args {
+    size_t struct_size;
+    kda_dtype dtype;         /* of x, weight, bias, y and the states */
+    int B, T, C, W;          /* x [B, T, C]; W in {2, 3, 4}. Decode: B sequences, T == 1 */
+    int activation;          /* 0: y = p; 1: y = p sigmoid(p) (SiLU) */
+    const void *x;
+    int64_t x_stride;
+    const void *weight;      /* [C, W] */
+    const void *bias;        /* [C] or NULL */
+    const int32_t *cu_seqlens; /* NULL or int32 [n_seqs + 1] (B == 1); not for decode */
+    int n_seqs;
+    const void *initial_state; /* [N, W - 1, C], a pool of such slots with indices, or NULL; not for decode */
+    const int32_t *initial_state_indices; /* NULL or int32 [N] */
+    const int32_t *final_state_indices;   /* NULL or int32 [N]. Decode: NULL means the initial slots */
+    int state_pool_size;
+} kda_conv_args;
+
+/* y [B, T, C]; final_state [N, W - 1, C] (or the pool) or NULL; may be initial_state's memory. */
+KDA_API kda_status kda_conv_prefill(const kda_conv_args *args, void *y, void *final_state, kda_stream_t stream);
+
+/* One token for each of B sequences: x [B, C], y [B, C]; state [B, W - 1, C] (or the pool) is shifted in place. */
+KDA_API kda_status kda_conv_decode_step(const kda_conv_args *args, void *state, void *y, kda_stream_t stream);
+
+/* Gradients of sum(dy * y) + sum(d_final_state * final_state): dx [B, T, C], dweight [C, W], dbias [C] or NULL,
+ * d_initial_state [N, W - 1, C] or NULL, all fp32 and written in full. dy [B, T, C] in `dtype`; d_final_state
+ * fp32 [N, W - 1, C] or NULL (zero). No state pools. workspace: kda_conv_backward_workspace_size() bytes, 16-byte aligned. */
+KDA_API kda_status kda_conv_backward(const kda_conv_args *args, const void *dy, const float *d_final_state, float *dx,
+                                     float *dweight, float *dbias, float *d_initial_state, void *workspace,
+                                     size_t workspace_bytes, kda_stream_t stream);
+KDA_API size_t kda_conv_backward_workspace_size(const kda_conv_args *args);
+
+/*
+ * Selective state space scan: per channel c with N states, group g(c) = c / (D / G),
+ *     dt'_t = dt_t + dt_bias, through softplus if asked;   u_t = dt'_t x_t
+ *     h_t[c, n] = exp(dt'_t[c] A[c, n]) h_{t-1}[c, n] + u_t[c] B_t[g, n]
+ *     y_t[c] = sum_n C_t[g, n] h_t[c, n] + Dskip[c] x_t[c],   times z_t[c] sigmoid(z_t[c]) with a gate z.
+ * States are fp32 [N_seqs, D, N]; all arithmetic is fp32.
+ */
+typedef struct kda_scan_args {
+    size_t struct_size;
+    kda_dtype dtype;         /* of x, dt, Bm, Cm, z and y */
+    int B, T, D, N, G;       /* x [B, T, D]; N states per channel, 1 to 256; G groups, D a multiple of G */
+    int dt_softplus;         /* non-zero: dt' = log(1 + exp(dt + dt_bias)) */
+    const void *x, *dt;      /* [B, T, D] */
+    const void *Bm, *Cm;     /* [B, T, G, N] */
+    const void *z;           /* [B, T, D] or NULL */
+    int64_t x_stride, dt_stride, B_stride, C_stride, z_stride;
+    const float *A;          /* fp32 [D, N] (not its logarithm) */
+    const float *Dskip;      /* fp32 [D] or NULL */
+    const float *dt_bias;    /* fp32 [D] or NULL */
+    const int32_t *cu_seqlens;
+    int n_seqs;
+    const float *initial_state; /* not for decode */
+    const int32_t *initial_state_indices, *final_state_indices; /* as kda_conv_args */
+    int state_pool_size;
+} kda_scan_args;
+
+/* y [B, T, D]; final_state fp32 [N_seqs, D, N] (or the pool) or NULL; may be initial_state's memory.
+ * workspace: kda_scan_prefill_workspace_size() bytes (may be 0), 16-byte aligned. */
+KDA_API kda_status kda_scan_prefill(const kda_scan_args *args, void *y, float *final_state, void *workspace,
+                                    size_t workspace_bytes, kda_stream_t stream);
+KDA_API size_t kda_scan_prefill_workspace_size(const kda_scan_args *args);
+
+/* One token for each of B sequences (T == 1): state fp32 [B, D, N] (or the pool) is updated in place. */
+KDA_API kda_status kda_scan_decode_step(const kda_scan_args *args, float *state, void *y, kda_stream_t stream);
+
+/* Gradients of sum(dy * y) + sum(d_final_state * final_state), all fp32 and written in full. dDskip, dz and ddt_bias are
+ * given exactly when Dskip, z and dt_bias are (NULL otherwise); d_initial_state may be NULL. No state pools.
+ * workspace: kda_scan_backward_workspace_size() bytes, 16-byte aligned. */
+typedef struct kda_scan_grads {
+    size_t struct_size;
+    const void *dy;             /* [B, T, D] in `dtype`, dense */
+    const float *d_final_state; /* fp32 [N_seqs, D, N] or NULL (zero) */
+    float *dx, *ddt;            /* [B, T, D] (ddt: with respect to dt) */
+    float *dA;                  /* [D, N] */
+    float *dB, *dC;             /* [B, T, G, N] */
+    float *dDskip, *dz, *ddt_bias;
+    float *d_initial_state;     /* [N_seqs, D, N] or NULL */
+} kda_scan_grads;
+KDA_API kda_status kda_scan_backward(const kda_scan_args *args, const kda_scan_grads *grads, void *workspace,
+                                     size_t workspace_bytes, kda_stream_t stream);
+KDA_API size_t kda_scan_backward_workspace_size(const kda_scan_args *args);
+
+/*
+ * Norm of every head's row of q and k, and the position rotation, in one pass: with x one row of
+ * `head` values,
+ *     u = x weight / sqrt(mean(x^2) + eps)  (norm 0, RMS)   or   x weight / sqrt(sum(x^2) + eps)  (norm 1, L2)
+ * and then each pair (a, b) of the first 2 * half values, with the angle i of the row's position,
+ *     a' = a cos_i - b sin_i,   b' = b cos_i + a sin_i;   pairs (i, half + i), or (2i, 2i + 1) if interleaved.
+ * L2 with eps 1e-6 is what kda_prefill takes as unit rows (qk_l2norm), and a rotation keeps it so.
+ */
+typedef struct kda_rotary_args {
+    size_t struct_size;
+    kda_dtype dtype;         /* of q, k, the weights and the outputs */
+    int64_t rows;            /* tokens */
+    int q_heads, k_heads;    /* either may be 0 (its pointers are then not read) */
+    int head;                /* values per head: a multiple of 8, at most 256 */
+    int half;                /* rotated pairs: 0 (no rotation), or 2 * half <= head and half a multiple of 8
+                                (of 4 if interleaved) */
+    int norm;                /* 0 RMS, 1 L2 */
+    int interleaved;
+    float eps;               /* >= 0 */
+    const void *q, *k;       /* [rows, heads, head] */
+    int64_t q_stride, k_stride;
+    const void *q_weight, *k_weight; /* [head] or NULL (ones) */
+    const float *cos_table, *sin_table; /* fp32 [table_rows, half] */
+    const int32_t *positions;           /* int32 [rows]: the row's line of the tables. One outside them leaves the row
+                                           unrotated and sets KDA_ERR_INVALID_ARG in the error word */
+    int64_t table_rows;
+} kda_rotary_args;
+
+/* q_out [rows, q_heads, head], k_out [rows, k_heads, head], dense. */
+KDA_API kda_status kda_qk_norm_rotary(const kda_rotary_args *args, void *q_out, void *k_out, kda_stream_t stream);
+
+/* Gradients of sum(dq_out * q_out) + sum(dk_out * k_out): dq, dk like q_out, k_out; dq_weight, dk_weight [head], given
+ * exactly when the weights are (NULL otherwise); all fp32. workspace: kda_qk_norm_rotary_backward_workspace_size() bytes. */
+KDA_API kda_status kda_qk_norm_rotary_backward(const kda_rotary_args *args, const void *dq_out, const void *dk_out,
+                                               float *dq, float *dk, float *dq_weight, float *dk_weight, void *workspace,
+                                               size_t workspace_bytes, kda_stream_t stream);
+KDA_API size_t kda_qk_norm_rotary_backward_workspace_size(const kda_rotary_args *args);
+
+/*
  * kda_check_status -- synchronise `stream`, then read and clear the device error word of the
- * current device. Returns KDA_OK, KDA_ERR_INVALID_ARG (bad cu_seqlens or a state slot past
- * the pool end seen by a kernel), KDA_ERR_TIMEOUT (a bounded pipeline wait gave up; that
+ * current device. Returns KDA_OK, KDA_ERR_INVALID_ARG (bad cu_seqlens, a state slot past the pool
+ * end or a position past the rotation tables seen by a kernel), KDA_ERR_TIMEOUT (a bounded pipeline wait gave up; that
  * (sequence, head) is left unfinished) or KDA_ERR_CUDA (the synchronisation itself failed).
  */
 KDA_API kda_status kda_check_status(kda_stream_t stream);
