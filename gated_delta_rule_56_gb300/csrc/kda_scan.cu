@@ -2,75 +2,252 @@
 //
 //     h_t[c, n] = exp(dt_t[c] A[c, n]) h_{t-1}[c, n] + dt_t[c] x_t[c] B_t[n],   y_t[c] = sum_n C_t[n] h_t[c, n] + D[c] x_t[c]
 //
-// Prompts: one lane per channel holds up to 16 states in registers (more states: 2 to 16 lanes per channel,
-// their parts of y added by shuffles) and walks down its sequence.
+// Prompts: one lane per channel holds up to 16 states in registers (more states: 2 to 16 lanes per channel, their parts of y
+// added by shuffles) and walks down the rows; a block's B and C rows lie in shared memory in fp32, read as broadcasts. Per
+// (token, channel, state) that is 1 exponential and 4 multiply-adds: with 32 exponentials and 128 multiply-adds per SM
+// and cycle both units are busy equally long and HBM waits for them.
+//
+// A sequence has few channels for 152 SMs, so the rows are cut into chunks that run side by side. The state after
+// a chunk is linear in the state before it, h_end = exp(A sum dt) h_begin + (the end state from zeros):
+// a first kernel computes the end states from zeros and the sums of dt, a second one walks over the chunks to get the
+// state before each, and the main kernel runs every chunk from there. That is a second round of exponentials, and it is
+// left out where whole sequences fill the GPU.
 #include "kda_scan.cuh"
 
 namespace kda {
 namespace {
 
-template <typename T, int S, int L>
-__global__ void __launch_bounds__(32) scan_prefill_kernel(ScanParams p, T *__restrict__ y, float *fin) {
-    if (blockIdx.x == 0 && blockIdx.y == 0) check_seqs(p.seqs, p.err);
-    const int per = p.C / p.G;  // channels per group
-    const int blocks = (per * L + 31) / 32;
+constexpr int kUnroll = 8;  // tokens whose inputs are loaded ahead
+
+template <int NP>
+struct Tile {  // tokens of B and C in shared memory at a time: at most 16 KB
+    static constexpr int tokens = NP <= 64 ? 32 : 2048 / NP;
+};
+
+// ENDS: only the end state of the chunk's last sequence (from zeros, or from its initial state if it begins in the chunk).
+template <typename T, int S, int L, bool ENDS>
+__global__ void __launch_bounds__(kScanThreads, 4)
+    scan_prefill_kernel(ScanParams p, T *__restrict__ y, float *fin, ScanPlan plan, Carries carry) {
+    constexpr int NP = S * L, TT = Tile<NP>::tokens, SIDES = ENDS ? 1 : 2;
+    constexpr int EACH = TT * SIDES * NP / kScanThreads;  // values of a tile that a thread brings
+    static_assert(TT % kUnroll == 0 && TT * SIDES * NP % kScanThreads == 0, "tile");
+    __shared__ __align__(16) float tile[2][TT][SIDES][NP];
+    if (!ENDS && blockIdx.x == 0 && blockIdx.y == 0) check_seqs(p.seqs, p.err);
+    const int per = p.C / p.G;
+    const int blocks = (per * L + kScanThreads - 1) / kScanThreads;
     const int g = blockIdx.y / blocks;
-    const int k = (blockIdx.y % blocks) * (32 / L) + threadIdx.x / L, n0 = (threadIdx.x % L) * S;
+    const int k = (blockIdx.y % blocks) * (kScanThreads / L) + threadIdx.x / L, n0 = (threadIdx.x % L) * S;
     const bool live = k < per;
-    const int c = g * per + (live ? k : 0), n = blockIdx.x;
-    const long long bos = p.seqs.begin(n), eos = p.seqs.end(n);
-    if (bos < 0 || eos < bos || eos > p.seqs.rows) return;
-    const long long from = p.init ? state_slot(p.init_idx, p.pool, n, p.err) : -1;
-    float h[S], A[S];
+    const int c = g * per + (live ? k : 0);
+    const long long at_state = (long long)c * p.N + n0, chunk_states = (long long)p.C * p.N;
+    const long long r0 = blockIdx.x * plan.rows, stop = min(r0 + plan.rows, p.seqs.rows);
+
+    f32x2 h[S / 2], A[S / 2];
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-        const bool in = n0 + i < p.N;
-        A[i] = in ? p.A[(long long)c * p.N + n0 + i] * kLog2e : 0.f;
-        h[i] = in && from >= 0 ? p.init[(from * p.C + c) * p.N + n0 + i] : 0.f;
+    for (int i = 0; i < S / 2; ++i) {
+        const int n = n0 + 2 * i;
+        A[i] = pair(n < p.N ? p.A[at_state + 2 * i] * kLog2e : 0.f, n + 1 < p.N ? p.A[at_state + 2 * i + 1] * kLog2e : 0.f);
+        h[i] = 0;
     }
-    const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, skip = p.D ? p.D[c] : 0.f;
-    const T *X = static_cast<const T *>(p.x), *DT = static_cast<const T *>(p.dt), *Z = static_cast<const T *>(p.z);
-    const T *B = static_cast<const T *>(p.Bm) + g * p.N + n0, *Cm = static_cast<const T *>(p.Cm) + g * p.N + n0;
-    for (long long r = bos; r < eos; ++r) {
-        const float x = to_float(X[r * p.x_stride + c]);
-        float dt = to_float(DT[r * p.dt_stride + c]) + bias;
-        if (p.softplus) dt = softplus(dt);
-        const float u = dt * x;
-        float sum = 0.f;
+    auto load = [&](const float *from) {  // the lane's states of one sequence or chunk
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-            if (n0 + i < p.N) {
-                h[i] = fmaf(exp2f(dt * A[i]), h[i], u * to_float(B[r * p.B_stride + i]));
-                sum = fmaf(to_float(Cm[r * p.C_stride + i]), h[i], sum);
+        for (int i = 0; i < S / 2; ++i) {
+            const int n = n0 + 2 * i;
+            h[i] = pair(n < p.N ? from[at_state + 2 * i] : 0.f, n + 1 < p.N ? from[at_state + 2 * i + 1] : 0.f);
+        }
+    };
+    auto store = [&](float *to) {
+        if (!live) return;
+#pragma unroll
+        for (int i = 0; i < S / 2; ++i) {
+            const int n = n0 + 2 * i;
+            float a, b;
+            unpair(h[i], a, b);
+            if (n < p.N) to[at_state + 2 * i] = a;
+            if (n + 1 < p.N) to[at_state + 2 * i + 1] = b;
+        }
+    };
+    auto initial = [&](int n) {
+        const long long slot = p.init ? state_slot(p.init_idx, p.pool, n, p.err) : -1;
+        if (slot >= 0) {
+            load(p.init + slot * chunk_states);
+        } else {
+#pragma unroll
+            for (int i = 0; i < S / 2; ++i) h[i] = 0;
+        }
+    };
+    auto final_state = [&](int n) {
+        if (!fin) return;
+        const long long slot = state_slot(p.fin_idx, p.pool, n, p.err);
+        if (slot >= 0) store(fin + slot * chunk_states);
+    };
+    // After the end of sequence n: its final state, and those of the empty sequences behind it.
+    auto close_sequence = [&](int n) {
+        final_state(n);
+        for (++n; n < p.seqs.n_seqs && p.seqs.begin(n) == p.seqs.end(n); ++n) {
+            initial(n);
+            final_state(n);
+        }
+        return n;
+    };
+
+    long long r = r0;
+    int seq = 0;
+    if constexpr (ENDS) {
+        seq = p.seqs.at(stop - 1);
+        const long long bos = p.seqs.begin(seq);
+        if (bos >= r0 && bos < stop) {
+            r = bos;
+            initial(seq);
+            store(carry.first + blockIdx.x * chunk_states);
+        }
+    } else {
+        if (blockIdx.x == 0)  // empty sequences before the first row
+            for (; seq < p.seqs.n_seqs && p.seqs.begin(seq) == p.seqs.end(seq) && p.seqs.begin(seq) == 0; ++seq) {
+                initial(seq);
+                final_state(seq);
+            }
+        if (r0 >= stop) return;
+        seq = p.seqs.at(r0);
+        if (plan.carries && p.seqs.begin(seq) < r0) load(carry.state + blockIdx.x * chunk_states);
+    }
+    // The row at which the next sequence begins; the last sequence that begins here and goes on after the chunk
+    // takes its initial state from the first kernel's copy, because another block may write its final state there.
+    long long end = p.seqs.end(seq);
+    auto begin_sequence = [&](int n) {
+        end = p.seqs.end(n);
+        if (plan.carries && end > stop && blockIdx.x + 1 < plan.chunks)
+            load(carry.first + blockIdx.x * chunk_states);
+        else
+            initial(n);
+    };
+    if (!ENDS && p.seqs.begin(seq) == r0) begin_sequence(seq);
+
+    const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, skip = p.D ? p.D[c] : 0.f;
+    const T *X = static_cast<const T *>(p.x) + c, *DT = static_cast<const T *>(p.dt) + c;
+    const T *Z = p.z ? static_cast<const T *>(p.z) + c : nullptr;
+    const T *Bm = static_cast<const T *>(p.Bm) + g * p.N, *Cm = static_cast<const T *>(p.Cm) + g * p.N;
+
+    T ahead[EACH];
+    auto fetch = [&](long long first) {  // the next tile's values of this thread
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int v = i * kScanThreads + threadIdx.x, n = v % NP, side = (v / NP) % SIDES;
+            const long long row = first + v / (NP * SIDES);
+            ahead[i] = row < stop && n < p.N ? (side ? Cm[row * p.C_stride + n] : Bm[row * p.B_stride + n]) : from_float<T>(0.f);
+        }
+    };
+    T rx[kUnroll], rdt[kUnroll], rz[kUnroll];
+    auto fetch_rows = [&](long long first) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const long long row = min(first + u, stop - 1);
+            rx[u] = X[row * p.x_stride];
+            rdt[u] = DT[row * p.dt_stride];
+            if (!ENDS && Z) rz[u] = Z[row * p.z_stride];
+        }
+    };
+    float total = 0.f;
+    fetch(r);
+    fetch_rows(r);
+    for (int buf = 0; r < stop; buf ^= 1) {
+        float *mine = &tile[buf][0][0][0];
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) mine[i * kScanThreads + threadIdx.x] = to_float(ahead[i]);
+        __syncthreads();  // two buffers: the one written next was last read before this barrier
+        fetch(r + TT);
+        for (int t0 = 0; t0 < TT && r < stop; t0 += kUnroll) {
+            float xs[kUnroll], dts[kUnroll], zs[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                xs[u] = to_float(rx[u]);
+                dts[u] = to_float(rdt[u]) + bias;
+                zs[u] = !ENDS && Z ? to_float(rz[u]) : 0.f;
+            }
+            fetch_rows(r + kUnroll);
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u, ++r) {
+                if (r >= stop) break;
+                if (!ENDS && r == end) {
+                    seq = close_sequence(seq);
+                    if (seq >= p.seqs.n_seqs) return;  // rows past the last sequence: a bad cu_seqlens
+                    begin_sequence(seq);
+                }
+                const float dt = p.softplus ? softplus(dts[u]) : dts[u];
+                const f32x2 dt2 = pair(dt, dt), u2 = pair(dt * xs[u], dt * xs[u]);
+                const f32x2 *B2 = reinterpret_cast<const f32x2 *>(&tile[buf][t0 + u][0][n0]);
+                const f32x2 *C2 = reinterpret_cast<const f32x2 *>(&tile[buf][t0 + u][SIDES - 1][n0]);
+                f32x2 sum2 = 0;
+#pragma unroll
+                for (int i = 0; i < S / 2; ++i) {
+                    h[i] = fma2(ex2_pair(mul2(dt2, A[i])), h[i], mul2(u2, B2[i]));
+                    if constexpr (!ENDS) sum2 = fma2(C2[i], h[i], sum2);
+                }
+                if constexpr (ENDS) {
+                    total += dt;
+                } else {
+                    float sum, other;
+                    unpair(sum2, sum, other);
+                    sum += other;
+#pragma unroll
+                    for (int m = L / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+                    sum = fmaf(skip, xs[u], sum);
+                    if (Z) sum *= zs[u] * sigmoid(zs[u]);
+                    if (live && n0 == 0) y[r * p.C + c] = from_float<T>(sum);
+                }
             }
         }
-#pragma unroll
-        for (int m = L / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        sum = fmaf(skip, x, sum);
-        if (Z) {
-            const float z = to_float(Z[r * p.z_stride + c]);
-            sum *= z * sigmoid(z);
-        }
-        if (live && n0 == 0) y[r * p.C + c] = from_float<T>(sum);
     }
-    if (!fin || !live) return;
-    const long long to = state_slot(p.fin_idx, p.pool, n, p.err);
-    if (to < 0) return;
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-        if (n0 + i < p.N) fin[(to * p.C + c) * p.N + n0 + i] = h[i];
+    if constexpr (ENDS) {
+        store(carry.state + blockIdx.x * chunk_states);
+        if (live && n0 == 0) carry.time[(long long)blockIdx.x * p.C + c] = total;
+    } else {
+        if (stop == end) close_sequence(seq);
+    }
+}
+
+// From the chunks' end states to the states before them, one thread per (channel, state).
+__global__ void __launch_bounds__(256) scan_carry_kernel(ScanParams p, ScanPlan plan, Carries carry) {
+    const long long size = (long long)p.C * p.N, i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= size) return;
+    const float A = p.A[i] * kLog2e;
+    const long long c = i / p.N;
+    float before = 0.f;
+    for (int j = 0; j < plan.chunks; ++j) {
+        const float local = j + 1 < plan.chunks ? carry.state[j * size + i] : 0.f;
+        const float time = j + 1 < plan.chunks ? carry.time[(long long)j * p.C + c] : 0.f;
+        carry.state[j * size + i] = before;
+        if (j + 1 == plan.chunks) break;
+        const long long r0 = j * plan.rows, last = min(r0 + plan.rows, p.seqs.rows) - 1;
+        const bool fresh = p.seqs.begin(p.seqs.at(last)) >= r0;
+        before = fresh ? local : fmaf(ex2(A * time), before, local);
+    }
+}
+
+Carries carries_in(const kda_scan_args &a, const ScanPlan &plan, void *ws) {
+    const size_t states = (size_t)plan.chunks * a.D * a.N;
+    float *f = static_cast<float *>(ws);
+    return Carries{f, f + states, f + 2 * states};
 }
 
 struct PrefillLaunch {
     ScanParams p;
     void *y;
     float *fin;
+    ScanPlan plan;
+    Carries carry;
     cudaStream_t s;
     template <typename T, int S, int L>
     void operator()() {
         const int per = p.C / p.G;
-        scan_prefill_kernel<T, S, L><<<dim3((unsigned)p.seqs.n_seqs, (unsigned)(((per * L + 31) / 32) * p.G)), 32, 0, s>>>(
-            p, static_cast<T *>(y), fin);
+        const unsigned blocks = (unsigned)(((per * L + kScanThreads - 1) / kScanThreads) * p.G);
+        if (plan.carries) {
+            scan_prefill_kernel<T, S, L, true><<<dim3((unsigned)plan.chunks - 1, blocks), kScanThreads, 0, s>>>(p, nullptr, nullptr, plan, carry);
+            const long long size = (long long)p.C * p.N;
+            scan_carry_kernel<<<(unsigned)((size + 255) / 256), 256, 0, s>>>(p, plan, carry);
+        }
+        scan_prefill_kernel<T, S, L, false><<<dim3((unsigned)plan.chunks, blocks), kScanThreads, 0, s>>>(
+            p, static_cast<T *>(y), fin, plan, carry);
     }
 };
 
@@ -141,11 +318,29 @@ void launch_decode(const ScanParams &p, float *state, void *y, cudaStream_t s) {
 
 }  // namespace
 
-size_t scan_prefill_workspace_bytes(const kda_scan_args &, int) { return 0; }
+// Whole sequences where they give every SM a block; otherwise chunks that give it four, of at least 64 rows. (Half as many or
+// twice as many were slower on one sequence of 16384 rows and 4096 channels.)
+ScanPlan scan_plan(const kda_scan_args &a, int sms) {
+    const long long rows = (long long)a.B * a.T, blocks = (long long)scan_blocks(a) * a.G;
+    if (rows == 0) return ScanPlan{1, 1, false};
+    if (sms <= 0) sms = 152;
+    if (!a.cu_seqlens && (a.B * blocks >= sms || a.T <= 64)) return ScanPlan{a.B, a.T, false};
+    long long chunks = 4LL * sms / blocks, most = (rows + 63) / 64;
+    chunks = chunks < 1 ? 1 : chunks > most ? most : chunks;
+    long long per = ((rows + chunks - 1) / chunks + 31) / 32 * 32;
+    chunks = (rows + per - 1) / per;
+    return ScanPlan{(int)chunks, per, chunks > 1};
+}
 
-cudaError_t launch_scan_prefill(const kda_scan_args &a, void *y, float *final_state, void *, int, unsigned *err,
+size_t scan_prefill_workspace_bytes(const kda_scan_args &a, int sms) {
+    const ScanPlan plan = scan_plan(a, sms);
+    return plan.carries ? (size_t)plan.chunks * a.D * (2 * a.N + 1) * sizeof(float) : 0;
+}
+
+cudaError_t launch_scan_prefill(const kda_scan_args &a, void *y, float *final_state, void *ws, int sms, unsigned *err,
                                 cudaStream_t s) {
-    return scan_by_type(a, PrefillLaunch{scan_params(a, err), y, final_state, s});
+    const ScanPlan plan = scan_plan(a, sms);
+    return scan_by_type(a, PrefillLaunch{scan_params(a, err), y, final_state, plan, carries_in(a, plan, ws), s});
 }
 
 cudaError_t launch_scan_decode(const kda_scan_args &a, float *state, void *y, unsigned *err, cudaStream_t s) {

@@ -145,15 +145,9 @@ struct BackwardLaunch {
     }
 };
 
-int lanes_per_channel(int N) {
-    int L = 1;
-    while (L * 16 < N) L *= 2;
-    return L;
-}
-
 size_t layout(const kda_scan_args &a, GradParams *q, char *ws) {
     const long long rows = (long long)a.B * a.T, n = a.cu_seqlens ? a.n_seqs : a.B;
-    const int blocks = (a.D / a.G * lanes_per_channel(a.N) + 31) / 32;
+    const int blocks = (a.D / a.G * scan_lanes(a.N) + 31) / 32;
     size_t at = 0;
     auto take = [&](size_t count) {
         float *r = reinterpret_cast<float *>(ws + at);
