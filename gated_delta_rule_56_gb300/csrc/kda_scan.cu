@@ -124,8 +124,7 @@ __global__ void __launch_bounds__(kScanThreads, 4)
     if (!ENDS && p.seqs.begin(seq) == r0) begin_sequence(seq);
 
     const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, skip = p.D ? p.D[c] : 0.f;
-    const T *X = static_cast<const T *>(p.x) + c, *DT = static_cast<const T *>(p.dt) + c;
-    const T *Z = p.z ? static_cast<const T *>(p.z) + c : nullptr;
+    const T *X = static_cast<const T *>(p.x), *DT = static_cast<const T *>(p.dt), *Z = static_cast<const T *>(p.z);
     const T *Bm = static_cast<const T *>(p.Bm) + g * p.N, *Cm = static_cast<const T *>(p.Cm) + g * p.N;
 
     T ahead[EACH];
@@ -137,90 +136,135 @@ __global__ void __launch_bounds__(kScanThreads, 4)
             ahead[i] = row < stop && n < p.N ? (side ? Cm[row * p.C_stride + n] : Bm[row * p.B_stride + n]) : from_float<T>(0.f);
         }
     };
-    T rx[kUnroll], rdt[kUnroll], rz[kUnroll];
+    T rx[kUnroll], rdt[kUnroll], rz[kUnroll];  // the inputs of rows ahead_row .. ahead_row + kUnroll - 1
+    long long ahead_row = -1;
     auto fetch_rows = [&](long long first) {
+        const T *xr = X + first * p.x_stride, *dtr = DT + first * p.dt_stride, *zr = Z + first * p.z_stride;
+        ahead_row = first;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const long long row = min(first + u, stop - 1);
-            rx[u] = X[row * p.x_stride];
-            rdt[u] = DT[row * p.dt_stride];
-            if (!ENDS && Z) rz[u] = Z[row * p.z_stride];
+            rx[u] = xr[u * p.x_stride + c];
+            rdt[u] = dtr[u * p.dt_stride + c];
+            if (!ENDS && Z) rz[u] = zr[u * p.z_stride + c];
         }
     };
-    float total = 0.f;
+    f32x2 total = 0;
+    // Two tokens, both of the running sequence, with B and C rows at `bc`; the second only if `two`.
+    auto step = [&](float x0, float x1, float dt0, float dt1, float z0, float z1, const float *bc, T *out, bool two) {
+        const f32x2 x2 = pair(x0, x1);
+        f32x2 dt2 = add2(pair(dt0, dt1), both(bias));
+        if (p.softplus) dt2 = softplus2(dt2);
+        float dts[2], us[2], sums[2];
+        unpair(dt2, dts[0], dts[1]);
+        unpair(mul2(dt2, x2), us[0], us[1]);
+        if constexpr (ENDS) total = add2(total, two ? dt2 : pair(dts[0], 0.f));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (j == 1 && !two) break;
+            const f32x2 *B2 = reinterpret_cast<const f32x2 *>(bc + j * SIDES * NP);
+            const f32x2 *C2 = reinterpret_cast<const f32x2 *>(bc + (j * SIDES + SIDES - 1) * NP);
+            const f32x2 t2 = both(dts[j]), u2 = both(us[j]);
+            f32x2 sum2 = 0;
+#pragma unroll
+            for (int i = 0; i < S / 2; ++i) {
+                h[i] = fma2(ex2_pair(mul2(t2, A[i])), h[i], mul2(u2, B2[i]));
+                if constexpr (!ENDS) sum2 = i == 0 ? mul2(C2[i], h[i]) : fma2(C2[i], h[i], sum2);
+            }
+            if constexpr (!ENDS) {
+                float other;
+                unpair(sum2, sums[j], other);
+                sums[j] += other;
+#pragma unroll
+                for (int m = L / 2; m > 0; m >>= 1) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], m);
+            }
+        }
+        if constexpr (!ENDS) {
+            f32x2 y2 = fma2(both(skip), x2, pair(sums[0], two ? sums[1] : 0.f));
+            if (Z) y2 = mul2(y2, silu2(pair(z0, z1)));
+            unpair(y2, sums[0], sums[1]);
+            if (live && n0 == 0) {
+                out[c] = from_float<T>(sums[0]);
+                if (two) out[p.C + c] = from_float<T>(sums[1]);
+            }
+        }
+    };
     fetch(r);
-    fetch_rows(r);
     for (int buf = 0; r < stop; buf ^= 1) {
         float *mine = &tile[buf][0][0][0];
 #pragma unroll
         for (int i = 0; i < EACH; ++i) mine[i * kScanThreads + threadIdx.x] = to_float(ahead[i]);
         __syncthreads();  // two buffers: the one written next was last read before this barrier
         fetch(r + TT);
-        for (int t0 = 0; t0 < TT && r < stop; t0 += kUnroll) {
-            float xs[kUnroll], dts[kUnroll], zs[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                xs[u] = to_float(rx[u]);
-                dts[u] = to_float(rdt[u]) + bias;
-                zs[u] = !ENDS && Z ? to_float(rz[u]) : 0.f;
+        const float *bc = mine + n0;
+        const long long tile_end = min(r + TT, stop);
+        while (r < tile_end) {
+            if (!ENDS && r == end) {
+                seq = close_sequence(seq);
+                if (seq >= p.seqs.n_seqs) return;  // rows past the last sequence: a bad cu_seqlens
+                begin_sequence(seq);
             }
-            fetch_rows(r + kUnroll);
+            const long long until = !ENDS && end > r && end < tile_end ? end : tile_end;
+            for (; r + kUnroll <= until; r += kUnroll, bc += kUnroll * SIDES * NP) {
+                if (ahead_row != r) fetch_rows(r);
+                float xs[kUnroll], dts[kUnroll], zs[kUnroll];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u, ++r) {
-                if (r >= stop) break;
-                if (!ENDS && r == end) {
-                    seq = close_sequence(seq);
-                    if (seq >= p.seqs.n_seqs) return;  // rows past the last sequence: a bad cu_seqlens
-                    begin_sequence(seq);
+                for (int u = 0; u < kUnroll; ++u) {
+                    xs[u] = to_float(rx[u]);
+                    dts[u] = to_float(rdt[u]);
+                    zs[u] = !ENDS && Z ? to_float(rz[u]) : 0.f;
                 }
-                const float dt = p.softplus ? softplus(dts[u]) : dts[u];
-                const f32x2 dt2 = pair(dt, dt), u2 = pair(dt * xs[u], dt * xs[u]);
-                const f32x2 *B2 = reinterpret_cast<const f32x2 *>(&tile[buf][t0 + u][0][n0]);
-                const f32x2 *C2 = reinterpret_cast<const f32x2 *>(&tile[buf][t0 + u][SIDES - 1][n0]);
-                f32x2 sum2 = 0;
+                if (r + 2 * kUnroll <= stop) fetch_rows(r + kUnroll);
+                T *out = y + r * p.C;
 #pragma unroll
-                for (int i = 0; i < S / 2; ++i) {
-                    h[i] = fma2(ex2_pair(mul2(dt2, A[i])), h[i], mul2(u2, B2[i]));
-                    if constexpr (!ENDS) sum2 = fma2(C2[i], h[i], sum2);
-                }
-                if constexpr (ENDS) {
-                    total += dt;
-                } else {
-                    float sum, other;
-                    unpair(sum2, sum, other);
-                    sum += other;
-#pragma unroll
-                    for (int m = L / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-                    sum = fmaf(skip, xs[u], sum);
-                    if (Z) sum *= zs[u] * sigmoid(zs[u]);
-                    if (live && n0 == 0) y[r * p.C + c] = from_float<T>(sum);
-                }
+                for (int u = 0; u < kUnroll; u += 2)
+                    step(xs[u], xs[u + 1], dts[u], dts[u + 1], zs[u], zs[u + 1], bc + u * SIDES * NP, out + u * p.C, true);
+            }
+#pragma unroll 1
+            for (; r < until; ++r, bc += SIDES * NP) {  // a few tokens before an end
+                const float x0 = to_float(X[r * p.x_stride + c]), dt0 = to_float(DT[r * p.dt_stride + c]);
+                const float z0 = !ENDS && Z ? to_float(Z[r * p.z_stride + c]) : 0.f;
+                step(x0, 0.f, dt0, 0.f, z0, 0.f, bc, y + r * p.C, false);
             }
         }
     }
     if constexpr (ENDS) {
         store(carry.state + blockIdx.x * chunk_states);
-        if (live && n0 == 0) carry.time[(long long)blockIdx.x * p.C + c] = total;
+        float even, odd;
+        unpair(total, even, odd);
+        if (live && n0 == 0) carry.time[(long long)blockIdx.x * p.C + c] = even + odd;
     } else {
         if (stop == end) close_sequence(seq);
     }
 }
 
-// From the chunks' end states to the states before them, one thread per (channel, state).
-__global__ void __launch_bounds__(256) scan_carry_kernel(ScanParams p, ScanPlan plan, Carries carry) {
-    const long long size = (long long)p.C * p.N, i = (long long)blockIdx.x * 256 + threadIdx.x;
+// From the chunks' end states to the states before them, one thread per (channel, state). A batch of chunks is
+// loaded before the walk over it, which is bound by the latency of those loads.
+constexpr int kCarryBatch = 16;
+__global__ void __launch_bounds__(128) scan_carry_kernel(ScanParams p, ScanPlan plan, Carries carry) {
+    extern __shared__ unsigned char fresh[];  // chunk j's last sequence begins in it
+    for (int j = threadIdx.x; j < plan.chunks - 1; j += 128) {
+        const long long r0 = j * plan.rows;
+        fresh[j] = p.seqs.begin(p.seqs.at(r0 + plan.rows - 1)) >= r0;
+    }
+    __syncthreads();
+    const long long size = (long long)p.C * p.N, i = (long long)blockIdx.x * 128 + threadIdx.x;
     if (i >= size) return;
     const float A = p.A[i] * kLog2e;
     const long long c = i / p.N;
     float before = 0.f;
-    for (int j = 0; j < plan.chunks; ++j) {
-        const float local = j + 1 < plan.chunks ? carry.state[j * size + i] : 0.f;
-        const float time = j + 1 < plan.chunks ? carry.time[(long long)j * p.C + c] : 0.f;
-        carry.state[j * size + i] = before;
-        if (j + 1 == plan.chunks) break;
-        const long long r0 = j * plan.rows, last = min(r0 + plan.rows, p.seqs.rows) - 1;
-        const bool fresh = p.seqs.begin(p.seqs.at(last)) >= r0;
-        before = fresh ? local : fmaf(ex2(A * time), before, local);
+    for (int j0 = 0; j0 < plan.chunks; j0 += kCarryBatch) {
+        float local[kCarryBatch], time[kCarryBatch];
+#pragma unroll
+        for (int b = 0; b < kCarryBatch; ++b) {
+            const bool in = j0 + b + 1 < plan.chunks;  // nothing follows the last chunk
+            local[b] = in ? carry.state[(j0 + b) * size + i] : 0.f;
+            time[b] = in ? carry.time[(long long)(j0 + b) * p.C + c] : 0.f;
+        }
+#pragma unroll
+        for (int b = 0; b < kCarryBatch; ++b) {
+            if (j0 + b < plan.chunks) carry.state[(j0 + b) * size + i] = before;
+            if (j0 + b + 1 < plan.chunks) before = fresh[j0 + b] ? local[b] : fmaf(ex2(A * time[b]), before, local[b]);
+        }
     }
 }
 
@@ -244,7 +288,7 @@ struct PrefillLaunch {
         if (plan.carries) {
             scan_prefill_kernel<T, S, L, true><<<dim3((unsigned)plan.chunks - 1, blocks), kScanThreads, 0, s>>>(p, nullptr, nullptr, plan, carry);
             const long long size = (long long)p.C * p.N;
-            scan_carry_kernel<<<(unsigned)((size + 255) / 256), 256, 0, s>>>(p, plan, carry);
+            scan_carry_kernel<<<(unsigned)((size + 127) / 128), 128, (size_t)plan.chunks, s>>>(p, plan, carry);
         }
         scan_prefill_kernel<T, S, L, false><<<dim3((unsigned)plan.chunks, blocks), kScanThreads, 0, s>>>(
             p, static_cast<T *>(y), fin, plan, carry);
