@@ -2,7 +2,7 @@
 //
 //     h_t[c, n] = exp(dt_t[c] A[c, n]) h_{t-1}[c, n] + dt_t[c] x_t[c] B_t[n],   y_t[c] = sum_n C_t[n] h_t[c, n] + D[c] x_t[c]
 //
-// Prompts: one lane per channel holds up to 16 states in registers (more states: 2 to 16 lanes per channel, their parts of y
+// Prompts: one lane per two channels holds up to 16 states of each in registers (more states: 2 to 16 lanes, their parts of y
 // added by shuffles) and walks down the rows; a block's B and C rows lie in shared memory in fp32, read as broadcasts. Per
 // (token, channel, state) that is 1 exponential and 4 multiply-adds: with 32 exponentials and 128 multiply-adds per SM
 // and cycle both units are busy equally long and HBM waits for them.
@@ -17,64 +17,91 @@
 namespace kda {
 namespace {
 
-constexpr int kUnroll = 8;  // tokens whose inputs are loaded ahead
+constexpr int kWarps = kScanThreads / 32;
+template <typename T>
+constexpr int kBlock = 16 / sizeof(T);  // tokens that are loaded together and computed without a look at sequence ends
 
 template <int NP>
 struct Tile {  // tokens of B and C in shared memory at a time: at most 16 KB
     static constexpr int tokens = NP <= 64 ? 32 : 2048 / NP;
 };
 
+// A lane's two channels of one row.
+template <typename T>
+struct alignas(2 * sizeof(T)) Two {
+    T a, b;
+};
+template <typename T>
+__device__ __forceinline__ f32x2 to_pair(Two<T> v) { return pair(to_float(v.a), to_float(v.b)); }
+
+__device__ __forceinline__ void copy16(void *to, const void *from) {  // global -> shared, asynchronous
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copies_arrived() { asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory"); }
+
 // ENDS: only the end state of the chunk's last sequence (from zeros, or from its initial state if it begins in the chunk).
-template <typename T, int S, int L, bool ENDS>
-__global__ void __launch_bounds__(kScanThreads, 4)
+// WIDE: every row's channels lie on 16-byte boundaries. A lane holds S states of two channels, which share the reads of B and C.
+// The rows of x, dt and z come through a ring in shared memory, each warp its own channels' rows, STAGES - 1 blocks ahead:
+// loads into registers were moved back to their use by the compiler, and a third of the time was spent waiting for them.
+template <typename T, int S, int L, bool WIDE, bool ENDS>
+__global__ void __launch_bounds__(kScanThreads, 3)
     scan_prefill_kernel(ScanParams p, T *__restrict__ y, float *fin, ScanPlan plan, Carries carry) {
+    constexpr int BLK = kBlock<T>;
     constexpr int NP = S * L, TT = Tile<NP>::tokens, SIDES = ENDS ? 1 : 2;
     constexpr int EACH = TT * SIDES * NP / kScanThreads;  // values of a tile that a thread brings
-    static_assert(TT % kUnroll == 0 && TT * SIDES * NP % kScanThreads == 0, "tile");
+    static_assert(TT % BLK == 0 && TT * SIDES * NP % kScanThreads == 0, "tile");
     __shared__ __align__(16) float tile[2][TT][SIDES][NP];
     if (!ENDS && blockIdx.x == 0 && blockIdx.y == 0) check_seqs(p.seqs, p.err);
     const int per = p.C / p.G;
-    const int blocks = (per * L + kScanThreads - 1) / kScanThreads;
+    const int blocks = (per * L + 2 * kScanThreads - 1) / (2 * kScanThreads);
     const int g = blockIdx.y / blocks;
-    const int k = (blockIdx.y % blocks) * (kScanThreads / L) + threadIdx.x / L, n0 = (threadIdx.x % L) * S;
-    const bool live = k < per;
-    const int c = g * per + (live ? k : 0);
-    const long long at_state = (long long)c * p.N + n0, chunk_states = (long long)p.C * p.N;
+    const int k = ((blockIdx.y % blocks) * (kScanThreads / L) + threadIdx.x / L) * 2, n0 = (threadIdx.x % L) * S;
+    const bool live = k < per, live1 = k + 1 < per;
+    const int c = g * per + (live ? k : 0), c1 = live1 ? c + 1 : c;
+    const long long chunk_states = (long long)p.C * p.N;
     const long long r0 = blockIdx.x * plan.rows, stop = min(r0 + plan.rows, p.seqs.rows);
 
-    f32x2 h[S / 2], A[S / 2];
+    f32x2 h[2][S / 2], A[2][S / 2];
+    auto load_states = [&](const float *from, f32x2(&to)[2][S / 2], float scale) {  // a tensor [C][N]
 #pragma unroll
-    for (int i = 0; i < S / 2; ++i) {
-        const int n = n0 + 2 * i;
-        A[i] = pair(n < p.N ? p.A[at_state + 2 * i] * kLog2e : 0.f, n + 1 < p.N ? p.A[at_state + 2 * i + 1] * kLog2e : 0.f);
-        h[i] = 0;
-    }
-    auto load = [&](const float *from) {  // the lane's states of one sequence or chunk
+        for (int j = 0; j < 2; ++j) {
+            const float *row = from + (long long)(j ? c1 : c) * p.N + n0;
 #pragma unroll
-        for (int i = 0; i < S / 2; ++i) {
-            const int n = n0 + 2 * i;
-            h[i] = pair(n < p.N ? from[at_state + 2 * i] : 0.f, n + 1 < p.N ? from[at_state + 2 * i + 1] : 0.f);
+            for (int i = 0; i < S / 2; ++i) {
+                const int n = n0 + 2 * i;
+                to[j][i] = pair(n < p.N ? row[2 * i] * scale : 0.f, n + 1 < p.N ? row[2 * i + 1] * scale : 0.f);
+            }
         }
     };
-    auto store = [&](float *to) {
-        if (!live) return;
+    load_states(p.A, A, kLog2e);
+    auto clear = [&]() {
 #pragma unroll
-        for (int i = 0; i < S / 2; ++i) {
-            const int n = n0 + 2 * i;
-            float a, b;
-            unpair(h[i], a, b);
-            if (n < p.N) to[at_state + 2 * i] = a;
-            if (n + 1 < p.N) to[at_state + 2 * i + 1] = b;
+        for (int i = 0; i < S / 2; ++i) h[0][i] = h[1][i] = 0;
+    };
+    clear();
+    auto store = [&](float *to) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (!(j ? live1 : live)) continue;
+            float *row = to + (long long)(c + j) * p.N + n0;
+#pragma unroll
+            for (int i = 0; i < S / 2; ++i) {
+                const int n = n0 + 2 * i;
+                float v0, v1;
+                unpair(h[j][i], v0, v1);
+                if (n < p.N) row[2 * i] = v0;
+                if (n + 1 < p.N) row[2 * i + 1] = v1;
+            }
         }
     };
     auto initial = [&](int n) {
         const long long slot = p.init ? state_slot(p.init_idx, p.pool, n, p.err) : -1;
-        if (slot >= 0) {
-            load(p.init + slot * chunk_states);
-        } else {
-#pragma unroll
-            for (int i = 0; i < S / 2; ++i) h[i] = 0;
-        }
+        if (slot >= 0)
+            load_states(p.init + slot * chunk_states, h, 1.f);
+        else
+            clear();
     };
     auto final_state = [&](int n) {
         if (!fin) return;
@@ -109,7 +136,7 @@ __global__ void __launch_bounds__(kScanThreads, 4)
             }
         if (r0 >= stop) return;
         seq = p.seqs.at(r0);
-        if (plan.carries && p.seqs.begin(seq) < r0) load(carry.state + blockIdx.x * chunk_states);
+        if (plan.carries && p.seqs.begin(seq) < r0) load_states(carry.state + blockIdx.x * chunk_states, h, 1.f);
     }
     // The row at which the next sequence begins; the last sequence that begins here and goes on after the chunk
     // takes its initial state from the first kernel's copy, because another block may write its final state there.
@@ -117,13 +144,13 @@ __global__ void __launch_bounds__(kScanThreads, 4)
     auto begin_sequence = [&](int n) {
         end = p.seqs.end(n);
         if (plan.carries && end > stop && blockIdx.x + 1 < plan.chunks)
-            load(carry.first + blockIdx.x * chunk_states);
+            load_states(carry.first + blockIdx.x * chunk_states, h, 1.f);
         else
             initial(n);
     };
     if (!ENDS && p.seqs.begin(seq) == r0) begin_sequence(seq);
 
-    const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, skip = p.D ? p.D[c] : 0.f;
+    const f32x2 bias = p.dt_bias ? pair(p.dt_bias[c], p.dt_bias[c1]) : 0, skip = p.D ? pair(p.D[c], p.D[c1]) : 0;
     const T *X = static_cast<const T *>(p.x), *DT = static_cast<const T *>(p.dt), *Z = static_cast<const T *>(p.z);
     const T *Bm = static_cast<const T *>(p.Bm) + g * p.N, *Cm = static_cast<const T *>(p.Cm) + g * p.N;
 
@@ -136,102 +163,129 @@ __global__ void __launch_bounds__(kScanThreads, 4)
             ahead[i] = row < stop && n < p.N ? (side ? Cm[row * p.C_stride + n] : Bm[row * p.B_stride + n]) : from_float<T>(0.f);
         }
     };
-    T rx[kUnroll], rdt[kUnroll], rz[kUnroll];  // the inputs of rows ahead_row .. ahead_row + kUnroll - 1
-    long long ahead_row = -1;
-    auto fetch_rows = [&](long long first) {
-        const T *xr = X + first * p.x_stride, *dtr = DT + first * p.dt_stride, *zr = Z + first * p.z_stride;
-        ahead_row = first;
+    constexpr int CW = 64 / L, ROWS = ENDS ? 2 : 3, STAGES = 4;  // channels of a warp, tensors
+    __shared__ __align__(16) T ring[kWarps][STAGES][ROWS][BLK][CW];
+    auto &mine = ring[threadIdx.x / 32];
+    const int lane = threadIdx.x % 32;
+    const int w0 = ((blockIdx.y % blocks) * kWarps + threadIdx.x / 32) * CW;  // the warp's first channel in the group
+    // Brings the block of rows that starts at `first` into its stage.
+    auto bring = [&](long long first, int stage) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            rx[u] = xr[u * p.x_stride + c];
-            rdt[u] = dtr[u * p.dt_stride + c];
-            if (!ENDS && Z) rz[u] = zr[u * p.z_stride + c];
+        for (int t = 0; t < ROWS; ++t) {
+            const T *from = (t == 0 ? X : t == 1 ? DT : Z) + g * per + w0;
+            const long long stride = t == 0 ? p.x_stride : t == 1 ? p.dt_stride : p.z_stride;
+            if (t == 2 && !Z) break;
+            if constexpr (WIDE && CW * sizeof(T) >= 16) {
+                constexpr int PER = 16 / sizeof(T), WORDS = CW / PER;  // values per copy, copies per row
+#pragma unroll
+                for (int i = lane; i < BLK * WORDS; i += 32) {
+                    const int u = i / WORDS, k0 = (i % WORDS) * PER;
+                    if (first + u < stop && w0 + k0 < per) copy16(&mine[stage][t][u][k0], from + (first + u) * stride + k0);
+                }
+            } else {
+                for (int i = lane; i < BLK * CW; i += 32) {
+                    const int u = i / CW, k0 = i % CW;
+                    if (first + u < stop && w0 + k0 < per) mine[stage][t][u][k0] = from[(first + u) * stride + k0];
+                }
+            }
         }
+        copies_issued();
+    };
+    auto row_pair = [&](int stage, int t, int u) {
+        return to_pair(*reinterpret_cast<const Two<T> *>(&mine[stage][t][u][lane / L * 2]));
     };
     f32x2 total = 0;
-    // Two tokens, both of the running sequence, with B and C rows at `bc`; the second only if `two`.
-    auto step = [&](float x0, float x1, float dt0, float dt1, float z0, float z1, const float *bc, T *out, bool two) {
-        const f32x2 x2 = pair(x0, x1);
-        f32x2 dt2 = add2(pair(dt0, dt1), both(bias));
-        if (p.softplus) dt2 = softplus2(dt2);
+    auto step = [&](f32x2 x, f32x2 dt, f32x2 z, const float *bc, T *out) {  // one token, with its B and C at `bc`
+        dt = add2(dt, bias);
+        if (p.softplus) dt = softplus2(dt);
         float dts[2], us[2], sums[2];
-        unpair(dt2, dts[0], dts[1]);
-        unpair(mul2(dt2, x2), us[0], us[1]);
-        if constexpr (ENDS) total = add2(total, two ? dt2 : pair(dts[0], 0.f));
+        unpair(dt, dts[0], dts[1]);
+        unpair(mul2(dt, x), us[0], us[1]);
+        if constexpr (ENDS) total = add2(total, dt);
+        const f32x2 *B2 = reinterpret_cast<const f32x2 *>(bc), *C2 = reinterpret_cast<const f32x2 *>(bc + (SIDES - 1) * NP);
+        const f32x2 t0 = both(dts[0]), t1 = both(dts[1]), u0 = both(us[0]), u1 = both(us[1]);
+        f32x2 s0 = 0, s1 = 0;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (j == 1 && !two) break;
-            const f32x2 *B2 = reinterpret_cast<const f32x2 *>(bc + j * SIDES * NP);
-            const f32x2 *C2 = reinterpret_cast<const f32x2 *>(bc + (j * SIDES + SIDES - 1) * NP);
-            const f32x2 t2 = both(dts[j]), u2 = both(us[j]);
-            f32x2 sum2 = 0;
-#pragma unroll
-            for (int i = 0; i < S / 2; ++i) {
-                h[i] = fma2(ex2_pair(mul2(t2, A[i])), h[i], mul2(u2, B2[i]));
-                if constexpr (!ENDS) sum2 = i == 0 ? mul2(C2[i], h[i]) : fma2(C2[i], h[i], sum2);
-            }
+        for (int i = 0; i < S / 2; ++i) {
+            const f32x2 b = B2[i];
+            h[0][i] = fma2(ex2_pair(mul2(t0, A[0][i])), h[0][i], mul2(u0, b));
+            h[1][i] = fma2(ex2_pair(mul2(t1, A[1][i])), h[1][i], mul2(u1, b));
             if constexpr (!ENDS) {
-                float other;
-                unpair(sum2, sums[j], other);
-                sums[j] += other;
-#pragma unroll
-                for (int m = L / 2; m > 0; m >>= 1) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], m);
+                const f32x2 cc = C2[i];
+                s0 = i == 0 ? mul2(cc, h[0][i]) : fma2(cc, h[0][i], s0);
+                s1 = i == 0 ? mul2(cc, h[1][i]) : fma2(cc, h[1][i], s1);
             }
         }
         if constexpr (!ENDS) {
-            f32x2 y2 = fma2(both(skip), x2, pair(sums[0], two ? sums[1] : 0.f));
-            if (Z) y2 = mul2(y2, silu2(pair(z0, z1)));
+            float other[2];
+            unpair(s0, sums[0], other[0]);
+            unpair(s1, sums[1], other[1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                sums[j] += other[j];
+#pragma unroll
+                for (int m = L / 2; m > 0; m >>= 1) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], m);
+            }
+            f32x2 y2 = fma2(skip, x, pair(sums[0], sums[1]));
+            if (Z) y2 = mul2(y2, silu2(z));
             unpair(y2, sums[0], sums[1]);
-            if (live && n0 == 0) {
-                out[c] = from_float<T>(sums[0]);
-                if (two) out[p.C + c] = from_float<T>(sums[1]);
+            if (n0 == 0) {
+                if constexpr (WIDE) {
+                    if (live) *reinterpret_cast<Two<T> *>(out + c) = Two<T>{from_float<T>(sums[0]), from_float<T>(sums[1])};
+                } else {
+                    if (live) out[c] = from_float<T>(sums[0]);
+                    if (live1) out[c1] = from_float<T>(sums[1]);
+                }
             }
         }
     };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) bring(r + i * BLK, i);
+    int stage = 0;
     fetch(r);
     for (int buf = 0; r < stop; buf ^= 1) {
-        float *mine = &tile[buf][0][0][0];
+        float *bc = &tile[buf][0][0][0];
 #pragma unroll
-        for (int i = 0; i < EACH; ++i) mine[i * kScanThreads + threadIdx.x] = to_float(ahead[i]);
+        for (int i = 0; i < EACH; ++i) bc[i * kScanThreads + threadIdx.x] = to_float(ahead[i]);
         __syncthreads();  // two buffers: the one written next was last read before this barrier
         fetch(r + TT);
-        const float *bc = mine + n0;
-        const long long tile_end = min(r + TT, stop);
-        while (r < tile_end) {
-            if (!ENDS && r == end) {
-                seq = close_sequence(seq);
-                if (seq >= p.seqs.n_seqs) return;  // rows past the last sequence: a bad cu_seqlens
-                begin_sequence(seq);
-            }
-            const long long until = !ENDS && end > r && end < tile_end ? end : tile_end;
-            for (; r + kUnroll <= until; r += kUnroll, bc += kUnroll * SIDES * NP) {
-                if (ahead_row != r) fetch_rows(r);
-                float xs[kUnroll], dts[kUnroll], zs[kUnroll];
+        bc += n0;
+        for (int t0 = 0; t0 < TT && r < stop; t0 += BLK, bc += BLK * SIDES * NP) {
+            copies_arrived<STAGES - 2>();
+            __syncwarp();  // every lane's copies of this block are there, and the block before is read
+            bring(r + (STAGES - 1) * BLK, stage == 0 ? STAGES - 1 : stage - 1);
+            T *out = y + r * p.C;
+            if (r + BLK <= stop && (ENDS || r + BLK <= end || end < r)) {
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    xs[u] = to_float(rx[u]);
-                    dts[u] = to_float(rdt[u]);
-                    zs[u] = !ENDS && Z ? to_float(rz[u]) : 0.f;
-                }
-                if (r + 2 * kUnroll <= stop) fetch_rows(r + kUnroll);
-                T *out = y + r * p.C;
-#pragma unroll
-                for (int u = 0; u < kUnroll; u += 2)
-                    step(xs[u], xs[u + 1], dts[u], dts[u + 1], zs[u], zs[u + 1], bc + u * SIDES * NP, out + u * p.C, true);
-            }
+                for (int u = 0; u < BLK; ++u)
+                    step(row_pair(stage, 0, u), row_pair(stage, 1, u), !ENDS && Z ? row_pair(stage, ROWS - 1, u) : 0,
+                         bc + u * SIDES * NP, out + u * p.C);
+                r += BLK;
+            } else {  // a sequence ends in the block, or the chunk does
 #pragma unroll 1
-            for (; r < until; ++r, bc += SIDES * NP) {  // a few tokens before an end
-                const float x0 = to_float(X[r * p.x_stride + c]), dt0 = to_float(DT[r * p.dt_stride + c]);
-                const float z0 = !ENDS && Z ? to_float(Z[r * p.z_stride + c]) : 0.f;
-                step(x0, 0.f, dt0, 0.f, z0, 0.f, bc, y + r * p.C, false);
+                for (int u = 0; u < BLK && r < stop; ++u, ++r) {
+                    if (!ENDS && r == end) {
+                        seq = close_sequence(seq);
+                        if (seq >= p.seqs.n_seqs) {  // rows past the last sequence: a bad cu_seqlens
+                            copies_arrived<0>();
+                            return;
+                        }
+                        begin_sequence(seq);
+                    }
+                    step(row_pair(stage, 0, u), row_pair(stage, 1, u), !ENDS && Z ? row_pair(stage, ROWS - 1, u) : 0,
+                         bc + u * SIDES * NP, out + u * p.C);
+                }
             }
+            stage = stage == STAGES - 1 ? 0 : stage + 1;
         }
     }
+    copies_arrived<0>();
     if constexpr (ENDS) {
         store(carry.state + blockIdx.x * chunk_states);
-        float even, odd;
-        unpair(total, even, odd);
-        if (live && n0 == 0) carry.time[(long long)blockIdx.x * p.C + c] = even + odd;
+        float t0, t1;
+        unpair(total, t0, t1);
+        if (live && n0 == 0) carry.time[(long long)blockIdx.x * p.C + c] = t0;
+        if (live1 && n0 == 0) carry.time[(long long)blockIdx.x * p.C + c1] = t1;
     } else {
         if (stop == end) close_sequence(seq);
     }
@@ -280,18 +334,27 @@ struct PrefillLaunch {
     float *fin;
     ScanPlan plan;
     Carries carry;
+    int blocks;
     cudaStream_t s;
-    template <typename T, int S, int L>
-    void operator()() {
-        const int per = p.C / p.G;
-        const unsigned blocks = (unsigned)(((per * L + kScanThreads - 1) / kScanThreads) * p.G);
+    template <typename T, int S, int L, bool WIDE>
+    void launch() {
         if (plan.carries) {
-            scan_prefill_kernel<T, S, L, true><<<dim3((unsigned)plan.chunks - 1, blocks), kScanThreads, 0, s>>>(p, nullptr, nullptr, plan, carry);
+            scan_prefill_kernel<T, S, L, WIDE, true><<<dim3((unsigned)plan.chunks - 1, (unsigned)blocks), kScanThreads, 0, s>>>(
+                p, nullptr, nullptr, plan, carry);
             const long long size = (long long)p.C * p.N;
             scan_carry_kernel<<<(unsigned)((size + 127) / 128), 128, (size_t)plan.chunks, s>>>(p, plan, carry);
         }
-        scan_prefill_kernel<T, S, L, false><<<dim3((unsigned)plan.chunks, blocks), kScanThreads, 0, s>>>(
+        scan_prefill_kernel<T, S, L, WIDE, false><<<dim3((unsigned)plan.chunks, (unsigned)blocks), kScanThreads, 0, s>>>(
             p, static_cast<T *>(y), fin, plan, carry);
+    }
+    template <typename T, int S, int L>
+    void operator()() {
+        const uintptr_t bits = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.dt) |
+                               reinterpret_cast<uintptr_t>(p.z) | reinterpret_cast<uintptr_t>(y);
+        constexpr int per = 16 / sizeof(T);
+        const bool wide = bits % 16 == 0 && (p.C / p.G) % per == 0 && p.x_stride % per == 0 && p.dt_stride % per == 0 &&
+                          (!p.z || p.z_stride % per == 0);
+        wide ? launch<T, S, L, true>() : launch<T, S, L, false>();
     }
 };
 
@@ -362,14 +425,14 @@ void launch_decode(const ScanParams &p, float *state, void *y, cudaStream_t s) {
 
 }  // namespace
 
-// Whole sequences where they give every SM a block; otherwise chunks that give it four, of at least 64 rows. (Half as many or
+// Whole sequences where they give every SM a block; otherwise chunks that give it three, of at least 64 rows. (Half as many or
 // twice as many were slower on one sequence of 16384 rows and 4096 channels.)
 ScanPlan scan_plan(const kda_scan_args &a, int sms) {
-    const long long rows = (long long)a.B * a.T, blocks = (long long)scan_blocks(a) * a.G;
+    const long long rows = (long long)a.B * a.T, blocks = scan_blocks(a);
     if (rows == 0) return ScanPlan{1, 1, false};
     if (sms <= 0) sms = 152;
     if (!a.cu_seqlens && (a.B * blocks >= sms || a.T <= 64)) return ScanPlan{a.B, a.T, false};
-    long long chunks = 4LL * sms / blocks, most = (rows + 63) / 64;
+    long long chunks = 3LL * sms / blocks, most = (rows + 63) / 64;
     chunks = chunks < 1 ? 1 : chunks > most ? most : chunks;
     long long per = ((rows + chunks - 1) / chunks + 31) / 32 * 32;
     chunks = (rows + per - 1) / per;
@@ -384,7 +447,7 @@ size_t scan_prefill_workspace_bytes(const kda_scan_args &a, int sms) {
 cudaError_t launch_scan_prefill(const kda_scan_args &a, void *y, float *final_state, void *ws, int sms, unsigned *err,
                                 cudaStream_t s) {
     const ScanPlan plan = scan_plan(a, sms);
-    return scan_by_type(a, PrefillLaunch{scan_params(a, err), y, final_state, plan, carries_in(a, plan, ws), s});
+    return scan_by_type(a, PrefillLaunch{scan_params(a, err), y, final_state, plan, carries_in(a, plan, ws), scan_blocks(a), s});
 }
 
 cudaError_t launch_scan_decode(const kda_scan_args &a, float *state, void *y, unsigned *err, cudaStream_t s) {

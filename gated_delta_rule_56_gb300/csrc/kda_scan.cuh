@@ -144,8 +144,9 @@ inline int scan_lanes(int N) {  // lanes per channel, 16 states each
     while (L * 16 < N) L *= 2;
     return L;
 }
-inline int scan_blocks(const kda_scan_args &a) {  // channel blocks per group
-    return (int)(((long long)a.D / a.G * scan_lanes(a.N) + kScanThreads - 1) / kScanThreads);
+inline int scan_blocks(const kda_scan_args &a) {  // channel blocks of all groups, two channels per lane
+    const long long per = (long long)a.D / a.G * scan_lanes(a.N);
+    return (int)((per + 2 * kScanThreads - 1) / (2 * kScanThreads)) * a.G;
 }
 
 // States handed from chunk to chunk, in the workspace.
