@@ -34,6 +34,8 @@ struct alignas(2 * sizeof(T)) Two {
 template <typename T>
 __device__ __forceinline__ f32x2 to_pair(Two<T> v) { return pair(to_float(v.a), to_float(v.b)); }
 
+__device__ __forceinline__ bool on_16_bytes(const float *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 __device__ __forceinline__ void copy16(void *to, const void *from) {  // global -> shared, asynchronous
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from) : "memory");
 }
@@ -41,19 +43,25 @@ __device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_
 template <int PENDING>
 __device__ __forceinline__ void copies_arrived() { asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory"); }
 
-// ENDS: only the end state of the chunk's last sequence (from zeros, or from its initial state if it begins in the chunk).
+// What a kernel makes of its chunk:
+//   kOutputs   y and the sequences' final states
+//   kEnds      the end state of the chunk's last sequence (from zeros, or from its initial state if it begins in the chunk)
+//   kStates    for the backward pass: that end state, and the states before every kScanWindow-th row
+//   kBackEnds  for the backward pass, rows taken from the last to the first: the gradient at the state before the chunk of its
+//              first sequence, from zeros, or from its final state's gradient if it ends in the chunk; B is C and u is dy here
 // WIDE: every row's channels lie on 16-byte boundaries. A lane holds S states of two channels, which share the reads of B and C.
 // The rows of x, dt and z come through a ring in shared memory, each warp its own channels' rows, STAGES - 1 blocks ahead:
 // loads into registers were moved back to their use by the compiler, and a third of the time was spent waiting for them.
-template <typename T, int S, int L, bool WIDE, bool ENDS>
+template <typename T, int S, int L, bool WIDE, int MODE>
 __global__ void __launch_bounds__(kScanThreads, 3)
-    scan_prefill_kernel(ScanParams p, T *__restrict__ y, float *fin, ScanPlan plan, Carries carry) {
+    scan_rows_kernel(ScanParams p, T *__restrict__ y, float *fin, ScanPlan plan, Carries carry) {
+    constexpr bool OUT = MODE == kOutputs, BACK = MODE == kBackEnds;
     constexpr int BLK = kBlock<T>;
-    constexpr int NP = S * L, TT = Tile<NP>::tokens, SIDES = ENDS ? 1 : 2;
+    constexpr int NP = S * L, TT = Tile<NP>::tokens, SIDES = OUT ? 2 : 1;
     constexpr int EACH = TT * SIDES * NP / kScanThreads;  // values of a tile that a thread brings
     static_assert(TT % BLK == 0 && TT * SIDES * NP % kScanThreads == 0, "tile");
     __shared__ __align__(16) float tile[2][TT][SIDES][NP];
-    if (!ENDS && blockIdx.x == 0 && blockIdx.y == 0) check_seqs(p.seqs, p.err);
+    if ((OUT || MODE == kStates) && blockIdx.x == 0 && blockIdx.y == 0) check_seqs(p.seqs, p.err);
     const int per = p.C / p.G;
     const int blocks = (per * L + 2 * kScanThreads - 1) / (2 * kScanThreads);
     const int g = blockIdx.y / blocks;
@@ -61,13 +69,24 @@ __global__ void __launch_bounds__(kScanThreads, 3)
     const bool live = k < per, live1 = k + 1 < per;
     const int c = g * per + (live ? k : 0), c1 = live1 ? c + 1 : c;
     const long long chunk_states = (long long)p.C * p.N;
-    const long long r0 = blockIdx.x * plan.rows, stop = min(r0 + plan.rows, p.seqs.rows);
+    const int chunk = BACK ? blockIdx.x + 1 : blockIdx.x;  // nothing comes before the first
+    const long long r0 = chunk * plan.rows;
+    long long stop = min(r0 + plan.rows, p.seqs.rows);
 
     f32x2 h[2][S / 2], A[2][S / 2];
     auto load_states = [&](const float *from, f32x2(&to)[2][S / 2], float scale) {  // a tensor [C][N]
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const float *row = from + (long long)(j ? c1 : c) * p.N + n0;
+            if (p.N == NP && on_16_bytes(from)) {
+#pragma unroll
+                for (int i = 0; i < S / 4; ++i) {
+                    const float4 v = reinterpret_cast<const float4 *>(row)[i];
+                    to[j][2 * i] = pair(v.x * scale, v.y * scale);
+                    to[j][2 * i + 1] = pair(v.z * scale, v.w * scale);
+                }
+                continue;
+            }
 #pragma unroll
             for (int i = 0; i < S / 2; ++i) {
                 const int n = n0 + 2 * i;
@@ -86,6 +105,16 @@ __global__ void __launch_bounds__(kScanThreads, 3)
         for (int j = 0; j < 2; ++j) {
             if (!(j ? live1 : live)) continue;
             float *row = to + (long long)(c + j) * p.N + n0;
+            if (p.N == NP && on_16_bytes(to)) {
+#pragma unroll
+                for (int i = 0; i < S / 4; ++i) {
+                    float4 v;
+                    unpair(h[j][2 * i], v.x, v.y);
+                    unpair(h[j][2 * i + 1], v.z, v.w);
+                    reinterpret_cast<float4 *>(row)[i] = v;
+                }
+                continue;
+            }
 #pragma unroll
             for (int i = 0; i < S / 2; ++i) {
                 const int n = n0 + 2 * i;
@@ -104,7 +133,7 @@ __global__ void __launch_bounds__(kScanThreads, 3)
             clear();
     };
     auto final_state = [&](int n) {
-        if (!fin) return;
+        if (!OUT || !fin) return;
         const long long slot = state_slot(p.fin_idx, p.pool, n, p.err);
         if (slot >= 0) store(fin + slot * chunk_states);
     };
@@ -112,6 +141,7 @@ __global__ void __launch_bounds__(kScanThreads, 3)
     auto close_sequence = [&](int n) {
         final_state(n);
         for (++n; n < p.seqs.n_seqs && p.seqs.begin(n) == p.seqs.end(n); ++n) {
+            if (!OUT) continue;
             initial(n);
             final_state(n);
         }
@@ -120,54 +150,64 @@ __global__ void __launch_bounds__(kScanThreads, 3)
 
     long long r = r0;
     int seq = 0;
-    if constexpr (ENDS) {
+    if constexpr (MODE == kEnds) {
         seq = p.seqs.at(stop - 1);
         const long long bos = p.seqs.begin(seq);
         if (bos >= r0 && bos < stop) {
             r = bos;
             initial(seq);
-            store(carry.first + blockIdx.x * chunk_states);
+            store(carry.first + chunk * chunk_states);
+        }
+    } else if constexpr (BACK) {
+        seq = p.seqs.at(r0);
+        const long long eos = p.seqs.end(seq);
+        if (eos <= stop && eos > r0) {
+            stop = eos;
+            if (fin) load_states(fin + (long long)seq * chunk_states, h, 1.f);
         }
     } else {
-        if (blockIdx.x == 0)  // empty sequences before the first row
+        if (OUT && chunk == 0)  // empty sequences before the first row
             for (; seq < p.seqs.n_seqs && p.seqs.begin(seq) == p.seqs.end(seq) && p.seqs.begin(seq) == 0; ++seq) {
                 initial(seq);
                 final_state(seq);
             }
         if (r0 >= stop) return;
         seq = p.seqs.at(r0);
-        if (plan.carries && p.seqs.begin(seq) < r0) load_states(carry.state + blockIdx.x * chunk_states, h, 1.f);
+        if (OUT && plan.carries && p.seqs.begin(seq) < r0) load_states(carry.state + chunk * chunk_states, h, 1.f);
     }
-    // The row at which the next sequence begins; the last sequence that begins here and goes on after the chunk
-    // takes its initial state from the first kernel's copy, because another block may write its final state there.
+    // The row at which the next sequence begins. The last sequence that begins here and goes on after the chunk takes
+    // its initial state from the first kernel's copy, because another block may write its final state there.
     long long end = p.seqs.end(seq);
     auto begin_sequence = [&](int n) {
         end = p.seqs.end(n);
-        if (plan.carries && end > stop && blockIdx.x + 1 < plan.chunks)
-            load_states(carry.first + blockIdx.x * chunk_states, h, 1.f);
+        if (OUT && plan.carries && end > stop && chunk + 1 < plan.chunks)
+            load_states(carry.first + chunk * chunk_states, h, 1.f);
         else
             initial(n);
     };
-    if (!ENDS && p.seqs.begin(seq) == r0) begin_sequence(seq);
+    if ((OUT || MODE == kStates) && p.seqs.begin(seq) == r0) begin_sequence(seq);
 
     const f32x2 bias = p.dt_bias ? pair(p.dt_bias[c], p.dt_bias[c1]) : 0, skip = p.D ? pair(p.D[c], p.D[c1]) : 0;
     const T *X = static_cast<const T *>(p.x), *DT = static_cast<const T *>(p.dt), *Z = static_cast<const T *>(p.z);
-    const T *Bm = static_cast<const T *>(p.Bm) + g * p.N, *Cm = static_cast<const T *>(p.Cm) + g * p.N;
+    const long long B_stride = BACK ? p.C_stride : p.B_stride;
+    const T *Bm = static_cast<const T *>(BACK ? p.Cm : p.Bm) + g * p.N, *Cm = static_cast<const T *>(p.Cm) + g * p.N;
 
+    f32x2 total = 0;  // of the time steps
     T ahead[EACH];
     auto fetch = [&](long long first) {  // the next tile's values of this thread
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
             const int v = i * kScanThreads + threadIdx.x, n = v % NP, side = (v / NP) % SIDES;
-            const long long row = first + v / (NP * SIDES);
-            ahead[i] = row < stop && n < p.N ? (side ? Cm[row * p.C_stride + n] : Bm[row * p.B_stride + n]) : from_float<T>(0.f);
+            const long long at = first + v / (NP * SIDES), row = BACK ? r0 + stop - 1 - at : at;
+            ahead[i] = at < stop && n < p.N ? (side ? Cm[row * p.C_stride + n] : Bm[row * B_stride + n]) : from_float<T>(0.f);
         }
     };
-    constexpr int CW = 64 / L, ROWS = ENDS ? 2 : 3, STAGES = 4;  // channels of a warp, tensors
+    constexpr int CW = 64 / L, ROWS = OUT || BACK ? 3 : 2, STAGES = 4;  // channels of a warp, tensors
     __shared__ __align__(16) T ring[kWarps][STAGES][ROWS][BLK][CW];
     auto &mine = ring[threadIdx.x / 32];
     const int lane = threadIdx.x % 32;
     const int w0 = ((blockIdx.y % blocks) * kWarps + threadIdx.x / 32) * CW;  // the warp's first channel in the group
+    auto row_at = [&](long long at) { return BACK ? r0 + stop - 1 - at : at; };
     // Brings the block of rows that starts at `first` into its stage.
     auto bring = [&](long long first, int stage) {
 #pragma unroll
@@ -180,44 +220,57 @@ __global__ void __launch_bounds__(kScanThreads, 3)
 #pragma unroll
                 for (int i = lane; i < BLK * WORDS; i += 32) {
                     const int u = i / WORDS, k0 = (i % WORDS) * PER;
-                    if (first + u < stop && w0 + k0 < per) copy16(&mine[stage][t][u][k0], from + (first + u) * stride + k0);
+                    if (first + u < stop && w0 + k0 < per) copy16(&mine[stage][t][u][k0], from + row_at(first + u) * stride + k0);
                 }
             } else {
                 for (int i = lane; i < BLK * CW; i += 32) {
                     const int u = i / CW, k0 = i % CW;
-                    if (first + u < stop && w0 + k0 < per) mine[stage][t][u][k0] = from[(first + u) * stride + k0];
+                    if (first + u < stop && w0 + k0 < per) mine[stage][t][u][k0] = from[row_at(first + u) * stride + k0];
                 }
             }
         }
         copies_issued();
     };
+    // The state before a window, and the time since the chunk's first row.
+    auto keep = [&](long long window) {
+        const long long at = chunk * plan.windows() + window;
+        store(carry.kept + at * chunk_states);
+        float t0, t1;
+        unpair(total, t0, t1);
+        if (live && n0 == 0) carry.kept_time[at * p.C + c] = t0;
+        if (live1 && n0 == 0) carry.kept_time[at * p.C + c1] = t1;
+    };
     auto row_pair = [&](int stage, int t, int u) {
         return to_pair(*reinterpret_cast<const Two<T> *>(&mine[stage][t][u][lane / L * 2]));
     };
-    f32x2 total = 0;
     auto step = [&](f32x2 x, f32x2 dt, f32x2 z, const float *bc, T *out) {  // one token, with its B and C at `bc`
         dt = add2(dt, bias);
         if (p.softplus) dt = softplus2(dt);
-        float dts[2], us[2], sums[2];
+        float dts[2], us[2];
         unpair(dt, dts[0], dts[1]);
-        unpair(mul2(dt, x), us[0], us[1]);
-        if constexpr (ENDS) total = add2(total, dt);
+        if constexpr (BACK) {
+            if (Z) x = mul2(x, silu2(z));
+            unpair(x, us[0], us[1]);
+        } else {
+            unpair(mul2(dt, x), us[0], us[1]);
+        }
+        if constexpr (!OUT) total = add2(total, dt);
         const f32x2 *B2 = reinterpret_cast<const f32x2 *>(bc), *C2 = reinterpret_cast<const f32x2 *>(bc + (SIDES - 1) * NP);
         const f32x2 t0 = both(dts[0]), t1 = both(dts[1]), u0 = both(us[0]), u1 = both(us[1]);
         f32x2 s0 = 0, s1 = 0;
 #pragma unroll
         for (int i = 0; i < S / 2; ++i) {
-            const f32x2 b = B2[i];
-            h[0][i] = fma2(ex2_pair(mul2(t0, A[0][i])), h[0][i], mul2(u0, b));
-            h[1][i] = fma2(ex2_pair(mul2(t1, A[1][i])), h[1][i], mul2(u1, b));
-            if constexpr (!ENDS) {
+            const f32x2 b = B2[i], a0 = ex2_pair(mul2(t0, A[0][i])), a1 = ex2_pair(mul2(t1, A[1][i]));
+            h[0][i] = BACK ? mul2(a0, fma2(u0, b, h[0][i])) : fma2(a0, h[0][i], mul2(u0, b));
+            h[1][i] = BACK ? mul2(a1, fma2(u1, b, h[1][i])) : fma2(a1, h[1][i], mul2(u1, b));
+            if constexpr (OUT) {
                 const f32x2 cc = C2[i];
                 s0 = i == 0 ? mul2(cc, h[0][i]) : fma2(cc, h[0][i], s0);
                 s1 = i == 0 ? mul2(cc, h[1][i]) : fma2(cc, h[1][i], s1);
             }
         }
-        if constexpr (!ENDS) {
-            float other[2];
+        if constexpr (OUT) {
+            float sums[2], other[2];
             unpair(s0, sums[0], other[0]);
             unpair(s1, sums[1], other[1]);
 #pragma unroll
@@ -255,16 +308,17 @@ __global__ void __launch_bounds__(kScanThreads, 3)
             __syncwarp();  // every lane's copies of this block are there, and the block before is read
             bring(r + (STAGES - 1) * BLK, stage == 0 ? STAGES - 1 : stage - 1);
             T *out = y + r * p.C;
-            if (r + BLK <= stop && (ENDS || r + BLK <= end || end < r)) {
+            if (MODE == kStates && (r - r0) % kScanWindow == 0) keep((r - r0) / kScanWindow);
+            if (r + BLK <= stop && (MODE == kEnds || BACK || r + BLK <= end || end < r)) {
 #pragma unroll
                 for (int u = 0; u < BLK; ++u)
-                    step(row_pair(stage, 0, u), row_pair(stage, 1, u), !ENDS && Z ? row_pair(stage, ROWS - 1, u) : 0,
+                    step(row_pair(stage, 0, u), row_pair(stage, 1, u), (OUT || BACK) && Z ? row_pair(stage, ROWS - 1, u) : 0,
                          bc + u * SIDES * NP, out + u * p.C);
                 r += BLK;
             } else {  // a sequence ends in the block, or the chunk does
 #pragma unroll 1
                 for (int u = 0; u < BLK && r < stop; ++u, ++r) {
-                    if (!ENDS && r == end) {
+                    if ((OUT || MODE == kStates) && r == end) {
                         seq = close_sequence(seq);
                         if (seq >= p.seqs.n_seqs) {  // rows past the last sequence: a bad cu_seqlens
                             copies_arrived<0>();
@@ -272,7 +326,7 @@ __global__ void __launch_bounds__(kScanThreads, 3)
                         }
                         begin_sequence(seq);
                     }
-                    step(row_pair(stage, 0, u), row_pair(stage, 1, u), !ENDS && Z ? row_pair(stage, ROWS - 1, u) : 0,
+                    step(row_pair(stage, 0, u), row_pair(stage, 1, u), (OUT || BACK) && Z ? row_pair(stage, ROWS - 1, u) : 0,
                          bc + u * SIDES * NP, out + u * p.C);
                 }
             }
@@ -280,14 +334,14 @@ __global__ void __launch_bounds__(kScanThreads, 3)
         }
     }
     copies_arrived<0>();
-    if constexpr (ENDS) {
-        store(carry.state + blockIdx.x * chunk_states);
+    if constexpr (OUT) {
+        if (stop == end) close_sequence(seq);
+    } else {
+        store(carry.state + chunk * chunk_states);
         float t0, t1;
         unpair(total, t0, t1);
-        if (live && n0 == 0) carry.time[(long long)blockIdx.x * p.C + c] = t0;
-        if (live1 && n0 == 0) carry.time[(long long)blockIdx.x * p.C + c1] = t1;
-    } else {
-        if (stop == end) close_sequence(seq);
+        if (live && n0 == 0) carry.time[(long long)chunk * p.C + c] = t0;
+        if (live1 && n0 == 0) carry.time[(long long)chunk * p.C + c1] = t1;
     }
 }
 
@@ -322,10 +376,50 @@ __global__ void __launch_bounds__(128) scan_carry_kernel(ScanParams p, ScanPlan 
     }
 }
 
+// The same from the last chunk to the first for the gradients at the states.
+__global__ void __launch_bounds__(128) scan_back_carry_kernel(ScanParams p, ScanPlan plan, Carries carry) {
+    extern __shared__ unsigned char goes_on[];  // chunk j's first sequence goes on after it
+    for (int j = threadIdx.x; j < plan.chunks; j += 128) {
+        const long long r0 = j * plan.rows;
+        goes_on[j] = p.seqs.end(p.seqs.at(r0)) > min(r0 + plan.rows, p.seqs.rows);
+    }
+    __syncthreads();
+    const long long size = (long long)p.C * p.N, i = (long long)blockIdx.x * 128 + threadIdx.x;
+    if (i >= size) return;
+    const float A = p.A[i] * kLog2e;
+    const long long c = i / p.N;
+    float after = 0.f;
+    for (int j0 = plan.chunks - 1; j0 >= 0; j0 -= kCarryBatch) {
+        float local[kCarryBatch], time[kCarryBatch];
+#pragma unroll
+        for (int b = 0; b < kCarryBatch; ++b) {
+            const bool in = j0 - b > 0;  // nothing comes before the first chunk
+            local[b] = in ? carry.state[(j0 - b) * size + i] : 0.f;
+            time[b] = in ? carry.time[(long long)(j0 - b) * p.C + c] : 0.f;
+        }
+#pragma unroll
+        for (int b = 0; b < kCarryBatch; ++b) {
+            if (j0 - b < 0) break;
+            carry.state[(j0 - b) * size + i] = after;
+            after = goes_on[j0 - b] ? fmaf(ex2(A * time[b]), after, local[b]) : local[b];
+        }
+    }
+}
+
 Carries carries_in(const kda_scan_args &a, const ScanPlan &plan, void *ws) {
     const size_t states = (size_t)plan.chunks * a.D * a.N;
     float *f = static_cast<float *>(ws);
-    return Carries{f, f + states, f + 2 * states};
+    return Carries{f, f + states, f + 2 * states, nullptr, nullptr};
+}
+
+// Every row's channels of x, dt, z and the output on 16-byte boundaries.
+template <typename T>
+bool wide_rows(const ScanParams &p, const void *out) {
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.dt) | reinterpret_cast<uintptr_t>(p.z) |
+                           reinterpret_cast<uintptr_t>(out);
+    constexpr int per = 16 / sizeof(T);
+    return bits % 16 == 0 && (p.C / p.G) % per == 0 && p.x_stride % per == 0 && p.dt_stride % per == 0 &&
+           (!p.z || p.z_stride % per == 0);
 }
 
 struct PrefillLaunch {
@@ -339,22 +433,57 @@ struct PrefillLaunch {
     template <typename T, int S, int L, bool WIDE>
     void launch() {
         if (plan.carries) {
-            scan_prefill_kernel<T, S, L, WIDE, true><<<dim3((unsigned)plan.chunks - 1, (unsigned)blocks), kScanThreads, 0, s>>>(
+            scan_rows_kernel<T, S, L, WIDE, kEnds><<<dim3((unsigned)plan.chunks - 1, (unsigned)blocks), kScanThreads, 0, s>>>(
                 p, nullptr, nullptr, plan, carry);
             const long long size = (long long)p.C * p.N;
             scan_carry_kernel<<<(unsigned)((size + 127) / 128), 128, (size_t)plan.chunks, s>>>(p, plan, carry);
         }
-        scan_prefill_kernel<T, S, L, WIDE, false><<<dim3((unsigned)plan.chunks, (unsigned)blocks), kScanThreads, 0, s>>>(
+        scan_rows_kernel<T, S, L, WIDE, kOutputs><<<dim3((unsigned)plan.chunks, (unsigned)blocks), kScanThreads, 0, s>>>(
             p, static_cast<T *>(y), fin, plan, carry);
     }
     template <typename T, int S, int L>
     void operator()() {
-        const uintptr_t bits = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.dt) |
-                               reinterpret_cast<uintptr_t>(p.z) | reinterpret_cast<uintptr_t>(y);
-        constexpr int per = 16 / sizeof(T);
-        const bool wide = bits % 16 == 0 && (p.C / p.G) % per == 0 && p.x_stride % per == 0 && p.dt_stride % per == 0 &&
-                          (!p.z || p.z_stride % per == 0);
-        wide ? launch<T, S, L, true>() : launch<T, S, L, false>();
+        wide_rows<T>(p, y) ? launch<T, S, L, true>() : launch<T, S, L, false>();
+    }
+};
+
+struct StatesLaunch {
+    ScanParams p;
+    ScanPlan plan;
+    Carries carry;
+    int blocks;
+    cudaStream_t s;
+    template <typename T, int S, int L, bool WIDE>
+    void launch() {
+        scan_rows_kernel<T, S, L, WIDE, kStates><<<dim3((unsigned)plan.chunks, (unsigned)blocks), kScanThreads, 0, s>>>(
+            p, nullptr, nullptr, plan, carry);
+        if (!plan.carries) return;
+        const long long size = (long long)p.C * p.N;
+        scan_carry_kernel<<<(unsigned)((size + 127) / 128), 128, (size_t)plan.chunks, s>>>(p, plan, carry);
+    }
+    template <typename T, int S, int L>
+    void operator()() {
+        wide_rows<T>(p, nullptr) ? launch<T, S, L, true>() : launch<T, S, L, false>();
+    }
+};
+
+struct BackEndsLaunch {
+    ScanParams p;  // x is dy
+    float *d_fin;
+    ScanPlan plan;
+    Carries carry;
+    int blocks;
+    cudaStream_t s;
+    template <typename T, int S, int L, bool WIDE>
+    void launch() {
+        scan_rows_kernel<T, S, L, WIDE, kBackEnds><<<dim3((unsigned)plan.chunks - 1, (unsigned)blocks), kScanThreads, 0, s>>>(
+            p, nullptr, d_fin, plan, carry);
+        const long long size = (long long)p.C * p.N;
+        scan_back_carry_kernel<<<(unsigned)((size + 127) / 128), 128, (size_t)plan.chunks, s>>>(p, plan, carry);
+    }
+    template <typename T, int S, int L>
+    void operator()() {
+        wide_rows<T>(p, nullptr) ? launch<T, S, L, true>() : launch<T, S, L, false>();
     }
 };
 
@@ -448,6 +577,18 @@ cudaError_t launch_scan_prefill(const kda_scan_args &a, void *y, float *final_st
                                 cudaStream_t s) {
     const ScanPlan plan = scan_plan(a, sms);
     return scan_by_type(a, PrefillLaunch{scan_params(a, err), y, final_state, plan, carries_in(a, plan, ws), scan_blocks(a), s});
+}
+
+cudaError_t launch_scan_states(const kda_scan_args &a, const ScanPlan &plan, const Carries &carry, unsigned *err, cudaStream_t s) {
+    return scan_by_type(a, StatesLaunch{scan_params(a, err), plan, carry, scan_blocks(a), s});
+}
+
+cudaError_t launch_scan_back_ends(const kda_scan_args &a, const void *dy, const float *d_final, const ScanPlan &plan,
+                                  const Carries &carry, unsigned *err, cudaStream_t s) {
+    ScanParams p = scan_params(a, err);
+    p.x = dy;
+    p.x_stride = a.D;
+    return scan_by_type(a, BackEndsLaunch{p, const_cast<float *>(d_final), plan, carry, scan_blocks(a), s});
 }
 
 cudaError_t launch_scan_decode(const kda_scan_args &a, float *state, void *y, unsigned *err, cudaStream_t s) {

@@ -136,7 +136,10 @@ struct ScanPlan {
     int chunks;
     long long rows;
     bool carries;
+    __host__ __device__ long long windows() const { return (rows + 7) / 8; }  // of kScanWindow rows in a chunk
 };
+constexpr int kScanWindow = 8;  // rows between the states that the backward pass keeps
+enum { kOutputs, kEnds, kStates, kBackEnds };
 constexpr int kScanThreads = 128;
 ScanPlan scan_plan(const kda_scan_args &a, int sms);
 inline int scan_lanes(int N) {  // lanes per channel, 16 states each
@@ -154,7 +157,15 @@ struct Carries {
     float *state;  // [chunks][C][N]: the chunk's own end state, then the state before the chunk
     float *first;  // [chunks][C][N]: initial state of the sequence that begins in the chunk and goes on after it
     float *time;   // [chunks][C]: sum of the time steps over the chunk's part of its last sequence
+    // Backward pass: per window of a chunk, the state before it as the chunk alone gives it, [C][N], and the sum of the time steps
+    // since the chunk's first row, [C].
+    float *kept, *kept_time;
 };
+
+// The states before the windows and the chunks; the gradients at the states after the chunks.
+cudaError_t launch_scan_states(const kda_scan_args &a, const ScanPlan &plan, const Carries &carry, unsigned *err, cudaStream_t s);
+cudaError_t launch_scan_back_ends(const kda_scan_args &a, const void *dy, const float *d_final, const ScanPlan &plan,
+                                  const Carries &carry, unsigned *err, cudaStream_t s);
 
 // Calls f.operator()<T, S, L>() with S states per lane and L lanes per channel, S * L >= N (at most 256).
 template <typename F>

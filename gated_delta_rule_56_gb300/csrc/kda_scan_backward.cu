@@ -5,124 +5,411 @@
 //     dC_t[n] = sum_c dy'_t h_t,    dB_t[n] = sum_c g_t dt_t x_t          (over the channels of the group)
 //     dx_t = D dy'_t + dt_t sum_n g_t B_t,   ddt'_t = sum_n g_t (A a_t h_{t-1} + B_t x_t)
 //     dA = sum_t g_t dt_t a_t h_{t-1},  dD = sum_t dy'_t x_t,  the initial state's gradient: a_first g_first.
-// The states of all tokens are kept in the workspace by a forward walk; a second walk goes back.
+//
+// The rows are cut into chunks as for prompts. Kernels: (1) forward over every chunk from zeros, keeping the state before
+// every 8th row (4 N / 8 bytes per row and channel; keeping all would be 4 N), and the walk over the chunks' end
+// states; (2) the same backwards for the gradients at the states after each chunk, where chunks are joined at all;
+// (3) the main kernel, every chunk from its last window of 8 rows to its first; (4) sums over the blocks' parts.
+//
+// Main kernel: a thread holds a tile of 4 channels x 4 states, a warp N / 4 of those along the states and the rest along
+// the channels. The sums over channels (dB, dC) and over states (dx, ddt, y) are both taken in the thread's registers first;
+// tiles that are narrow in one direction move 1.3 times as many values between lanes. A window's
+// states are recomputed from the kept one into registers, one of every two rows; the row between is recomputed from its
+// decay, which the way back needs anyway. That is 15 multiply-adds and 1.75 exponentials per (row, channel, state).
+#include <algorithm>
+
 #include "kda_scan.cuh"
 
 namespace kda {
 namespace {
 
+constexpr int kWarps = kScanThreads / 32;
+constexpr int kRows = kScanWindow;
+
 struct GradParams {
     const void *dy;
     const float *d_fin;
     float *dx, *ddt, *dz, *d_init;
-    float *states;         // [rows][C][N]
-    float *part_B, *part_C;  // [blocks per group][rows][G][N]
-    float *part_A;         // [n_seqs][C][N]
-    float *part_D, *part_bias;  // [n_seqs][C]
-    int blocks;            // channel blocks per group
+    float *part_B, *part_C;     // [blocks per group][rows][G][N]
+    float *part_A;              // [chunks][C][N]
+    float *part_D, *part_bias;  // [chunks][C]
+    const float *after;         // [chunks][C][N]: gradient at the state after a chunk whose last sequence goes on, or nullptr
 };
 
-__device__ __forceinline__ float warp_sum_from(float x, int first) {  // over the lanes that differ by multiples of `first`
-    for (int m = 16; m >= first; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-    return x;
+// EC channels x EN states per thread, NL lanes along the states.
+template <int EC, int EN, int NL>
+struct Shape {
+    static constexpr int NP = EN * NL, CL = 32 / NL, CH = kWarps * CL * EC, PARTS = kWarps * CL;
+};
+
+template <typename T, typename SH>
+struct Shared {
+    alignas(16) T raw[2][4][kRows][SH::CH];       // x, dt, dy, z as they are in memory
+    alignas(16) float pre[3][kRows][SH::CH];      // dt', u = dt' x, dy'
+    alignas(16) float sum[3][kRows][SH::CH];      // over the states: g B, g a h A, C h
+    alignas(16) float bc[kRows][2][SH::NP][2];    // B and C, every value twice: one for each channel of a pair
+    alignas(16) float part[kRows][2][SH::PARTS][SH::NP];  // dB and dC of each thread's channels
+};
+
+__device__ __forceinline__ void copy16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from) : "memory");
 }
 
-template <typename T, int S, int L>
-__global__ void __launch_bounds__(32) scan_backward_kernel(ScanParams p, GradParams q) {
-    if (blockIdx.x == 0 && blockIdx.y == 0) check_seqs(p.seqs, p.err);
-    const int per = p.C / p.G;
-    const int g = blockIdx.y / q.blocks, blk = blockIdx.y % q.blocks;
-    const int k = blk * (32 / L) + threadIdx.x / L, n0 = (threadIdx.x % L) * S;
-    const bool live = k < per;
-    const int c = g * per + (live ? k : 0), n = blockIdx.x;
-    const long long bos = p.seqs.begin(n), eos = p.seqs.end(n);
-    if (bos < 0 || eos < bos || eos > p.seqs.rows) return;
-    float h[S], A[S], A2[S], dA[S], gr[S];
+template <typename T, int EC, int EN, int NL, bool WIDE>
+__global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanParams p, GradParams q, ScanPlan plan, Carries carry) {
+    using SH = Shape<EC, EN, NL>;
+    constexpr int NP = SH::NP, CL = SH::CL, CH = SH::CH, PARTS = SH::PARTS, PAIRS = EC / 2;
+    extern __shared__ __align__(16) unsigned char memory[];
+    Shared<T, SH> &sm = *reinterpret_cast<Shared<T, SH> *>(memory);
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, nl = lane % NL, cl = lane / NL;
+    const int per = p.C / p.G, blocks = (per + CH - 1) / CH;
+    const int g = blockIdx.y / blocks, blk = blockIdx.y % blocks;
+    const int first_k = blk * CH;                       // the block's first channel in the group
+    const int tile_k = (warp * CL + cl) * EC, n0 = nl * EN;  // the thread's first channel in the block, its first state
+    const int chunk = blockIdx.x;
+    const long long r0 = chunk * plan.rows, stop = min(r0 + plan.rows, p.seqs.rows);
+    const long long chunk_states = (long long)p.C * p.N;
+    if (r0 >= stop) return;
+
+    // A tensor [C][N] at the thread's tile; pairs run along the channels.
+    auto load_tile = [&](const float *from, f32x2(&to)[PAIRS][EN], float scale) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-        const bool in = n0 + i < p.N;
-        const long long at = ((long long)n * p.C + c) * p.N + n0 + i;
-        A[i] = in ? p.A[(long long)c * p.N + n0 + i] : 0.f;
-        A2[i] = A[i] * kLog2e;
-        h[i] = in && p.init ? p.init[at] : 0.f;
-        gr[i] = in && q.d_fin && live ? q.d_fin[at] : 0.f;
-        dA[i] = 0.f;
-    }
-    const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, skip = p.D ? p.D[c] : 0.f;
+        for (int j = 0; j < PAIRS; ++j)
+#pragma unroll
+            for (int i = 0; i < EN; ++i) {
+                float v[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int k = first_k + tile_k + 2 * j + e;
+                    v[e] = k < per && n0 + i < p.N ? from[(long long)(g * per + k) * p.N + n0 + i] * scale : 0.f;
+                }
+                to[j][i] = pair(v[0], v[1]);
+            }
+    };
+    auto store_tile = [&](float *to, const f32x2(&from)[PAIRS][EN]) {
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j)
+#pragma unroll
+            for (int i = 0; i < EN; ++i) {
+                float v[2];
+                unpair(from[j][i], v[0], v[1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int k = first_k + tile_k + 2 * j + e;
+                    if (k < per && n0 + i < p.N) to[(long long)(g * per + k) * p.N + n0 + i] = v[e];
+                }
+            }
+    };
+    f32x2 A[PAIRS][EN], dA[PAIRS][EN], gr[PAIRS][EN], H[kRows / 2][PAIRS][EN];
+    load_tile(p.A, A, kLog2e);
+#pragma unroll
+    for (int j = 0; j < PAIRS; ++j)
+#pragma unroll
+        for (int i = 0; i < EN; ++i) dA[j][i] = gr[j][i] = 0;
+    auto tile_or_zero = [&](const float *from, f32x2(&to)[PAIRS][EN]) {
+        if (from) {
+            load_tile(from, to, 1.f);
+        } else {
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j)
+#pragma unroll
+                for (int i = 0; i < EN; ++i) to[j][i] = 0;
+        }
+    };
+    auto of_sequence = [&](const float *all, long long row) {  // a state tensor's part of the sequence of a row
+        return all ? all + p.seqs.at(row) * chunk_states : nullptr;
+    };
+    if (q.after && p.seqs.end(p.seqs.at(stop - 1)) > stop) load_tile(q.after + chunk * chunk_states, gr, 1.f);
+
     const T *X = static_cast<const T *>(p.x), *DT = static_cast<const T *>(p.dt), *Z = static_cast<const T *>(p.z);
-    const T *B = static_cast<const T *>(p.Bm) + g * p.N + n0, *Cm = static_cast<const T *>(p.Cm) + g * p.N + n0;
     const T *DY = static_cast<const T *>(q.dy);
-    for (long long r = bos; r < eos; ++r) {
-        const float x = to_float(X[r * p.x_stride + c]);
-        float dt = to_float(DT[r * p.dt_stride + c]) + bias;
-        if (p.softplus) dt = softplus(dt);
+    const T *Bm = static_cast<const T *>(p.Bm) + g * p.N, *Cm = static_cast<const T *>(p.Cm) + g * p.N;
+    const int c0 = g * per + first_k;
+    auto bring = [&](long long w0, int buf) {  // a window's rows into shared memory
 #pragma unroll
-        for (int i = 0; i < S; ++i)
-            if (n0 + i < p.N) {
-                h[i] = fmaf(exp2f(dt * A2[i]), h[i], dt * x * to_float(B[r * p.B_stride + i]));
-                if (live) q.states[(r * p.C + c) * p.N + n0 + i] = h[i];
+        for (int t = 0; t < 4; ++t) {
+            if (t == 3 && !Z) break;
+            const T *from = (t == 0 ? X : t == 1 ? DT : t == 2 ? DY : Z) + c0;
+            const long long stride = t == 0 ? p.x_stride : t == 1 ? p.dt_stride : t == 2 ? p.C : p.z_stride;
+            constexpr int VALUES = WIDE ? 16 / sizeof(T) : 1, WORDS = CH / VALUES;
+            for (int i = tid; i < kRows * WORDS; i += kScanThreads) {
+                const int u = i / WORDS, k = (i % WORDS) * VALUES;
+                if (w0 + u >= stop || first_k + k >= per) continue;
+                if constexpr (WIDE)
+                    copy16(&sm.raw[buf][t][u][k], from + (w0 + u) * stride + k);
+                else
+                    sm.raw[buf][t][u][k] = from[(w0 + u) * stride + k];
             }
-    }
-    float dD = 0.f, dbias = 0.f;
-    for (long long r = eos - 1; r >= bos; --r) {
-        const float x = to_float(X[r * p.x_stride + c]), raw = to_float(DT[r * p.dt_stride + c]) + bias;
-        const float dt = p.softplus ? softplus(raw) : raw;
-        const float dy0 = live ? to_float(DY[r * p.C + c]) : 0.f;
-        float z = 0.f, sz = 1.f, dy = dy0;
-        if (Z) {
-            z = to_float(Z[r * p.z_stride + c]);
-            sz = sigmoid(z);
-            dy = dy0 * (z * sz);
         }
-        float out = 0.f, gB = 0.f, gA = 0.f;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    // A thread's channels in the passes over (row, channel): one if the block has at most as many channels as threads.
+    constexpr int OWN = CH > kScanThreads ? CH / kScanThreads : 1;
+    float sum_D[OWN], sum_bias[OWN];
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-            const bool in = n0 + i < p.N;
-            const float Bv = in ? to_float(B[r * p.B_stride + i]) : 0.f, Cv = in ? to_float(Cm[r * p.C_stride + i]) : 0.f;
-            const float before = !in ? 0.f : r > bos ? (live ? q.states[((r - 1) * p.C + c) * p.N + n0 + i] : 0.f)
-                                                    : (p.init ? p.init[((long long)n * p.C + c) * p.N + n0 + i] : 0.f);
-            gr[i] = fmaf(Cv, dy, gr[i]);
-            out = fmaf(Cv, h[i], out);
-            const float sB = warp_sum_from(gr[i] * (dt * x), L), sC = warp_sum_from(dy * h[i], L);
-            if (in && threadIdx.x < L) {
-                const long long at = (((long long)blk * p.seqs.rows + r) * p.G + g) * p.N + n0 + i;
-                q.part_B[at] = sB;
-                q.part_C[at] = sC;
+    for (int i = 0; i < OWN; ++i) sum_D[i] = sum_bias[i] = 0.f;
+
+    long long w = (stop - r0 - 1) / kRows;
+    bring(r0 + w * kRows, 0);
+    for (int buf = 0; w >= 0; --w, buf ^= 1) {
+        const long long w0 = r0 + w * kRows;
+        const int rows = (int)min((long long)kRows, stop - w0);
+        // B and C of the window; rows and states past the end are zeros, which leave states and gradients as they are.
+        for (int i = tid; i < kRows * 2 * NP; i += kScanThreads) {
+            const int n = i % NP, side = (i / NP) % 2, u = i / (2 * NP);
+            float v = 0.f;
+            if (u < rows && n < p.N) v = to_float(side ? Cm[(w0 + u) * p.C_stride + n] : Bm[(w0 + u) * p.B_stride + n]);
+            *reinterpret_cast<float2 *>(sm.bc[u][side][n]) = make_float2(v, v);
+        }
+        // The state before the window: the kept one, and what the state before the chunk has become by then.
+        tile_or_zero(carry.kept + (chunk * plan.windows() + w) * chunk_states, H[0]);
+        const int seq0 = p.seqs.at(w0);
+        if (plan.carries && p.seqs.begin(seq0) < r0) {
+            f32x2 X0[PAIRS][EN];
+            load_tile(carry.state + chunk * chunk_states, X0, 1.f);
+            const float *time = carry.kept_time + (chunk * plan.windows() + w) * p.C + c0;
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) {
+                const int k = tile_k + 2 * j;
+                const f32x2 t2 = pair(first_k + k < per ? time[k] : 0.f, first_k + k + 1 < per ? time[k + 1] : 0.f);
+#pragma unroll
+                for (int i = 0; i < EN; ++i) H[0][j][i] = fma2(ex2_pair(mul2(t2, A[j][i])), X0[j][i], H[0][j][i]);
             }
-            gB = fmaf(gr[i], Bv, gB);
-            gr[i] *= exp2f(dt * A2[i]);
-            const float w = gr[i] * before;
-            gA = fmaf(w, A[i], gA);
-            dA[i] = fmaf(w, dt, dA[i]);
-            h[i] = before;
+        }
+        // Rows of the window that begin or end a sequence, as bits.
+        unsigned begins = 0, ends = 0;
+        {
+            const long long w1 = w0 + rows;
+            if (p.seqs.begin(seq0) == w0) begins |= 1u;
+            int n = seq0;
+            for (; n < p.seqs.n_seqs && p.seqs.end(n) < w1; ++n) {
+                const long long b = p.seqs.end(n);
+                if (b > w0) {
+                    begins |= 1u << (int)(b - w0);
+                    ends |= 1u << (int)(b - w0 - 1);
+                }
+            }
+            if (n < p.seqs.n_seqs && p.seqs.end(n) == w1) ends |= 1u << (rows - 1);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // the window's rows are there, and the last window's sums are read
+        if (w > 0) bring(w0 - kRows, buf ^ 1);
+#pragma unroll
+        for (int i = 0; i < (kRows * CH + kScanThreads - 1) / kScanThreads; ++i) {
+            const int v = i * kScanThreads + tid, u = v / CH, k = v % CH;
+            if (kRows * CH % kScanThreads != 0 && u >= kRows) break;
+            float dt = 0.f, uu = 0.f, dy = 0.f;
+            if (u < rows && first_k + k < per) {
+                dt = to_float(sm.raw[buf][1][u][k]) + (p.dt_bias ? p.dt_bias[c0 + k] : 0.f);
+                if (p.softplus) dt = softplus(dt);
+                uu = dt * to_float(sm.raw[buf][0][u][k]);
+                dy = to_float(sm.raw[buf][2][u][k]);
+                if (Z) {
+                    const float z = to_float(sm.raw[buf][3][u][k]);
+                    dy *= z * sigmoid(z);
+                }
+            }
+            sm.pre[0][u][k] = dt;
+            sm.pre[1][u][k] = uu;
+            sm.pre[2][u][k] = dy;
+        }
+        __syncthreads();
+
+        auto row_pairs = [&](int what, int u, f32x2(&to)[PAIRS]) {
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) to[j] = *reinterpret_cast<const f32x2 *>(&sm.pre[what][u][tile_k + 2 * j]);
+        };
+        auto row_states = [&](int side, int u, f32x2(&to)[EN]) {
+#pragma unroll
+            for (int i = 0; i < EN; ++i) to[i] = *reinterpret_cast<const f32x2 *>(sm.bc[u][side][n0 + i]);
+        };
+        if (begins & 1u) tile_or_zero(of_sequence(p.init, w0), H[0]);
+#pragma unroll
+        for (int u = 0; u < kRows - 2; ++u) {  // the states before rows 2, 4 and 6
+            f32x2 dt[PAIRS], uu[PAIRS], b[EN];
+            row_pairs(0, u, dt);
+            row_pairs(1, u, uu);
+            row_states(0, u, b);
+            const int from = u / 2, to = (u + 1) / 2;
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j)
+#pragma unroll
+                for (int i = 0; i < EN; ++i) {
+                    const f32x2 before = u % 2 ? H[to][j][i] : H[from][j][i];
+                    H[u / 2 + 1][j][i] = fma2(ex2_pair(mul2(dt[j], A[j][i])), before, mul2(uu[j], b[i]));
+                }
+            if (begins >> (u + 1) & 1u) tile_or_zero(of_sequence(p.init, w0 + u + 1), H[u / 2 + 1]);
         }
 #pragma unroll
-        for (int m = L / 2; m > 0; m >>= 1) {
-            out += __shfl_xor_sync(0xffffffffu, out, m);
-            gB += __shfl_xor_sync(0xffffffffu, gB, m);
-            gA += __shfl_xor_sync(0xffffffffu, gA, m);
+        for (int q2 = kRows / 2 - 1; q2 >= 0; --q2) {
+            // Row u0's decay and the state after it, which is the one before row u0 + 1 unless a sequence begins there.
+            const int u0 = 2 * q2;
+            f32x2 a0[PAIRS][EN], mid[PAIRS][EN];
+            {
+                f32x2 dt[PAIRS], uu[PAIRS], b[EN];
+                row_pairs(0, u0, dt);
+                row_pairs(1, u0, uu);
+                row_states(0, u0, b);
+#pragma unroll
+                for (int j = 0; j < PAIRS; ++j)
+#pragma unroll
+                    for (int i = 0; i < EN; ++i) {
+                        a0[j][i] = ex2_pair(mul2(dt[j], A[j][i]));
+                        mid[j][i] = fma2(a0[j][i], H[q2][j][i], mul2(uu[j], b[i]));
+                    }
+            }
+            if (begins >> (u0 + 1) & 1u) tile_or_zero(of_sequence(p.init, w0 + u0 + 1), mid);
+#pragma unroll
+            for (int e = 1; e >= 0; --e) {
+                const int u = u0 + e;
+                if (ends >> u & 1u) tile_or_zero(of_sequence(q.d_fin, w0 + u), gr);
+                f32x2 dt[PAIRS], uu[PAIRS], b[EN], dy[PAIRS], cc[EN], gB[PAIRS], gA[PAIRS], out[PAIRS], dB[EN], dC[EN];
+                row_pairs(0, u, dt);
+                row_pairs(1, u, uu);
+                row_states(0, u, b);
+                row_pairs(2, u, dy);
+                row_states(1, u, cc);
+#pragma unroll
+                for (int j = 0; j < PAIRS; ++j)
+#pragma unroll
+                    for (int i = 0; i < EN; ++i) {
+                        const f32x2 before = e ? mid[j][i] : H[q2][j][i];
+                        const f32x2 a = e ? ex2_pair(mul2(dt[j], A[j][i])) : a0[j][i];
+                        const f32x2 after = fma2(a, before, mul2(uu[j], b[i]));
+                        f32x2 gg = fma2(cc[i], dy[j], gr[j][i]);
+                        dC[i] = j == 0 ? mul2(dy[j], after) : fma2(dy[j], after, dC[i]);
+                        dB[i] = j == 0 ? mul2(gg, uu[j]) : fma2(gg, uu[j], dB[i]);
+                        gB[j] = i == 0 ? mul2(gg, b[i]) : fma2(gg, b[i], gB[j]);
+                        if (Z) out[j] = i == 0 ? mul2(cc[i], after) : fma2(cc[i], after, out[j]);
+                        gg = mul2(gg, a);
+                        gr[j][i] = gg;
+                        const f32x2 kept = mul2(gg, before);
+                        dA[j][i] = fma2(kept, dt[j], dA[j][i]);
+                        gA[j] = i == 0 ? mul2(kept, A[j][i]) : fma2(kept, A[j][i], gA[j]);
+                    }
+                // Over the thread's channels, to be added over the block's threads below.
+                float sB[EN], sC[EN];
+#pragma unroll
+                for (int i = 0; i < EN; ++i) {
+                    float lo, hi;
+                    unpair(dB[i], lo, hi);
+                    sB[i] = lo + hi;
+                    unpair(dC[i], lo, hi);
+                    sC[i] = lo + hi;
+                }
+                store_floats<EN>(&sm.part[u][0][warp * CL + cl][n0], sB);
+                store_floats<EN>(&sm.part[u][1][warp * CL + cl][n0], sC);
+                // Over the states' lanes: each step halves the channels that a lane keeps.
+                float v[3][EC];
+#pragma unroll
+                for (int j = 0; j < PAIRS; ++j) {
+                    unpair(gB[j], v[0][2 * j], v[0][2 * j + 1]);
+                    unpair(gA[j], v[1][2 * j], v[1][2 * j + 1]);
+                    if (Z) unpair(out[j], v[2][2 * j], v[2][2 * j + 1]);
+                }
+                constexpr int FOLD = NL < EC ? NL : EC;  // lanes that share out the channels
+                int offset = 0;
+#pragma unroll
+                for (int t = 0; t < 3; ++t) {
+                    if (t == 2 && !Z) break;
+#pragma unroll
+                    for (int m = NL / 2; m >= FOLD && m > 0; m >>= 1)
+#pragma unroll
+                        for (int k = 0; k < EC; ++k) v[t][k] += __shfl_xor_sync(0xffffffffu, v[t][k], m);
+                    int count = EC;
+                    offset = 0;
+#pragma unroll
+                    for (int m = FOLD / 2; m > 0; m >>= 1) {
+                        count /= 2;
+                        const bool upper = nl & m;
+#pragma unroll
+                        for (int k = 0; k < EC / 2; ++k) {
+                            if (k >= count) break;
+                            const float keep = upper ? v[t][count + k] : v[t][k], send = upper ? v[t][k] : v[t][count + k];
+                            v[t][k] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+                        }
+                        if (upper) offset += count;
+                    }
+                    if (nl < FOLD) {
+#pragma unroll
+                        for (int k = 0; k < EC / FOLD; ++k) sm.sum[t][u][tile_k + offset + k] = v[t][k];
+                    }
+                }
+                if (begins >> u & 1u) {
+                    if (q.d_init) store_tile(const_cast<float *>(of_sequence(q.d_init, w0 + u)), gr);
+                }
+            }
         }
-        float ddt = fmaf(gB, x, gA);
-        if (p.softplus) ddt *= sigmoid(raw);
-        dD = fmaf(dy, x, dD);
-        dbias += ddt;
-        if (live && n0 == 0) {
-            q.dx[r * p.C + c] = fmaf(gB, dt, dy * skip);
-            q.ddt[r * p.C + c] = ddt;
-            if (Z) q.dz[r * p.C + c] = dy0 * fmaf(skip, x, out) * (sz * fmaf(z, 1.f - sz, 1.f));
+        __syncthreads();
+
+        // Per (row, channel).
+#pragma unroll
+        for (int i = 0; i < (kRows * CH + kScanThreads - 1) / kScanThreads; ++i) {
+            const int v = i * kScanThreads + tid, u = v / CH, k = v % CH;
+            if (kRows * CH % kScanThreads != 0 && u >= kRows) break;
+            if (u >= rows || first_k + k >= per) continue;
+            const long long at = (w0 + u) * p.C + c0 + k;
+            const float x = to_float(sm.raw[buf][0][u][k]), dt = sm.pre[0][u][k], dy = sm.pre[2][u][k];
+            const float gB = sm.sum[0][u][k], skip = p.D ? p.D[c0 + k] : 0.f;
+            float ddt = fmaf(gB, x, sm.sum[1][u][k] * 0.69314718f);  // A was taken with log2(e)
+            if (p.softplus) ddt *= sigmoid(to_float(sm.raw[buf][1][u][k]) + (p.dt_bias ? p.dt_bias[c0 + k] : 0.f));
+            q.dx[at] = fmaf(gB, dt, dy * skip);
+            q.ddt[at] = ddt;
+            if (Z) {
+                const float z = to_float(sm.raw[buf][3][u][k]), s = sigmoid(z);
+                q.dz[at] = to_float(sm.raw[buf][2][u][k]) * fmaf(skip, x, sm.sum[2][u][k]) * (s * fmaf(z, 1.f - s, 1.f));
+            }
+            sum_D[i % OWN] = fmaf(dy, x, sum_D[i % OWN]);
+            sum_bias[i % OWN] += ddt;
+        }
+        // dB and dC of the block's channels: four states per thread, the parts shared out over SPLIT lanes.
+        constexpr int ITEMS = kRows * 2 * NP / 4, SPLIT = ITEMS < kScanThreads ? kScanThreads / ITEMS : 1;
+#pragma unroll
+        for (int i = tid; i < ITEMS * SPLIT; i += kScanThreads) {
+            const int n = i % (NP / 4) * 4, s = i / (NP / 4) % SPLIT, side = i / (NP / 4 * SPLIT) % 2, u = i / (NP / 4 * SPLIT * 2);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < PARTS / SPLIT; ++k) {
+                const float4 o = *reinterpret_cast<const float4 *>(&sm.part[u][side][k * SPLIT + s][n]);
+                v.x += o.x;
+                v.y += o.y;
+                v.z += o.z;
+                v.w += o.w;
+            }
+#pragma unroll
+            for (int m = SPLIT / 2; m > 0; m >>= 1) {
+                v.x += __shfl_xor_sync(0xffffffffu, v.x, m * (NP / 4));
+                v.y += __shfl_xor_sync(0xffffffffu, v.y, m * (NP / 4));
+                v.z += __shfl_xor_sync(0xffffffffu, v.z, m * (NP / 4));
+                v.w += __shfl_xor_sync(0xffffffffu, v.w, m * (NP / 4));
+            }
+            if (s != 0 || u >= rows) continue;
+            float *to = (side ? q.part_C : q.part_B) + (((long long)blk * p.seqs.rows + w0 + u) * p.G + g) * p.N + n;
+            const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (n + k < p.N) to[k] = e[k];
         }
     }
-    if (!live) return;
+    store_tile(q.part_A + chunk * chunk_states, dA);
+    // dD and ddt_bias: the threads that share a channel, in order.
+    __syncthreads();
+    float *both = &sm.pre[0][0][0];
 #pragma unroll
-    for (int i = 0; i < S; ++i)
-        if (n0 + i < p.N) {
-            const long long at = ((long long)n * p.C + c) * p.N + n0 + i;
-            if (q.d_init) q.d_init[at] = gr[i];
-            q.part_A[at] = dA[i];
+    for (int i = 0; i < OWN; ++i) {
+        both[i * kScanThreads + tid] = sum_D[i];
+        both[(OWN + i) * kScanThreads + tid] = sum_bias[i];
+    }
+    __syncthreads();
+    for (int k = tid; k < CH && first_k + k < per; k += kScanThreads) {
+        float d = 0.f, s = 0.f;
+        for (int i = k; i < OWN * kScanThreads; i += CH) {
+            d += both[i];
+            s += both[OWN * kScanThreads + i];
         }
-    if (n0 == 0) {
-        q.part_D[(long long)n * p.C + c] = dD;
-        q.part_bias[(long long)n * p.C + c] = dbias;
+        q.part_D[(long long)chunk * p.C + c0 + k] = d;
+        q.part_bias[(long long)chunk * p.C + c0 + k] = s;
     }
 }
 
@@ -131,39 +418,112 @@ __global__ void scan_reduce_kernel(const float *__restrict__ in, long long size,
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= size) return;
     double sum = 0.0;
+#pragma unroll 8
     for (int j = 0; j < count; ++j) sum += in[j * size + i];
     out[i] = (float)sum;
 }
 
+// The initial-state gradients of empty sequences are their final states'.
+__global__ void scan_empty_kernel(Seqs seqs, long long size, const float *__restrict__ d_fin, float *__restrict__ d_init) {
+    const int n = blockIdx.x;
+    if (seqs.begin(n) != seqs.end(n)) return;
+    for (long long i = threadIdx.x; i < size; i += blockDim.x) d_init[n * size + i] = d_fin ? d_fin[n * size + i] : 0.f;
+}
+
+template <typename F>
+cudaError_t by_states(int N, F &&f) {
+    if (N <= 4) return f.template operator()<2, 4, 1>();
+    if (N <= 8) return f.template operator()<4, 4, 2>();
+    if (N <= 16) return f.template operator()<4, 4, 4>();
+    if (N <= 32) return f.template operator()<4, 4, 8>();
+    if (N <= 64) return f.template operator()<4, 4, 16>();
+    if (N <= 128) return f.template operator()<4, 4, 32>();
+    return f.template operator()<2, 8, 32>();
+}
+
+struct ChannelsOf {
+    template <int EC, int EN, int NL>
+    cudaError_t operator()() {
+        channels = Shape<EC, EN, NL>::CH;
+        return cudaSuccess;
+    }
+    int channels = 0;
+};
+
+int blocks_per_group(const kda_scan_args &a) {
+    ChannelsOf c;
+    by_states(a.N, c);
+    return (a.D / a.G + c.channels - 1) / c.channels;
+}
+
 struct BackwardLaunch {
+    kda_dtype dtype;
     ScanParams p;
     GradParams q;
+    ScanPlan plan;
+    Carries carry;
+    bool wide;
+    int blocks;
     cudaStream_t s;
-    template <typename T, int S, int L>
-    void operator()() {
-        scan_backward_kernel<T, S, L><<<dim3((unsigned)p.seqs.n_seqs, (unsigned)(q.blocks * p.G)), 32, 0, s>>>(p, q);
+    template <typename T, int EC, int EN, int NL, bool WIDE>
+    cudaError_t launch() {
+        constexpr int bytes = sizeof(Shared<T, Shape<EC, EN, NL>>);
+        auto *kernel = scan_backward_kernel<T, EC, EN, NL, WIDE>;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        kernel<<<dim3((unsigned)plan.chunks, (unsigned)blocks), kScanThreads, bytes, s>>>(p, q, plan, carry);
+        return cudaGetLastError();
+    }
+    template <int EC, int EN, int NL>
+    cudaError_t operator()() {
+        if (dtype == KDA_BF16)
+            return wide ? launch<__nv_bfloat16, EC, EN, NL, true>() : launch<__nv_bfloat16, EC, EN, NL, false>();
+        return wide ? launch<float, EC, EN, NL, true>() : launch<float, EC, EN, NL, false>();
     }
 };
 
-size_t layout(const kda_scan_args &a, GradParams *q, char *ws) {
-    const long long rows = (long long)a.B * a.T, n = a.cu_seqlens ? a.n_seqs : a.B;
-    const int blocks = (a.D / a.G * scan_lanes(a.N) + 31) / 32;
-    size_t at = 0;
+// Whole sequences where they give every SM three blocks; otherwise chunks that give it four, of at least 64 rows.
+ScanPlan backward_plan(const kda_scan_args &a, int sms) {
+    const long long rows = (long long)a.B * a.T, blocks = (long long)blocks_per_group(a) * a.G;
+    if (rows == 0) return ScanPlan{0, 1, false};
+    if (sms <= 0) sms = 152;
+    if (!a.cu_seqlens && (a.B * blocks >= 3 * sms || a.T <= 64)) return ScanPlan{a.B, a.T, false};
+    const long long most = (rows + 63) / 64, chunks = std::max(1LL, std::min(most, 4LL * sms / blocks));
+    const long long per = ((rows + chunks - 1) / chunks + 31) / 32 * 32;
+    const int count = (int)((rows + per - 1) / per);
+    return ScanPlan{count, per, count > 1};
+}
+
+struct Layout {
+    GradParams q{};
+    Carries forward{}, back{};
+    size_t bytes = 0;
+};
+
+Layout layout(const kda_scan_args &a, const ScanPlan &plan, char *ws) {
+    const long long rows = (long long)a.B * a.T;
+    const size_t states = (size_t)a.D * a.N, chunks = plan.chunks, windows = chunks * plan.windows();
+    const int blocks = blocks_per_group(a);
+    Layout l;
     auto take = [&](size_t count) {
-        float *r = reinterpret_cast<float *>(ws + at);
-        at += (count * sizeof(float) + 255) / 256 * 256;
+        float *r = reinterpret_cast<float *>(ws + l.bytes);
+        l.bytes += (count * sizeof(float) + 255) / 256 * 256;
         return r;
     };
-    GradParams t{};
-    t.blocks = blocks;
-    t.states = take((size_t)rows * a.D * a.N);
-    t.part_B = take((size_t)blocks * rows * a.G * a.N);
-    t.part_C = take((size_t)blocks * rows * a.G * a.N);
-    t.part_A = take((size_t)n * a.D * a.N);
-    t.part_D = take((size_t)n * a.D);
-    t.part_bias = take((size_t)n * a.D);
-    if (q) *q = t;
-    return at;
+    l.forward.kept = take(windows * states);
+    l.forward.kept_time = take(windows * a.D);
+    l.forward.state = take(chunks * states);
+    l.forward.time = take(chunks * a.D);
+    if (plan.carries) {
+        l.back.state = take(chunks * states);
+        l.back.time = take(chunks * a.D);
+    }
+    l.q.part_B = take((size_t)blocks * rows * a.G * a.N);
+    l.q.part_C = take((size_t)blocks * rows * a.G * a.N);
+    l.q.part_A = take(chunks * states);
+    l.q.part_D = take(chunks * a.D);
+    l.q.part_bias = take(chunks * a.D);
+    return l;
 }
 
 void reduce(const float *in, long long size, int count, float *out, cudaStream_t s) {
@@ -172,27 +532,43 @@ void reduce(const float *in, long long size, int count, float *out, cudaStream_t
 
 }  // namespace
 
-size_t scan_backward_workspace_bytes(const kda_scan_args &a, int) { return layout(a, nullptr, nullptr); }
+size_t scan_backward_workspace_bytes(const kda_scan_args &a, int sms) {
+    return layout(a, backward_plan(a, sms), nullptr).bytes;
+}
 
-cudaError_t launch_scan_backward(const kda_scan_args &a, const kda_scan_grads &g, void *ws, int, unsigned *err,
+cudaError_t launch_scan_backward(const kda_scan_args &a, const kda_scan_grads &g, void *ws, int sms, unsigned *err,
                                  cudaStream_t s) {
-    BackwardLaunch l{scan_params(a, err), {}, s};
-    layout(a, &l.q, static_cast<char *>(ws));
-    l.q.dy = g.dy;
-    l.q.d_fin = g.d_final_state;
-    l.q.dx = g.dx;
-    l.q.ddt = g.ddt;
-    l.q.dz = g.dz;
-    l.q.d_init = g.d_initial_state;
-    const cudaError_t e = scan_by_type(a, l);
-    if (e != cudaSuccess) return e;
-    const long long rows = l.p.seqs.rows;
-    const int n = l.p.seqs.n_seqs;
-    reduce(l.q.part_B, rows * a.G * a.N, l.q.blocks, g.dB, s);
-    reduce(l.q.part_C, rows * a.G * a.N, l.q.blocks, g.dC, s);
-    reduce(l.q.part_A, (long long)a.D * a.N, n, g.dA, s);
-    reduce(l.q.part_D, a.D, n, g.dDskip, s);
-    reduce(l.q.part_bias, a.D, n, g.ddt_bias, s);
+    const ScanPlan plan = backward_plan(a, sms);
+    const Layout l = layout(a, plan, static_cast<char *>(ws));
+    const ScanParams p = scan_params(a, err);
+    GradParams q = l.q;
+    q.dy = g.dy;
+    q.d_fin = g.d_final_state;
+    q.dx = g.dx;
+    q.ddt = g.ddt;
+    q.dz = g.dz;
+    q.d_init = g.d_initial_state;
+    const int blocks = blocks_per_group(a);
+    cudaError_t e = cudaSuccess;
+    if (plan.chunks > 0) {
+        if ((e = launch_scan_states(a, plan, l.forward, err, s)) != cudaSuccess) return e;
+        if (plan.carries) {
+            if ((e = launch_scan_back_ends(a, g.dy, g.d_final_state, plan, l.back, err, s)) != cudaSuccess) return e;
+            q.after = l.back.state;
+        }
+        const int e16 = a.dtype == KDA_BF16 ? 8 : 4;  // values in 16 bytes
+        const bool wide = aligned16(p.x) && aligned16(p.dt) && aligned16(p.z) && aligned16(q.dy) && (a.D / a.G) % e16 == 0 &&
+                          p.x_stride % e16 == 0 && p.dt_stride % e16 == 0 && (!p.z || p.z_stride % e16 == 0);
+        if ((e = by_states(a.N, BackwardLaunch{a.dtype, p, q, plan, l.forward, wide, blocks * a.G, s})) != cudaSuccess) return e;
+    }
+    const long long rows = p.seqs.rows;
+    reduce(q.part_B, rows * a.G * a.N, blocks, g.dB, s);
+    reduce(q.part_C, rows * a.G * a.N, blocks, g.dC, s);
+    reduce(q.part_A, (long long)a.D * a.N, plan.chunks, g.dA, s);
+    reduce(q.part_D, a.D, plan.chunks, g.dDskip, s);
+    reduce(q.part_bias, a.D, plan.chunks, g.ddt_bias, s);
+    if (g.d_initial_state && p.seqs.n_seqs > 0 && (a.cu_seqlens || a.T == 0))
+        scan_empty_kernel<<<(unsigned)p.seqs.n_seqs, 256, 0, s>>>(p.seqs, (long long)a.D * a.N, g.d_final_state, g.d_initial_state);
     return cudaGetLastError();
 }
 
