@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kScanThreads, 3)
         f32x2 s0 = 0, s1 = 0;
 #pragma unroll
         for (int i = 0; i < S / 2; ++i) {
-            const f32x2 b = B2[i], a0 = ex2_pair(mul2(t0, A[0][i])), a1 = ex2_pair(mul2(t1, A[1][i]));
+            const f32x2 b = B2[i], a0 = decay2(t0, A[0][i]), a1 = decay2(t1, A[1][i]);
             h[0][i] = BACK ? mul2(a0, fma2(u0, b, h[0][i])) : fma2(a0, h[0][i], mul2(u0, b));
             h[1][i] = BACK ? mul2(a1, fma2(u1, b, h[1][i])) : fma2(a1, h[1][i], mul2(u1, b));
             if constexpr (OUT) {

@@ -13,9 +13,11 @@
 //
 // Main kernel: a thread holds a tile of 4 channels x 4 states, a warp N / 4 of those along the states and the rest along
 // the channels. The sums over channels (dB, dC) and over states (dx, ddt, y) are both taken in the thread's registers first;
-// tiles that are narrow in one direction move 1.3 times as many values between lanes. A window's
-// states are recomputed from the kept one into registers, one of every two rows; the row between is recomputed from its
-// decay, which the way back needs anyway. That is 15 multiply-adds and 1.75 exponentials per (row, channel, state).
+// tiles that are narrow in one direction move 1.3 times as many values between lanes. A window's states are recomputed from
+// the kept one, and those before every second row are held in shared memory, each thread its own; the row between is
+// recomputed from its decay, which the way back needs anyway. That is 15 multiply-adds and 1.75 exponentials per (row, channel,
+// state). With the whole window unrolled and its states in registers the kernel was twice as slow: spills and a
+// loop that did not fit the instruction cache.
 #include <algorithm>
 
 #include "kda_scan.cuh"
@@ -39,6 +41,7 @@ struct GradParams {
 // EC channels x EN states per thread, NL lanes along the states.
 template <int EC, int EN, int NL>
 struct Shape {
+    static constexpr int EC_ = EC, EN_ = EN;
     static constexpr int NP = EN * NL, CL = 32 / NL, CH = kWarps * CL * EC, PARTS = kWarps * CL;
 };
 
@@ -49,6 +52,8 @@ struct Shared {
     alignas(16) float sum[3][kRows][SH::CH];      // over the states: g B, g a h A, C h
     alignas(16) float bc[kRows][2][SH::NP][2];    // B and C, every value twice: one for each channel of a pair
     alignas(16) float part[kRows][2][SH::PARTS][SH::NP];  // dB and dC of each thread's channels
+    alignas(16) float4 kept[2][SH::EC_ * SH::EN_ / 4][kScanThreads];  // the state before a window, per thread
+    alignas(16) ulonglong2 states[2][SH::EC_ * SH::EN_ / 4][kScanThreads];  // the states before rows 2 and 4, per thread
 };
 
 __device__ __forceinline__ void copy16(void *to, const void *from) {
@@ -100,7 +105,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
                 }
             }
     };
-    f32x2 A[PAIRS][EN], dA[PAIRS][EN], gr[PAIRS][EN], H[kRows / 2][PAIRS][EN];
+    f32x2 A[PAIRS][EN], dA[PAIRS][EN], gr[PAIRS][EN], h[PAIRS][EN];
     load_tile(p.A, A, kLog2e);
 #pragma unroll
     for (int j = 0; j < PAIRS; ++j)
@@ -125,6 +130,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
     const T *DY = static_cast<const T *>(q.dy);
     const T *Bm = static_cast<const T *>(p.Bm) + g * p.N, *Cm = static_cast<const T *>(p.Cm) + g * p.N;
     const int c0 = g * per + first_k;
+    const bool vectors = p.N % 4 == 0;  // the workspace's states lie on 16-byte boundaries
     auto bring = [&](long long w0, int buf) {  // a window's rows into shared memory
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -141,6 +147,25 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
                     sm.raw[buf][t][u][k] = from[(w0 + u) * stride + k];
             }
         }
+        // The state that was kept before the window: a thread brings what it will read itself.
+        const float *kept = carry.kept + (chunk * plan.windows() + (w0 - r0) / kRows) * chunk_states;
+#pragma unroll
+        for (int e = 0; e < EC; ++e) {
+            const int k = first_k + tile_k + e;
+            const float *from = kept + (long long)(g * per + k) * p.N + n0;
+#pragma unroll
+            for (int i = 0; i < EN; i += 4) {
+                float4 *to = &sm.kept[buf][(e * EN + i) / 4][tid];
+                if (vectors && k < per && n0 + i + 4 <= p.N) {
+                    copy16(to, from + i);
+                } else {
+                    float v[4];
+#pragma unroll
+                    for (int o = 0; o < 4; ++o) v[o] = k < per && n0 + i + o < p.N ? from[i + o] : 0.f;
+                    *to = make_float4(v[0], v[1], v[2], v[3]);
+                }
+            }
+        }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
@@ -150,39 +175,41 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
 #pragma unroll
     for (int i = 0; i < OWN; ++i) sum_D[i] = sum_bias[i] = 0.f;
 
+    // B and C of a window, fetched one window ahead; rows and states past the end are zeros, which leave states and gradients
+    // as they are.
+    constexpr int EACH = (kRows * 2 * NP + kScanThreads - 1) / kScanThreads;
+    T ahead[EACH];
+    auto fetch = [&](long long w0) {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int v = i * kScanThreads + tid, n = v % NP, side = v / NP % 2;
+            const long long row = w0 + v / (2 * NP);
+            ahead[i] = v < kRows * 2 * NP && row < stop && n < p.N
+                           ? (side ? Cm[row * p.C_stride + n] : Bm[row * p.B_stride + n]) : from_float<T>(0.f);
+        }
+    };
     long long w = (stop - r0 - 1) / kRows;
     bring(r0 + w * kRows, 0);
+    fetch(r0 + w * kRows);
+    long long begin = 0, end = -1;  // of the sequence last looked at
     for (int buf = 0; w >= 0; --w, buf ^= 1) {
-        const long long w0 = r0 + w * kRows;
-        const int rows = (int)min((long long)kRows, stop - w0);
-        // B and C of the window; rows and states past the end are zeros, which leave states and gradients as they are.
-        for (int i = tid; i < kRows * 2 * NP; i += kScanThreads) {
-            const int n = i % NP, side = (i / NP) % 2, u = i / (2 * NP);
-            float v = 0.f;
-            if (u < rows && n < p.N) v = to_float(side ? Cm[(w0 + u) * p.C_stride + n] : Bm[(w0 + u) * p.B_stride + n]);
-            *reinterpret_cast<float2 *>(sm.bc[u][side][n]) = make_float2(v, v);
-        }
-        // The state before the window: the kept one, and what the state before the chunk has become by then.
-        tile_or_zero(carry.kept + (chunk * plan.windows() + w) * chunk_states, H[0]);
-        const int seq0 = p.seqs.at(w0);
-        if (plan.carries && p.seqs.begin(seq0) < r0) {
-            f32x2 X0[PAIRS][EN];
-            load_tile(carry.state + chunk * chunk_states, X0, 1.f);
-            const float *time = carry.kept_time + (chunk * plan.windows() + w) * p.C + c0;
+        const long long w0 = r0 + w * kRows, w1 = min(w0 + kRows, stop);
+        const int rows = (int)(w1 - w0);
 #pragma unroll
-            for (int j = 0; j < PAIRS; ++j) {
-                const int k = tile_k + 2 * j;
-                const f32x2 t2 = pair(first_k + k < per ? time[k] : 0.f, first_k + k + 1 < per ? time[k + 1] : 0.f);
-#pragma unroll
-                for (int i = 0; i < EN; ++i) H[0][j][i] = fma2(ex2_pair(mul2(t2, A[j][i])), X0[j][i], H[0][j][i]);
+        for (int i = 0; i < EACH; ++i) {
+            const int v = i * kScanThreads + tid;
+            if (v < kRows * 2 * NP) {
+                const float f = to_float(ahead[i]);
+                *reinterpret_cast<float2 *>(sm.bc[v / (2 * NP)][v / NP % 2][v % NP]) = make_float2(f, f);
             }
         }
-        // Rows of the window that begin or end a sequence, as bits.
+        // Rows of the window that begin or end a sequence, as bits; none where the window lies inside one.
         unsigned begins = 0, ends = 0;
-        {
-            const long long w1 = w0 + rows;
-            if (p.seqs.begin(seq0) == w0) begins |= 1u;
-            int n = seq0;
+        if (!(begin < w0 && w1 < end)) {
+            int n = p.seqs.at(w0);
+            begin = p.seqs.begin(n);
+            end = p.seqs.end(n);
+            if (begin == w0) begins |= 1u;
             for (; n < p.seqs.n_seqs && p.seqs.end(n) < w1; ++n) {
                 const long long b = p.seqs.end(n);
                 if (b > w0) {
@@ -194,25 +221,61 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();  // the window's rows are there, and the last window's sums are read
-        if (w > 0) bring(w0 - kRows, buf ^ 1);
+        if (w > 0) {
+            bring(w0 - kRows, buf ^ 1);
+            fetch(w0 - kRows);
+        }
+        // dt', u and dy' per (row, channel), two at a time.
+        constexpr int ITEMS_P = (kRows * CH + kScanThreads - 1) / kScanThreads;
 #pragma unroll
-        for (int i = 0; i < (kRows * CH + kScanThreads - 1) / kScanThreads; ++i) {
-            const int v = i * kScanThreads + tid, u = v / CH, k = v % CH;
-            if (kRows * CH % kScanThreads != 0 && u >= kRows) break;
-            float dt = 0.f, uu = 0.f, dy = 0.f;
-            if (u < rows && first_k + k < per) {
-                dt = to_float(sm.raw[buf][1][u][k]) + (p.dt_bias ? p.dt_bias[c0 + k] : 0.f);
-                if (p.softplus) dt = softplus(dt);
-                uu = dt * to_float(sm.raw[buf][0][u][k]);
-                dy = to_float(sm.raw[buf][2][u][k]);
-                if (Z) {
-                    const float z = to_float(sm.raw[buf][3][u][k]);
-                    dy *= z * sigmoid(z);
-                }
+        for (int i = 0; i < ITEMS_P; i += 2) {
+            float x[2], dt[2], dy[2], z[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int v = (i + e) * kScanThreads + tid, u = v / CH, k = v % CH;
+                const bool in = (ITEMS_P > 1 || e == 0) && u < rows && first_k + k < per;
+                x[e] = in ? to_float(sm.raw[buf][0][u][k]) : 0.f;
+                dt[e] = in ? to_float(sm.raw[buf][1][u][k]) + (p.dt_bias ? p.dt_bias[c0 + k] : 0.f) : 0.f;
+                dy[e] = in ? to_float(sm.raw[buf][2][u][k]) : 0.f;
+                z[e] = in && Z ? to_float(sm.raw[buf][3][u][k]) : 0.f;
             }
-            sm.pre[0][u][k] = dt;
-            sm.pre[1][u][k] = uu;
-            sm.pre[2][u][k] = dy;
+            f32x2 dt2 = pair(dt[0], dt[1]), dy2 = pair(dy[0], dy[1]);
+            if (p.softplus) dt2 = softplus2(dt2);
+            if (Z) dy2 = mul2(dy2, silu2(pair(z[0], z[1])));
+            unpair(dt2, dt[0], dt[1]);
+            unpair(dy2, dy[0], dy[1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int v = (i + e) * kScanThreads + tid, u = v / CH, k = v % CH;
+                if ((ITEMS_P == 1 && e == 1) || u >= kRows) break;
+                const bool in = u < rows && first_k + k < per;
+                sm.pre[0][u][k] = in ? dt[e] : 0.f;
+                sm.pre[1][u][k] = in ? dt[e] * x[e] : 0.f;
+                sm.pre[2][u][k] = dy[e];
+            }
+        }
+        // The state before the window: the kept one, and what the state before the chunk has become by then.
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j)
+#pragma unroll
+            for (int i = 0; i < EN; i += 4) {
+                const float4 v = sm.kept[buf][(2 * j * EN + i) / 4][tid], o = sm.kept[buf][((2 * j + 1) * EN + i) / 4][tid];
+                h[j][i] = pair(v.x, o.x);
+                h[j][i + 1] = pair(v.y, o.y);
+                h[j][i + 2] = pair(v.z, o.z);
+                h[j][i + 3] = pair(v.w, o.w);
+            }
+        if (plan.carries && begin < r0) {
+            f32x2 X0[PAIRS][EN];
+            load_tile(carry.state + chunk * chunk_states, X0, 1.f);
+            const float *time = carry.kept_time + (chunk * plan.windows() + w) * p.C + c0;
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) {
+                const int k = tile_k + 2 * j;
+                const f32x2 t2 = pair(first_k + k < per ? time[k] : 0.f, first_k + k + 1 < per ? time[k + 1] : 0.f);
+#pragma unroll
+                for (int i = 0; i < EN; ++i) h[j][i] = fma2(decay2(t2, A[j][i]), X0[j][i], h[j][i]);
+            }
         }
         __syncthreads();
 
@@ -224,25 +287,44 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
 #pragma unroll
             for (int i = 0; i < EN; ++i) to[i] = *reinterpret_cast<const f32x2 *>(sm.bc[u][side][n0 + i]);
         };
-        if (begins & 1u) tile_or_zero(of_sequence(p.init, w0), H[0]);
+        // Tiles in the thread's own places of shared memory: before row 0 where the kept state was, then rows 2 and 4.
+        auto place = [&](int q2) {
+            return q2 == 0 ? reinterpret_cast<ulonglong2 *>(&sm.kept[buf][0][tid]) : &sm.states[q2 - 1][0][tid];
+        };
+        constexpr int WORDS = PAIRS * EN / 2;
+        auto save = [&](int q2) {
+            ulonglong2 *to = place(q2);
+            f32x2 *flat = &h[0][0];
 #pragma unroll
-        for (int u = 0; u < kRows - 2; ++u) {  // the states before rows 2, 4 and 6
+            for (int i = 0; i < WORDS; ++i) to[i * kScanThreads] = make_ulonglong2(flat[2 * i], flat[2 * i + 1]);
+        };
+        auto restore = [&](int q2) {
+            const ulonglong2 *from = place(q2);
+            f32x2 *flat = &h[0][0];
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+                const ulonglong2 v = from[i * kScanThreads];
+                flat[2 * i] = v.x;
+                flat[2 * i + 1] = v.y;
+            }
+        };
+        if (begins & 1u) tile_or_zero(of_sequence(p.init, w0), h);
+#pragma unroll 1
+        for (int u = 0; u < kRows - 2; ++u) {  // up to the state before row 6
+            if (u % 2 == 0) save(u / 2);
             f32x2 dt[PAIRS], uu[PAIRS], b[EN];
             row_pairs(0, u, dt);
             row_pairs(1, u, uu);
             row_states(0, u, b);
-            const int from = u / 2, to = (u + 1) / 2;
 #pragma unroll
             for (int j = 0; j < PAIRS; ++j)
 #pragma unroll
-                for (int i = 0; i < EN; ++i) {
-                    const f32x2 before = u % 2 ? H[to][j][i] : H[from][j][i];
-                    H[u / 2 + 1][j][i] = fma2(ex2_pair(mul2(dt[j], A[j][i])), before, mul2(uu[j], b[i]));
-                }
-            if (begins >> (u + 1) & 1u) tile_or_zero(of_sequence(p.init, w0 + u + 1), H[u / 2 + 1]);
+                for (int i = 0; i < EN; ++i) h[j][i] = fma2(decay2(dt[j], A[j][i]), h[j][i], mul2(uu[j], b[i]));
+            if (begins >> (u + 1) & 1u) tile_or_zero(of_sequence(p.init, w0 + u + 1), h);
         }
-#pragma unroll
+#pragma unroll 1
         for (int q2 = kRows / 2 - 1; q2 >= 0; --q2) {
+            if (q2 < kRows / 2 - 1) restore(q2);
             // Row u0's decay and the state after it, which is the one before row u0 + 1 unless a sequence begins there.
             const int u0 = 2 * q2;
             f32x2 a0[PAIRS][EN], mid[PAIRS][EN];
@@ -255,8 +337,8 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
                 for (int j = 0; j < PAIRS; ++j)
 #pragma unroll
                     for (int i = 0; i < EN; ++i) {
-                        a0[j][i] = ex2_pair(mul2(dt[j], A[j][i]));
-                        mid[j][i] = fma2(a0[j][i], H[q2][j][i], mul2(uu[j], b[i]));
+                        a0[j][i] = decay2(dt[j], A[j][i]);
+                        mid[j][i] = fma2(a0[j][i], h[j][i], mul2(uu[j], b[i]));
                     }
             }
             if (begins >> (u0 + 1) & 1u) tile_or_zero(of_sequence(p.init, w0 + u0 + 1), mid);
@@ -274,14 +356,14 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
                 for (int j = 0; j < PAIRS; ++j)
 #pragma unroll
                     for (int i = 0; i < EN; ++i) {
-                        const f32x2 before = e ? mid[j][i] : H[q2][j][i];
-                        const f32x2 a = e ? ex2_pair(mul2(dt[j], A[j][i])) : a0[j][i];
+                        const f32x2 before = e ? mid[j][i] : h[j][i];
+                        const f32x2 a = e ? decay2(dt[j], A[j][i]) : a0[j][i];
                         const f32x2 after = fma2(a, before, mul2(uu[j], b[i]));
                         f32x2 gg = fma2(cc[i], dy[j], gr[j][i]);
                         dC[i] = j == 0 ? mul2(dy[j], after) : fma2(dy[j], after, dC[i]);
                         dB[i] = j == 0 ? mul2(gg, uu[j]) : fma2(gg, uu[j], dB[i]);
                         gB[j] = i == 0 ? mul2(gg, b[i]) : fma2(gg, b[i], gB[j]);
-                        if (Z) out[j] = i == 0 ? mul2(cc[i], after) : fma2(cc[i], after, out[j]);
+                        out[j] = i == 0 ? mul2(cc[i], after) : fma2(cc[i], after, out[j]);
                         gg = mul2(gg, a);
                         gr[j][i] = gg;
                         const f32x2 kept = mul2(gg, before);
@@ -306,13 +388,12 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
                 for (int j = 0; j < PAIRS; ++j) {
                     unpair(gB[j], v[0][2 * j], v[0][2 * j + 1]);
                     unpair(gA[j], v[1][2 * j], v[1][2 * j + 1]);
-                    if (Z) unpair(out[j], v[2][2 * j], v[2][2 * j + 1]);
+                    unpair(out[j], v[2][2 * j], v[2][2 * j + 1]);
                 }
                 constexpr int FOLD = NL < EC ? NL : EC;  // lanes that share out the channels
                 int offset = 0;
 #pragma unroll
                 for (int t = 0; t < 3; ++t) {
-                    if (t == 2 && !Z) break;
 #pragma unroll
                     for (int m = NL / 2; m >= FOLD && m > 0; m >>= 1)
 #pragma unroll
@@ -343,7 +424,10 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
         }
         __syncthreads();
 
-        // Per (row, channel).
+        // Per (row, channel). Long sums are taken in two levels, a window's and then the chunk's.
+        float part_D[OWN], part_bias[OWN];
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) part_D[i] = part_bias[i] = 0.f;
 #pragma unroll
         for (int i = 0; i < (kRows * CH + kScanThreads - 1) / kScanThreads; ++i) {
             const int v = i * kScanThreads + tid, u = v / CH, k = v % CH;
@@ -360,8 +444,13 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
                 const float z = to_float(sm.raw[buf][3][u][k]), s = sigmoid(z);
                 q.dz[at] = to_float(sm.raw[buf][2][u][k]) * fmaf(skip, x, sm.sum[2][u][k]) * (s * fmaf(z, 1.f - s, 1.f));
             }
-            sum_D[i % OWN] = fmaf(dy, x, sum_D[i % OWN]);
-            sum_bias[i % OWN] += ddt;
+            part_D[i % OWN] = fmaf(dy, x, part_D[i % OWN]);
+            part_bias[i % OWN] += ddt;
+        }
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            sum_D[i] += part_D[i];
+            sum_bias[i] += part_bias[i];
         }
         // dB and dC of the block's channels: four states per thread, the parts shared out over SPLIT lanes.
         constexpr int ITEMS = kRows * 2 * NP / 4, SPLIT = ITEMS < kScanThreads ? kScanThreads / ITEMS : 1;
