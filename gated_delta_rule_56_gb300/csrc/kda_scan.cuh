@@ -124,12 +124,13 @@ __device__ __forceinline__ float softplus(float x) {
     unpair(softplus2(both(x)), a, b);
     return a;
 }
-// z sigmoid(z), two at a time.
-__device__ __forceinline__ f32x2 silu2(f32x2 z) {
+// sigmoid(z) and z sigmoid(z), two at a time.
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 z) {
     float a, b;
     unpair(mul2(z, both(-kLog2e)), a, b);
-    return mul2(z, pair(rcp(1.f + ex2(a)), rcp(1.f + ex2(b))));
+    return pair(rcp(1.f + ex2(a)), rcp(1.f + ex2(b)));
 }
+__device__ __forceinline__ f32x2 silu2(f32x2 z) { return mul2(z, sigmoid2(z)); }
 
 // How a call's rows are cut: `chunks` chunks of `rows` rows over all sequences' rows (a chunk may hold several sequences, a
 // sequence several chunks). Whole sequences (not packed, enough of them) need no carries between chunks.

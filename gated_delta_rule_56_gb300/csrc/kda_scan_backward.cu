@@ -48,12 +48,14 @@ struct Shape {
 template <typename T, typename SH>
 struct Shared {
     alignas(16) T raw[2][4][kRows][SH::CH];       // x, dt, dy, z as they are in memory
-    alignas(16) float pre[3][kRows][SH::CH];      // dt', u = dt' x, dy'
-    alignas(16) float sum[3][kRows][SH::CH];      // over the states: g B, g a h A, C h
+    alignas(16) float pre[3][kRows][SH::CH];      // dt', dy', u = dt' x; u's place takes the sum of g B when its row is done
+    alignas(16) float sum[2][kRows][SH::CH];      // over the states: g a h A, C h
     alignas(16) float bc[kRows][2][SH::NP][2];    // B and C, every value twice: one for each channel of a pair
     alignas(16) float part[kRows][2][SH::PARTS][SH::NP];  // dB and dC of each thread's channels
     alignas(16) float4 kept[2][SH::EC_ * SH::EN_ / 4][kScanThreads];  // the state before a window, per thread
     alignas(16) ulonglong2 states[2][SH::EC_ * SH::EN_ / 4][kScanThreads];  // the states before rows 2 and 4, per thread
+    alignas(16) ulonglong2 first[SH::EC_ * SH::EN_ / 4][kScanThreads];      // the state before the chunk, per thread
+    alignas(16) float time[2][SH::CH];                                      // from the chunk's first row to the window's
 };
 
 __device__ __forceinline__ void copy16(void *to, const void *from) {
@@ -166,6 +168,14 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
                 }
             }
         }
+        if (plan.carries) {
+            const float *from = carry.kept_time + (chunk * plan.windows() + (w0 - r0) / kRows) * p.C + c0;
+            for (int k = tid; k < CH; k += kScanThreads)
+                if (first_k + k < per)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((unsigned)__cvta_generic_to_shared(&sm.time[buf][k])),
+                                 "l"(from + k)
+                                 : "memory");
+        }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
@@ -174,6 +184,20 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
     float sum_D[OWN], sum_bias[OWN];
 #pragma unroll
     for (int i = 0; i < OWN; ++i) sum_D[i] = sum_bias[i] = 0.f;
+    float own_bias[OWN], own_skip[OWN];
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        const int k = (i * kScanThreads + tid) % CH;
+        const bool in = first_k + k < per;
+        own_bias[i] = in && p.dt_bias ? p.dt_bias[c0 + k] : 0.f;
+        own_skip[i] = in && p.D ? p.D[c0 + k] : 0.f;
+    }
+    const bool joined = plan.carries && p.seqs.begin(p.seqs.at(r0)) < r0;  // the chunk's first sequence came in from before
+    if (joined) {
+        load_tile(carry.state + chunk * chunk_states, h, 1.f);
+#pragma unroll
+        for (int i = 0; i < PAIRS * EN / 2; ++i) sm.first[i][tid] = make_ulonglong2((&h[0][0])[2 * i], (&h[0][0])[2 * i + 1]);
+    }
 
     // B and C of a window, fetched one window ahead; rows and states past the end are zeros, which leave states and gradients
     // as they are.
@@ -235,7 +259,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
                 const int v = (i + e) * kScanThreads + tid, u = v / CH, k = v % CH;
                 const bool in = (ITEMS_P > 1 || e == 0) && u < rows && first_k + k < per;
                 x[e] = in ? to_float(sm.raw[buf][0][u][k]) : 0.f;
-                dt[e] = in ? to_float(sm.raw[buf][1][u][k]) + (p.dt_bias ? p.dt_bias[c0 + k] : 0.f) : 0.f;
+                dt[e] = in ? to_float(sm.raw[buf][1][u][k]) + own_bias[(i + e) % OWN] : 0.f;
                 dy[e] = in ? to_float(sm.raw[buf][2][u][k]) : 0.f;
                 z[e] = in && Z ? to_float(sm.raw[buf][3][u][k]) : 0.f;
             }
@@ -250,8 +274,8 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
                 if ((ITEMS_P == 1 && e == 1) || u >= kRows) break;
                 const bool in = u < rows && first_k + k < per;
                 sm.pre[0][u][k] = in ? dt[e] : 0.f;
-                sm.pre[1][u][k] = in ? dt[e] * x[e] : 0.f;
-                sm.pre[2][u][k] = dy[e];
+                sm.pre[1][u][k] = dy[e];
+                sm.pre[2][u][k] = in ? dt[e] * x[e] : 0.f;
             }
         }
         // The state before the window: the kept one, and what the state before the chunk has become by then.
@@ -265,16 +289,16 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
                 h[j][i + 2] = pair(v.z, o.z);
                 h[j][i + 3] = pair(v.w, o.w);
             }
-        if (plan.carries && begin < r0) {
-            f32x2 X0[PAIRS][EN];
-            load_tile(carry.state + chunk * chunk_states, X0, 1.f);
-            const float *time = carry.kept_time + (chunk * plan.windows() + w) * p.C + c0;
+        if (joined && begin < r0) {
 #pragma unroll
             for (int j = 0; j < PAIRS; ++j) {
-                const int k = tile_k + 2 * j;
-                const f32x2 t2 = pair(first_k + k < per ? time[k] : 0.f, first_k + k + 1 < per ? time[k + 1] : 0.f);
+                const f32x2 t2 = *reinterpret_cast<const f32x2 *>(&sm.time[buf][tile_k + 2 * j]);
 #pragma unroll
-                for (int i = 0; i < EN; ++i) h[j][i] = fma2(decay2(t2, A[j][i]), X0[j][i], h[j][i]);
+                for (int i = 0; i < EN; i += 2) {
+                    const ulonglong2 v = sm.first[(j * EN + i) / 2][tid];
+                    h[j][i] = fma2(decay2(t2, A[j][i]), v.x, h[j][i]);
+                    h[j][i + 1] = fma2(decay2(t2, A[j][i + 1]), v.y, h[j][i + 1]);
+                }
             }
         }
         __syncthreads();
@@ -314,7 +338,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
             if (u % 2 == 0) save(u / 2);
             f32x2 dt[PAIRS], uu[PAIRS], b[EN];
             row_pairs(0, u, dt);
-            row_pairs(1, u, uu);
+            row_pairs(2, u, uu);
             row_states(0, u, b);
 #pragma unroll
             for (int j = 0; j < PAIRS; ++j)
@@ -331,7 +355,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
             {
                 f32x2 dt[PAIRS], uu[PAIRS], b[EN];
                 row_pairs(0, u0, dt);
-                row_pairs(1, u0, uu);
+                row_pairs(2, u0, uu);
                 row_states(0, u0, b);
 #pragma unroll
                 for (int j = 0; j < PAIRS; ++j)
@@ -348,9 +372,9 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
                 if (ends >> u & 1u) tile_or_zero(of_sequence(q.d_fin, w0 + u), gr);
                 f32x2 dt[PAIRS], uu[PAIRS], b[EN], dy[PAIRS], cc[EN], gB[PAIRS], gA[PAIRS], out[PAIRS], dB[EN], dC[EN];
                 row_pairs(0, u, dt);
-                row_pairs(1, u, uu);
+                row_pairs(2, u, uu);
                 row_states(0, u, b);
-                row_pairs(2, u, dy);
+                row_pairs(1, u, dy);
                 row_states(1, u, cc);
 #pragma unroll
                 for (int j = 0; j < PAIRS; ++j)
@@ -414,7 +438,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
                     }
                     if (nl < FOLD) {
 #pragma unroll
-                        for (int k = 0; k < EC / FOLD; ++k) sm.sum[t][u][tile_k + offset + k] = v[t][k];
+                        for (int k = 0; k < EC / FOLD; ++k) (t == 0 ? sm.pre[2] : sm.sum[t - 1])[u][tile_k + offset + k] = v[t][k];
                     }
                 }
                 if (begins >> u & 1u) {
@@ -424,28 +448,61 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
         }
         __syncthreads();
 
-        // Per (row, channel). Long sums are taken in two levels, a window's and then the chunk's.
+        // Per (row, channel), two at a time. Long sums are taken in two levels, a window's and then the chunk's.
         float part_D[OWN], part_bias[OWN];
 #pragma unroll
         for (int i = 0; i < OWN; ++i) part_D[i] = part_bias[i] = 0.f;
+        const long long at0 = w0 * p.C + c0;
 #pragma unroll
-        for (int i = 0; i < (kRows * CH + kScanThreads - 1) / kScanThreads; ++i) {
-            const int v = i * kScanThreads + tid, u = v / CH, k = v % CH;
-            if (kRows * CH % kScanThreads != 0 && u >= kRows) break;
-            if (u >= rows || first_k + k >= per) continue;
-            const long long at = (w0 + u) * p.C + c0 + k;
-            const float x = to_float(sm.raw[buf][0][u][k]), dt = sm.pre[0][u][k], dy = sm.pre[2][u][k];
-            const float gB = sm.sum[0][u][k], skip = p.D ? p.D[c0 + k] : 0.f;
-            float ddt = fmaf(gB, x, sm.sum[1][u][k] * 0.69314718f);  // A was taken with log2(e)
-            if (p.softplus) ddt *= sigmoid(to_float(sm.raw[buf][1][u][k]) + (p.dt_bias ? p.dt_bias[c0 + k] : 0.f));
-            q.dx[at] = fmaf(gB, dt, dy * skip);
-            q.ddt[at] = ddt;
-            if (Z) {
-                const float z = to_float(sm.raw[buf][3][u][k]), s = sigmoid(z);
-                q.dz[at] = to_float(sm.raw[buf][2][u][k]) * fmaf(skip, x, sm.sum[2][u][k]) * (s * fmaf(z, 1.f - s, 1.f));
+        for (int i = 0; i < ITEMS_P; i += 2) {
+            float x[2], dt[2], dy[2], raw[2], gB[2], gA[2];
+            bool in[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int v = (i + e) * kScanThreads + tid, u = ITEMS_P == 1 && e == 1 ? kRows : v / CH, k = v % CH;
+                in[e] = u < rows && first_k + k < per;
+                const int u_ = in[e] ? u : 0, k_ = in[e] ? k : 0;
+                x[e] = to_float(sm.raw[buf][0][u_][k_]);
+                raw[e] = to_float(sm.raw[buf][1][u_][k_]) + own_bias[(i + e) % OWN];
+                dt[e] = sm.pre[0][u_][k_];
+                dy[e] = sm.pre[1][u_][k_];
+                gB[e] = sm.pre[2][u_][k_];
+                gA[e] = sm.sum[0][u_][k_];
             }
-            part_D[i % OWN] = fmaf(dy, x, part_D[i % OWN]);
-            part_bias[i % OWN] += ddt;
+            const f32x2 x2 = pair(x[0], x[1]), gB2 = pair(gB[0], gB[1]), dy2 = pair(dy[0], dy[1]);
+            const f32x2 skip2 = pair(own_skip[i % OWN], own_skip[(i + 1) % OWN]);
+            f32x2 ddt2 = fma2(gB2, x2, mul2(pair(gA[0], gA[1]), both(0.69314718f)));  // A was taken with log2(e)
+            if (p.softplus) ddt2 = mul2(ddt2, sigmoid2(pair(raw[0], raw[1])));
+            float dx[2], ddt[2];
+            unpair(fma2(gB2, pair(dt[0], dt[1]), mul2(dy2, skip2)), dx[0], dx[1]);
+            unpair(ddt2, ddt[0], ddt[1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int v = (i + e) * kScanThreads + tid, u = v / CH, k = v % CH;
+                if (!in[e]) continue;
+                q.dx[at0 + (long long)u * p.C + k] = dx[e];
+                q.ddt[at0 + (long long)u * p.C + k] = ddt[e];
+                part_D[(i + e) % OWN] = fmaf(dy[e], x[e], part_D[(i + e) % OWN]);
+                part_bias[(i + e) % OWN] += ddt[e];
+            }
+            if (Z) {
+                float z[2], dy0[2], out[2], dz[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int v = (i + e) * kScanThreads + tid, u = in[e] ? v / CH : 0, k = in[e] ? v % CH : 0;
+                    z[e] = to_float(sm.raw[buf][3][u][k]);
+                    dy0[e] = to_float(sm.raw[buf][2][u][k]);
+                    out[e] = sm.sum[1][u][k];
+                }
+                const f32x2 z2 = pair(z[0], z[1]), s2 = sigmoid2(z2), y2 = fma2(skip2, x2, pair(out[0], out[1]));
+                const f32x2 slope = mul2(s2, fma2(z2, fma2(s2, both(-1.f), both(1.f)), both(1.f)));  // of z sigmoid(z)
+                unpair(mul2(mul2(pair(dy0[0], dy0[1]), y2), slope), dz[0], dz[1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int v = (i + e) * kScanThreads + tid;
+                    if (in[e]) q.dz[at0 + (long long)(v / CH) * p.C + v % CH] = dz[e];
+                }
+            }
         }
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
