@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from ._lib import _check, _check_indices, _DTYPES, _ptr, _raise_if, _stream, load
+from ._lib import _check, _check_indices, _DTYPES, _raise_if, load
 
 _vp, _i, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 
@@ -73,39 +73,71 @@ def _device(t):
         raise TypeError("inputs must be torch tensors")
     if t.dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    if t.device.type != "cuda":
+    device = t.device
+    if device.type != "cuda":
         raise ValueError("inputs must be CUDA tensors")
-    return t.device
+    return device
+
+
+def _dense(name, t, dtype, shape, device):
+    """``_check``, with the common case decided in a few comparisons (these calls run once per token)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device):
+        _check(name, t, dtype, shape, device)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(device, function, *args):
+    """Calls an entry point with the device's current stream behind ``args``, on that device."""
+    if device.index == torch.cuda.current_device():
+        status = function(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            status = function(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if status:
+        _raise_if(status)
+
+
+def _on_device(device, function, arg):
+    """A sizing call, which goes by the current device."""
+    if device.index == torch.cuda.current_device():
+        return function(arg)
+    with torch.cuda.device(device):
+        return function(arg)
 
 
 def _row_stride(name, t, dtype, shape, lead, device):
     """Checks an input whose first ``lead`` dimensions are rows; returns the elements between rows."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device:
+        if t.numel() == 0:
+            return 0
+        if t.is_contiguous():
+            return shape[-1] if len(shape) == lead + 1 else shape[-1] * shape[-2]
+    else:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    strides = t.stride()
     width = 1
-    if t.numel() == 0:
-        return 0
-    for d in range(t.dim() - 1, lead - 1, -1):
-        if t.shape[d] != 1 and t.stride(d) != width:
+    for d in range(len(shape) - 1, lead - 1, -1):
+        if shape[d] != 1 and strides[d] != width:
             raise ValueError(f"{name}: the values of a row must be dense")
-        width *= t.shape[d]
-    stride, rows = None, 1
+        width *= shape[d]
+    stride, rows = width, 1
     for d in range(lead - 1, -1, -1):
-        if t.shape[d] != 1:
-            if stride is None:
-                stride = t.stride(d)
-            elif t.stride(d) != stride * rows:
+        if shape[d] != 1:
+            if rows == 1:
+                stride = strides[d]
+            elif strides[d] != stride * rows:
                 raise ValueError(f"{name}: rows must lie at one uniform distance")
-            rows *= t.shape[d]
-    if stride is None:
-        return width
-    if stride < width:
+            rows *= shape[d]
+    if rows > 1 and stride < width:
         raise ValueError(f"{name}: rows must not overlap")
     return stride
 
@@ -115,7 +147,7 @@ def _sequences(cu_seqlens, batch, device):
         return batch
     if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be a 1-D int32 tensor [N+1]")
-    _check("cu_seqlens", cu_seqlens, torch.int32, (cu_seqlens.numel(),), device)
+    _dense("cu_seqlens", cu_seqlens, torch.int32, (cu_seqlens.numel(),), device)
     if batch != 1:
         raise ValueError("cu_seqlens needs a batch of 1 (packed rows)")
     return cu_seqlens.numel() - 1
@@ -135,14 +167,14 @@ def _states(initial, final, initial_indices, final_indices, n, shape, dtype, dev
     _check_indices("final_state_indices", final_indices, n, device)
     for name, t, i in (("initial_state", initial, initial_indices), ("final_state", final, final_indices)):
         if t is not None:
-            _check(name, t, dtype, (pool if i is not None else n, *shape), device)
+            _dense(name, t, dtype, (pool if i is not None else n, *shape), device)
     return pool
 
 
 def _output(name, t, dtype, shape, device):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _check(name, t, dtype, shape, device)
+    _dense(name, t, dtype, shape, device)
     return t
 
 
@@ -163,9 +195,9 @@ def _conv_args(x, weight, bias, activation, lead):
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a tensor [C, W]")
     W = weight.shape[1]
-    _check("weight", weight, x.dtype, (C, W), dev)
+    _dense("weight", weight, x.dtype, (C, W), dev)
     if bias is not None:
-        _check("bias", bias, x.dtype, (C,), dev)
+        _dense("bias", bias, x.dtype, (C,), dev)
     stride = _row_stride("x", x, x.dtype, tuple(x.shape), lead, dev)
     a = ConvArgs(struct_size=ctypes.sizeof(ConvArgs), dtype=_DTYPES[x.dtype], B=x.shape[0], T=x.shape[1] if lead == 2 else 1,
                  C=C, W=W, activation=1 if activation == "silu" else 0, x=x.data_ptr(), x_stride=stride,
@@ -191,11 +223,10 @@ def conv_prefill(x, weight, bias=None, activation="silu", cu_seqlens=None, initi
     y = _output("y", y, x.dtype, tuple(x.shape), dev)
     if final_state is None and output_final_state:
         final_state = torch.empty(n, W - 1, C, dtype=x.dtype, device=dev)
-    a.cu_seqlens, a.n_seqs, a.initial_state = _ptr(cu_seqlens), n, _ptr(initial_state)
-    a.initial_state_indices, a.final_state_indices = _ptr(initial_state_indices), _ptr(final_state_indices)
+    a.cu_seqlens, a.n_seqs, a.initial_state = _address(cu_seqlens), n, _address(initial_state)
+    a.initial_state_indices, a.final_state_indices = _address(initial_state_indices), _address(final_state_indices)
     a.state_pool_size = pool
-    with torch.cuda.device(dev):
-        _raise_if(lib.kda_conv_prefill(ctypes.byref(a), _ptr(y), _ptr(final_state), _stream(dev)))
+    _call(dev, lib.kda_conv_prefill, ctypes.byref(a), _address(y), _address(final_state))
     return y, final_state
 
 
@@ -210,11 +241,10 @@ def conv_decode_step(x, weight, state, bias=None, activation="silu", state_indic
     _check_indices("state_indices", state_indices, n, dev)
     _check_indices("final_state_indices", final_state_indices, n, dev)
     pool = state.shape[0] if state_indices is not None and state.dim() == 3 else 0
-    _check("state", state, x.dtype, (pool if state_indices is not None else n, W - 1, C), dev)
+    _dense("state", state, x.dtype, (pool if state_indices is not None else n, W - 1, C), dev)
     y = _output("y", y, x.dtype, (n, C), dev)
-    a.initial_state_indices, a.final_state_indices, a.state_pool_size = _ptr(state_indices), _ptr(final_state_indices), pool
-    with torch.cuda.device(dev):
-        _raise_if(lib.kda_conv_decode_step(ctypes.byref(a), _ptr(state), _ptr(y), _stream(dev)))
+    a.initial_state_indices, a.final_state_indices, a.state_pool_size = _address(state_indices), _address(final_state_indices), pool
+    _call(dev, lib.kda_conv_decode_step, ctypes.byref(a), _address(state), _address(y))
     return y
 
 
@@ -226,20 +256,19 @@ def conv_backward(x, weight, dy, bias=None, activation="silu", cu_seqlens=None, 
     lib = _library()
     a, dev, C, W = _conv_args(x, weight, bias, activation, 2)
     n = _sequences(cu_seqlens, x.shape[0], dev)
-    _check("dy", dy, x.dtype, tuple(x.shape), dev)
+    _dense("dy", dy, x.dtype, tuple(x.shape), dev)
     _states(initial_state, None, None, None, n, (W - 1, C), x.dtype, dev)
     if d_final_state is not None:
-        _check("d_final_state", d_final_state, torch.float32, (n, W - 1, C), dev)
+        _dense("d_final_state", d_final_state, torch.float32, (n, W - 1, C), dev)
     f32 = dict(dtype=torch.float32, device=dev)
     out = dict(dx=torch.empty(tuple(x.shape), **f32), dweight=torch.empty(C, W, **f32),
                dbias=None if bias is None else torch.empty(C, **f32),
                d_initial_state=torch.empty(n, W - 1, C, **f32) if want_d_initial_state else None)
-    a.cu_seqlens, a.n_seqs, a.initial_state = _ptr(cu_seqlens), n, _ptr(initial_state)
-    with torch.cuda.device(dev):
-        ws_bytes = int(lib.kda_conv_backward_workspace_size(ctypes.byref(a)))
-        ws = _workspace(ws_bytes, dev)
-        _raise_if(lib.kda_conv_backward(ctypes.byref(a), _ptr(dy), _ptr(d_final_state), _ptr(out["dx"]), _ptr(out["dweight"]),
-                                        _ptr(out["dbias"]), _ptr(out["d_initial_state"]), _ptr(ws), ws_bytes, _stream(dev)))
+    a.cu_seqlens, a.n_seqs, a.initial_state = _address(cu_seqlens), n, _address(initial_state)
+    ws_bytes = _on_device(dev, lib.kda_conv_backward_workspace_size, ctypes.byref(a))
+    ws = _workspace(ws_bytes, dev)
+    _call(dev, lib.kda_conv_backward, ctypes.byref(a), _address(dy), _address(d_final_state),
+          *(_address(out[n]) for n in ("dx", "dweight", "dbias", "d_initial_state")), _address(ws), ws_bytes)
     return out
 
 
@@ -262,10 +291,10 @@ def _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, lead):
     for name, t, shape in (("x", x, (*rows, ch)), ("dt", dt, (*rows, ch)), ("B", B, (*rows, G, N)), ("C", C, (*rows, G, N)),
                            ("z", z, (*rows, ch))):
         strides[name] = 0 if name == "z" and t is None else _row_stride(name, t, x.dtype, shape, lead, dev)
-    _check("A", A, torch.float32, (ch, N), dev)
+    _dense("A", A, torch.float32, (ch, N), dev)
     for name, t in (("D", D), ("dt_bias", dt_bias)):
         if t is not None:
-            _check(name, t, torch.float32, (ch,), dev)
+            _dense(name, t, torch.float32, (ch,), dev)
     a = ScanArgs(struct_size=ctypes.sizeof(ScanArgs), dtype=_DTYPES[x.dtype], B=x.shape[0], T=x.shape[1] if lead == 2 else 1,
                  D=ch, N=N, G=G, dt_softplus=1 if dt_softplus else 0, x=x.data_ptr(), dt=dt.data_ptr(), Bm=B.data_ptr(),
                  Cm=C.data_ptr(), z=None if z is None else z.data_ptr(), x_stride=strides["x"], dt_stride=strides["dt"],
@@ -290,13 +319,12 @@ def scan_prefill(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True,
     y = _output("y", y, x.dtype, tuple(x.shape), dev)
     if final_state is None and output_final_state:
         final_state = torch.empty(n, ch, N, dtype=torch.float32, device=dev)
-    a.cu_seqlens, a.n_seqs, a.initial_state = _ptr(cu_seqlens), n, _ptr(initial_state)
-    a.initial_state_indices, a.final_state_indices = _ptr(initial_state_indices), _ptr(final_state_indices)
+    a.cu_seqlens, a.n_seqs, a.initial_state = _address(cu_seqlens), n, _address(initial_state)
+    a.initial_state_indices, a.final_state_indices = _address(initial_state_indices), _address(final_state_indices)
     a.state_pool_size = pool
-    with torch.cuda.device(dev):
-        ws_bytes = int(lib.kda_scan_prefill_workspace_size(ctypes.byref(a)))
-        ws = _workspace(ws_bytes, dev)
-        _raise_if(lib.kda_scan_prefill(ctypes.byref(a), _ptr(y), _ptr(final_state), _ptr(ws), ws_bytes, _stream(dev)))
+    ws_bytes = _on_device(dev, lib.kda_scan_prefill_workspace_size, ctypes.byref(a))
+    ws = _workspace(ws_bytes, dev)
+    _call(dev, lib.kda_scan_prefill, ctypes.byref(a), _address(y), _address(final_state), _address(ws), ws_bytes)
     return y, final_state
 
 
@@ -312,11 +340,10 @@ def scan_decode_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_sof
     _check_indices("state_indices", state_indices, n, dev)
     _check_indices("final_state_indices", final_state_indices, n, dev)
     pool = state.shape[0] if state_indices is not None and state.dim() == 3 else 0
-    _check("state", state, torch.float32, (pool if state_indices is not None else n, ch, N), dev)
+    _dense("state", state, torch.float32, (pool if state_indices is not None else n, ch, N), dev)
     y = _output("y", y, x.dtype, (n, ch), dev)
-    a.initial_state_indices, a.final_state_indices, a.state_pool_size = _ptr(state_indices), _ptr(final_state_indices), pool
-    with torch.cuda.device(dev):
-        _raise_if(lib.kda_scan_decode_step(ctypes.byref(a), _ptr(state), _ptr(y), _stream(dev)))
+    a.initial_state_indices, a.final_state_indices, a.state_pool_size = _address(state_indices), _address(final_state_indices), pool
+    _call(dev, lib.kda_scan_decode_step, ctypes.byref(a), _address(state), _address(y))
     return y
 
 
@@ -328,10 +355,10 @@ def scan_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_softplus=
     lib = _library()
     a, dev, ch, N, G = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 2)
     n = _sequences(cu_seqlens, x.shape[0], dev)
-    _check("dy", dy, x.dtype, tuple(x.shape), dev)
+    _dense("dy", dy, x.dtype, tuple(x.shape), dev)
     _states(initial_state, None, None, None, n, (ch, N), torch.float32, dev)
     if d_final_state is not None:
-        _check("d_final_state", d_final_state, torch.float32, (n, ch, N), dev)
+        _dense("d_final_state", d_final_state, torch.float32, (n, ch, N), dev)
     f32 = dict(dtype=torch.float32, device=dev)
     rows = tuple(x.shape[:-1])
     out = dict(dx=torch.empty(*rows, ch, **f32), ddt=torch.empty(*rows, ch, **f32), dA=torch.empty(ch, N, **f32),
@@ -339,14 +366,13 @@ def scan_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_softplus=
                dD=None if D is None else torch.empty(ch, **f32), dz=None if z is None else torch.empty(*rows, ch, **f32),
                ddt_bias=None if dt_bias is None else torch.empty(ch, **f32),
                d_initial_state=torch.empty(n, ch, N, **f32) if want_d_initial_state else None)
-    a.cu_seqlens, a.n_seqs, a.initial_state = _ptr(cu_seqlens), n, _ptr(initial_state)
-    g = ScanGrads(struct_size=ctypes.sizeof(ScanGrads), dy=_ptr(dy), d_final_state=_ptr(d_final_state), dx=_ptr(out["dx"]),
-                  ddt=_ptr(out["ddt"]), dA=_ptr(out["dA"]), dB=_ptr(out["dB"]), dC=_ptr(out["dC"]), dDskip=_ptr(out["dD"]),
-                  dz=_ptr(out["dz"]), ddt_bias=_ptr(out["ddt_bias"]), d_initial_state=_ptr(out["d_initial_state"]))
-    with torch.cuda.device(dev):
-        ws_bytes = int(lib.kda_scan_backward_workspace_size(ctypes.byref(a)))
-        ws = _workspace(ws_bytes, dev)
-        _raise_if(lib.kda_scan_backward(ctypes.byref(a), ctypes.byref(g), _ptr(ws), ws_bytes, _stream(dev)))
+    a.cu_seqlens, a.n_seqs, a.initial_state = _address(cu_seqlens), n, _address(initial_state)
+    g = ScanGrads(struct_size=ctypes.sizeof(ScanGrads), dy=_address(dy), d_final_state=_address(d_final_state), dx=_address(out["dx"]),
+                  ddt=_address(out["ddt"]), dA=_address(out["dA"]), dB=_address(out["dB"]), dC=_address(out["dC"]), dDskip=_address(out["dD"]),
+                  dz=_address(out["dz"]), ddt_bias=_address(out["ddt_bias"]), d_initial_state=_address(out["d_initial_state"]))
+    ws_bytes = _on_device(dev, lib.kda_scan_backward_workspace_size, ctypes.byref(a))
+    ws = _workspace(ws_bytes, dev)
+    _call(dev, lib.kda_scan_backward, ctypes.byref(a), ctypes.byref(g), _address(ws), ws_bytes)
     return out
 
 
@@ -365,7 +391,7 @@ def _rotary_args(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, inter
     k_stride = _row_stride("k", k, q.dtype, (*rows, k.shape[-2], head), lead, dev)
     for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
         if t is not None:
-            _check(name, t, q.dtype, (head,), dev)
+            _dense(name, t, q.dtype, (head,), dev)
     count = 1
     for r in rows:
         count *= r
@@ -379,11 +405,11 @@ def _rotary_args(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, inter
     if cos is not None:
         if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
             raise ValueError("cos must be a tensor [table rows, rotated pairs]")
-        _check("cos", cos, torch.float32, tuple(cos.shape), dev)
-        _check("sin", sin, torch.float32, tuple(cos.shape), dev)
-        _check("positions", positions, torch.int32, rows, dev)
+        _dense("cos", cos, torch.float32, tuple(cos.shape), dev)
+        _dense("sin", sin, torch.float32, tuple(cos.shape), dev)
+        _dense("positions", positions, torch.int32, rows, dev)
         a.half, a.table_rows = cos.shape[1], cos.shape[0]
-        a.cos_table, a.sin_table, a.positions = _ptr(cos), _ptr(sin), _ptr(positions)
+        a.cos_table, a.sin_table, a.positions = _address(cos), _address(sin), _address(positions)
     return a, dev
 
 
@@ -400,8 +426,7 @@ def qk_norm_rotary(q, k, cos=None, sin=None, positions=None, q_weight=None, k_we
     a, dev = _rotary_args(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
     q_out = _output("q_out", q_out, q.dtype, tuple(q.shape), dev)
     k_out = _output("k_out", k_out, q.dtype, tuple(k.shape), dev)
-    with torch.cuda.device(dev):
-        _raise_if(lib.kda_qk_norm_rotary(ctypes.byref(a), _ptr(q_out), _ptr(k_out), _stream(dev)))
+    _call(dev, lib.kda_qk_norm_rotary, ctypes.byref(a), _address(q_out), _address(k_out))
     return q_out, k_out
 
 
@@ -411,16 +436,14 @@ def qk_norm_rotary_backward(q, k, cos, sin, positions, dq_out, dk_out, q_weight=
     dq_weight, dk_weight (None without the weight). dq_out, dk_out have the outputs' layout and dtype."""
     lib = _library()
     a, dev = _rotary_args(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
-    _check("dq_out", dq_out, q.dtype, tuple(q.shape), dev)
-    _check("dk_out", dk_out, q.dtype, tuple(k.shape), dev)
+    _dense("dq_out", dq_out, q.dtype, tuple(q.shape), dev)
+    _dense("dk_out", dk_out, q.dtype, tuple(k.shape), dev)
     f32 = dict(dtype=torch.float32, device=dev)
     out = dict(dq=torch.empty(tuple(q.shape), **f32), dk=torch.empty(tuple(k.shape), **f32),
                dq_weight=None if q_weight is None else torch.empty(q.shape[-1], **f32),
                dk_weight=None if k_weight is None else torch.empty(q.shape[-1], **f32))
-    with torch.cuda.device(dev):
-        ws_bytes = int(lib.kda_qk_norm_rotary_backward_workspace_size(ctypes.byref(a)))
-        ws = _workspace(ws_bytes, dev)
-        _raise_if(lib.kda_qk_norm_rotary_backward(ctypes.byref(a), _ptr(dq_out), _ptr(dk_out), _ptr(out["dq"]), _ptr(out["dk"]),
-                                                  _ptr(out["dq_weight"]), _ptr(out["dk_weight"]), _ptr(ws), ws_bytes,
-                                                  _stream(dev)))
+    ws_bytes = _on_device(dev, lib.kda_qk_norm_rotary_backward_workspace_size, ctypes.byref(a))
+    ws = _workspace(ws_bytes, dev)
+    _call(dev, lib.kda_qk_norm_rotary_backward, ctypes.byref(a), _address(dq_out), _address(dk_out),
+          *(_address(out[n]) for n in ("dq", "dk", "dq_weight", "dk_weight")), _address(ws), ws_bytes)
     return out
