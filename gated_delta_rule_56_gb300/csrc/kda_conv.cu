@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kLanes = 32;  // threads along the channels
 constexpr int kRuns = 8;    // row runs per block
+constexpr int kBatch = 4;   // rows loaded together
 
 struct ConvParams {
     const void *x, *w, *bias;
@@ -27,9 +28,45 @@ struct ConvParams {
     unsigned *err;
 };
 
+// V channels as pairs (one channel: a pair whose second half is not used).
+template <int V>
+struct Row {
+    static constexpr int P = V == 1 ? 1 : V / 2;
+    f32x2 v[P];
+};
+
+template <typename T, int V>
+__device__ __forceinline__ Row<V> to_row(const Pack<T, V> &in) {
+    Row<V> r;
+#pragma unroll
+    for (int i = 0; i < Row<V>::P; ++i) r.v[i] = pair(to_float(in.e[2 * i]), V == 1 ? 0.f : to_float(in.e[V == 1 ? 0 : 2 * i + 1]));
+    return r;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> from_row(const Row<V> &r) {
+    Pack<T, V> out;
+#pragma unroll
+    for (int i = 0; i < Row<V>::P; ++i) {
+        float a, b;
+        unpair(r.v[i], a, b);
+        out.e[2 * i] = from_float<T>(a);
+        if constexpr (V > 1) out.e[2 * i + 1] = from_float<T>(b);
+    }
+    return out;
+}
+
+template <int V>
+__device__ __forceinline__ Row<V> zero_row() {
+    Row<V> r;
+#pragma unroll
+    for (int i = 0; i < Row<V>::P; ++i) r.v[i] = 0;
+    return r;
+}
+
 template <int W, int V>
 struct Filter {
-    float w[W][V], b[V];
+    Row<V> w[W], b;
 };
 
 template <typename T, int W, int V>
@@ -43,17 +80,33 @@ __device__ __forceinline__ void load_filter(const ConvParams &p, int c, Filter<W
         for (int v = 0; v < V; ++v) w[i * V + v] = part.e[v];
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int j = 0; j < W; ++j) {
+        Pack<T, V> column;
 #pragma unroll
-        for (int j = 0; j < W; ++j) f.w[j][v] = to_float(w[v * W + j]);
-    if (p.bias) {
-        const Pack<T, V> b = load_pack<T, V>(static_cast<const T *>(p.bias) + c);
-#pragma unroll
-        for (int v = 0; v < V; ++v) f.b[v] = to_float(b.e[v]);
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) f.b[v] = 0.f;
+        for (int v = 0; v < V; ++v) column.e[v] = w[v * W + j];
+        f.w[j] = to_row(column);
     }
+    f.b = p.bias ? to_row(load_pack<T, V>(static_cast<const T *>(p.bias) + c)) : zero_row<V>();
+}
+
+// The filter over W rows, newest last.
+template <int W, int V>
+__device__ __forceinline__ Row<V> filtered(const Filter<W, V> &f, const Row<V> *x) {
+    Row<V> a = f.b;
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+        for (int i = 0; i < Row<V>::P; ++i) a.v[i] = fma2(f.w[j].v[i], x[j].v[i], a.v[i]);
+    return a;
+}
+
+template <int V>
+__device__ __forceinline__ Row<V> activated(Row<V> a, bool silu) {
+    if (silu) {
+#pragma unroll
+        for (int i = 0; i < Row<V>::P; ++i) a.v[i] = silu2(a.v[i]);
+    }
+    return a;
 }
 
 // The input of sequence n at row r of the tensor, from the state for the W - 1 rows before `bos`.
@@ -82,29 +135,29 @@ __global__ void __launch_bounds__(kLanes *kRuns) conv_prefill_kernel(ConvParams 
         const long long bos = p.seqs.begin(n), end = min(p.seqs.end(n), stop);
         if (end <= r || bos > r || bos < 0) continue;  // empty (or a bad cu_seqlens)
         const long long slot = p.init ? state_slot(p.init_idx, p.pool, n, p.err) : -1;
-        float x[W][V];  // the last W inputs
+        // The last W - 1 inputs, then a batch of kBatch rows whose loads are issued together.
+        Row<V> x[W - 1 + kBatch];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-            const Pack<T, V> in = input_at<T, W, V>(p, r - (W - 1) + j, bos, slot, c);
-#pragma unroll
-            for (int v = 0; v < V; ++v) x[j][v] = to_float(in.e[v]);
-        }
+        for (int j = 0; j < W - 1; ++j) x[j] = to_row(input_at<T, W, V>(p, r - (W - 1) + j, bos, slot, c));
         const T *px = static_cast<const T *>(p.x) + r * p.x_stride + c;
         T *py = y + r * p.C + c;
-        for (; r < end; ++r, px += p.x_stride, py += p.C) {
-            const Pack<T, V> in = load_pack<T, V>(px);
-            Pack<T, V> out;
+        for (; r + kBatch <= end; r += kBatch, px += kBatch * p.x_stride, py += kBatch * (long long)p.C) {
+            Pack<T, V> in[kBatch];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                x[W - 1][v] = to_float(in.e[v]);
-                float a = f.b[v];
+            for (int u = 0; u < kBatch; ++u) in[u] = load_pack<T, V>(px + u * p.x_stride);
 #pragma unroll
-                for (int j = 0; j < W; ++j) a = fmaf(f.w[j][v], x[j][v], a);
-                out.e[v] = from_float<T>(p.silu ? a * sigmoid(a) : a);
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) x[j][v] = x[j + 1][v];
+            for (int u = 0; u < kBatch; ++u) {
+                x[W - 1 + u] = to_row(in[u]);
+                store_pack<T, V>(py + u * (long long)p.C, from_row<T, V>(activated<V>(filtered<W, V>(f, x + u), p.silu)));
             }
-            store_pack<T, V>(py, out);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) x[j] = x[kBatch + j];
+        }
+        for (; r < end; ++r, px += p.x_stride, py += p.C) {
+            x[W - 1] = to_row(load_pack<T, V>(px));
+            store_pack<T, V>(py, from_row<T, V>(activated<V>(filtered<W, V>(f, x), p.silu)));
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) x[j] = x[j + 1];
         }
     }
 }
@@ -128,32 +181,38 @@ __global__ void conv_state_kernel(ConvParams p, T *fin) {
     for (int j = 0; j < W - 1; ++j) store_pack<T, V>(fin + (to * (W - 1) + j) * p.C + c, in[j]);
 }
 
-template <typename T, int W, int V>
-__global__ void conv_decode_kernel(ConvParams p, T *state, T *__restrict__ y) {
-    const int c = (blockIdx.y * kLanes + threadIdx.x) * V;
-    const int n = blockIdx.x;
+// One token. A thread keeps its filter and takes several sequences, whose loads are issued together.
+template <typename T, int W, int V, int SEQS>
+__global__ void __launch_bounds__(kLanes *kRuns) conv_decode_kernel(ConvParams p, T *state, T *__restrict__ y) {
+    const int c = (blockIdx.y * kLanes * kRuns + threadIdx.y * kLanes + threadIdx.x) * V;
     if (c >= p.C) return;
-    const long long from = state_slot(p.init_idx, p.pool, n, p.err);
-    const long long to = p.fin_idx == p.init_idx ? from : state_slot(p.fin_idx, p.pool, n, p.err);
     p.init = state;
-    Pack<T, V> in[W];
+    Pack<T, V> in[SEQS][W];
+    long long to[SEQS];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) in[j] = input_at<T, W, V>(p, j - (W - 1), 0, from, c);
-    in[W - 1] = load_pack<T, V>(static_cast<const T *>(p.x) + n * p.x_stride + c);
+    for (int s = 0; s < SEQS; ++s) {
+        const int n = blockIdx.x * SEQS + s;
+        if (n >= p.seqs.n_seqs) break;
+        const long long from = state_slot(p.init_idx, p.pool, n, p.err);
+        to[s] = p.fin_idx == p.init_idx ? from : state_slot(p.fin_idx, p.pool, n, p.err);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) in[s][j] = input_at<T, W, V>(p, j - (W - 1), 0, from, c);
+        in[s][W - 1] = load_pack<T, V>(static_cast<const T *>(p.x) + n * p.x_stride + c);
+    }
     Filter<W, V> f;
     load_filter<T, W, V>(p, c, f);
-    Pack<T, V> out;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float a = f.b[v];
+    for (int s = 0; s < SEQS; ++s) {
+        const int n = blockIdx.x * SEQS + s;
+        if (n >= p.seqs.n_seqs) break;
+        Row<V> x[W];
 #pragma unroll
-        for (int j = 0; j < W; ++j) a = fmaf(f.w[j][v], to_float(in[j].e[v]), a);
-        out.e[v] = from_float<T>(p.silu ? a * sigmoid(a) : a);
-    }
-    store_pack<T, V>(y + (long long)n * p.C + c, out);
-    if (to >= 0) {
+        for (int j = 0; j < W; ++j) x[j] = to_row(in[s][j]);
+        store_pack<T, V>(y + (long long)n * p.C + c, from_row<T, V>(activated<V>(filtered<W, V>(f, x), p.silu)));
+        if (to[s] >= 0) {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) store_pack<T, V>(state + (to * (W - 1) + j) * p.C + c, in[j + 1]);
+            for (int j = 0; j < W - 1; ++j) store_pack<T, V>(state + (to[s] * (W - 1) + j) * p.C + c, in[s][j + 1]);
+        }
     }
 }
 
@@ -166,14 +225,13 @@ __global__ void __launch_bounds__(kLanes *kRuns) conv_backward_kernel(ConvParams
                                                                        const float *__restrict__ d_fin,
                                                                        float *__restrict__ dx, float *__restrict__ d_init,
                                                                        float *__restrict__ part, int run_rows) {
-    __shared__ float sums[kRuns][W + 1][kLanes * V];
+    constexpr int P = Row<V>::P;
+    __shared__ float sums[kRuns][kLanes * V];
     if (blockIdx.x == 0 && blockIdx.y == 0) check_seqs(p.seqs, p.err);
     const int c = (blockIdx.y * kLanes + threadIdx.x) * V;
-    float dw[W + 1][V];
+    Row<V> dw[W + 1];
 #pragma unroll
-    for (int j = 0; j <= W; ++j)
-#pragma unroll
-        for (int v = 0; v < V; ++v) dw[j][v] = 0.f;
+    for (int j = 0; j <= W; ++j) dw[j] = zero_row<V>();
     long long r = ((long long)blockIdx.x * kRuns + threadIdx.y) * run_rows;
     const long long stop = min(r + run_rows, p.seqs.rows);
     if (c < p.C && r < stop) {
@@ -183,52 +241,65 @@ __global__ void __launch_bounds__(kLanes *kRuns) conv_backward_kernel(ConvParams
             const long long bos = p.seqs.begin(n), eos = min(p.seqs.end(n), p.seqs.rows), end = min(eos, stop);
             if (end <= r || bos > r || bos < 0) continue;
             const long long slot = p.init ? n : -1, first = r;
-            float x[W][V], dp[W][V];  // the last W inputs and gradients
+            Row<V> x[W], dp[W];  // the last W inputs and gradients of p
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) {
-                const Pack<T, V> in = input_at<T, W, V>(p, r - (W - 1) + j, bos, slot, c);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    x[j][v] = to_float(in.e[v]);
-                    dp[j][v] = 0.f;
-                }
+                x[j] = to_row(input_at<T, W, V>(p, r - (W - 1) + j, bos, slot, c));
+                dp[j] = zero_row<V>();
             }
-            for (; r < end + W - 1; ++r) {
-                if (r < eos) {
-                    const Pack<T, V> in = load_pack<T, V>(static_cast<const T *>(p.x) + r * p.x_stride + c);
-                    const Pack<T, V> d = load_pack<T, V>(dy + r * p.C + c);
+            // One row: its dp into dp[W - 1], its share of the filter's gradient if the row is this run's.
+            auto advance = [&](const Pack<T, V> &in, const Pack<T, V> &d, bool mine) {
+                x[W - 1] = to_row(in);
+                Row<V> g = to_row(d);
+                if (p.silu) {
+                    const Row<V> a = filtered<W, V>(f, x);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        x[W - 1][v] = to_float(in.e[v]);
-                        float g = to_float(d.e[v]);
-                        if (p.silu) {
-                            float a = f.b[v];
-#pragma unroll
-                            for (int j = 0; j < W; ++j) a = fmaf(f.w[j][v], x[j][v], a);
-                            const float sg = sigmoid(a);
-                            g *= sg * fmaf(a, 1.f - sg, 1.f);
-                        }
-                        dp[W - 1][v] = g;
-                        if (r < end) {
-#pragma unroll
-                            for (int j = 0; j < W; ++j) dw[j][v] = fmaf(g, x[j][v], dw[j][v]);
-                            dw[W][v] += g;
-                        }
+                    for (int i = 0; i < P; ++i) {
+                        const f32x2 s = sigmoid2(a.v[i]);
+                        g.v[i] = mul2(g.v[i], mul2(s, fma2(a.v[i], fma2(s, both(-1.f), both(1.f)), both(1.f))));
                     }
-                } else {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) dp[W - 1][v] = 0.f;
                 }
-                // Row q of the sequence has all its gradients now; q < bos is a row of the initial state.
-                const long long q = r - (W - 1);
+                dp[W - 1] = g;
+                if (mine) {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+#pragma unroll
+                        for (int j = 0; j < W; ++j) dw[j].v[i] = fma2(g.v[i], x[j].v[i], dw[j].v[i]);
+                        dw[W].v[i] = add2(dw[W].v[i], g.v[i]);
+                    }
+                }
+            };
+            auto shift = [&]() {
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) {
+                    x[j] = x[j + 1];
+                    dp[j] = dp[j + 1];
+                }
+            };
+            auto gradient = [&](float(&g)[V]) {  // of the row W - 1 before the newest
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    f32x2 a = mul2(f.w[W - 1].v[i], dp[0].v[i]);
+#pragma unroll
+                    for (int k = 1; k < W; ++k) a = fma2(f.w[W - 1 - k].v[i], dp[k].v[i], a);
+                    float lo, hi;
+                    unpair(a, lo, hi);
+                    g[2 * i] = lo;
+                    if constexpr (V > 1) g[2 * i + 1] = hi;
+                }
+            };
+            // Any row: past the sequence's end dp is zero; q < bos is a row of the initial state.
+            auto any_row = [&](long long row) {
+                if (row < eos) {
+                    advance(load_pack<T, V>(static_cast<const T *>(p.x) + row * p.x_stride + c), load_pack<T, V>(dy + row * p.C + c),
+                            row < end);
+                } else {
+                    dp[W - 1] = zero_row<V>();
+                }
+                const long long q = row - (W - 1);
                 if (q >= first || (first == bos && d_init)) {
                     float g[V];
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        g[v] = 0.f;
-#pragma unroll
-                        for (int k = 0; k < W; ++k) g[v] = fmaf(f.w[W - 1 - k][v], dp[k][v], g[v]);
-                    }
+                    gradient(g);
                     if (d_fin && q >= eos - (W - 1)) {
                         const float *df = d_fin + ((long long)n * (W - 1) + (q - (eos - (W - 1)))) * p.C + c;
 #pragma unroll
@@ -237,29 +308,49 @@ __global__ void __launch_bounds__(kLanes *kRuns) conv_backward_kernel(ConvParams
                     store_floats<V>(q >= bos ? dx + q * p.C + c : d_init + ((long long)n * (W - 1) + (W - 1) + (q - bos)) * p.C + c,
                                     g);
                 }
+                shift();
+            };
+            for (; r < first + W - 1 && r < end + W - 1; ++r) any_row(r);
+            // Rows whose gradients go to the run's own rows, below the rows that a final state reaches; loads in batches.
+            for (; r + kBatch <= end; r += kBatch) {
+                Pack<T, V> in[kBatch], d[kBatch];
 #pragma unroll
-                for (int v = 0; v < V; ++v)
+                for (int u = 0; u < kBatch; ++u) {
+                    in[u] = load_pack<T, V>(static_cast<const T *>(p.x) + (r + u) * p.x_stride + c);
+                    d[u] = load_pack<T, V>(dy + (r + u) * p.C + c);
+                }
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) {
-                        x[j][v] = x[j + 1][v];
-                        dp[j][v] = dp[j + 1][v];
-                    }
+                for (int u = 0; u < kBatch; ++u) {
+                    advance(in[u], d[u], true);
+                    float g[V];
+                    gradient(g);
+                    store_floats<V>(dx + (r + u - (W - 1)) * p.C + c, g);
+                    shift();
+                }
             }
+            for (; r < end + W - 1; ++r) any_row(r);
             r = end;
         }
     }
+    // The runs' sums, one of the filter's places at a time.
 #pragma unroll
-    for (int j = 0; j <= W; ++j)
+    for (int j = 0; j <= W; ++j) {
+        float lo, hi;
 #pragma unroll
-        for (int v = 0; v < V; ++v) sums[threadIdx.y][j][v * kLanes + threadIdx.x] = dw[j][v];
-    __syncthreads();
-    for (int i = threadIdx.y * kLanes + threadIdx.x; i < (W + 1) * kLanes * V; i += kLanes * kRuns) {
-        const int j = i / (kLanes * V), k = i % (kLanes * V);  // k: channel lane * V + v
-        const int ch = blockIdx.y * kLanes * V + k;
-        float sum = 0.f;
+        for (int i = 0; i < P; ++i) {
+            unpair(dw[j].v[i], lo, hi);
+            sums[threadIdx.y][2 * i * kLanes + threadIdx.x] = lo;
+            if constexpr (V > 1) sums[threadIdx.y][(2 * i + 1) * kLanes + threadIdx.x] = hi;
+        }
+        __syncthreads();
+        for (int k = threadIdx.y * kLanes + threadIdx.x; k < kLanes * V; k += kLanes * kRuns) {
+            const int ch = blockIdx.y * kLanes * V + k;
+            float sum = 0.f;
 #pragma unroll
-        for (int y = 0; y < kRuns; ++y) sum += sums[y][j][(k % V) * kLanes + k / V];
-        if (ch < p.C) part[((long long)blockIdx.x * (W + 1) + j) * p.C + ch] = sum;
+            for (int run = 0; run < kRuns; ++run) sum += sums[run][(k % V) * kLanes + k / V];
+            if (ch < p.C) part[((long long)blockIdx.x * (W + 1) + j) * p.C + ch] = sum;
+        }
+        __syncthreads();
     }
 }
 
@@ -363,9 +454,15 @@ struct DecodeLaunch {
     cudaStream_t s;
     template <typename T, int W, int V>
     void operator()() {
-        const unsigned cols = (unsigned)((p.C + kLanes * V - 1) / (kLanes * V));
-        conv_decode_kernel<T, W, V><<<dim3((unsigned)p.seqs.n_seqs, cols), kLanes, 0, s>>>(p, static_cast<T *>(state),
-                                                                                       static_cast<T *>(y));
+        // Four sequences per thread where that still gives every SM two blocks: the filter is loaded once for them.
+        const unsigned cols = (unsigned)((p.C + kLanes * kRuns * V - 1) / (kLanes * kRuns * V));
+        const dim3 block(kLanes, kRuns);
+        T *st = static_cast<T *>(state), *out = static_cast<T *>(y);
+        const unsigned fours = (unsigned)(p.seqs.n_seqs + 3) / 4;
+        if ((long long)fours * cols >= 304)
+            conv_decode_kernel<T, W, V, 4><<<dim3(fours, cols), block, 0, s>>>(p, st, out);
+        else
+            conv_decode_kernel<T, W, V, 1><<<dim3((unsigned)p.seqs.n_seqs, cols), block, 0, s>>>(p, st, out);
     }
 };
 

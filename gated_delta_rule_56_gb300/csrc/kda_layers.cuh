@@ -15,9 +15,9 @@ __device__ __forceinline__ float from_float<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// V consecutive elements. V > 1: 16 bytes or a multiple of it (fp32: 4 per 16 bytes, bf16: 8), 16-byte aligned.
+// V consecutive elements, loaded and stored in 16-byte words (one 8-byte word if that is all); aligned to them.
 template <typename T, int V>
-struct alignas(V == 1 ? sizeof(T) : 16) Pack {
+struct alignas(V == 1 ? sizeof(T) : V * sizeof(T) >= 16 ? 16 : 8) Pack {
     T e[V];
 };
 
@@ -26,6 +26,8 @@ __device__ __forceinline__ Pack<T, V> load_pack(const T *p) {
     Pack<T, V> r;
     if constexpr (V == 1) {
         r.e[0] = *p;
+    } else if constexpr (V * sizeof(T) == 8) {
+        reinterpret_cast<uint2 &>(r) = *reinterpret_cast<const uint2 *>(p);
     } else {
         static_assert(V * sizeof(T) % 16 == 0, "whole 16-byte words");
 #pragma unroll
@@ -39,6 +41,8 @@ template <typename T, int V>
 __device__ __forceinline__ void store_pack(T *p, const Pack<T, V> &r) {
     if constexpr (V == 1) {
         *p = r.e[0];
+    } else if constexpr (V * sizeof(T) == 8) {
+        *reinterpret_cast<uint2 *>(p) = reinterpret_cast<const uint2 &>(r);
     } else {
 #pragma unroll
         for (int i = 0; i < (int)(V * sizeof(T) / 16); ++i)
@@ -58,9 +62,90 @@ __device__ __forceinline__ void store_floats(float *p, const float (&x)[V]) {
     }
 }
 
-// sigmoid(x) from the fast exponential and division: relative error below 2^-21 for the results that
-// matter in fp32 (an underflowing result becomes 0).
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Two fp32 values in one register pair: sm_103a multiplies and adds both in one instruction.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(f32x2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// 2^x: at most 2^-22.7 off relatively, 2^x < 2^-126 becomes 0.
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// A step's decays exp(dt A), from A log2(e). A state multiplies up as many of them as it remembers tokens, so their mean error
+// counts: the instruction rounds results below 1 down, by 5e-9 to 3e-8 on average for exponents above -0.1. The small
+// constant takes a half to all of that back (measured: a state with a memory of 500 tokens is 2e-6 off instead of 5e-6); 2^constant is still 1.
+__device__ __forceinline__ f32x2 decay2(f32x2 dt, f32x2 A) {
+    float a, b;
+    unpair(fma2(dt, A, pair(1.2e-8f, 1.2e-8f)), a, b);
+    return pair(ex2(a), ex2(b));
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ f32x2 both(float a) { return pair(a, a); }
+
+// log(1 + exp(x)) without overflow or loss for small results, two at a time: max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1].
+// The exponent's product with log2(e) is taken with its rounding error. log1p(e) / e is a polynomial of degree 9, fitted
+// to it at the Chebyshev nodes of [0, 1]: 3e-8 off at most, as its coefficients are rounded here. NaN and +inf stay what they are.
+__device__ __forceinline__ f32x2 softplus2(f32x2 x) {
+    float x0, x1, m0, m1;
+    unpair(x, x0, x1);
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m0) : "f"(x0));
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m1) : "f"(x1));
+    const f32x2 a = pair(fmaxf(-fabsf(x0), -87.f), fmaxf(-fabsf(x1), -87.f));
+    const f32x2 minus = mul2(a, both(-kLog2e)), rest = fma2(a, both(kLog2e), minus);
+    float t0, t1;
+    unpair(minus, t0, t1);
+    f32x2 e = pair(ex2(-t0), ex2(-t1));
+    e = fma2(mul2(e, rest), both(0.69314718f), e);
+    f32x2 q = both(-0x1.aad1eep-9f);
+    q = fma2(q, e, both(0x1.4628b0p-6f));
+    q = fma2(q, e, both(-0x1.d3784ep-5f));
+    q = fma2(q, e, both(0x1.b2c2a2p-4f));
+    q = fma2(q, e, both(-0x1.399642p-3f));
+    q = fma2(q, e, both(0x1.930202p-3f));
+    q = fma2(q, e, both(-0x1.ff11c2p-3f));
+    q = fma2(q, e, both(0x1.554c9cp-2f));
+    q = fma2(q, e, both(-0x1.ffffc0p-2f));
+    q = fma2(q, e, both(1.f));
+    return fma2(e, q, pair(m0, m1));
+}
+__device__ __forceinline__ float softplus(float x) {
+    float a, b;
+    unpair(softplus2(both(x)), a, b);
+    return a;
+}
+// sigmoid(z) and z sigmoid(z), two at a time.
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 z) {
+    float a, b;
+    unpair(mul2(z, both(-kLog2e)), a, b);
+    return pair(rcp(1.f + ex2(a)), rcp(1.f + ex2(b)));
+}
+__device__ __forceinline__ f32x2 silu2(f32x2 z) { return mul2(z, sigmoid2(z)); }
 
 // The sequences over the rows: n_seqs of T rows each, or packed ones from cu_seqlens.
 struct Seqs {

@@ -13,6 +13,7 @@ namespace kda {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kBatch = 4, kBackBatch = 2;  // heads of a lane group whose loads are issued together
 
 struct RotaryParams {
     const void *q, *k, *qw, *kw;
@@ -122,23 +123,30 @@ __global__ void __launch_bounds__(kWarps * 32) rotary_kernel(RotaryParams p, T *
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] = wt && live ? to_float(wt[e0 + i]) : 1.f;
         const int step = parts * GROUPS;
-        for (int h0 = part * GROUPS; h0 < heads; h0 += step) {
-            const int h = h0 + grp;
-            const bool on = live && h < heads;
-            float x[8] = {};
-            if (on) load8<T, WIDE>(in + (long long)h * p.head, x);
-            float ss = 0.f;
+        for (int h0 = part * GROUPS; h0 < heads; h0 += kBatch * step) {
+            float x[kBatch][8] = {};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-            const float r = rsqrtf(fmaf(group_sum<LANES>(ss), p.inv_size, p.eps));
+            for (int b = 0; b < kBatch; ++b) {
+                const int h = h0 + b * step + grp;
+                if (live && h < heads) load8<T, WIDE>(in + (long long)h * p.head, x[b]);
+            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] *= r * g[i];
-            rotate(x, t, 1.f, p.interleaved, partner);
-            if (on) {
-                Pack<T, 8> o;
+            for (int b = 0; b < kBatch; ++b) {
+                if (h0 + b * step >= heads) break;
+                const int h = h0 + b * step + grp;
+                float ss = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o.e[i] = from_float<T>(x[i]);
-                store_pack<T, 8>(out + (long long)h * p.head, o);
+                for (int i = 0; i < 8; ++i) ss = fmaf(x[b][i], x[b][i], ss);
+                const float r = rsqrtf(fmaf(group_sum<LANES>(ss), p.inv_size, p.eps));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[b][i] *= r * g[i];
+                rotate(x[b], t, 1.f, p.interleaved, partner);
+                if (live && h < heads) {
+                    Pack<T, 8> o;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o.e[i] = from_float<T>(x[b][i]);
+                    store_pack<T, 8>(out + (long long)h * p.head, o);
+                }
             }
         }
     }
@@ -175,31 +183,38 @@ __global__ void __launch_bounds__(kWarps * 32) rotary_backward_kernel(RotaryPara
             load_turn(p, row, e0, t);
             const T *in = static_cast<const T *>(side ? p.k : p.q) + row * (side ? p.k_stride : p.q_stride) + e0;
             const long long at = row * heads * p.head + e0;
-            for (int h0 = 0; h0 < heads; h0 += GROUPS) {
-                const int h = h0 + grp;
-                const bool on = live && h < heads;
-                float x[8] = {}, d[8] = {};
-                if (on) {
-                    load8<T, WIDE>(in + (long long)h * p.head, x);
-                    load8<T, WIDE>(dout + at + (long long)h * p.head, d);
-                }
-                rotate(d, t, -1.f, p.interleaved, partner);
-                float ss = 0.f, dot = 0.f;
+            for (int h0 = 0; h0 < heads; h0 += kBackBatch * GROUPS) {
+                float x[kBackBatch][8] = {}, d[kBackBatch][8] = {};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ss = fmaf(x[i], x[i], ss);
-                    dot = fmaf(d[i] * g[i], x[i], dot);
+                for (int b = 0; b < kBackBatch; ++b) {
+                    const int h = h0 + b * GROUPS + grp;
+                    if (live && h < heads) {
+                        load8<T, WIDE>(in + (long long)h * p.head, x[b]);
+                        load8<T, WIDE>(dout + at + (long long)h * p.head, d[b]);
+                    }
                 }
-                ss = group_sum<LANES>(ss);
-                dot = group_sum<LANES>(dot);
-                const float r = rsqrtf(fmaf(ss, p.inv_size, p.eps)), k = r * r * dot * p.inv_size;
-                float o[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dw[i] = fmaf(d[i], x[i] * r, dw[i]);
-                    o[i] = r * (d[i] * g[i] - x[i] * k);
+                for (int b = 0; b < kBackBatch; ++b) {
+                    if (h0 + b * GROUPS >= heads) break;
+                    const int h = h0 + b * GROUPS + grp;
+                    rotate(d[b], t, -1.f, p.interleaved, partner);
+                    float ss = 0.f, dot = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        ss = fmaf(x[b][i], x[b][i], ss);
+                        dot = fmaf(d[b][i] * g[i], x[b][i], dot);
+                    }
+                    ss = group_sum<LANES>(ss);
+                    dot = group_sum<LANES>(dot);
+                    const float r = rsqrtf(fmaf(ss, p.inv_size, p.eps)), k = r * r * dot * p.inv_size;
+                    float o[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        dw[i] = fmaf(d[b][i], x[b][i] * r, dw[i]);
+                        o[i] = r * (d[b][i] * g[i] - x[b][i] * k);
+                    }
+                    if (live && h < heads) store_floats<8>(din + at + (long long)h * p.head, o);
                 }
-                if (on) store_floats<8>(din + at + (long long)h * p.head, o);
             }
         }
         if (part) {

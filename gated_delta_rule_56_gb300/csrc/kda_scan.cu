@@ -487,58 +487,119 @@ struct BackEndsLaunch {
     }
 };
 
-// One token: bound by HBM, the state is read and written once. LP lanes hold a channel's states, V consecutive
-// ones each (16 bytes where N and the state's address allow it), so that a warp streams whole
-// 512-byte runs of the state; the parts of y are added by shuffles.
-template <typename T, int LP, int V>
-__global__ void __launch_bounds__(128) scan_decode_kernel(ScanParams p, float *state, T *__restrict__ y) {
+// One token: bound by HBM, the state is read and written once. LP lanes hold a channel's states, V consecutive ones each
+// (16 bytes where N and the addresses allow it), so that a warp streams whole 512-byte runs of the state; the parts of y
+// are added by shuffles. A thread keeps its A and takes PAIRS * 2 sequences, whose loads are issued together.
+template <typename T, int LP, int V, int PAIRS>
+__global__ void __launch_bounds__(128) scan_decode_kernel(ScanParams p, float *state, T *__restrict__ y, bool wide_bc) {
+    constexpr int SEQS = 2 * PAIRS;
     const int k = blockIdx.y * (128 / LP) + threadIdx.x / LP, l = threadIdx.x % LP;
-    const int n = blockIdx.x;
     const bool live = k < p.C;
     const int c = live ? k : p.C - 1;
     const int g = c / (p.C / p.G);
-    const long long from = state_slot(p.init_idx, p.pool, n, p.err);
-    const long long to = p.fin_idx == p.init_idx ? from : state_slot(p.fin_idx, p.pool, n, p.err);
-    const float x = to_float(static_cast<const T *>(p.x)[n * p.x_stride + c]);
-    float dt = to_float(static_cast<const T *>(p.dt)[n * p.dt_stride + c]) + (p.dt_bias ? p.dt_bias[c] : 0.f);
-    if (p.softplus) dt = softplus(dt);
-    const float u = dt * x;
-    const T *B = static_cast<const T *>(p.Bm) + n * p.B_stride + g * p.N;
-    const T *Cm = static_cast<const T *>(p.Cm) + n * p.C_stride + g * p.N;
-    float sum = 0.f;
-    for (int n0 = l * V; n0 < p.N; n0 += LP * V) {
-        Pack<float, V> a = load_pack<float, V>(p.A + (long long)c * p.N + n0), h;
-        if (from >= 0) {
-            h = load_pack<float, V>(state + (from * p.C + c) * p.N + n0);
+    const int first = blockIdx.x * SEQS;
+    long long from[SEQS], to[SEQS];
+    float x[SEQS], dt[SEQS], z[SEQS];
+    Pack<float, V> h[SEQS];
+    Pack<T, V> bs[SEQS], cs[SEQS];
+    const T *Z = static_cast<const T *>(p.z);
+    auto load = [&](int s, int n0) {  // the states n0.. of sequence s, and B and C at them
+        const int n = first + s;
+        if (from[s] >= 0) {
+            h[s] = load_pack<float, V>(state + (from[s] * p.C + c) * p.N + n0);
         } else {
 #pragma unroll
-            for (int v = 0; v < V; ++v) h.e[v] = 0.f;
+            for (int v = 0; v < V; ++v) h[s].e[v] = 0.f;
+        }
+        const T *B = static_cast<const T *>(p.Bm) + n * p.B_stride + g * p.N + n0;
+        const T *Cm = static_cast<const T *>(p.Cm) + n * p.C_stride + g * p.N + n0;
+        if (wide_bc) {
+            bs[s] = load_pack<T, V>(B);
+            cs[s] = load_pack<T, V>(Cm);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                bs[s].e[v] = B[v];
+                cs[s].e[v] = Cm[v];
+            }
+        }
+    };
+    const int start = l * V;
+#pragma unroll
+    for (int s = 0; s < SEQS; ++s) {
+        const int n = first + s;
+        from[s] = to[s] = -1;
+        x[s] = dt[s] = z[s] = 0.f;
+        if (n >= p.seqs.n_seqs) continue;
+        from[s] = state_slot(p.init_idx, p.pool, n, p.err);
+        to[s] = p.fin_idx == p.init_idx ? from[s] : state_slot(p.fin_idx, p.pool, n, p.err);
+        x[s] = to_float(static_cast<const T *>(p.x)[n * p.x_stride + c]);
+        dt[s] = to_float(static_cast<const T *>(p.dt)[n * p.dt_stride + c]);
+        if (Z) z[s] = to_float(Z[n * p.z_stride + c]);
+        if (start < p.N) load(s, start);
+    }
+    const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, skip = p.D ? p.D[c] : 0.f;
+    Pack<float, V> a;
+    if (start < p.N) a = load_pack<float, V>(p.A + (long long)c * p.N + start);
+#pragma unroll
+    for (int q = 0; q < PAIRS; ++q) {
+        f32x2 dt2 = add2(pair(dt[2 * q], dt[2 * q + 1]), both(bias));
+        if (p.softplus) dt2 = softplus2(dt2);
+        unpair(dt2, dt[2 * q], dt[2 * q + 1]);
+    }
+    float sum[SEQS];
+#pragma unroll
+    for (int s = 0; s < SEQS; ++s) {
+        const int n = first + s;
+        sum[s] = 0.f;
+        if (n >= p.seqs.n_seqs) continue;
+        const float u = dt[s] * x[s];
+        for (int n0 = start; n0 < p.N; n0 += LP * V) {
+            if (n0 != start) {
+                load(s, n0);
+                a = load_pack<float, V>(p.A + (long long)c * p.N + n0);
+            } else if (s > 0 && start + LP * V < p.N) {
+                a = load_pack<float, V>(p.A + (long long)c * p.N + n0);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                h[s].e[v] = fmaf(ex2(dt[s] * (a.e[v] * kLog2e)), h[s].e[v], u * to_float(bs[s].e[v]));
+                sum[s] = fmaf(to_float(cs[s].e[v]), h[s].e[v], sum[s]);
+            }
+            if (to[s] >= 0 && live) store_pack<float, V>(state + (to[s] * p.C + c) * p.N + n0, h[s]);
         }
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            h.e[v] = fmaf(exp2f(dt * (a.e[v] * kLog2e)), h.e[v], u * to_float(B[n0 + v]));
-            sum = fmaf(to_float(Cm[n0 + v]), h.e[v], sum);
-        }
-        if (to >= 0 && live) store_pack<float, V>(state + (to * p.C + c) * p.N + n0, h);
+        for (int m = LP / 2; m > 0; m >>= 1) sum[s] += __shfl_xor_sync(0xffffffffu, sum[s], m);
     }
 #pragma unroll
-    for (int m = LP / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    if (!live || l != 0) return;
-    if (p.D) sum = fmaf(p.D[c], x, sum);
-    if (p.z) {
-        const float z = to_float(static_cast<const T *>(p.z)[n * p.z_stride + c]);
-        sum *= z * sigmoid(z);
+    for (int q = 0; q < PAIRS; ++q) {
+        f32x2 y2 = fma2(both(skip), pair(x[2 * q], x[2 * q + 1]), pair(sum[2 * q], sum[2 * q + 1]));
+        if (Z) y2 = mul2(y2, silu2(pair(z[2 * q], z[2 * q + 1])));
+        float out[2];
+        unpair(y2, out[0], out[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int n = first + 2 * q + e;
+            if (live && l == 0 && n < p.seqs.n_seqs) y[(long long)n * p.C + c] = from_float<T>(out[e]);
+        }
     }
-    y[(long long)n * p.C + c] = from_float<T>(sum);
 }
 
 template <typename T, int V>
 void launch_decode(const ScanParams &p, float *state, void *y, cudaStream_t s) {
     const int words = (p.N + V - 1) / V;
     T *out = static_cast<T *>(y);
-#define KDA_DECODE(LP)                                                                                              \
-    scan_decode_kernel<T, LP, V><<<dim3((unsigned)p.seqs.n_seqs, (unsigned)((p.C + 128 / LP - 1) / (128 / LP))), 128, 0, s>>>( \
-        p, state, out)
+    const bool wide_bc = (reinterpret_cast<uintptr_t>(p.Bm) | reinterpret_cast<uintptr_t>(p.Cm)) % (V * sizeof(T)) == 0 &&
+                         p.B_stride % V == 0 && p.C_stride % V == 0;
+    // Four sequences per thread where that still gives every SM eight blocks, else two.
+#define KDA_DECODE(LP)                                                                                             \
+    do {                                                                                                            \
+        const unsigned cols = (unsigned)((p.C + 128 / LP - 1) / (128 / LP)), n = (unsigned)p.seqs.n_seqs;           \
+        if ((long long)((n + 3) / 4) * cols >= 152 * 8)                                                             \
+            scan_decode_kernel<T, LP, V, 2><<<dim3((n + 3) / 4, cols), 128, 0, s>>>(p, state, out, wide_bc);        \
+        else                                                                                                        \
+            scan_decode_kernel<T, LP, V, 1><<<dim3((n + 1) / 2, cols), 128, 0, s>>>(p, state, out, wide_bc);        \
+    } while (0)
     if (words <= 1)
         KDA_DECODE(1);
     else if (words <= 2)
@@ -594,7 +655,7 @@ cudaError_t launch_scan_back_ends(const kda_scan_args &a, const void *dy, const 
 cudaError_t launch_scan_decode(const kda_scan_args &a, float *state, void *y, unsigned *err, cudaStream_t s) {
     ScanParams p = scan_params(a, err);
     if (!p.fin_idx) p.fin_idx = p.init_idx;
-    const bool wide = p.N % 4 == 0 && aligned16(state) && aligned16(p.A);
+    const bool wide = p.N % 4 == 0 && aligned16(state) && aligned16(p.A);  // four states per load
     if (a.dtype == KDA_BF16)
         wide ? launch_decode<__nv_bfloat16, 4>(p, state, y, s) : launch_decode<__nv_bfloat16, 1>(p, state, y, s);
     else

@@ -192,6 +192,8 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
         own_bias[i] = in && p.dt_bias ? p.dt_bias[c0 + k] : 0.f;
         own_skip[i] = in && p.D ? p.D[c0 + k] : 0.f;
     }
+    for (int k = tid; k < CH; k += kScanThreads)  // channels past the group's: nothing is copied there
+        if (first_k + k >= per) sm.time[0][k] = sm.time[1][k] = 0.f;
     const bool joined = plan.carries && p.seqs.begin(p.seqs.at(r0)) < r0;  // the chunk's first sequence came in from before
     if (joined) {
         load_tile(carry.state + chunk * chunk_states, h, 1.f);
