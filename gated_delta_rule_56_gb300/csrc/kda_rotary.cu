@@ -79,15 +79,17 @@ __device__ __forceinline__ void rotate(float (&x)[8], const Turn &t, float sign,
 }
 
 template <typename T, bool WIDE>
-__device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
-    if constexpr (WIDE) {
-        const Pack<T, 8> v = load_pack<T, 8>(p);
+__device__ __forceinline__ Pack<T, 8> load8(const T *p) {
+    if constexpr (WIDE) return load_pack<T, 8>(p);
+    Pack<T, 8> r;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = to_float(v.e[i]);
-    } else {
+    for (int i = 0; i < 8; ++i) r.e[i] = p[i];
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void to_floats(const Pack<T, 8> &v, float (&x)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = to_float(p[i]);
-    }
+    for (int i = 0; i < 8; ++i) x[i] = to_float(v.e[i]);
 }
 
 template <int LANES>
@@ -99,7 +101,7 @@ __device__ __forceinline__ float group_sum(float x) {
 
 // One warp per (token, part of its heads): LANES lanes per head, 32 / LANES heads at a time.
 template <typename T, int LANES, bool WIDE>
-__global__ void __launch_bounds__(kWarps * 32) rotary_kernel(RotaryParams p, T *__restrict__ q_out, T *__restrict__ k_out,
+__global__ void __launch_bounds__(kWarps * 32, 4) rotary_kernel(RotaryParams p, T *__restrict__ q_out, T *__restrict__ k_out,
                                                              int parts) {
     constexpr int GROUPS = 32 / LANES;
     const int lane = threadIdx.x & 31, l = lane % LANES, grp = lane / LANES;
@@ -124,27 +126,29 @@ __global__ void __launch_bounds__(kWarps * 32) rotary_kernel(RotaryParams p, T *
         for (int i = 0; i < 8; ++i) g[i] = wt && live ? to_float(wt[e0 + i]) : 1.f;
         const int step = parts * GROUPS;
         for (int h0 = part * GROUPS; h0 < heads; h0 += kBatch * step) {
-            float x[kBatch][8] = {};
+            Pack<T, 8> raw[kBatch];  // a head that is not there takes another's place and is not stored
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
-                const int h = h0 + b * step + grp;
-                if (live && h < heads) load8<T, WIDE>(in + (long long)h * p.head, x[b]);
+                const int h = min(h0 + b * step + grp, heads - 1);
+                raw[b] = load8<T, WIDE>(in + (live ? 0 : -e0) + (long long)h * p.head);
             }
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
                 if (h0 + b * step >= heads) break;
                 const int h = h0 + b * step + grp;
-                float ss = 0.f;
+                float x[8], ss = 0.f;
+                to_floats(raw[b], x);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(x[b][i], x[b][i], ss);
+                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+                if (!live) ss = 0.f;
                 const float r = rsqrtf(fmaf(group_sum<LANES>(ss), p.inv_size, p.eps));
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[b][i] *= r * g[i];
-                rotate(x[b], t, 1.f, p.interleaved, partner);
+                for (int i = 0; i < 8; ++i) x[i] *= r * g[i];
+                rotate(x, t, 1.f, p.interleaved, partner);
                 if (live && h < heads) {
                     Pack<T, 8> o;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o.e[i] = from_float<T>(x[b][i]);
+                    for (int i = 0; i < 8; ++i) o.e[i] = from_float<T>(x[i]);
                     store_pack<T, 8>(out + (long long)h * p.head, o);
                 }
             }
@@ -184,25 +188,30 @@ __global__ void __launch_bounds__(kWarps * 32) rotary_backward_kernel(RotaryPara
             const T *in = static_cast<const T *>(side ? p.k : p.q) + row * (side ? p.k_stride : p.q_stride) + e0;
             const long long at = row * heads * p.head + e0;
             for (int h0 = 0; h0 < heads; h0 += kBackBatch * GROUPS) {
-                float x[kBackBatch][8] = {}, d[kBackBatch][8] = {};
+                Pack<T, 8> raw[kBackBatch], raw_d[kBackBatch];
 #pragma unroll
                 for (int b = 0; b < kBackBatch; ++b) {
-                    const int h = h0 + b * GROUPS + grp;
-                    if (live && h < heads) {
-                        load8<T, WIDE>(in + (long long)h * p.head, x[b]);
-                        load8<T, WIDE>(dout + at + (long long)h * p.head, d[b]);
-                    }
+                    const long long h = (long long)min(h0 + b * GROUPS + grp, heads - 1) * p.head - (live ? 0 : e0);
+                    raw[b] = load8<T, WIDE>(in + h);
+                    raw_d[b] = load8<T, WIDE>(dout + at + h);
                 }
 #pragma unroll
                 for (int b = 0; b < kBackBatch; ++b) {
                     if (h0 + b * GROUPS >= heads) break;
                     const int h = h0 + b * GROUPS + grp;
-                    rotate(d[b], t, -1.f, p.interleaved, partner);
+                    float x[8], d[8];
+                    to_floats(raw[b], x);
+                    to_floats(raw_d[b], d);
+                    if (!live || h >= heads) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = d[i] = 0.f;
+                    }
+                    rotate(d, t, -1.f, p.interleaved, partner);
                     float ss = 0.f, dot = 0.f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        ss = fmaf(x[b][i], x[b][i], ss);
-                        dot = fmaf(d[b][i] * g[i], x[b][i], dot);
+                        ss = fmaf(x[i], x[i], ss);
+                        dot = fmaf(d[i] * g[i], x[i], dot);
                     }
                     ss = group_sum<LANES>(ss);
                     dot = group_sum<LANES>(dot);
@@ -210,8 +219,8 @@ __global__ void __launch_bounds__(kWarps * 32) rotary_backward_kernel(RotaryPara
                     float o[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        dw[i] = fmaf(d[b][i], x[b][i] * r, dw[i]);
-                        o[i] = r * (d[b][i] * g[i] - x[b][i] * k);
+                        dw[i] = fmaf(d[i], x[i] * r, dw[i]);
+                        o[i] = r * (d[i] * g[i] - x[i] * k);
                     }
                     if (live && h < heads) store_floats<8>(din + at + (long long)h * p.head, o);
                 }
