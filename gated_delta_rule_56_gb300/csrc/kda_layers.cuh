@@ -101,6 +101,7 @@ __device__ __forceinline__ f32x2 decay2(f32x2 dt, f32x2 A) {
     unpair(fma2(dt, A, pair(1.2e-8f, 1.2e-8f)), a, b);
     return pair(ex2(a), ex2(b));
 }
+__device__ __forceinline__ float decay(float dt, float A) { return ex2(fmaf(dt, A, 1.2e-8f)); }
 __device__ __forceinline__ float rcp(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

@@ -489,10 +489,10 @@ struct BackEndsLaunch {
 
 // One token: bound by HBM, the state is read and written once. LP lanes hold a channel's states, V consecutive ones each
 // (16 bytes where N and the addresses allow it), so that a warp streams whole 512-byte runs of the state; the parts of y
-// are added by shuffles. A thread keeps its A and takes PAIRS * 2 sequences, whose loads are issued together.
-template <typename T, int LP, int V, int PAIRS>
+// are added by shuffles. This form takes any sizes and addresses, two sequences per thread.
+template <typename T, int LP, int V>
 __global__ void __launch_bounds__(128) scan_decode_kernel(ScanParams p, float *state, T *__restrict__ y, bool wide_bc) {
-    constexpr int SEQS = 2 * PAIRS;
+    constexpr int PAIRS = 1, SEQS = 2 * PAIRS;
     const int k = blockIdx.y * (128 / LP) + threadIdx.x / LP, l = threadIdx.x % LP;
     const bool live = k < p.C;
     const int c = live ? k : p.C - 1;
@@ -562,10 +562,15 @@ __global__ void __launch_bounds__(128) scan_decode_kernel(ScanParams p, float *s
                 a = load_pack<float, V>(p.A + (long long)c * p.N + n0);
             }
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                h[s].e[v] = fmaf(ex2(dt[s] * (a.e[v] * kLog2e)), h[s].e[v], u * to_float(bs[s].e[v]));
-                sum[s] = fmaf(to_float(cs[s].e[v]), h[s].e[v], sum[s]);
+            for (int v = 0; v < V; ++v)
+                h[s].e[v] = fmaf(decay(dt[s], a.e[v] * kLog2e), h[s].e[v], u * to_float(bs[s].e[v]));
+            float part = to_float(cs[s].e[0]) * h[s].e[0];
+            if constexpr (V == 4) {  // in the other form's order, so that alignment does not change a result
+                const float *hv = h[s].e;
+                part = fmaf(to_float(cs[s].e[0]), hv[0], to_float(cs[s].e[2]) * hv[2]) +
+                       fmaf(to_float(cs[s].e[1]), hv[1], to_float(cs[s].e[3]) * hv[3]);
             }
+            sum[s] = n0 == start ? part : sum[s] + part;
             if (to[s] >= 0 && live) store_pack<float, V>(state + (to[s] * p.C + c) * p.N + n0, h[s]);
         }
 #pragma unroll
@@ -585,21 +590,217 @@ __global__ void __launch_bounds__(128) scan_decode_kernel(ScanParams p, float *s
     }
 }
 
+// The same for the usual sizes (up to 64 states, rows on 4-byte boundaries): a warp keeps the A of its channels (32 of them
+// with up to 16 states) and walks over sequences, whose states and inputs come through a ring in shared memory two steps of two
+// sequences ahead. The time steps and the gate are computed by one lane per channel and handed to the lanes of its
+// states. 256 sequences of 4096 channels x 16 states: 18.5 us, against 50 us for the form above, whose short-lived blocks have no load
+// in flight half of their time and whose lanes repeat a channel's time step.
+constexpr int kStreamBlocks = 4;
+
+template <typename T, int LP>
+struct Decode {
+    static constexpr int R = LP < 4 ? LP : 4, CH = 32 / LP, CW = R * CH;  // words per lane, channels per word, channels
+    struct Stage {
+        float4 state[R][32];
+        T x[CW], dt[CW], z[CW];
+        T B[4 * LP], C[4 * LP];
+    };
+};
+
+template <typename T, int LP>
+__global__ void __launch_bounds__(128) scan_decode_stream_kernel(ScanParams p, float *state, T *__restrict__ y, int walkers) {
+    using D = Decode<T, LP>;
+    constexpr int R = D::R, CH = D::CH, CW = D::CW, STAGES = 3;
+    extern __shared__ __align__(16) unsigned char memory[];
+    const int lane = threadIdx.x % 32, l = lane % LP;
+    const int block = blockIdx.x * 4 + threadIdx.x / 32;  // the warp's channel block
+    if (block * CW >= p.C) return;
+    const int c0 = block * CW, g = c0 / (p.C / p.G);
+    const int own = lane % CW;                            // the channel that the lane computes time step and gate of
+    const bool in = 4 * l < p.N;
+    auto mine = reinterpret_cast<typename D::Stage(*)[2]>(memory) + threadIdx.x / 32 * STAGES;
+    const int walker = blockIdx.y;
+    const int count = (p.seqs.n_seqs - walker + walkers - 1) / walkers;  // the warp's sequences: walker, walker + walkers, ...
+    const T *Z = static_cast<const T *>(p.z);
+    int from32 = 0, to32 = 0;  // the slots of 32 of them, one per lane
+    auto slots = [&](int i0) {
+        const int n = walker + (i0 + lane) * walkers;
+        from32 = to32 = -1;
+        if (n < p.seqs.n_seqs) {
+            from32 = (int)state_slot(p.init_idx, p.pool, n, p.err);
+            to32 = p.fin_idx == p.init_idx ? from32 : (int)state_slot(p.fin_idx, p.pool, n, p.err);
+        }
+    };
+    auto words = [&](T *to, const T *from, int values) {  // at most 32 words of 4 bytes, one per lane; more for fp32 B and C
+        constexpr int PER = 4 / sizeof(T);
+        for (int i = lane * PER; i < values; i += 32 * PER)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((unsigned)__cvta_generic_to_shared(to + i)), "l"(from + i)
+                         : "memory");
+    };
+    const long long at_lane = (long long)(c0 + lane / LP) * p.N + 4 * l;  // of the lane's first word in a state
+    auto bring = [&](int i, int stage) {  // sequences i and i + 1 of the warp's
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int slot = __shfl_sync(0xffffffffu, from32, (i + e) % 32);
+            if (i + e >= count) continue;
+            const long long n = walker + (long long)(i + e) * walkers;
+            typename D::Stage &st = mine[stage][e];
+            if (in && slot >= 0) {
+                const float *from = state + (long long)slot * p.C * p.N + at_lane;
+#pragma unroll
+                for (int j = 0; j < R; ++j) copy16(&st.state[j][lane], from + j * CH * p.N);
+            }
+            words(st.x, static_cast<const T *>(p.x) + n * p.x_stride + c0, CW);
+            words(st.dt, static_cast<const T *>(p.dt) + n * p.dt_stride + c0, CW);
+            if (Z) words(st.z, Z + n * p.z_stride + c0, CW);
+            words(st.B, static_cast<const T *>(p.Bm) + n * p.B_stride + g * p.N, p.N);
+            words(st.C, static_cast<const T *>(p.Cm) + n * p.C_stride + g * p.N, p.N);
+        }
+        copies_issued();
+    };
+    f32x2 A[R][2];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const float4 v = in ? *reinterpret_cast<const float4 *>(p.A + at_lane + j * CH * p.N) : make_float4(0.f, 0.f, 0.f, 0.f);
+        A[j][0] = pair(v.x * kLog2e, v.y * kLog2e);
+        A[j][1] = pair(v.z * kLog2e, v.w * kLog2e);
+    }
+    const f32x2 bias = both(p.dt_bias ? p.dt_bias[c0 + own] : 0.f), skip = both(p.D ? p.D[c0 + own] : 0.f);
+    for (int i0 = 0; i0 < count; i0 += 32) {
+        slots(i0);
+        const int stop = min(count, i0 + 32);
+        auto bring_up_to = [&](int i, int stage) {
+            if (i < stop)
+                bring(i, stage);
+            else
+                copies_issued();
+        };
+#pragma unroll
+        for (int k = 0; k < STAGES - 1; ++k) bring_up_to(i0 + 2 * k, k);
+        int stage = 0;
+        for (int i = i0; i < stop; i += 2) {
+            copies_arrived<STAGES - 2>();
+            __syncwarp();  // every lane's copies of this step are there, and the step before is read
+            bring_up_to(i + 2 * (STAGES - 1), stage == 0 ? STAGES - 1 : stage - 1);
+            const auto &st = mine[stage];
+            f32x2 dt = add2(pair(to_float(st[0].dt[own]), to_float(st[1].dt[own])), bias);
+            if (p.softplus) dt = softplus2(dt);
+            const f32x2 x = pair(to_float(st[0].x[own]), to_float(st[1].x[own]));
+            float dts[2], us[2], sums[2];
+            unpair(dt, dts[0], dts[1]);
+            unpair(mul2(dt, x), us[0], us[1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int from = __shfl_sync(0xffffffffu, from32, (i + e) % 32), to = __shfl_sync(0xffffffffu, to32, (i + e) % 32);
+                f32x2 b01 = 0, b23 = 0, c01 = 0, c23 = 0;
+                if (in) {
+                    const T *b = st[e].B + 4 * l, *cc = st[e].C + 4 * l;
+                    b01 = pair(to_float(b[0]), to_float(b[1]));
+                    b23 = pair(to_float(b[2]), to_float(b[3]));
+                    c01 = pair(to_float(cc[0]), to_float(cc[1]));
+                    c23 = pair(to_float(cc[2]), to_float(cc[3]));
+                }
+                float v[R];  // the lane's part of y of its channels
+                float *out = state + (long long)to * p.C * p.N + at_lane;
+                const bool write = i + e < stop && to >= 0 && in;
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    const float4 h = in && from >= 0 ? st[e].state[j][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    const f32x2 t2 = both(__shfl_sync(0xffffffffu, dts[e], j * CH + lane / LP));
+                    const f32x2 u2 = both(__shfl_sync(0xffffffffu, us[e], j * CH + lane / LP));
+                    const f32x2 h01 = fma2(decay2(t2, A[j][0]), pair(h.x, h.y), mul2(u2, b01));
+                    const f32x2 h23 = fma2(decay2(t2, A[j][1]), pair(h.z, h.w), mul2(u2, b23));
+                    float lo, hi;
+                    unpair(fma2(c01, h01, mul2(c23, h23)), lo, hi);
+                    v[j] = lo + hi;
+                    if (write) {
+                        float4 o;
+                        unpair(h01, o.x, o.y);
+                        unpair(h23, o.z, o.w);
+                        *reinterpret_cast<float4 *>(out + j * CH * p.N) = o;
+                    }
+                }
+                // Over the lanes of a channel, each step halving the channels that a lane keeps.
+#pragma unroll
+                for (int m = LP / 2; m >= R; m >>= 1)
+#pragma unroll
+                    for (int j = 0; j < R; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], m);
+                int left = R;
+#pragma unroll
+                for (int m = R / 2; m > 0; m >>= 1) {
+                    left /= 2;
+                    const bool upper = l & m;
+#pragma unroll
+                    for (int j = 0; j < R / 2; ++j) {
+                        if (j >= left) break;
+                        const float keep = upper ? v[left + j] : v[j], send = upper ? v[j] : v[left + j];
+                        v[j] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+                    }
+                }
+                sums[e] = __shfl_sync(0xffffffffu, v[0], own % CH * LP + own / CH);  // to the lane that owns the channel
+            }
+            f32x2 y2 = fma2(skip, x, pair(sums[0], sums[1]));
+            if (Z) y2 = mul2(y2, silu2(pair(to_float(st[0].z[own]), to_float(st[1].z[own]))));
+            unpair(y2, sums[0], sums[1]);
+            if (lane < CW) {
+                const long long n = walker + (long long)i * walkers;
+                y[n * p.C + c0 + own] = from_float<T>(sums[0]);
+                if (i + 1 < stop) y[(n + walkers) * p.C + c0 + own] = from_float<T>(sums[1]);
+            }
+            stage = stage == STAGES - 1 ? 0 : stage + 1;
+        }
+        copies_arrived<0>();
+        __syncwarp();
+    }
+}
+
+template <typename T, int LP>
+cudaError_t launch_stream(const ScanParams &p, float *state, void *y, cudaStream_t s) {
+    using D = Decode<T, LP>;
+    constexpr int bytes = 4 * 3 * 2 * sizeof(typename D::Stage);
+    static_assert(bytes <= 100 * 1024, "two blocks per SM");
+    const cudaError_t e = cudaFuncSetAttribute(scan_decode_stream_kernel<T, LP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    // Walkers per channel block: kStreamBlocks blocks per SM in all, two sequences at least for each.
+    const unsigned cols = (unsigned)((p.C / D::CW + 3) / 4);
+    const int most = (p.seqs.n_seqs + 1) / 2;
+    int walkers = (int)(152LL * kStreamBlocks / cols);
+    walkers = walkers < 1 ? 1 : walkers > most ? most : walkers;
+    scan_decode_stream_kernel<T, LP><<<dim3(cols, (unsigned)walkers), 128, bytes, s>>>(p, state, static_cast<T *>(y), walkers);
+    return cudaGetLastError();
+}
+
+// Whether the streaming form fits the call, and its launch.
+template <typename T>
+bool launch_decode_stream(const ScanParams &p, float *state, void *y, cudaStream_t s, cudaError_t &e) {
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.dt) | reinterpret_cast<uintptr_t>(p.z) |
+                           reinterpret_cast<uintptr_t>(p.Bm) | reinterpret_cast<uintptr_t>(p.Cm);
+    const long long strides = p.x_stride | p.dt_stride | p.z_stride | p.B_stride | p.C_stride;
+    int LP = 1;
+    while (4 * LP < p.N) LP *= 2;
+    const int channels = LP <= 4 ? 32 : 128 / LP;
+    if (p.N % 4 != 0 || LP > 16 || bits % 4 != 0 || strides % (4 / (long long)sizeof(T)) != 0 || (p.C / p.G) % channels != 0 ||
+        !aligned16(state) || !aligned16(p.A))
+        return false;
+    switch (LP) {
+        case 1: e = launch_stream<T, 1>(p, state, y, s); break;
+        case 2: e = launch_stream<T, 2>(p, state, y, s); break;
+        case 4: e = launch_stream<T, 4>(p, state, y, s); break;
+        case 8: e = launch_stream<T, 8>(p, state, y, s); break;
+        default: e = launch_stream<T, 16>(p, state, y, s); break;
+    }
+    return true;
+}
+
 template <typename T, int V>
 void launch_decode(const ScanParams &p, float *state, void *y, cudaStream_t s) {
     const int words = (p.N + V - 1) / V;
     T *out = static_cast<T *>(y);
     const bool wide_bc = (reinterpret_cast<uintptr_t>(p.Bm) | reinterpret_cast<uintptr_t>(p.Cm)) % (V * sizeof(T)) == 0 &&
                          p.B_stride % V == 0 && p.C_stride % V == 0;
-    // Four sequences per thread where that still gives every SM eight blocks, else two.
-#define KDA_DECODE(LP)                                                                                             \
-    do {                                                                                                            \
-        const unsigned cols = (unsigned)((p.C + 128 / LP - 1) / (128 / LP)), n = (unsigned)p.seqs.n_seqs;           \
-        if ((long long)((n + 3) / 4) * cols >= 152 * 8)                                                             \
-            scan_decode_kernel<T, LP, V, 2><<<dim3((n + 3) / 4, cols), 128, 0, s>>>(p, state, out, wide_bc);        \
-        else                                                                                                        \
-            scan_decode_kernel<T, LP, V, 1><<<dim3((n + 1) / 2, cols), 128, 0, s>>>(p, state, out, wide_bc);        \
-    } while (0)
+#define KDA_DECODE(LP)                                                                                                    \
+    scan_decode_kernel<T, LP, V><<<dim3((unsigned)(p.seqs.n_seqs + 1) / 2, (unsigned)((p.C + 128 / LP - 1) / (128 / LP))), \
+                                   128, 0, s>>>(p, state, out, wide_bc)
     if (words <= 1)
         KDA_DECODE(1);
     else if (words <= 2)
@@ -655,6 +856,9 @@ cudaError_t launch_scan_back_ends(const kda_scan_args &a, const void *dy, const 
 cudaError_t launch_scan_decode(const kda_scan_args &a, float *state, void *y, unsigned *err, cudaStream_t s) {
     ScanParams p = scan_params(a, err);
     if (!p.fin_idx) p.fin_idx = p.init_idx;
+    cudaError_t e = cudaSuccess;
+    if (a.dtype == KDA_BF16 ? launch_decode_stream<__nv_bfloat16>(p, state, y, s, e) : launch_decode_stream<float>(p, state, y, s, e))
+        return e;
     const bool wide = p.N % 4 == 0 && aligned16(state) && aligned16(p.A);  // four states per load
     if (a.dtype == KDA_BF16)
         wide ? launch_decode<__nv_bfloat16, 4>(p, state, y, s) : launch_decode<__nv_bfloat16, 1>(p, state, y, s);

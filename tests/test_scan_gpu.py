@@ -280,3 +280,25 @@ def test_another_stream_and_a_captured_graph():
     torch.cuda.synchronize()
     assert torch.equal(y3, y) and torch.equal(fin3, fin) and all(torch.equal(g3[k], g[k]) for k in g)
     kda.check_status()
+
+
+@pytest.mark.parametrize("dtype,D,N,G", [(torch.bfloat16, 64, 16, 1), (torch.float32, 64, 16, 2), (torch.bfloat16, 64, 4, 1),
+                                         (torch.float32, 32, 8, 1), (torch.bfloat16, 48, 32, 1), (torch.bfloat16, 32, 64, 2),
+                                         (torch.float32, 96, 12, 1), (torch.bfloat16, 128, 16, 4), (torch.float32, 64, 52, 1)])
+def test_tokens_of_whole_warps(dtype, D, N, G):
+    """Channels in whole warps: the form of the token step that streams the states of many sequences."""
+    test_prefill_then_tokens(dtype, D, N, G)
+
+
+@pytest.mark.parametrize("n", [1, 2, 69, 200])
+@pytest.mark.parametrize("off", ["", "gate", "skip", "bias", "softplus"])
+def test_many_sequences_take_one_token(n, off):
+    c = Case(torch.float32, n, 1, 64, 16, 1, seed=17, **({off: False} if off else {}))
+    pool = torch.zeros(n + 5, 64, 16, device=DEV)
+    slots = torch.randperm(n + 5)[:n].to(torch.int32).to(DEV)
+    pool[slots.long()] = c.state
+    args = [t[:, 0] for t in (c.x, c.dt)], [t[:, 0] for t in (c.B, c.C)]
+    more = dict(D=c.D, z=None if c.z is None else c.z[:, 0], dt_bias=c.dt_bias, dt_softplus=c.softplus)
+    y = kda.scan_decode_step(*args[0], c.A, *args[1], pool, state_indices=slots, **more)
+    kda.check_status()
+    c.check_prefill(y, pool[slots.long()])
