@@ -9,6 +9,7 @@ uniform distance; everything else is contiguous. There is no fallback without th
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -40,6 +41,24 @@ RotaryArgs = _struct("kda_rotary_args", [
     ("q_weight", _vp), ("k_weight", _vp), ("cos_table", _vp), ("sin_table", _vp), ("positions", _vp),
     ("table_rows", _i64)])
 
+_CODES = {_i: "i", _i64: "q", _sz: "N", _vp: "P", ctypes.c_float: "f"}
+
+
+def _packer(cls):
+    """Makes an argument struct from its fields in order (without struct_size; None is a NULL pointer). Packing bytes costs a
+    third of filling a ctypes structure, and a token step has little else to do on the host."""
+    size = ctypes.sizeof(cls)
+    pack = struct.Struct("@" + "".join(_CODES[t] for _, t in cls._fields_)).pack
+
+    def make(*fields):
+        return pack(size, *fields)
+
+    return make
+
+
+_conv_struct, _scan_struct, _rotary_struct = _packer(ConvArgs), _packer(ScanArgs), _packer(RotaryArgs)
+_grads_struct = _packer(ScanGrads)
+
 _typed = None
 
 
@@ -48,22 +67,21 @@ def _library():
     global _typed
     lib = load()
     if _typed is not lib:
-        P = ctypes.POINTER
-        for name, args in (("kda_conv_prefill", [P(ConvArgs), _vp, _vp, _vp]),
-                           ("kda_conv_decode_step", [P(ConvArgs), _vp, _vp, _vp]),
-                           ("kda_conv_backward", [P(ConvArgs)] + [_vp] * 7 + [_sz, _vp]),
-                           ("kda_scan_prefill", [P(ScanArgs), _vp, _vp, _vp, _sz, _vp]),
-                           ("kda_scan_decode_step", [P(ScanArgs), _vp, _vp, _vp]),
-                           ("kda_scan_backward", [P(ScanArgs), P(ScanGrads), _vp, _sz, _vp]),
-                           ("kda_qk_norm_rotary", [P(RotaryArgs), _vp, _vp, _vp]),
-                           ("kda_qk_norm_rotary_backward", [P(RotaryArgs)] + [_vp] * 7 + [_sz, _vp])):
+        for name, args in (("kda_conv_prefill", [_vp, _vp, _vp, _vp]),
+                           ("kda_conv_decode_step", [_vp, _vp, _vp, _vp]),
+                           ("kda_conv_backward", [_vp] + [_vp] * 7 + [_sz, _vp]),
+                           ("kda_scan_prefill", [_vp, _vp, _vp, _vp, _sz, _vp]),
+                           ("kda_scan_decode_step", [_vp, _vp, _vp, _vp]),
+                           ("kda_scan_backward", [_vp, _vp, _vp, _sz, _vp]),
+                           ("kda_qk_norm_rotary", [_vp, _vp, _vp, _vp]),
+                           ("kda_qk_norm_rotary_backward", [_vp] + [_vp] * 7 + [_sz, _vp])):
             f = getattr(lib, name)
             f.argtypes, f.restype = args, _i
         for name, arg in (("kda_conv_backward_workspace_size", ConvArgs), ("kda_scan_prefill_workspace_size", ScanArgs),
                           ("kda_scan_backward_workspace_size", ScanArgs),
                           ("kda_qk_norm_rotary_backward_workspace_size", RotaryArgs)):
             f = getattr(lib, name)
-            f.argtypes, f.restype = [P(arg)], _sz
+            f.argtypes, f.restype = [_vp], _sz
         _typed = lib
     return lib
 
@@ -86,7 +104,7 @@ def _dense(name, t, dtype, shape, device):
 
 
 def _address(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
 def _call(device, function, *args):
@@ -115,6 +133,13 @@ def _row_stride(name, t, dtype, shape, lead, device):
             return 0
         if t.is_contiguous():
             return shape[-1] if len(shape) == lead + 1 else shape[-1] * shape[-2]
+        strides = t.stride()  # a slice of a wider projection
+        width = shape[-1]
+        if strides[-1] == 1 and (len(shape) == lead + 1 or strides[-2] == width):
+            if len(shape) == lead + 2:
+                width *= shape[-2]
+            if strides[lead - 1] >= width and (lead == 1 or (lead == 2 and strides[0] == strides[1] * shape[1])):
+                return strides[lead - 1]
     else:
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -171,10 +196,22 @@ def _states(initial, final, initial_indices, final_indices, n, shape, dtype, dev
     return pool
 
 
-def _output(name, t, dtype, shape, device):
+def _decode_slots(state, state_indices, final_state_indices, n, device):
+    """Checks the slots of a decode call; returns the pool's size (0 without a pool)."""
+    if state_indices is None:
+        if final_state_indices is not None:
+            raise ValueError("final_state_indices needs state_indices")
+        return 0
+    _check_indices("state_indices", state_indices, n, device)
+    _check_indices("final_state_indices", final_state_indices, n, device)
+    return state.shape[0] if isinstance(state, torch.Tensor) and state.dim() else 0
+
+
+def _output(name, t, like, shape):
+    """``t``, or a new dense tensor of the type and device of ``like``."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _dense(name, t, dtype, shape, device)
+        return like.new_empty(shape)
+    _dense(name, t, like.dtype, shape, like.device)
     return t
 
 
@@ -185,24 +222,24 @@ def _workspace(nbytes, device):
 # ------------------------------------------------------------------ short convolution ---
 
 
-def _conv_args(x, weight, bias, activation, lead):
+def _conv_front(x, weight, bias, activation, lead):
+    """Checks the inputs that all calls share; returns the leading fields of their struct, the device, C and W."""
     dev = _device(x)
     if x.dim() != lead + 1:
         raise ValueError(f"x must have {lead + 1} dimensions")
-    if activation not in (None, "silu"):
+    if activation is not None and activation != "silu":
         raise ValueError(f"unknown activation {activation!r}: None or 'silu'")
-    C = x.shape[-1]
+    shape, dtype = x.shape, x.dtype
+    C = shape[-1]
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a tensor [C, W]")
     W = weight.shape[1]
-    _dense("weight", weight, x.dtype, (C, W), dev)
+    _dense("weight", weight, dtype, (C, W), dev)
     if bias is not None:
-        _dense("bias", bias, x.dtype, (C,), dev)
-    stride = _row_stride("x", x, x.dtype, tuple(x.shape), lead, dev)
-    a = ConvArgs(struct_size=ctypes.sizeof(ConvArgs), dtype=_DTYPES[x.dtype], B=x.shape[0], T=x.shape[1] if lead == 2 else 1,
-                 C=C, W=W, activation=1 if activation == "silu" else 0, x=x.data_ptr(), x_stride=stride,
-                 weight=weight.data_ptr(), bias=None if bias is None else bias.data_ptr())
-    return a, dev, C, W
+        _dense("bias", bias, dtype, (C,), dev)
+    stride = _row_stride("x", x, dtype, shape, lead, dev)
+    return (_DTYPES[dtype], shape[0], shape[1] if lead == 2 else 1, C, W, 1 if activation else 0, x.data_ptr(), stride,
+            weight.data_ptr(), _address(bias)), dev, C, W
 
 
 def conv_prefill(x, weight, bias=None, activation="silu", cu_seqlens=None, initial_state=None, output_final_state=True,
@@ -217,16 +254,15 @@ def conv_prefill(x, weight, bias=None, activation="silu", cu_seqlens=None, initi
     ``prefill``. ``final_state`` may be ``initial_state``'s memory. Returns (y [B, T, C], final_state or None).
     """
     lib = _library()
-    a, dev, C, W = _conv_args(x, weight, bias, activation, 2)
+    front, dev, C, W = _conv_front(x, weight, bias, activation, 2)
     n = _sequences(cu_seqlens, x.shape[0], dev)
     pool = _states(initial_state, final_state, initial_state_indices, final_state_indices, n, (W - 1, C), x.dtype, dev)
-    y = _output("y", y, x.dtype, tuple(x.shape), dev)
+    y = _output("y", y, x, x.shape)
     if final_state is None and output_final_state:
-        final_state = torch.empty(n, W - 1, C, dtype=x.dtype, device=dev)
-    a.cu_seqlens, a.n_seqs, a.initial_state = _address(cu_seqlens), n, _address(initial_state)
-    a.initial_state_indices, a.final_state_indices = _address(initial_state_indices), _address(final_state_indices)
-    a.state_pool_size = pool
-    _call(dev, lib.kda_conv_prefill, ctypes.byref(a), _address(y), _address(final_state))
+        final_state = x.new_empty((n, W - 1, C))
+    a = _conv_struct(*front, _address(cu_seqlens), n, _address(initial_state), _address(initial_state_indices),
+                     _address(final_state_indices), pool)
+    _call(dev, lib.kda_conv_prefill, a, y.data_ptr(), _address(final_state))
     return y, final_state
 
 
@@ -234,17 +270,13 @@ def conv_decode_step(x, weight, state, bias=None, activation="silu", state_indic
     """One token of the convolution for N sequences: x [N, C]; ``state`` [N, W-1, C] (or a pool with
     ``state_indices`` int32 [N], as in ``decode_step``) is shifted in place. Returns y [N, C]."""
     lib = _library()
-    a, dev, C, W = _conv_args(x, weight, bias, activation, 1)
+    front, dev, C, W = _conv_front(x, weight, bias, activation, 1)
     n = x.shape[0]
-    if final_state_indices is not None and state_indices is None:
-        raise ValueError("final_state_indices needs state_indices")
-    _check_indices("state_indices", state_indices, n, dev)
-    _check_indices("final_state_indices", final_state_indices, n, dev)
-    pool = state.shape[0] if state_indices is not None and state.dim() == 3 else 0
-    _dense("state", state, x.dtype, (pool if state_indices is not None else n, W - 1, C), dev)
-    y = _output("y", y, x.dtype, (n, C), dev)
-    a.initial_state_indices, a.final_state_indices, a.state_pool_size = _address(state_indices), _address(final_state_indices), pool
-    _call(dev, lib.kda_conv_decode_step, ctypes.byref(a), _address(state), _address(y))
+    pool = _decode_slots(state, state_indices, final_state_indices, n, dev)
+    _dense("state", state, x.dtype, (n if state_indices is None else pool, W - 1, C), dev)
+    y = _output("y", y, x, x.shape)
+    a = _conv_struct(*front, 0, 0, 0, _address(state_indices), _address(final_state_indices), pool)
+    _call(dev, lib.kda_conv_decode_step, a, state.data_ptr(), y.data_ptr())
     return y
 
 
@@ -254,9 +286,9 @@ def conv_backward(x, weight, dy, bias=None, activation="silu", cu_seqlens=None, 
     dy has y's layout and dtype; d_final_state fp32 [N, W-1, C] or None. Returns a dict of fp32 tensors: dx
     [B, T, C], dweight [C, W], dbias [C] (None without a bias), d_initial_state [N, W-1, C] (or None)."""
     lib = _library()
-    a, dev, C, W = _conv_args(x, weight, bias, activation, 2)
+    front, dev, C, W = _conv_front(x, weight, bias, activation, 2)
     n = _sequences(cu_seqlens, x.shape[0], dev)
-    _dense("dy", dy, x.dtype, tuple(x.shape), dev)
+    _dense("dy", dy, x.dtype, x.shape, dev)
     _states(initial_state, None, None, None, n, (W - 1, C), x.dtype, dev)
     if d_final_state is not None:
         _dense("d_final_state", d_final_state, torch.float32, (n, W - 1, C), dev)
@@ -264,43 +296,44 @@ def conv_backward(x, weight, dy, bias=None, activation="silu", cu_seqlens=None, 
     out = dict(dx=torch.empty(tuple(x.shape), **f32), dweight=torch.empty(C, W, **f32),
                dbias=None if bias is None else torch.empty(C, **f32),
                d_initial_state=torch.empty(n, W - 1, C, **f32) if want_d_initial_state else None)
-    a.cu_seqlens, a.n_seqs, a.initial_state = _address(cu_seqlens), n, _address(initial_state)
-    ws_bytes = _on_device(dev, lib.kda_conv_backward_workspace_size, ctypes.byref(a))
+    a = _conv_struct(*front, _address(cu_seqlens), n, _address(initial_state), 0, 0, 0)
+    ws_bytes = _on_device(dev, lib.kda_conv_backward_workspace_size, a)
     ws = _workspace(ws_bytes, dev)
-    _call(dev, lib.kda_conv_backward, ctypes.byref(a), _address(dy), _address(d_final_state),
-          *(_address(out[n]) for n in ("dx", "dweight", "dbias", "d_initial_state")), _address(ws), ws_bytes)
+    _call(dev, lib.kda_conv_backward, a, dy.data_ptr(), _address(d_final_state),
+          *(_address(out[k]) for k in ("dx", "dweight", "dbias", "d_initial_state")), _address(ws), ws_bytes)
     return out
 
 
 # -------------------------------------------------------------- selective state space ---
 
 
-def _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, lead):
+def _scan_front(x, dt, A, B, C, D, z, dt_bias, dt_softplus, lead):
+    """Checks the inputs that all calls share; returns the leading fields of their struct, the device, channels, N and G."""
     dev = _device(x)
     if x.dim() != lead + 1:
         raise ValueError(f"x must have {lead + 1} dimensions")
-    ch = x.shape[-1]
+    shape, dtype = x.shape, x.dtype
+    ch = shape[-1]
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
         raise ValueError("A must be a tensor [D, N]")
     N = A.shape[1]
     if not isinstance(B, torch.Tensor) or B.dim() != lead + 2:
         raise ValueError(f"B must have {lead + 2} dimensions")
     G = B.shape[-2]
-    rows = tuple(x.shape[:-1])
-    strides = {}
-    for name, t, shape in (("x", x, (*rows, ch)), ("dt", dt, (*rows, ch)), ("B", B, (*rows, G, N)), ("C", C, (*rows, G, N)),
-                           ("z", z, (*rows, ch))):
-        strides[name] = 0 if name == "z" and t is None else _row_stride(name, t, x.dtype, shape, lead, dev)
+    small = shape[:-1] + (G, N)
+    x_stride = _row_stride("x", x, dtype, shape, lead, dev)
+    dt_stride = _row_stride("dt", dt, dtype, shape, lead, dev)
+    B_stride = _row_stride("B", B, dtype, small, lead, dev)
+    C_stride = _row_stride("C", C, dtype, small, lead, dev)
+    z_stride = 0 if z is None else _row_stride("z", z, dtype, shape, lead, dev)
     _dense("A", A, torch.float32, (ch, N), dev)
-    for name, t in (("D", D), ("dt_bias", dt_bias)):
-        if t is not None:
-            _dense(name, t, torch.float32, (ch,), dev)
-    a = ScanArgs(struct_size=ctypes.sizeof(ScanArgs), dtype=_DTYPES[x.dtype], B=x.shape[0], T=x.shape[1] if lead == 2 else 1,
-                 D=ch, N=N, G=G, dt_softplus=1 if dt_softplus else 0, x=x.data_ptr(), dt=dt.data_ptr(), Bm=B.data_ptr(),
-                 Cm=C.data_ptr(), z=None if z is None else z.data_ptr(), x_stride=strides["x"], dt_stride=strides["dt"],
-                 B_stride=strides["B"], C_stride=strides["C"], z_stride=strides["z"], A=A.data_ptr(),
-                 Dskip=None if D is None else D.data_ptr(), dt_bias=None if dt_bias is None else dt_bias.data_ptr())
-    return a, dev, ch, N, G
+    if D is not None:
+        _dense("D", D, torch.float32, (ch,), dev)
+    if dt_bias is not None:
+        _dense("dt_bias", dt_bias, torch.float32, (ch,), dev)
+    return (_DTYPES[dtype], shape[0], shape[1] if lead == 2 else 1, ch, N, G, 1 if dt_softplus else 0, x.data_ptr(), dt.data_ptr(),
+            B.data_ptr(), C.data_ptr(), _address(z), x_stride, dt_stride, B_stride, C_stride, z_stride, A.data_ptr(), _address(D),
+            _address(dt_bias)), dev, ch, N, G
 
 
 def scan_prefill(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, cu_seqlens=None, initial_state=None,
@@ -313,18 +346,17 @@ def scan_prefill(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True,
     ``cu_seqlens``, states (fp32 [N_seqs, D, N]) and pools as in ``prefill``. Returns (y [B, T, D], final_state or None).
     """
     lib = _library()
-    a, dev, ch, N, _ = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 2)
+    front, dev, ch, N, _ = _scan_front(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 2)
     n = _sequences(cu_seqlens, x.shape[0], dev)
     pool = _states(initial_state, final_state, initial_state_indices, final_state_indices, n, (ch, N), torch.float32, dev)
-    y = _output("y", y, x.dtype, tuple(x.shape), dev)
+    y = _output("y", y, x, x.shape)
     if final_state is None and output_final_state:
-        final_state = torch.empty(n, ch, N, dtype=torch.float32, device=dev)
-    a.cu_seqlens, a.n_seqs, a.initial_state = _address(cu_seqlens), n, _address(initial_state)
-    a.initial_state_indices, a.final_state_indices = _address(initial_state_indices), _address(final_state_indices)
-    a.state_pool_size = pool
-    ws_bytes = _on_device(dev, lib.kda_scan_prefill_workspace_size, ctypes.byref(a))
+        final_state = A.new_empty((n, ch, N))
+    a = _scan_struct(*front, _address(cu_seqlens), n, _address(initial_state), _address(initial_state_indices),
+                     _address(final_state_indices), pool)
+    ws_bytes = _on_device(dev, lib.kda_scan_prefill_workspace_size, a)
     ws = _workspace(ws_bytes, dev)
-    _call(dev, lib.kda_scan_prefill, ctypes.byref(a), _address(y), _address(final_state), _address(ws), ws_bytes)
+    _call(dev, lib.kda_scan_prefill, a, y.data_ptr(), _address(final_state), _address(ws), ws_bytes)
     return y, final_state
 
 
@@ -333,17 +365,13 @@ def scan_decode_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_sof
     """One token of the scan for N sequences: x, dt, z [N, D], B, C [N, G, N_states]; ``state`` fp32
     [N, D, N_states] (or a pool with ``state_indices`` int32 [N]) is updated in place. Returns y [N, D]."""
     lib = _library()
-    a, dev, ch, N, _ = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 1)
+    front, dev, ch, N, _ = _scan_front(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 1)
     n = x.shape[0]
-    if final_state_indices is not None and state_indices is None:
-        raise ValueError("final_state_indices needs state_indices")
-    _check_indices("state_indices", state_indices, n, dev)
-    _check_indices("final_state_indices", final_state_indices, n, dev)
-    pool = state.shape[0] if state_indices is not None and state.dim() == 3 else 0
-    _dense("state", state, torch.float32, (pool if state_indices is not None else n, ch, N), dev)
-    y = _output("y", y, x.dtype, (n, ch), dev)
-    a.initial_state_indices, a.final_state_indices, a.state_pool_size = _address(state_indices), _address(final_state_indices), pool
-    _call(dev, lib.kda_scan_decode_step, ctypes.byref(a), _address(state), _address(y))
+    pool = _decode_slots(state, state_indices, final_state_indices, n, dev)
+    _dense("state", state, torch.float32, (n if state_indices is None else pool, ch, N), dev)
+    y = _output("y", y, x, x.shape)
+    a = _scan_struct(*front, 0, 0, 0, _address(state_indices), _address(final_state_indices), pool)
+    _call(dev, lib.kda_scan_decode_step, a, state.data_ptr(), y.data_ptr())
     return y
 
 
@@ -353,9 +381,9 @@ def scan_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_softplus=
     dict of fp32 tensors shaped like their inputs: dx, ddt, dA, dB, dC, dD, dz, ddt_bias (the last three None
     without their input) and d_initial_state [N_seqs, D, N] (or None)."""
     lib = _library()
-    a, dev, ch, N, G = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 2)
+    front, dev, ch, N, G = _scan_front(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 2)
     n = _sequences(cu_seqlens, x.shape[0], dev)
-    _dense("dy", dy, x.dtype, tuple(x.shape), dev)
+    _dense("dy", dy, x.dtype, x.shape, dev)
     _states(initial_state, None, None, None, n, (ch, N), torch.float32, dev)
     if d_final_state is not None:
         _dense("d_final_state", d_final_state, torch.float32, (n, ch, N), dev)
@@ -366,13 +394,12 @@ def scan_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_softplus=
                dD=None if D is None else torch.empty(ch, **f32), dz=None if z is None else torch.empty(*rows, ch, **f32),
                ddt_bias=None if dt_bias is None else torch.empty(ch, **f32),
                d_initial_state=torch.empty(n, ch, N, **f32) if want_d_initial_state else None)
-    a.cu_seqlens, a.n_seqs, a.initial_state = _address(cu_seqlens), n, _address(initial_state)
-    g = ScanGrads(struct_size=ctypes.sizeof(ScanGrads), dy=_address(dy), d_final_state=_address(d_final_state), dx=_address(out["dx"]),
-                  ddt=_address(out["ddt"]), dA=_address(out["dA"]), dB=_address(out["dB"]), dC=_address(out["dC"]), dDskip=_address(out["dD"]),
-                  dz=_address(out["dz"]), ddt_bias=_address(out["ddt_bias"]), d_initial_state=_address(out["d_initial_state"]))
-    ws_bytes = _on_device(dev, lib.kda_scan_backward_workspace_size, ctypes.byref(a))
+    a = _scan_struct(*front, _address(cu_seqlens), n, _address(initial_state), 0, 0, 0)
+    g = _grads_struct(dy.data_ptr(), _address(d_final_state),
+                      *(_address(out[k]) for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "d_initial_state")))
+    ws_bytes = _on_device(dev, lib.kda_scan_backward_workspace_size, a)
     ws = _workspace(ws_bytes, dev)
-    _call(dev, lib.kda_scan_backward, ctypes.byref(a), ctypes.byref(g), _address(ws), ws_bytes)
+    _call(dev, lib.kda_scan_backward, a, g, _address(ws), ws_bytes)
     return out
 
 
@@ -381,36 +408,33 @@ def scan_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_softplus=
 
 def _rotary_args(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved):
     dev = _device(q)
-    if q.dim() < 2 or not isinstance(k, torch.Tensor) or k.dim() != q.dim():
+    lead = q.dim() - 2
+    if lead < 0 or not isinstance(k, torch.Tensor) or k.dim() != lead + 2:
         raise ValueError("q and k must be tensors [..., heads, head] with the same rows")
-    if norm not in ("rms", "l2"):
+    if norm != "rms" and norm != "l2":
         raise ValueError(f"unknown norm {norm!r}: 'rms' or 'l2'")
-    lead, head = q.dim() - 2, q.shape[-1]
-    rows = tuple(q.shape[:-2])
-    q_stride = _row_stride("q", q, q.dtype, (*rows, q.shape[-2], head), lead, dev)
-    k_stride = _row_stride("k", k, q.dtype, (*rows, k.shape[-2], head), lead, dev)
-    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if t is not None:
-            _dense(name, t, q.dtype, (head,), dev)
-    count = 1
-    for r in rows:
-        count *= r
-    a = RotaryArgs(struct_size=ctypes.sizeof(RotaryArgs), dtype=_DTYPES[q.dtype], rows=count, q_heads=q.shape[-2],
-                   k_heads=k.shape[-2], head=head, norm=0 if norm == "rms" else 1, interleaved=1 if interleaved else 0,
-                   eps=float(eps), q=q.data_ptr(), k=k.data_ptr(), q_stride=q_stride, k_stride=k_stride,
-                   q_weight=None if q_weight is None else q_weight.data_ptr(),
-                   k_weight=None if k_weight is None else k_weight.data_ptr())
-    if (cos is None) != (sin is None) or (cos is None) != (positions is None):
-        raise ValueError("cos, sin and positions are given together or not at all")
-    if cos is not None:
+    dtype, q_shape, k_shape = q.dtype, q.shape, k.shape
+    rows, head = q_shape[:-2], q_shape[-1]
+    q_stride = _row_stride("q", q, dtype, q_shape, lead, dev)
+    k_stride = _row_stride("k", k, dtype, rows + (k_shape[-2], head), lead, dev)
+    if q_weight is not None:
+        _dense("q_weight", q_weight, dtype, (head,), dev)
+    if k_weight is not None:
+        _dense("k_weight", k_weight, dtype, (head,), dev)
+    half = table_rows = 0
+    if cos is not None or sin is not None or positions is not None:
+        if cos is None or sin is None or positions is None:
+            raise ValueError("cos, sin and positions are given together or not at all")
         if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
             raise ValueError("cos must be a tensor [table rows, rotated pairs]")
-        _dense("cos", cos, torch.float32, tuple(cos.shape), dev)
-        _dense("sin", sin, torch.float32, tuple(cos.shape), dev)
+        table = cos.shape
+        table_rows, half = table
+        _dense("cos", cos, torch.float32, table, dev)
+        _dense("sin", sin, torch.float32, table, dev)
         _dense("positions", positions, torch.int32, rows, dev)
-        a.half, a.table_rows = cos.shape[1], cos.shape[0]
-        a.cos_table, a.sin_table, a.positions = _address(cos), _address(sin), _address(positions)
-    return a, dev
+    return _rotary_struct(_DTYPES[dtype], rows.numel(), q_shape[-2], k_shape[-2], head, half, 0 if norm == "rms" else 1,
+                          1 if interleaved else 0, eps, q.data_ptr(), k.data_ptr(), q_stride, k_stride, _address(q_weight),
+                          _address(k_weight), _address(cos), _address(sin), _address(positions), table_rows), dev
 
 
 def qk_norm_rotary(q, k, cos=None, sin=None, positions=None, q_weight=None, k_weight=None, norm="rms", eps=1e-6,
@@ -424,9 +448,9 @@ def qk_norm_rotary(q, k, cos=None, sin=None, positions=None, q_weight=None, k_we
     rotation. Returns dense (q_out, k_out)."""
     lib = _library()
     a, dev = _rotary_args(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
-    q_out = _output("q_out", q_out, q.dtype, tuple(q.shape), dev)
-    k_out = _output("k_out", k_out, q.dtype, tuple(k.shape), dev)
-    _call(dev, lib.kda_qk_norm_rotary, ctypes.byref(a), _address(q_out), _address(k_out))
+    q_out = _output("q_out", q_out, q, q.shape)
+    k_out = _output("k_out", k_out, q, k.shape)
+    _call(dev, lib.kda_qk_norm_rotary, a, q_out.data_ptr(), k_out.data_ptr())
     return q_out, k_out
 
 
@@ -436,14 +460,14 @@ def qk_norm_rotary_backward(q, k, cos, sin, positions, dq_out, dk_out, q_weight=
     dq_weight, dk_weight (None without the weight). dq_out, dk_out have the outputs' layout and dtype."""
     lib = _library()
     a, dev = _rotary_args(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
-    _dense("dq_out", dq_out, q.dtype, tuple(q.shape), dev)
-    _dense("dk_out", dk_out, q.dtype, tuple(k.shape), dev)
+    _dense("dq_out", dq_out, q.dtype, q.shape, dev)
+    _dense("dk_out", dk_out, q.dtype, k.shape, dev)
     f32 = dict(dtype=torch.float32, device=dev)
     out = dict(dq=torch.empty(tuple(q.shape), **f32), dk=torch.empty(tuple(k.shape), **f32),
                dq_weight=None if q_weight is None else torch.empty(q.shape[-1], **f32),
                dk_weight=None if k_weight is None else torch.empty(q.shape[-1], **f32))
-    ws_bytes = _on_device(dev, lib.kda_qk_norm_rotary_backward_workspace_size, ctypes.byref(a))
+    ws_bytes = _on_device(dev, lib.kda_qk_norm_rotary_backward_workspace_size, a)
     ws = _workspace(ws_bytes, dev)
-    _call(dev, lib.kda_qk_norm_rotary_backward, ctypes.byref(a), _address(dq_out), _address(dk_out),
+    _call(dev, lib.kda_qk_norm_rotary_backward, a, dq_out.data_ptr(), dk_out.data_ptr(),
           *(_address(out[n]) for n in ("dq", "dk", "dq_weight", "dk_weight")), _address(ws), ws_bytes)
     return out
