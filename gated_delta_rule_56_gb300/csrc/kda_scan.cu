@@ -12,6 +12,8 @@
 // a first kernel computes the end states from zeros and the sums of dt, a second one walks over the chunks to get the
 // state before each, and the main kernel runs every chunk from there. That is a second round of exponentials, and it is
 // left out where whole sequences fill the GPU.
+#include <algorithm>
+
 #include "kda_scan.cuh"
 
 namespace kda {
@@ -816,18 +818,20 @@ void launch_decode(const ScanParams &p, float *state, void *y, cudaStream_t s) {
 
 }  // namespace
 
-// Whole sequences where they give every SM a block; otherwise chunks that give it three, of at least 64 rows. (Half as many or
-// twice as many were slower on one sequence of 16384 rows and 4096 channels.)
+// Whole sequences where they give every SM a block; otherwise chunks that give it three. (With two or four, one sequence
+// of 16384 rows and 4096 channels took 3 to 4 % longer.) A row of a short chunk costs 0.35 us in both kernels together, a
+// chunk 1/16 us in the walk over them, so a chunk has at least sqrt(rows / 6) rows.
 ScanPlan scan_plan(const kda_scan_args &a, int sms) {
     const long long rows = (long long)a.B * a.T, blocks = scan_blocks(a);
     if (rows == 0) return ScanPlan{1, 1, false};
     if (sms <= 0) sms = 152;
-    if (!a.cu_seqlens && (a.B * blocks >= sms || a.T <= 64)) return ScanPlan{a.B, a.T, false};
-    long long chunks = 3LL * sms / blocks, most = (rows + 63) / 64;
-    chunks = chunks < 1 ? 1 : chunks > most ? most : chunks;
-    long long per = ((rows + chunks - 1) / chunks + 31) / 32 * 32;
-    chunks = (rows + per - 1) / per;
-    return ScanPlan{(int)chunks, per, chunks > 1};
+    if (!a.cu_seqlens && (a.B * blocks >= sms || a.T <= 32)) return ScanPlan{a.B, a.T, false};
+    long long least = 16;
+    while (least * least * 6 < rows) least += 16;
+    const long long chunks = std::max(1LL, std::min((rows + least - 1) / least, 3LL * sms / blocks));
+    const long long per = ((rows + chunks - 1) / chunks + 15) / 16 * 16;
+    const int count = (int)((rows + per - 1) / per);
+    return ScanPlan{count, per, count > 1};
 }
 
 size_t scan_prefill_workspace_bytes(const kda_scan_args &a, int sms) {

@@ -210,7 +210,7 @@ def _decode_slots(state, state_indices, final_state_indices, n, device):
 def _output(name, t, like, shape):
     """``t``, or a new dense tensor of the type and device of ``like``."""
     if t is None:
-        return like.new_empty(shape)
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
     _dense(name, t, like.dtype, shape, like.device)
     return t
 
@@ -259,7 +259,7 @@ def conv_prefill(x, weight, bias=None, activation="silu", cu_seqlens=None, initi
     pool = _states(initial_state, final_state, initial_state_indices, final_state_indices, n, (W - 1, C), x.dtype, dev)
     y = _output("y", y, x, x.shape)
     if final_state is None and output_final_state:
-        final_state = x.new_empty((n, W - 1, C))
+        final_state = torch.empty(n, W - 1, C, dtype=x.dtype, device=dev)
     a = _conv_struct(*front, _address(cu_seqlens), n, _address(initial_state), _address(initial_state_indices),
                      _address(final_state_indices), pool)
     _call(dev, lib.kda_conv_prefill, a, y.data_ptr(), _address(final_state))
@@ -351,7 +351,7 @@ def scan_prefill(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True,
     pool = _states(initial_state, final_state, initial_state_indices, final_state_indices, n, (ch, N), torch.float32, dev)
     y = _output("y", y, x, x.shape)
     if final_state is None and output_final_state:
-        final_state = A.new_empty((n, ch, N))
+        final_state = torch.empty(n, ch, N, dtype=torch.float32, device=dev)
     a = _scan_struct(*front, _address(cu_seqlens), n, _address(initial_state), _address(initial_state_indices),
                      _address(final_state_indices), pool)
     ws_bytes = _on_device(dev, lib.kda_scan_prefill_workspace_size, a)
