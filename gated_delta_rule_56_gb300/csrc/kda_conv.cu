@@ -369,13 +369,13 @@ __global__ void conv_reduce_kernel(const float *__restrict__ part, int blocks, i
                                    float *__restrict__ dbias) {
     const int c = blockIdx.x * blockDim.x + threadIdx.x, j = blockIdx.y;
     if (c >= C || (j == W && !dbias)) return;
-    double sum = 0.0;
+    ExactSum sum;
 #pragma unroll 16
-    for (int b = 0; b < blocks; ++b) sum += part[((long long)b * (W + 1) + j) * C + c];
+    for (int b = 0; b < blocks; ++b) sum.add(part[((long long)b * (W + 1) + j) * C + c]);
     if (j < W)
-        dweight[(long long)c * W + j] = (float)sum;
+        dweight[(long long)c * W + j] = sum.value();
     else
-        dbias[c] = (float)sum;
+        dbias[c] = sum.value();
 }
 
 __global__ void conv_empty_kernel(Seqs seqs, int W, int C, const float *__restrict__ d_fin, float *__restrict__ d_init) {

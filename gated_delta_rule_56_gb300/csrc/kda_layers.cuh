@@ -148,6 +148,17 @@ __device__ __forceinline__ f32x2 sigmoid2(f32x2 z) {
 }
 __device__ __forceinline__ f32x2 silu2(f32x2 z) { return mul2(z, sigmoid2(z)); }
 
+// A sum that keeps its rounding errors: as exact as one in 64 bits, which this GPU adds 64 times slower than one in 32.
+struct ExactSum {
+    float sum = 0.f, rest = 0.f;
+    __device__ __forceinline__ void add(float x) {  // the error of a two-term sum, by D. E. Knuth's branch-free formula
+        const float t = __fadd_rn(sum, x), b = __fsub_rn(t, sum);
+        rest = __fadd_rn(rest, __fadd_rn(__fsub_rn(sum, __fsub_rn(t, b)), __fsub_rn(x, b)));
+        sum = t;
+    }
+    __device__ __forceinline__ float value() const { return sum + rest; }
+};
+
 // The sequences over the rows: n_seqs of T rows each, or packed ones from cu_seqlens.
 struct Seqs {
     const int32_t *cu;

@@ -55,7 +55,7 @@ __device__ __forceinline__ void copies_arrived() { asm volatile("cp.async.wait_g
 // The rows of x, dt and z come through a ring in shared memory, each warp its own channels' rows, STAGES - 1 blocks ahead:
 // loads into registers were moved back to their use by the compiler, and a third of the time was spent waiting for them.
 template <typename T, int S, int L, bool WIDE, int MODE>
-__global__ void __launch_bounds__(kScanThreads, 3)
+__global__ void __launch_bounds__(kScanThreads, 2)
     scan_rows_kernel(ScanParams p, T *__restrict__ y, float *fin, ScanPlan plan, Carries carry) {
     constexpr bool OUT = MODE == kOutputs, BACK = MODE == kBackEnds;
     constexpr int BLK = kBlock<T>;
@@ -818,8 +818,8 @@ void launch_decode(const ScanParams &p, float *state, void *y, cudaStream_t s) {
 
 }  // namespace
 
-// Whole sequences where they give every SM a block; otherwise chunks that give it three. (With two or four, one sequence
-// of 16384 rows and 4096 channels took 3 to 4 % longer.) A row of a short chunk costs 0.35 us in both kernels together, a
+// Whole sequences where they give every SM a block; otherwise chunks that give it two: with three or
+// four, and registers for as many, one sequence of 16384 rows and 4096 channels took 3 and 8 % longer. A row of a short chunk costs 0.35 us in both kernels together, a
 // chunk 1/16 us in the walk over them, so a chunk has at least sqrt(rows / 6) rows.
 ScanPlan scan_plan(const kda_scan_args &a, int sms) {
     const long long rows = (long long)a.B * a.T, blocks = scan_blocks(a);
@@ -828,7 +828,7 @@ ScanPlan scan_plan(const kda_scan_args &a, int sms) {
     if (!a.cu_seqlens && (a.B * blocks >= sms || a.T <= 32)) return ScanPlan{a.B, a.T, false};
     long long least = 16;
     while (least * least * 6 < rows) least += 16;
-    const long long chunks = std::max(1LL, std::min((rows + least - 1) / least, 3LL * sms / blocks));
+    const long long chunks = std::max(1LL, std::min((rows + least - 1) / least, 2LL * sms / blocks));
     const long long per = ((rows + chunks - 1) / chunks + 15) / 16 * 16;
     const int count = (int)((rows + per - 1) / per);
     return ScanPlan{count, per, count > 1};

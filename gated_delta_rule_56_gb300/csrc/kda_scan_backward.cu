@@ -561,14 +561,24 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
     }
 }
 
-// out[i] = sum over j < count of in[j][i], in order.
-__global__ void scan_reduce_kernel(const float *__restrict__ in, long long size, int count, float *__restrict__ out) {
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+// out[i] = sum over j < count of in[j][i], in order, for the five tensors of partial sums in one launch.
+struct Sums {
+    const float *in[5];
+    float *out[5];
+    long long size[5];
+    int count[5];
+    unsigned first[6];  // the first block of each
+};
+__global__ void __launch_bounds__(128) scan_reduce_kernel(Sums s) {
+    int t = 0;
+    while (t < 4 && blockIdx.x >= s.first[t + 1]) ++t;
+    const long long i = (long long)(blockIdx.x - s.first[t]) * 128 + threadIdx.x, size = s.size[t];
     if (i >= size) return;
-    double sum = 0.0;
-#pragma unroll 8
-    for (int j = 0; j < count; ++j) sum += in[j * size + i];
-    out[i] = (float)sum;
+    const float *in = s.in[t] + i;
+    ExactSum sum;
+#pragma unroll 16
+    for (int j = 0; j < s.count[t]; ++j) sum.add(in[j * size]);
+    s.out[t][i] = sum.value();
 }
 
 // The initial-state gradients of empty sequences are their final states'.
@@ -674,10 +684,6 @@ Layout layout(const kda_scan_args &a, const ScanPlan &plan, char *ws) {
     return l;
 }
 
-void reduce(const float *in, long long size, int count, float *out, cudaStream_t s) {
-    if (out && size) scan_reduce_kernel<<<(unsigned)((size + 255) / 256), 256, 0, s>>>(in, size, count, out);
-}
-
 }  // namespace
 
 size_t scan_backward_workspace_bytes(const kda_scan_args &a, int sms) {
@@ -710,11 +716,17 @@ cudaError_t launch_scan_backward(const kda_scan_args &a, const kda_scan_grads &g
         if ((e = by_states(a.N, BackwardLaunch{a.dtype, p, q, plan, l.forward, wide, blocks * a.G, s})) != cudaSuccess) return e;
     }
     const long long rows = p.seqs.rows;
-    reduce(q.part_B, rows * a.G * a.N, blocks, g.dB, s);
-    reduce(q.part_C, rows * a.G * a.N, blocks, g.dC, s);
-    reduce(q.part_A, (long long)a.D * a.N, plan.chunks, g.dA, s);
-    reduce(q.part_D, a.D, plan.chunks, g.dDskip, s);
-    reduce(q.part_bias, a.D, plan.chunks, g.ddt_bias, s);
+    const long long states = (long long)a.D * a.N;
+    Sums sums{{q.part_B, q.part_C, q.part_A, q.part_D, q.part_bias},
+              {g.dB, g.dC, g.dA, g.dDskip, g.ddt_bias},
+              {rows * a.G * a.N, rows * a.G * a.N, states, a.D, a.D},
+              {blocks, blocks, plan.chunks, plan.chunks, plan.chunks},
+              {}};
+    for (int t = 0; t < 5; ++t) {
+        if (!sums.out[t]) sums.size[t] = 0;
+        sums.first[t + 1] = sums.first[t] + (unsigned)((sums.size[t] + 127) / 128);
+    }
+    scan_reduce_kernel<<<sums.first[5], 128, 0, s>>>(sums);  // dA at least
     if (g.d_initial_state && p.seqs.n_seqs > 0 && (a.cu_seqlens || a.T == 0))
         scan_empty_kernel<<<(unsigned)p.seqs.n_seqs, 256, 0, s>>>(p.seqs, (long long)a.D * a.N, g.d_final_state, g.d_initial_state);
     return cudaGetLastError();
