@@ -371,7 +371,7 @@ kda_status decode_impl(kda_dtype dtype, int N, int H, int dk, int dv, const void
 
 extern "C" {
 
-int kda_version(void) { return 2 * 10000 + 0 * 100 + 0; }
+int kda_version(void) { return 2 * 10000 + 1 * 100 + 0; }
 
 kda_status kda_selftest_wait_timeout(uint64_t limit_ns, kda_stream_t stream) {
     if (limit_ns < 1 || limit_ns > 1000000000ull)

@@ -2,10 +2,12 @@
 //
 //     p_t = bias + sum_j w_j x_{t-(W-1)+j},   y_t = p_t or p_t sigmoid(p_t)         (per channel)
 //
-// Bound by HBM: x is read once and y written once, 2 W + 4 operations per element. A thread owns one
-// 16-byte column of channels (8 in bf16, 4 in fp32) and walks down a run of rows with the last W - 1 inputs
-// and the filter in registers, so each x row is loaded once per run plus W - 1 rows before it (those hit L2:
-// another thread of the same launch streams them). Channels whose rows are not 16-byte aligned go one per thread.
+// Bound by HBM: x is read once and y written once, 2 W + 4 operations per element. A thread owns four channels (8 bytes in
+// bf16, 16 in fp32; a warp's row is 256 or 512 consecutive bytes) and walks down a run of rows with the last W - 1 inputs
+// and the filter in registers, as pairs that one instruction multiplies and adds; the loads of a batch of rows are issued
+// together. Eight channels per thread took twice the registers and left half the loads in flight (334 us where four take 265). Only the W - 1
+// rows before a run are read twice. Channels whose rows are not 16-byte aligned go one per thread.
+// Measured: 32768 rows x 12288 channels in bf16, W = 4, SiLU: 265 us, 6.1 TB/s of x and y (89 % of the measured copy rate).
 #include "kda_layers.cuh"
 #include "kda_layers.h"
 
@@ -230,6 +232,8 @@ __global__ void __launch_bounds__(kLanes *kRuns) conv_decode_kernel(ConvParams p
 // dw_j = sum_t dp_t x_{t-(W-1)+j},  db = sum_t dp_t; the rows before a sequence give its initial state's gradient.
 // A thread recomputes p over its run and the W - 1 rows after it. The filter's sums of the block's runs are
 // added in shared memory in a fixed order and written to `part` [block][W + 1][C]; conv_reduce_kernel adds those.
+// Measured: 32768 rows x 4096 channels in bf16: 228 us in all, 4.7 TB/s of x, dy and dx in fp32 (69 % of the copy rate); what
+// holds it is the latency of the loads at 16 warps per SM (125 registers for two windows, the filter and its sums).
 template <typename T, int W, int V>
 __global__ void __launch_bounds__(kLanes *kBackRuns) conv_backward_kernel(ConvParams p, const T *__restrict__ dy,
                                                                        const float *__restrict__ d_fin,

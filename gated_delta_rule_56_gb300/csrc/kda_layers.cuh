@@ -135,11 +135,6 @@ __device__ __forceinline__ f32x2 softplus2(f32x2 x) {
     q = fma2(q, e, both(1.f));
     return fma2(e, q, pair(m0, m1));
 }
-__device__ __forceinline__ float softplus(float x) {
-    float a, b;
-    unpair(softplus2(both(x)), a, b);
-    return a;
-}
 // sigmoid(z) and z sigmoid(z), two at a time.
 __device__ __forceinline__ f32x2 sigmoid2(f32x2 z) {
     float a, b;

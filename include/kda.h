@@ -470,7 +470,7 @@ KDA_API const char *kda_status_string(kda_status status);
 KDA_API const char *kda_last_error(void);
 
 /* Library ABI version: major * 10000 + minor * 100 + patch. Version 2 made packed calls to
- * kda_prefill_workspace_size explicit (the cu_seqlens argument). */
+ * kda_prefill_workspace_size explicit (the cu_seqlens argument); 2.1 added the operators around the mixer. */
 KDA_API int kda_version(void);
 
 #ifdef __cplusplus
