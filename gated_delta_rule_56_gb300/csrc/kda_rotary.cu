@@ -7,8 +7,8 @@
 // sines stay in registers while its warp goes over the heads of one token, so the tables are read once per
 // token and not once per head. Four heads' loads are issued together and kept as they were loaded until used: converted at
 // once they took twice the registers and the kernel 238 us where it takes 175 (32768 tokens x 64 heads of 128 in bf16: 6.1 TB/s
-// of q and k read and written, 90 % of the measured copy rate). The backward pass (8192 tokens x 40 heads): 91 us, 3.7 TB/s; its
-// two inputs, the gradient and the weights' sums take 109 registers, so 16 warps per SM.
+// of q and k read and written, 90 % of the measured copy rate). The backward pass (8192 tokens x 40 heads): 73 us, 4.6 TB/s; its
+// two inputs, the gradient and the weights' sums leave room for 16 warps per SM.
 #include "kda_layers.cuh"
 #include "kda_layers.h"
 
@@ -16,7 +16,7 @@ namespace kda {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kBatch = 4, kBackBatch = 2;  // heads of a lane group whose loads are issued together
+constexpr int kBatch = 4, kBackBatch = 4;  // heads of a lane group whose loads are issued together
 
 struct RotaryParams {
     const void *q, *k, *qw, *kw;
@@ -245,14 +245,16 @@ __global__ void __launch_bounds__(kWarps * 32) rotary_backward_kernel(RotaryPara
 
 __global__ void rotary_reduce_kernel(const float *__restrict__ part, int blocks, int head, float *__restrict__ dqw,
                                      float *__restrict__ dkw) {
-    // One warp per value of one weight: lane partial sums in 64 bits, then the warp's.
+    // One warp per value of one weight: the lanes' sums, then the warp's.
     const int i = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32, lane = threadIdx.x & 31;
     if (i >= 2 * head) return;
-    double sum = 0.0;
-    for (int b = lane; b < blocks; b += 32) sum += part[(long long)b * 2 * head + i];
+    ExactSum lanes;
+#pragma unroll 4
+    for (int b = lane; b < blocks; b += 32) lanes.add(part[(long long)b * 2 * head + i]);
+    float sum = lanes.value();
     for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
     float *out = i < head ? dqw : dkw;
-    if (lane == 0 && out) out[i % head] = (float)sum;
+    if (lane == 0 && out) out[i % head] = sum;
 }
 
 RotaryParams rotary_params(const kda_rotary_args &a, unsigned *err) {
@@ -340,7 +342,8 @@ struct Backward {
 };
 
 int backward_blocks(const kda_rotary_args &a, int sms) {
-    const long long need = (a.rows + kWarps - 1) / kWarps, most = 8LL * (sms > 0 ? sms : 152);
+    // Two blocks per SM are resident; with four times as many the weights' sums cost 8 us more on 8192 tokens x 40 heads.
+    const long long need = (a.rows + kWarps - 1) / kWarps, most = 2LL * (sms > 0 ? sms : 152);
     return (int)(need < most ? need : most);
 }
 
