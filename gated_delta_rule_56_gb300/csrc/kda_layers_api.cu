@@ -110,6 +110,7 @@ kda_status check_scan(const kda_scan_args &a, bool decode, bool pools) {
     if (a.N < 1 || a.G < 1) return fail(KDA_ERR_INVALID_ARG, "N=%d G=%d must be positive", a.N, a.G);
     if (a.N > 256) return fail(KDA_ERR_UNSUPPORTED, "N=%d: at most 256 states per channel", a.N);
     if (a.D > 65536) return fail(KDA_ERR_UNSUPPORTED, "D=%d: at most 65536 channels", a.D);
+    if (a.G > 32768) return fail(KDA_ERR_UNSUPPORTED, "G=%d: at most 32768 groups", a.G);
     if (a.D % a.G != 0) return fail(KDA_ERR_INVALID_ARG, "D=%d is not a multiple of G=%d", a.D, a.G);
     if (a.D == 0) return KDA_OK;
     const long long gn = (long long)a.G * a.N;

@@ -644,14 +644,14 @@ struct BackwardLaunch {
     }
 };
 
-// Whole sequences where they give every SM three blocks; otherwise chunks that give it four, of at least 64 rows.
+// Whole sequences where they give every SM three blocks; otherwise chunks that give it four (two full waves), of at least 64 rows.
 ScanPlan backward_plan(const kda_scan_args &a, int sms) {
     const long long rows = (long long)a.B * a.T, blocks = (long long)blocks_per_group(a) * a.G;
     if (rows == 0) return ScanPlan{0, 1, false};
     if (sms <= 0) sms = 152;
     if (!a.cu_seqlens && (a.B * blocks >= 3 * sms || a.T <= 64)) return ScanPlan{a.B, a.T, false};
     const long long most = (rows + 63) / 64, chunks = std::max(1LL, std::min(most, 4LL * sms / blocks));
-    const long long per = ((rows + chunks - 1) / chunks + 31) / 32 * 32;
+    const long long per = ((rows + chunks - 1) / chunks + kRows - 1) / kRows * kRows;
     const int count = (int)((rows + per - 1) / per);
     return ScanPlan{count, per, count > 1};
 }

@@ -363,7 +363,8 @@ KDA_API size_t kda_conv_backward_workspace_size(const kda_conv_args *args);
 typedef struct kda_scan_args {
     size_t struct_size;
     kda_dtype dtype;         /* of x, dt, Bm, Cm, z and y */
-    int B, T, D, N, G;       /* x [B, T, D]; N states per channel, 1 to 256; G groups, D a multiple of G */
+    int B, T, D, N, G;       /* x [B, T, D]; N states per channel, 1 to 256; G groups, at most 32768, D a
+                                multiple of G and at most 65536 */
     int dt_softplus;         /* non-zero: dt' = log(1 + exp(dt + dt_bias)) */
     const void *x, *dt;      /* [B, T, D] */
     const void *Bm, *Cm;     /* [B, T, G, N] */

@@ -258,3 +258,8 @@ def test_rows_without_one_distance_are_refused(make):
     t = make()
     with pytest.raises(ValueError):
         layers._row_stride("x", t, t.dtype, tuple(t.shape), 2, t.device)
+
+
+def test_too_many_groups_are_refused(lib):
+    a = _scan(D=65536, G=65536, N=1)
+    assert lib.kda_scan_prefill(ctypes.byref(a), PTR, None, PTR, 1 << 40, None) == UNSUPPORTED
