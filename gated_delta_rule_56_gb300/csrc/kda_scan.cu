@@ -179,7 +179,26 @@ __global__ void __launch_bounds__(kScanThreads, 2)
             }
         if (r0 >= stop) return;
         seq = p.seqs.at(r0);
-        if (OUT && plan.carries && p.seqs.begin(seq) < r0) load_states(carry.state + chunk * chunk_states, h, 1.f);
+        const long long bos = p.seqs.begin(seq);
+        if (OUT && plan.carries && bos < r0) {
+            if (plan.folded()) {  // from the end state of the chunk in which the sequence begins, over the chunks since
+                int j = bos > 0 ? (int)(bos / plan.rows) : 0;
+                load_states(carry.state + j * chunk_states, h, 1.f);
+                for (++j; j < chunk; ++j) {
+                    f32x2 local[2][S / 2];
+                    load_states(carry.state + j * chunk_states, local, 1.f);
+                    const float *time = carry.time + (long long)j * p.C;
+                    const f32x2 t0 = both(time[c]), t1 = both(time[c1]);
+#pragma unroll
+                    for (int i = 0; i < S / 2; ++i) {
+                        h[0][i] = fma2(decay2(t0, A[0][i]), h[0][i], local[0][i]);
+                        h[1][i] = fma2(decay2(t1, A[1][i]), h[1][i], local[1][i]);
+                    }
+                }
+            } else {
+                load_states(carry.state + chunk * chunk_states, h, 1.f);
+            }
+        }
     }
     // The row at which the next sequence begins. The last sequence that begins here and goes on after the chunk takes
     // its initial state from the first kernel's copy, because another block may write its final state there.
@@ -442,7 +461,7 @@ struct PrefillLaunch {
             scan_rows_kernel<T, S, L, WIDE, kEnds><<<dim3((unsigned)plan.chunks - 1, (unsigned)blocks), kScanThreads, 0, s>>>(
                 p, nullptr, nullptr, plan, carry);
             const long long size = (long long)p.C * p.N;
-            scan_carry_kernel<<<(unsigned)((size + 127) / 128), 128, (size_t)plan.chunks, s>>>(p, plan, carry);
+            if (!plan.folded()) scan_carry_kernel<<<(unsigned)((size + 127) / 128), 128, (size_t)plan.chunks, s>>>(p, plan, carry);
         }
         scan_rows_kernel<T, S, L, WIDE, kOutputs><<<dim3((unsigned)plan.chunks, (unsigned)blocks), kScanThreads, 0, s>>>(
             p, static_cast<T *>(y), fin, plan, carry);

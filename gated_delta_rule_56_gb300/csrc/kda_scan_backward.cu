@@ -18,8 +18,8 @@
 // recomputed from its decay, which the way back needs anyway. That is 15 multiply-adds and 1.75 exponentials per (row, channel,
 // state). With the whole window unrolled and its states in registers the kernel was twice as slow: spills and a
 // loop that did not fit the instruction cache.
-// Measured: 4 sequences of 2048 rows x 4096 channels x 16 states in bf16 with gate: 1.15 ms (forward 149 us, backward ends 135 us,
-// main kernel 818 us, the rest 45 us). The main kernel issues 436 warp instructions per 32 channels and row at 46 % of the
+// Measured: 4 sequences of 2048 rows x 4096 channels x 16 states in bf16 with gate: 1.11 ms (forward 145 us, backward ends 131 us,
+// main kernel 789 us, the rest 45 us). The main kernel issues 436 warp instructions per 32 channels and row at 46 % of the
 // issue slots: two blocks per SM (113 KB of shared memory, 235 registers) hide its latencies no better. A loop that prepares the
 // next window beside the passes over this one, with one barrier less, took the same time.
 #include <algorithm>
