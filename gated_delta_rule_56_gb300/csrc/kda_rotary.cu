@@ -367,7 +367,7 @@ cudaError_t launch_rotary_backward(const kda_rotary_args &a, const void *dq_out,
         const cudaError_t e = by_type(a.dtype, p, Backward{p, dq_out, dk_out, dq, dk, part, blocks, s});
         if (e != cudaSuccess) return e;
     }
-    if (part)
+    if (dq_weight || dk_weight)  // over no rows too: the sums are zeros
         rotary_reduce_kernel<<<(unsigned)((2 * a.head + 7) / 8), 256, 0, s>>>(part, blocks, a.head, dq_weight, dk_weight);
     return cudaGetLastError();
 }
