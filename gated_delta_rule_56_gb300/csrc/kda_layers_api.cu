@@ -87,6 +87,14 @@ long long sequences(const A &a) {
     return a.cu_seqlens ? a.n_seqs : a.B;
 }
 
+// Rows that belong to no sequence would be left out.
+template <typename A>
+kda_status check_some_sequence(const A &a) {
+    const long long rows = (long long)a.B * a.T;
+    if (sequences(a) == 0 && rows > 0) return fail(KDA_ERR_INVALID_ARG, "no sequences for %lld rows", rows);
+    return KDA_OK;
+}
+
 kda_status check_conv(const kda_conv_args &a, bool decode, bool pools) {
     kda_status st;
     if ((st = check_dtype(a.dtype)) || (st = check_sequences(a, decode, pools))) return st;
@@ -174,7 +182,9 @@ kda_status kda_conv_prefill(const kda_conv_args *args, void *y, void *final_stat
     if (a.final_state_indices && !final_state)
         return fail(KDA_ERR_INVALID_ARG, "final_state_indices given without final_state (the pool)");
     if ((st = check_optional(final_state, "final_state", e))) return st;
-    if (a.C == 0 || sequences(a) == 0) return ok();
+    if (a.C == 0) return ok();
+    if ((st = check_some_sequence(a))) return st;
+    if (sequences(a) == 0) return ok();
     if ((long long)a.B * a.T > 0 && (st = check_given(y, "y", e))) return st;
     unsigned *err = device_error_word();
     if (!err) return no_error_word();
@@ -212,7 +222,7 @@ kda_status kda_conv_backward(const kda_conv_args *args, const void *dy, const fl
         (st = check_optional(d_final_state, "d_final_state", 4)) || (st = check_optional(d_initial_state, "d_initial_state", 4)) ||
         (st = check_workspace(workspace, workspace_bytes, conv_backward_workspace_bytes(a))))
         return st;
-    if (sequences(a) == 0 && rows > 0) return fail(KDA_ERR_INVALID_ARG, "no sequences for %lld rows", rows);
+    if ((st = check_some_sequence(a))) return st;
     unsigned *err = device_error_word();
     if (!err) return no_error_word();
     return launched(launch_conv_backward(a, dy, d_final_state, dx, dweight, dbias, sequences(a) ? d_initial_state : nullptr,
@@ -234,7 +244,9 @@ kda_status kda_scan_prefill(const kda_scan_args *args, void *y, float *final_sta
     if (a.final_state_indices && !final_state)
         return fail(KDA_ERR_INVALID_ARG, "final_state_indices given without final_state (the pool)");
     if ((st = check_optional(final_state, "final_state", 4))) return st;
-    if (a.D == 0 || sequences(a) == 0) return ok();
+    if (a.D == 0) return ok();
+    if ((st = check_some_sequence(a))) return st;
+    if (sequences(a) == 0) return ok();
     if ((long long)a.B * a.T > 0 && (st = check_given(y, "y", esize(a.dtype)))) return st;
     const int sms = current_sms();
     if ((st = check_workspace(workspace, workspace_bytes, scan_prefill_workspace_bytes(a, sms)))) return st;
@@ -283,7 +295,7 @@ kda_status kda_scan_backward(const kda_scan_args *args, const kda_scan_grads *gr
         return fail(KDA_ERR_INVALID_ARG, "a gradient is asked for an input that is not given");
     if ((st = check_optional(g.d_final_state, "d_final_state", 4)) || (st = check_optional(g.d_initial_state, "d_initial_state", 4)))
         return st;
-    if (sequences(a) == 0 && rows > 0) return fail(KDA_ERR_INVALID_ARG, "no sequences for %lld rows", rows);
+    if ((st = check_some_sequence(a))) return st;
     const int sms = current_sms();
     if ((st = check_workspace(workspace, workspace_bytes, scan_backward_workspace_bytes(a, sms)))) return st;
     unsigned *err = device_error_word();

@@ -312,8 +312,8 @@ KDA_API kda_status kda_decode_step_gated(kda_dtype dtype, int N, int H, int dk, 
  * Outputs must not overlap inputs, except states updated in place. Packed sequences and state pools as in
  * kda_prefill and kda_options (a pool's slots have the shape of one sequence's state); a cu_seqlens that is
  * not a non-decreasing list from 0 to T sets KDA_ERR_INVALID_ARG in the error word and leaves the outputs
- * unspecified (nothing out of range is read or written). Gradients are fp32, and the same bits
- * every time (no atomics).
+ * unspecified (nothing out of range is read or written), and rows without any sequence (n_seqs == 0) are refused.
+ * Gradients are fp32, and the same bits every time (no atomics).
  */
 
 /*
