@@ -4,11 +4,14 @@
 #include <cmath>
 #include <cstring>
 
+#include "kda_layers.cuh"
 #include "kda_layers.h"
 
 using namespace kda;
 
 namespace {
+
+__global__ void __launch_bounds__(128) seqs_kernel(Seqs seqs, unsigned *err) { check_seqs(seqs, err); }
 
 // The caller's argument struct, read up to the size it was compiled with.
 template <typename A>
@@ -166,6 +169,14 @@ kda_status check_rotary(const kda_rotary_args &a) {
     return KDA_OK;
 }
 
+// Without rows no kernel goes over them and looks at cu_seqlens: this call does.
+template <typename A>
+kda_status check_no_rows(const A &a, unsigned *err, cudaStream_t s) {
+    if (!a.cu_seqlens || a.T > 0) return KDA_OK;
+    seqs_kernel<<<1, 128, 0, s>>>(Seqs{a.cu_seqlens, a.n_seqs, 0, 0}, err);
+    return launched(cudaGetLastError(), "cu_seqlens");
+}
+
 kda_status no_error_word() { return fail(KDA_ERR_CUDA, "cannot reach the device error word: %s", cudaGetErrorString(cudaGetLastError())); }
 
 cudaStream_t as_stream(kda_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
@@ -184,10 +195,11 @@ kda_status kda_conv_prefill(const kda_conv_args *args, void *y, void *final_stat
     if ((st = check_optional(final_state, "final_state", e))) return st;
     if (a.C == 0) return ok();
     if ((st = check_some_sequence(a))) return st;
-    if (sequences(a) == 0) return ok();
+    if (sequences(a) == 0 && !a.cu_seqlens) return ok();
     if ((long long)a.B * a.T > 0 && (st = check_given(y, "y", e))) return st;
     unsigned *err = device_error_word();
     if (!err) return no_error_word();
+    if ((st = check_no_rows(a, err, as_stream(stream))) || sequences(a) == 0) return st;
     return launched(launch_conv_prefill(a, y, final_state, err, as_stream(stream)), "convolution");
 }
 
@@ -225,6 +237,7 @@ kda_status kda_conv_backward(const kda_conv_args *args, const void *dy, const fl
     if ((st = check_some_sequence(a))) return st;
     unsigned *err = device_error_word();
     if (!err) return no_error_word();
+    if ((st = check_no_rows(a, err, as_stream(stream)))) return st;
     return launched(launch_conv_backward(a, dy, d_final_state, dx, dweight, dbias, sequences(a) ? d_initial_state : nullptr,
                                          workspace, err, as_stream(stream)),
                     "convolution backward");
@@ -246,12 +259,13 @@ kda_status kda_scan_prefill(const kda_scan_args *args, void *y, float *final_sta
     if ((st = check_optional(final_state, "final_state", 4))) return st;
     if (a.D == 0) return ok();
     if ((st = check_some_sequence(a))) return st;
-    if (sequences(a) == 0) return ok();
+    if (sequences(a) == 0 && !a.cu_seqlens) return ok();
     if ((long long)a.B * a.T > 0 && (st = check_given(y, "y", esize(a.dtype)))) return st;
     const int sms = current_sms();
     if ((st = check_workspace(workspace, workspace_bytes, scan_prefill_workspace_bytes(a, sms)))) return st;
     unsigned *err = device_error_word();
     if (!err) return no_error_word();
+    if ((st = check_no_rows(a, err, as_stream(stream))) || sequences(a) == 0) return st;
     return launched(launch_scan_prefill(a, y, final_state, workspace, sms, err, as_stream(stream)), "scan");
 }
 
@@ -300,6 +314,7 @@ kda_status kda_scan_backward(const kda_scan_args *args, const kda_scan_grads *gr
     if ((st = check_workspace(workspace, workspace_bytes, scan_backward_workspace_bytes(a, sms)))) return st;
     unsigned *err = device_error_word();
     if (!err) return no_error_word();
+    if ((st = check_no_rows(a, err, as_stream(stream)))) return st;
     return launched(launch_scan_backward(a, g, workspace, sms, err, as_stream(stream)), "scan backward");
 }
 

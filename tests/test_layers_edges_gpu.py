@@ -28,3 +28,25 @@ def test_weight_gradients_over_no_rows_are_zeros(which):
     kda.check_status()
     for n in "qk":
         assert g[f"d{n}_weight"] is None if n not in which else not g[f"d{n}_weight"].any()
+
+
+def test_a_bad_cu_seqlens_over_no_rows_is_reported():
+    x, w = torch.empty(1, 0, 8, device=DEV), torch.ones(8, 4, device=DEV)
+    B, A = torch.empty(1, 0, 1, 4, device=DEV), -torch.ones(8, 4, device=DEV)
+    pool = torch.ones(2, 3, 8, device=DEV)
+    calls = [lambda cu: kda.conv_prefill(x, w, cu_seqlens=cu), lambda cu: kda.conv_prefill(x, w, cu_seqlens=cu, output_final_state=False),
+             lambda cu: kda.conv_prefill(x, w, cu_seqlens=cu, initial_state=pool[:cu.numel() - 1], final_state=pool[:cu.numel() - 1]),
+             lambda cu: kda.conv_backward(x, w, x, cu_seqlens=cu),
+             lambda cu: kda.conv_backward(x, w, x, cu_seqlens=cu, want_d_initial_state=False),
+             lambda cu: kda.scan_prefill(x, x, A, B, B, cu_seqlens=cu), lambda cu: kda.scan_backward(x, x, A, B, B, x, cu_seqlens=cu),
+             lambda cu: kda.scan_backward(x, x, A, B, B, x, cu_seqlens=cu, want_d_initial_state=False)]
+    for i, call in enumerate(calls):
+        for bad in ([0, 5], [3], [0, 2, 0]):
+            call(torch.tensor(bad, dtype=torch.int32, device=DEV))
+            with pytest.raises(kda.KDAError, match="cu_seqlens"):
+                kda.check_status()
+                raise AssertionError((i, bad))
+        for good in ([0], [0, 0], [0, 0, 0]):
+            call(torch.tensor(good, dtype=torch.int32, device=DEV))
+            kda.check_status()
+    assert torch.equal(pool, torch.ones_like(pool))
