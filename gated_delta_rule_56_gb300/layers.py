@@ -48,7 +48,7 @@ def _packer(cls):
     """Makes an argument struct from its fields in order (without struct_size; None is a NULL pointer). Packing bytes costs a
     third of filling a ctypes structure, and a token step has little else to do on the host."""
     size = ctypes.sizeof(cls)
-    pack = struct.Struct("@" + "".join(_CODES[t] for _, t in cls._fields_)).pack
+    pack = struct.Struct("@" + "".join(_CODES[t] for _, t in cls._fields_) + "0P").pack  # 0P: up to the C struct's end
 
     def make(*fields):
         return pack(size, *fields)
