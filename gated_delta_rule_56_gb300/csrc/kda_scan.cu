@@ -431,6 +431,15 @@ __global__ void __launch_bounds__(128) scan_back_carry_kernel(ScanParams p, Scan
     }
 }
 
+// No rows: every sequence's final state is its initial one; nothing else is read, A neither.
+__global__ void __launch_bounds__(128) scan_no_rows_kernel(ScanParams p, float *fin) {
+    const int n = blockIdx.x;
+    const long long size = (long long)p.C * p.N, from = p.init ? state_slot(p.init_idx, p.pool, n, p.err) : -1;
+    const long long to = fin ? state_slot(p.fin_idx, p.pool, n, p.err) : -1;
+    if (to < 0) return;
+    for (long long i = threadIdx.x; i < size; i += 128) fin[to * size + i] = from >= 0 ? p.init[from * size + i] : 0.f;
+}
+
 Carries carries_in(const kda_scan_args &a, const ScanPlan &plan, void *ws) {
     const size_t states = (size_t)plan.chunks * a.D * a.N;
     float *f = static_cast<float *>(ws);
@@ -846,7 +855,7 @@ void launch_decode(const ScanParams &p, float *state, void *y, cudaStream_t s) {
 // chunk 1/16 us in the walk over them, so a chunk has at least sqrt(rows / 6) rows.
 ScanPlan scan_plan(const kda_scan_args &a, int sms) {
     const long long rows = (long long)a.B * a.T, blocks = scan_blocks(a);
-    if (rows == 0) return ScanPlan{1, 1, false};
+    if (rows == 0) return ScanPlan{0, 1, false};
     if (sms <= 0) sms = 152;
     if (!a.cu_seqlens && (a.B * blocks >= sms || a.T <= 32)) return ScanPlan{a.B, a.T, false};
     long long least = 16;
@@ -864,6 +873,11 @@ size_t scan_prefill_workspace_bytes(const kda_scan_args &a, int sms) {
 
 cudaError_t launch_scan_prefill(const kda_scan_args &a, void *y, float *final_state, void *ws, int sms, unsigned *err,
                                 cudaStream_t s) {
+    if ((long long)a.B * a.T == 0) {
+        const ScanParams p = scan_params(a, err);
+        scan_no_rows_kernel<<<(unsigned)p.seqs.n_seqs, 128, 0, s>>>(p, final_state);
+        return cudaGetLastError();
+    }
     const ScanPlan plan = scan_plan(a, sms);
     return scan_by_type(a, PrefillLaunch{scan_params(a, err), y, final_state, plan, carries_in(a, plan, ws), scan_blocks(a), s});
 }

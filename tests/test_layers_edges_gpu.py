@@ -6,7 +6,7 @@ import torch
 import gated_delta_rule_56_gb300 as kda
 from gated_delta_rule_56_gb300 import layers
 
-from layers_cases import DEV
+from layers_cases import DEV, cu_of, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,25 @@ def test_a_bad_cu_seqlens_over_no_rows_is_reported():
             call(torch.tensor(good, dtype=torch.int32, device=DEV))
             kda.check_status()
     assert torch.equal(pool, torch.ones_like(pool))
+
+
+def test_an_empty_prompt_reads_only_its_states():
+    """No rows: the C call needs neither the rows' inputs nor A."""
+    s, out = gen(1)(2, 8, 16), torch.full((2, 8, 16), float("nan"), device=DEV)
+    a = layers._scan_struct(1, 2, 0, 8, 16, 1, 1, *[0] * 5, *[0] * 5, 0, 0, 0, 0, 0, s.data_ptr(), 0, 0, 0)
+    layers._call(s.device, layers._library().kda_scan_prefill, a, 0, out.data_ptr(), 0, 0)
+    kda.check_status()
+    assert torch.equal(out, s)
+    x, B, A = torch.empty(1, 0, 8, device=DEV), torch.empty(1, 0, 1, 16, device=DEV), -torch.ones(8, 16, device=DEV)
+    cu, pool = cu_of([0, 0, 0]), gen(2)(5, 8, 16)
+    frm, to = (torch.tensor(v, dtype=torch.int32, device=DEV) for v in ([4, -1, 0], [1, 3, -1]))
+    want = pool.clone()
+    want[1], want[3] = pool[4], 0
+    kda.scan_prefill(x, x, A, B, B, cu_seqlens=cu, initial_state=pool, final_state=pool, initial_state_indices=frm, final_state_indices=to)
+    kda.check_status()
+    assert torch.equal(pool, want)
+    frm[0] = 5
+    y, fin = kda.scan_prefill(x, x, A, B, B, cu_seqlens=cu, initial_state=pool, initial_state_indices=frm)
+    with pytest.raises(kda.KDAError, match="pool"):
+        kda.check_status()
+    assert not fin[:2].any() and torch.equal(fin[2], pool[0])
