@@ -151,7 +151,8 @@ struct ExactSum {
         rest = __fadd_rn(rest, __fadd_rn(__fsub_rn(sum, __fsub_rn(t, b)), __fsub_rn(x, b)));
         sum = t;
     }
-    __device__ __forceinline__ float value() const { return sum + rest; }
+    // Past fp32's range the rest is NaN (inf - inf), and the sum alone what it rounds to.
+    __device__ __forceinline__ float value() const { return isfinite(sum) ? sum + rest : sum; }
 };
 
 // The sequences over the rows: n_seqs of T rows each, or packed ones from cu_seqlens.

@@ -72,3 +72,25 @@ def test_an_empty_prompt_reads_only_its_states():
     with pytest.raises(kda.KDAError, match="pool"):
         kda.check_status()
     assert not fin[:2].any() and torch.equal(fin[2], pool[0])
+
+
+def test_sums_past_the_largest_fp32_are_infinite():
+    """Weight gradients whose parts overflow: the infinity that the sum rounds to, as for any other sum, and not NaN."""
+    inf, big = float("inf"), 3e38
+    x, w, dy = torch.ones(1, 700, 8, device=DEV), torch.zeros(8, 4, device=DEV), torch.zeros(1, 700, 8, device=DEV)
+    dy[0, 10:14, 2] = big     # in one thread's run
+    dy[0, ::300, 5] = -big    # in several blocks' parts
+    g = kda.conv_backward(x, w, dy, torch.zeros(8, device=DEV), activation=None)
+    want = torch.zeros(8, device=DEV)
+    want[2], want[5] = inf, -inf
+    assert torch.equal(g["dbias"], want) and torch.equal(g["dweight"], want[:, None].expand(8, 4)) and not g["dx"].any()
+    zero = torch.zeros(1, 700, 1, 4, device=DEV)
+    g = kda.scan_backward(x, x, -torch.ones(8, 4, device=DEV), zero, zero, dy, D=torch.zeros(8, device=DEV), dt_softplus=False)
+    assert torch.equal(g["dD"], want) and not g["dA"].any() and not g["dx"].any()
+    q, d = torch.ones(700, 1, 8, device=DEV), dy.view(700, 1, 8)
+    g = kda.qk_norm_rotary_backward(q, q, None, None, None, d, d * 0, q_weight=torch.zeros(8, device=DEV), k_weight=torch.zeros(8, device=DEV))
+    kda.check_status()
+    assert torch.equal(g["dq_weight"], want) and not g["dk_weight"].any()
+    dy[0, 20, 3], dy[0, 600, 3] = inf, -inf
+    g = kda.conv_backward(x, w, dy, torch.zeros(8, device=DEV), activation=None)
+    assert torch.isnan(g["dbias"][3]) and g["dbias"][5] == -inf
