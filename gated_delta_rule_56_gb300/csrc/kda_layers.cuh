@@ -102,6 +102,23 @@ __device__ __forceinline__ f32x2 decay2(f32x2 dt, f32x2 A) {
     return pair(ex2(a), ex2(b));
 }
 __device__ __forceinline__ float decay(float dt, float A) { return ex2(fmaf(dt, A, 1.2e-8f)); }
+// Over many rows: h exp(time A) + to, the exponential in two factors. With a growing state (A or time steps of the other sign) one factor
+// leaves fp32's range where the product is still inside it, and an infinite one would make NaN of a zero. 2^127 twice takes every state but
+// zero past the range, so exponents stop there (NaN stays NaN). The constant: as above, for each factor.
+__device__ __forceinline__ float ex2_up_to_127(float x) {
+    asm("min.NaN.f32 %0, %0, 0f42FE0000;" : "+f"(x));
+    return ex2(x);
+}
+__device__ __forceinline__ float carried(float time, float A, float h, float to) {
+    const float s = ex2_up_to_127(fmaf(0.5f * time, A, 1.2e-8f));
+    return fmaf(s, s * h, to);
+}
+__device__ __forceinline__ f32x2 carried2(f32x2 time, f32x2 A, f32x2 h, f32x2 to) {
+    float a, b;
+    unpair(fma2(mul2(time, pair(0.5f, 0.5f)), A, pair(1.2e-8f, 1.2e-8f)), a, b);
+    const f32x2 s = pair(ex2_up_to_127(a), ex2_up_to_127(b));
+    return fma2(s, mul2(s, h), to);
+}
 __device__ __forceinline__ float rcp(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(kScanThreads, 2)
                     const f32x2 t0 = both(time[c]), t1 = both(time[c1]);
 #pragma unroll
                     for (int i = 0; i < S / 2; ++i) {
-                        h[0][i] = fma2(decay2(t0, A[0][i]), h[0][i], local[0][i]);
-                        h[1][i] = fma2(decay2(t1, A[1][i]), h[1][i], local[1][i]);
+                        h[0][i] = carried2(t0, A[0][i], h[0][i], local[0][i]);
+                        h[1][i] = carried2(t1, A[1][i], h[1][i], local[1][i]);
                     }
                 }
             } else {
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(128) scan_carry_kernel(ScanParams p, ScanPlan 
 #pragma unroll
         for (int b = 0; b < kCarryBatch; ++b) {
             if (j0 + b < plan.chunks) carry.state[(j0 + b) * size + i] = before;
-            if (j0 + b + 1 < plan.chunks) before = fresh[j0 + b] ? local[b] : fmaf(ex2(A * time[b]), before, local[b]);
+            if (j0 + b + 1 < plan.chunks) before = fresh[j0 + b] ? local[b] : carried(time[b], A, before, local[b]);
         }
     }
 }
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(128) scan_back_carry_kernel(ScanParams p, Scan
         for (int b = 0; b < kCarryBatch; ++b) {
             if (j0 - b < 0) break;
             carry.state[(j0 - b) * size + i] = after;
-            after = goes_on[j0 - b] ? fmaf(ex2(A * time[b]), after, local[b]) : local[b];
+            after = goes_on[j0 - b] ? carried(time[b], A, after, local[b]) : local[b];
         }
     }
 }

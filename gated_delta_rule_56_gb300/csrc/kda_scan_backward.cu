@@ -302,8 +302,8 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_backward_kernel(ScanPara
 #pragma unroll
                 for (int i = 0; i < EN; i += 2) {
                     const ulonglong2 v = sm.first[(j * EN + i) / 2][tid];
-                    h[j][i] = fma2(decay2(t2, A[j][i]), v.x, h[j][i]);
-                    h[j][i + 1] = fma2(decay2(t2, A[j][i + 1]), v.y, h[j][i + 1]);
+                    h[j][i] = carried2(t2, A[j][i], v.x, h[j][i]);
+                    h[j][i + 1] = carried2(t2, A[j][i + 1], v.y, h[j][i + 1]);
                 }
             }
         }

@@ -6,7 +6,8 @@ import torch
 import gated_delta_rule_56_gb300 as kda
 from gated_delta_rule_56_gb300 import layers
 
-from layers_cases import DEV, cu_of, gen
+import layers_ref as ref
+from layers_cases import DEV, ULP32, close, cu_of, d64, gen, near
 
 pytestmark = pytest.mark.gpu
 
@@ -94,3 +95,54 @@ def test_sums_past_the_largest_fp32_are_infinite():
     dy[0, 20, 3], dy[0, 600, 3] = inf, -inf
     g = kda.conv_backward(x, w, dy, torch.zeros(8, device=DEV), activation=None)
     assert torch.isnan(g["dbias"][3]) and g["dbias"][5] == -inf
+
+
+def _growing(lengths, at, rate, n):
+    """Packed sequences whose state grows by exp(rate) a row in the sequence `at` and hardly changes in the others."""
+    r, T, D = gen(2), sum(lengths), 8
+    lo, hi = ref.spans(1, T, cu_of(lengths).cpu())[at]
+    dt = torch.full((1, T, D), 2.0 ** -10, device=DEV)
+    dt[:, lo:hi] = rate
+    return torch.zeros(1, T, D, device=DEV), dt, torch.ones(D, n, device=DEV), r(1, T, 1, n), r(1, T, 1, n), lo, hi
+
+
+# 15 rows that are not its own, then chunks of 16 rows: the second sequence has one row before a whole chunk and one behind it.
+@pytest.mark.parametrize("lengths", [[15, 18, 15], [15, 18, 400]])
+@pytest.mark.parametrize("n", [4, 24])
+def test_states_that_grow_across_a_chunk(lengths, n):
+    """exp(A sum dt) over a chunk may pass fp32's range where the state after it does not."""
+    x, dt, A, B, C, lo, hi = _growing(lengths, 1, 6.0, n)
+    cu = cu_of(lengths)
+    y, fin = kda.scan_prefill(x, dt, A, B, C, dt_softplus=False, cu_seqlens=cu)
+    assert not y.any() and not fin.any()  # zeros stay zeros
+    init = gen(3)(len(lengths), 8, n) * 2.0 ** -100
+    y, fin = kda.scan_prefill(x, dt, A, B, C, dt_softplus=False, cu_seqlens=cu, initial_state=init)
+    kda.check_status()
+    a = ref.scan(d64(x)[0, lo:hi], d64(dt)[0, lo:hi], d64(A), *(d64(t)[0, lo:hi].expand(-1, 8, -1) for t in (B, C)), None, None, False,
+                 d64(init)[1])
+    # Each row's exponent, |dt A| log2(e) = 9 at most, takes three roundings (A log2(e), the product, the instruction's argument) of 9 half
+    # steps each, and the decay and the state 6 more: rows * (3 * 9 + 6) half steps, and over a chunk the same in one exponent.
+    tol = (hi - lo) * (3 * 9 + 6) * ULP32
+    close("final_state", fin[1], a[1], tol * a[1].abs())
+    mag = ref.scan(d64(x)[0, lo:hi], d64(dt)[0, lo:hi], d64(A), *(d64(t)[0, lo:hi].abs().expand(-1, 8, -1) for t in (B, C)), None, None, False,
+                   d64(init)[1].abs())[0]
+    close("y", y[0, lo:hi], a[0], (tol + 64 * ULP32) * mag)
+
+
+def test_gradients_of_states_that_grow_across_a_chunk():
+    # Chunks of 64 rows; 2.2 a row are 2^203 over a chunk.
+    x, dt, A, B, C, lo, hi = _growing([63, 66, 127], 1, 2.2, 4)
+    cu, dy = cu_of([63, 66, 127]), torch.zeros_like(x)
+    g = kda.scan_backward(x, dt, A, B, C, dy, dt_softplus=False, cu_seqlens=cu)
+    assert all(t is None or not t.any() for t in g.values())  # zeros stay zeros
+    init, df = (gen(s)(3, 8, 4) * 2.0 ** -100 for s in (4, 5))
+    g = kda.scan_backward(x, dt, A, B, C, dy, dt_softplus=False, cu_seqlens=cu, initial_state=init, d_final_state=df)
+    kda.check_status()
+    wide = [d64(t)[0, lo:hi].expand(-1, 8, -1) for t in (B, C)]
+    a = ref.scan_backward(d64(x)[0, lo:hi], d64(dt)[0, lo:hi], d64(A), *wide, None, None, False, d64(init)[1], d64(dy)[0, lo:hi], d64(df)[1])
+    # As above with exponents of 3.2, for the states and for their gradients; 4 for sums of both signs.
+    tol = 4 * 2 * (hi - lo) * (3 * 3.2 + 6) * ULP32
+    near("d_initial_state", g["d_initial_state"][1], a["d_init"], tol)
+    for k in ("dx", "ddt"):
+        near(k, g[k][0, lo:hi], a[k], tol)
+    assert torch.isfinite(g["dA"]).all()
