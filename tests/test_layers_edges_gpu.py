@@ -272,9 +272,9 @@ def test_whole_sequences_that_fill_the_gpu(dtype, B, T, D, N, G):
     near("d_initial_state", g["d_initial_state"].view(B * D, N), w["d_init"].cpu(), tol)
 
 
-@pytest.mark.parametrize("lengths", [[256], [250, 6], [33, 100, 123], [256, 3000], [1, 3, 252, 2000], [4000]])
+@pytest.mark.parametrize("lengths", [[96], [33], [5, 80, 1], [17, 46], [256], [250, 6], [33, 100, 123], [256, 3000], [1, 3, 252, 2000], [4000]])
 def test_slow_states_are_carried_whole(lengths):
-    """States that forget little over a chunk, joined by the main kernel (up to 16 chunks) and by the walk over the chunks (more)."""
+    """States that forget little over a chunk, joined by the main kernel (few chunks) or by the walk over them (more)."""
     T, D, N, r = sum(lengths), 96, 16, gen(12)
     x, dt, B, C, dy = r(1, T, D), torch.full((1, T, D), 2.0 ** -7, device=DEV), r(1, T, 1, N), r(1, T, 1, N), r(1, T, D)
     A, s, df, cu = -torch.rand(D, N, device=DEV) / 16, r(len(lengths), D, N), r(len(lengths), D, N), cu_of(lengths)
