@@ -109,10 +109,8 @@ __device__ __forceinline__ float ex2_up_to_127(float x) {
     asm("min.NaN.f32 %0, %0, 0f42FE0000;" : "+f"(x));
     return ex2(x);
 }
-__device__ __forceinline__ float carried(float time, float A, float h, float to) {
-    const float s = ex2_up_to_127(fmaf(0.5f * time, A, 1.2e-8f));
-    return fmaf(s, s * h, to);
-}
+__device__ __forceinline__ float root_decay(float time, float A) { return ex2_up_to_127(fmaf(0.5f * time, A, 1.2e-8f)); }
+__device__ __forceinline__ float carried(float root, float h, float to) { return fmaf(root, root * h, to); }
 __device__ __forceinline__ f32x2 carried2(f32x2 time, f32x2 A, f32x2 h, f32x2 to) {
     float a, b;
     unpair(fma2(mul2(time, pair(0.5f, 0.5f)), A, pair(1.2e-8f, 1.2e-8f)), a, b);

@@ -371,7 +371,8 @@ __global__ void __launch_bounds__(kScanThreads, 2)
 }
 
 // From the chunks' end states to the states before them, one thread per (channel, state). A batch of chunks is
-// loaded before the walk over it, which is bound by the latency of those loads.
+// loaded before the walk over it, which is bound by the latency of those loads; places past the ends load the last one's again (as
+// predicated loads they came one after another: 13 us instead of 10 for the gradients' walk below, 19 chunks of 4096 channels x 16 states).
 constexpr int kCarryBatch = 16;
 __global__ void __launch_bounds__(128) scan_carry_kernel(ScanParams p, ScanPlan plan, Carries carry) {
     extern __shared__ unsigned char fresh[];  // chunk j's last sequence begins in it
@@ -386,17 +387,17 @@ __global__ void __launch_bounds__(128) scan_carry_kernel(ScanParams p, ScanPlan 
     const long long c = i / p.N;
     float before = 0.f;
     for (int j0 = 0; j0 < plan.chunks; j0 += kCarryBatch) {
-        float local[kCarryBatch], time[kCarryBatch];
+        float local[kCarryBatch], root[kCarryBatch];
 #pragma unroll
         for (int b = 0; b < kCarryBatch; ++b) {
-            const bool in = j0 + b + 1 < plan.chunks;  // nothing follows the last chunk
-            local[b] = in ? carry.state[(j0 + b) * size + i] : 0.f;
-            time[b] = in ? carry.time[(long long)(j0 + b) * p.C + c] : 0.f;
+            const int j = min(j0 + b, plan.chunks - 2);  // nothing follows the last chunk
+            local[b] = carry.state[j * size + i];
+            root[b] = root_decay(carry.time[(long long)j * p.C + c], A);
         }
 #pragma unroll
         for (int b = 0; b < kCarryBatch; ++b) {
             if (j0 + b < plan.chunks) carry.state[(j0 + b) * size + i] = before;
-            if (j0 + b + 1 < plan.chunks) before = fresh[j0 + b] ? local[b] : carried(time[b], A, before, local[b]);
+            if (j0 + b + 1 < plan.chunks) before = fresh[j0 + b] ? local[b] : carried(root[b], before, local[b]);
         }
     }
 }
@@ -415,18 +416,18 @@ __global__ void __launch_bounds__(128) scan_back_carry_kernel(ScanParams p, Scan
     const long long c = i / p.N;
     float after = 0.f;
     for (int j0 = plan.chunks - 1; j0 >= 0; j0 -= kCarryBatch) {
-        float local[kCarryBatch], time[kCarryBatch];
+        float local[kCarryBatch], root[kCarryBatch];
 #pragma unroll
         for (int b = 0; b < kCarryBatch; ++b) {
-            const bool in = j0 - b > 0;  // nothing comes before the first chunk
-            local[b] = in ? carry.state[(j0 - b) * size + i] : 0.f;
-            time[b] = in ? carry.time[(long long)(j0 - b) * p.C + c] : 0.f;
+            const int j = max(j0 - b, 0);  // nothing comes before the first chunk
+            local[b] = carry.state[j * size + i];
+            root[b] = root_decay(carry.time[(long long)j * p.C + c], A);
         }
 #pragma unroll
         for (int b = 0; b < kCarryBatch; ++b) {
             if (j0 - b < 0) break;
             carry.state[(j0 - b) * size + i] = after;
-            after = goes_on[j0 - b] ? carried(time[b], A, after, local[b]) : local[b];
+            after = goes_on[j0 - b] ? carried(root[b], after, local[b]) : local[b];
         }
     }
 }
