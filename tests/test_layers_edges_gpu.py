@@ -356,3 +356,39 @@ def test_norm_and_convolution_gradients_past_32_bits():
     w = kda.conv_backward(x[:, -tail:].contiguous(), f, dy[:, -tail:].contiguous(), initial_state=x[:, -tail - 3:-tail].contiguous())
     kda.check_status()
     assert torch.equal(g["dx"][:, -tail:], w["dx"])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N", [16, 7])
+def test_infinities_and_nan_of_a_sequence_stay_in_it(dtype, N):
+    """Between packed neighbours, over chunk borders and in windows that hold several sequences, forward and backward."""
+    lengths, D, r = [70, 3, 400, 1, 0, 129, 5, 64, 200], 40, gen(22)
+    T, cu, spans = sum(lengths), cu_of(lengths), ref.spans(1, sum(lengths), cu_of(lengths).cpu())
+    x, dt, z, dy = (r(1, T, D).to(dtype) for _ in range(4))
+    B, C, w, b = r(1, T, 1, N).to(dtype), r(1, T, 1, N).to(dtype), r(D, 4).to(dtype), r(D).to(dtype)
+    A, s, df = -torch.rand(D, N, device=DEV), r(len(lengths), D, N), r(len(lengths), D, N)
+    cs, cdf = r(len(lengths), 3, D).to(dtype), r(len(lengths), 3, D)
+
+    def outputs():
+        scan = dict(z=z, cu_seqlens=cu, initial_state=s)
+        conv = dict(bias=b, cu_seqlens=cu, initial_state=cs)
+        y, fin = kda.scan_prefill(x, dt, A, B, C, **scan)
+        g = kda.scan_backward(x, dt, A, B, C, dy, d_final_state=df, **scan)
+        cy, cfin = kda.conv_prefill(x, w, **conv)
+        c = kda.conv_backward(x, w, dy, d_final_state=cdf, **conv)
+        rows = [t[0].clone() for t in (y, g["dx"], g["ddt"], g["dz"], g["dB"], g["dC"], cy, c["dx"])]
+        return rows, [fin, g["d_initial_state"], cfin, c["d_initial_state"]]
+
+    clean = outputs()
+    hit = [2, 6]
+    for n in hit:
+        for i, t in enumerate((x, dt, z, dy, B, C)):
+            t[0, spans[n][0] + i % lengths[n]] = (float("nan"), float("inf"), float("-inf"))[i % 3]
+        for t in (s, df, cs, cdf):
+            t[n] = float("nan")
+    dirty = outputs()
+    kda.check_status()
+    for n, (lo, hi) in enumerate(spans):
+        same = [torch.equal(u[lo:hi], v[lo:hi]) for u, v in zip(clean[0], dirty[0])]
+        states = [torch.equal(u[n], v[n]) for u, v in zip(clean[1], dirty[1])]
+        assert n in hit or (all(same) and all(states)), (n, same, states)
