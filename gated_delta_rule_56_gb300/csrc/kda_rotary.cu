@@ -6,9 +6,11 @@
 // each (one 16-byte load in bf16); the sum of squares goes through the group's shuffles. The lane's cosines and
 // sines stay in registers while its warp goes over the heads of one token, so the tables are read once per
 // token and not once per head. Four heads' loads are issued together and kept as they were loaded until used: converted at
-// once they took twice the registers and the kernel 238 us where it takes 175 (32768 tokens x 64 heads of 128 in bf16: 6.1 TB/s
-// of q and k read and written, 90 % of the measured copy rate). The backward pass (8192 tokens x 40 heads): 73 us, 4.6 TB/s; its
-// two inputs, the gradient and the weights' sums leave room for 16 warps per SM.
+// once they took twice the registers and the kernel 238 us where it takes 172 (32768 tokens x 64 heads of 128 in bf16: 6.2 TB/s
+// of q and k read and written, 92 % of the measured copy rate). The 64 registers of four blocks per SM hold that but for 12 to 24 bytes; in fp32,
+// and for rows that are not 16-byte aligned, 110 to 200 bytes per thread spill (fp32: 339 us, 6.3 TB/s all the same). The backward pass (8192 tokens x 40 heads):
+// 70 us, 4.8 TB/s; its two inputs, the gradient and the weights' sums leave room for 16 warps per SM (fp32: up to 147 registers, 8 warps, 101 us,
+// 5.0 TB/s).
 #include "kda_layers.cuh"
 #include "kda_layers.h"
 
@@ -161,7 +163,8 @@ __global__ void __launch_bounds__(kWarps * 32, 4) rotary_kernel(RotaryParams p, 
 
 // Gradients: d = the output's gradient rotated back;  dw = sum d x r;  dx = r (d w - x r^2 sum(d w x) / size).
 // A warp goes over tokens with a stride; the weights' sums of a block's warps are added in a fixed
-// order and written to `part` [block][2][head], which rotary_reduce_kernel adds.
+// order and written to `part` [block][2][head], which rotary_reduce_kernel adds. Plain fp32 within a block (a thread's tokens and heads in one
+// accumulator): 2e-7 off 64 bits in the 2-norm for 8192 tokens x 32 heads, where sums in 64 bits would leave 7e-8.
 template <typename T, int LANES, bool WIDE>
 __global__ void __launch_bounds__(kWarps * 32) rotary_backward_kernel(RotaryParams p, const T *__restrict__ dq_out,
                                                                       const T *__restrict__ dk_out, float *__restrict__ dq,
@@ -342,7 +345,8 @@ struct Backward {
 };
 
 int backward_blocks(const kda_rotary_args &a, int sms) {
-    // Two blocks per SM are resident; with four times as many the weights' sums cost 8 us more on 8192 tokens x 40 heads.
+    // Two blocks per SM are resident in bf16 (one in fp32, for most heads: the others follow it); with four times as many the weights' sums
+    // cost 8 us more on 8192 tokens x 40 heads.
     const long long need = (a.rows + kWarps - 1) / kWarps, most = 2LL * (sms > 0 ? sms : 152);
     return (int)(need < most ? need : most);
 }

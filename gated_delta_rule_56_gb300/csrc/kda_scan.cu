@@ -12,7 +12,7 @@
 // a first kernel computes the end states from zeros and the sums of dt, a second one walks over the chunks to get the
 // state before each, and the main kernel runs every chunk from there. That is a second round of exponentials, and it is
 // left out where whole sequences fill the GPU.
-// Measured: one sequence of 16384 rows x 4096 channels x 16 states in bf16 with gate: 489 us (190 us the end states, 290 us
+// Measured: one sequence of 16384 rows x 4096 channels x 16 states in bf16 with gate: 482 us (190 us the end states, 290 us
 // the rows; the exponentials alone are 112 us in each). Issue slots are half used: per 32 channels and row 100 warp instructions, of which 43
 // are paired multiply-adds at 2.4 cycles each and 19 are exponentials or reciprocals at 4 cycles, so both units are busy half of the time
 // and wait for each other's results the rest. With single instead of paired multiply-adds it takes 568 us.

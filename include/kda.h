@@ -308,7 +308,8 @@ KDA_API kda_status kda_decode_step_gated(kda_dtype dtype, int N, int H, int dk, 
  * Conventions beyond those at the top: "rows" are the B * T tokens (or the T packed ones). Inputs with a
  * *_stride field may have rows further apart than dense ones (slices of a fused projection): the stride
  * is in elements between consecutive rows, uniform over the batch, 0 for dense rows. Alignment to
- * the element size is enough for them; 16-byte aligned rows take the wide loads. Outputs are dense.
+ * the element size is enough for them; 16-byte aligned rows take the wide loads. Outputs are dense. An infinity or
+ * a NaN stays in the sequences, channels, groups and heads that the formulas put it in; which of the two it is there is not specified.
  * Outputs must not overlap inputs, except states updated in place. Packed sequences and state pools as in
  * kda_prefill and kda_options (a pool's slots have the shape of one sequence's state); a cu_seqlens that is
  * not a non-decreasing list from 0 to T sets KDA_ERR_INVALID_ARG in the error word and leaves the outputs
@@ -434,11 +435,12 @@ typedef struct kda_rotary_args {
     int64_t table_rows;
 } kda_rotary_args;
 
-/* q_out [rows, q_heads, head], k_out [rows, k_heads, head], dense. */
+/* q_out [rows, q_heads, head], k_out [rows, k_heads, head], dense and 16-byte aligned. */
 KDA_API kda_status kda_qk_norm_rotary(const kda_rotary_args *args, void *q_out, void *k_out, kda_stream_t stream);
 
 /* Gradients of sum(dq_out * q_out) + sum(dk_out * k_out): dq, dk like q_out, k_out; dq_weight, dk_weight [head], given
- * exactly when the weights are (NULL otherwise); all fp32. workspace: kda_qk_norm_rotary_backward_workspace_size() bytes. */
+ * exactly when the weights are (NULL otherwise); all fp32. dq_out, dk_out, dq, dk and the workspace are 16-byte aligned; workspace:
+ * kda_qk_norm_rotary_backward_workspace_size() bytes (0, and then NULL is enough, without rows). */
 KDA_API kda_status kda_qk_norm_rotary_backward(const kda_rotary_args *args, const void *dq_out, const void *dk_out,
                                                float *dq, float *dk, float *dq_weight, float *dk_weight, void *workspace,
                                                size_t workspace_bytes, kda_stream_t stream);
