@@ -55,7 +55,7 @@ struct ScanPlan {
     bool carries;
     // Few chunks: the main kernel's blocks walk over the ones before theirs themselves, and a launch is saved. Measured in a captured
     // graph, itself against the launch: 4 chunks 13.9 us against 15.2 with 128 channels, 16.2 against 20.5 with 8192; 6 chunks 15.6 against
-    // 15.6 and 23.2 against 24.7; from 7 on it is slower (16 chunks: 23.6 against 17.0 with 128 channels, 33.5 against 23.4 with 4096).
+    // 15.6 and 23.2 against 24.7; it is slower from 7 on with 128 to 1024 channels and from 8 on with all (16 chunks: 23.6 against 17.0 with 128 channels, 33.5 against 23.4 with 4096).
     // One eager call after another pays the launch only where the host is the longer side: 16 chunks of 128 channels 49 us against 52.
     __host__ __device__ bool folded() const { return chunks <= 6; }
     __host__ __device__ long long windows() const { return (rows + 7) / 8; }  // of kScanWindow rows in a chunk
