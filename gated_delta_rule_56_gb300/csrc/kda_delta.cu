@@ -1,0 +1,346 @@
+// kda_delta.cu -- the delta rule with one decay per value head, token by token on the CUDA cores: the step of a single
+// token, prompts in fp32 and short prompts.
+//
+// Per value head and token, with a = exp(g): u = b (v - a S^T k), S <- a S + k u^T, o = a S^T q + (q.k) u, where S is the state before
+// the token: both products read the old state, so one pass over it serves them and the update follows in registers.
+//
+// Columns of the state do not meet: a warp owns 16 of them, 8 groups of lanes the rows of 16 (dk = 128) each, a lane 4 columns.
+// Row pairs sit in register pairs, so decay, update and both products are two elements per instruction. The 8 partial sums of a lane (4
+// columns, k and q) meet in 7 shuffles that leave every lane one finished sum.
+//
+// Single token: bound by HBM, the fp32 state is read once and written once (16-byte accesses, all of a lane's loads in flight together).
+// Prompts: bound by a token's latency (the sums' shuffles between two dependent passes over the registers).
+#include "kda_delta.cuh"
+#include "kda_layers.h"
+
+namespace kda {
+namespace {
+
+constexpr int kCols = 16;       // columns of a warp
+constexpr int kStage = 8;       // tokens of a stage
+constexpr int kStages = 4;
+
+__device__ __forceinline__ f32x2 dup(float a) { return pair(a, a); }
+
+// One warp's part of a state: rows [r0, r0 + R) in pairs, 4 columns.
+template <int R>
+struct Tile {
+    f32x2 s[R / 2][4];
+
+    __device__ __forceinline__ void load(const float *p, int dv) {
+#pragma unroll
+        for (int r = 0; r < R; r += 2) {
+            const float4 a = __ldcs(reinterpret_cast<const float4 *>(p + (size_t)r * dv));
+            const float4 b = __ldcs(reinterpret_cast<const float4 *>(p + (size_t)(r + 1) * dv));
+            s[r / 2][0] = pair(a.x, b.x);
+            s[r / 2][1] = pair(a.y, b.y);
+            s[r / 2][2] = pair(a.z, b.z);
+            s[r / 2][3] = pair(a.w, b.w);
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int r = 0; r < R / 2; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[r][c] = 0ull;
+    }
+    __device__ __forceinline__ void store(float *p, int dv) const {
+#pragma unroll
+        for (int r = 0; r < R; r += 2) {
+            float4 a, b;
+            unpair(s[r / 2][0], a.x, b.x);
+            unpair(s[r / 2][1], a.y, b.y);
+            unpair(s[r / 2][2], a.z, b.z);
+            unpair(s[r / 2][3], a.w, b.w);
+            __stcs(reinterpret_cast<float4 *>(p + (size_t)r * dv), a);
+            __stcs(reinterpret_cast<float4 *>(p + (size_t)(r + 1) * dv), b);
+        }
+    }
+
+    // One token: k, q the lane's rows; v the value of column (lane / 4) % 4 of the lane's four. Returns o of that column in lanes 16 to 31.
+    __device__ __forceinline__ float step(const f32x2 (&k)[R / 2], const f32x2 (&q)[R / 2], float v, float a, float b, int lane) {
+        f32x2 ks[4], qs[4], kq = 0ull;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ks[c] = qs[c] = 0ull;
+#pragma unroll
+        for (int r = 0; r < R / 2; ++r) {
+            kq = fma2(k[r], q[r], kq);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                ks[c] = fma2(k[r], s[r][c], ks[c]);
+                qs[c] = fma2(q[r], s[r][c], qs[c]);
+            }
+        }
+        float x[8], lo, hi;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            unpair(ks[c], lo, hi);
+            x[c] = lo + hi;
+            unpair(qs[c], lo, hi);
+            x[4 + c] = lo + hi;
+        }
+        unpair(kq, lo, hi);
+        float dot = lo + hi;
+#pragma unroll
+        for (int m = 4; m < 32; m *= 2) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+        // Lane group rl = lane / 4 ends with the whole sum x[rl].
+        const bool up4 = lane & 16, up2 = lane & 8, up1 = lane & 4;
+        float y[4], z[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = (up4 ? x[4 + i] : x[i]) + __shfl_xor_sync(0xffffffffu, up4 ? x[i] : x[4 + i], 16);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) z[i] = (up2 ? y[2 + i] : y[i]) + __shfl_xor_sync(0xffffffffu, up2 ? y[i] : y[2 + i], 8);
+        const float sum = (up1 ? z[1] : z[0]) + __shfl_xor_sync(0xffffffffu, up1 ? z[0] : z[1], 4);
+        float u = b * (v - a * sum);  // in lanes 0 to 15
+        u = __shfl_sync(0xffffffffu, u, lane & 15);
+        const float o = fmaf(a, sum, dot * u);
+        const f32x2 a2 = dup(a);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const f32x2 uc = dup(__shfl_sync(0xffffffffu, u, c * 4 + (lane & 3)));
+#pragma unroll
+            for (int r = 0; r < R / 2; ++r) s[r][c] = fma2(k[r], uc, mul2(a2, s[r][c]));
+        }
+        return o;
+    }
+};
+
+// R consecutive values of a row as pairs of fp32.
+template <typename T, int R, bool WIDE>
+__device__ __forceinline__ void load_pairs(const T *p, f32x2 (&x)[R / 2]) {
+    if constexpr (WIDE) {
+        constexpr int V = R * sizeof(T) >= 16 ? 16 / sizeof(T) : R;
+#pragma unroll
+        for (int i = 0; i < R; i += V) {
+            const Pack<T, V> w = load_pack<T, V>(p + i);
+#pragma unroll
+            for (int j = 0; j < V; j += 2) x[(i + j) / 2] = pair(to_float(w.e[j]), to_float(w.e[j + 1]));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; i += 2) x[i / 2] = pair(to_float(p[i]), to_float(p[i + 1]));
+    }
+}
+
+// One token of every sequence. A block: one value head of one sequence, or part of its columns.
+template <typename T, int DK, bool WIDE>
+__global__ void __launch_bounds__(256) delta_token_kernel(DeltaParams p) {
+    constexpr int R = DK / 8;
+    const int lane = threadIdx.x & 31, rl = lane >> 2;
+    const int warps = p.dv / kCols;
+    const long long w = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int slice = (int)(w % warps);
+    const long long nh = w / warps;
+    const int h = (int)(nh % p.hv);
+    const long long n = nh / p.hv;
+    if (n >= p.seqs.n_seqs) return;
+    const int c0 = slice * kCols + (lane & 3) * 4, hk = h / p.per;
+    const long long from = p.init_idx ? state_slot(p.init_idx, p.pool, (int)n, p.err) : n;
+    const long long to = p.fin_idx ? state_slot(p.fin_idx, p.pool, (int)n, p.err) : from;
+    const size_t at = ((size_t)h * DK + rl * R) * p.dv + c0, one = (size_t)p.hv * DK * p.dv;
+    Tile<R> S;
+    if (from >= 0) S.load(p.init + from * one + at, p.dv); else S.clear();
+    f32x2 k[R / 2], q[R / 2];
+    load_pairs<T, R, WIDE>(static_cast<const T *>(p.k) + n * p.ks + hk * DK + rl * R, k);
+    load_pairs<T, R, WIDE>(static_cast<const T *>(p.q) + n * p.qs + hk * DK + rl * R, q);
+    const int col = c0 + (rl & 3);
+    const float v = to_float(static_cast<const T *>(p.v)[n * p.vs + (size_t)h * p.dv + col]);
+    const float a = expf(log_decay(p.g[n * p.hv + h])), b = p.beta[n * p.hv + h];
+    const float o = S.step(k, q, v, a, b, lane);
+    if (lane >= 16) static_cast<T *>(p.o)[(n * p.hv + h) * p.dv + col] = from_float<T>(o);
+    if (to >= 0) S.store(p.fin + to * one + at, p.dv);
+}
+
+__device__ __forceinline__ void copy_async(void *to, const void *from, int bytes) {
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    if (bytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Whole sequences. A block of W warps: one value head of one sequence, 16 W of its columns. The rows come through a ring of stages of 8
+// tokens in shared memory, so a token's latency holds none of HBM's.
+template <typename T, int DK, int W>
+struct Stage {
+    T k[kStage][DK], q[kStage][DK], v[kStage][W * kCols];
+    float g[kStage], b[kStage];
+};
+
+template <typename T, int DK, int W, bool WIDE>
+__device__ __forceinline__ void fill(Stage<T, DK, W> &s, const DeltaParams &p, long long row, int m, int h, int c0) {
+    const int hk = h / p.per, tid = threadIdx.x;
+    const T *k = static_cast<const T *>(p.k) + hk * DK, *q = static_cast<const T *>(p.q) + hk * DK;
+    const T *v = static_cast<const T *>(p.v) + (size_t)h * p.dv + c0;
+    constexpr int V = WIDE ? 16 / sizeof(T) : 1, KV = DK / V, VV = W * kCols / V;
+    for (int i = tid; i < m * (2 * KV + VV); i += W * 32) {
+        const int t = i / (2 * KV + VV), j = i % (2 * KV + VV);
+        const T *from = j < KV ? k + (row + t) * p.ks + j * V : j < 2 * KV ? q + (row + t) * p.qs + (j - KV) * V
+                                                                       : v + (row + t) * p.vs + (j - 2 * KV) * V;
+        T *to = j < KV ? &s.k[t][j * V] : j < 2 * KV ? &s.q[t][(j - KV) * V] : &s.v[t][(j - 2 * KV) * V];
+        if constexpr (WIDE) copy_async(to, from, 16); else *to = *from;
+    }
+    if (tid < 2 * m) {
+        const int t = tid >> 1;
+        copy_async(tid & 1 ? &s.b[t] : &s.g[t], (tid & 1 ? p.beta : p.g) + (row + t) * p.hv + h, 4);
+    }
+}
+
+// `kept` non-null: the state before every kept_rows-th row of a sequence goes there (kept_rows a multiple of a stage).
+template <typename T, int DK, int W, bool WIDE>
+__global__ void __launch_bounds__(W * 32) delta_rows_kernel(DeltaParams p, float *kept, int kept_rows) {
+    constexpr int R = DK / 8;
+    extern __shared__ __align__(16) unsigned char raw[];
+    Stage<T, DK, W> *ring = reinterpret_cast<Stage<T, DK, W> *>(raw);
+    const int lane = threadIdx.x & 31, rl = lane >> 2, warp = threadIdx.x >> 5;
+    const int slices = p.dv / (W * kCols);
+    const int slice = blockIdx.x % slices, h = (blockIdx.x / slices) % p.hv, n = blockIdx.x / slices / p.hv;
+    const int c0 = slice * W * kCols;
+    long long begin, end;
+    if (!rows_of(p, n, begin, end)) return;
+    const long long from = p.init ? state_slot(p.init_idx, p.pool, n, p.err) : -1;
+    const size_t at = ((size_t)h * DK + rl * R) * p.dv + c0 + warp * kCols + (lane & 3) * 4, one = (size_t)p.hv * DK * p.dv;
+    Tile<R> S;
+    if (from >= 0) S.load(p.init + from * one + at, p.dv); else S.clear();
+
+    const int stages = (int)((end - begin + kStage - 1) / kStage);
+    auto tokens = [&](int i) { return (int)min((long long)kStage, end - begin - (long long)i * kStage); };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (i < stages) fill<T, DK, W, WIDE>(ring[i], p, begin + (long long)i * kStage, tokens(i), h, c0);
+        copies_commit();
+    }
+    const int col = warp * kCols + (lane & 3) * 4 + (rl & 3);
+    for (int i = 0; i < stages; ++i) {
+        copies_wait<kStages - 2>();
+        __syncthreads();  // stage i is here, and everyone is done with stage i - 1
+        const int ahead = i + kStages - 1;
+        if (ahead < stages) fill<T, DK, W, WIDE>(ring[ahead % kStages], p, begin + (long long)ahead * kStage, tokens(ahead), h, c0);
+        copies_commit();
+        if (kept && (i * kStage) % kept_rows == 0) {
+            const long long chunk = first_chunk(begin, n, kept_rows) + i * kStage / kept_rows;
+            S.store(kept + chunk * one + at, p.dv);
+        }
+        const Stage<T, DK, W> &s = ring[i % kStages];
+        const int m = tokens(i);
+        for (int t = 0; t < m; ++t) {
+            f32x2 k[R / 2], q[R / 2];
+            load_pairs<T, R, true>(&s.k[t][rl * R], k);
+            load_pairs<T, R, true>(&s.q[t][rl * R], q);
+            const float o = S.step(k, q, to_float(s.v[t][col]), expf(log_decay(s.g[t])), s.b[t], lane);
+            if (p.o && lane >= 16)
+                static_cast<T *>(p.o)[((begin + (long long)i * kStage + t) * p.hv + h) * p.dv + c0 + col] = from_float<T>(o);
+        }
+    }
+    const long long to = p.fin ? state_slot(p.fin_idx, p.pool, n, p.err) : -1;
+    if (to >= 0) S.store(p.fin + to * one + at, p.dv);
+}
+
+template <typename T, int DK, bool WIDE>
+cudaError_t launch_token(const DeltaParams &p, cudaStream_t s) {
+    const long long warps = (long long)p.seqs.n_seqs * p.hv * (p.dv / kCols);
+    const int per = warps < 4096 ? 2 : 8;  // few warps go to more SMs
+    delta_token_kernel<T, DK, WIDE><<<(unsigned)((warps + per - 1) / per), per * 32, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, int DK, int W, bool WIDE>
+cudaError_t launch_rows_with(const DeltaParams &p, float *kept, int kept_rows, cudaStream_t s) {
+    const unsigned blocks = (unsigned)((long long)p.seqs.n_seqs * p.hv * (p.dv / (W * kCols)));
+    const size_t bytes = sizeof(Stage<T, DK, W>) * kStages;
+    auto *f = &delta_rows_kernel<T, DK, W, WIDE>;
+    if (bytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e != cudaSuccess) return e;
+    }
+    f<<<blocks, W * 32, bytes, s>>>(p, kept, kept_rows);
+    return cudaGetLastError();
+}
+
+template <typename T, int DK, bool WIDE>
+cudaError_t launch_rows(const DeltaParams &p, float *kept, int kept_rows, cudaStream_t s) {
+    return launch_rows_with<T, DK, 2, WIDE>(p, kept, kept_rows, s);
+}
+
+template <typename T>
+bool wide_rows(const DeltaParams &p) {
+    auto ok = [](const void *x, long long stride) { return aligned16(x) && stride * (long long)sizeof(T) % 16 == 0; };
+    return ok(p.q, p.qs) && ok(p.k, p.ks) && ok(p.v, p.vs);
+}
+
+template <typename T, typename F>
+cudaError_t by_size(const DeltaParams &p, F f) {
+    const bool wide = wide_rows<T>(p);
+    switch (p.dk) {
+        case 32: return wide ? f.template operator()<T, 32, true>() : f.template operator()<T, 32, false>();
+        case 64: return wide ? f.template operator()<T, 64, true>() : f.template operator()<T, 64, false>();
+        case 128: return wide ? f.template operator()<T, 128, true>() : f.template operator()<T, 128, false>();
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+struct Token {
+    const DeltaParams &p;
+    cudaStream_t s;
+    template <typename T, int DK, bool WIDE>
+    cudaError_t operator()() const { return launch_token<T, DK, WIDE>(p, s); }
+};
+struct Rows {
+    const DeltaParams &p;
+    float *kept;
+    int kept_rows;
+    cudaStream_t s;
+    template <typename T, int DK, bool WIDE>
+    cudaError_t operator()() const { return launch_rows<T, DK, WIDE>(p, kept, kept_rows, s); }
+};
+
+}  // namespace
+
+DeltaParams delta_params(const kda_delta_args &a, void *o, float *final_state, unsigned *err) {
+    DeltaParams p{};
+    p.q = a.q;
+    p.k = a.k;
+    p.v = a.v;
+    p.qs = a.q_stride ? a.q_stride : (long long)a.k_heads * a.dk;
+    p.ks = a.k_stride ? a.k_stride : (long long)a.k_heads * a.dk;
+    p.vs = a.v_stride ? a.v_stride : (long long)a.v_heads * a.dv;
+    p.g = a.g;
+    p.beta = a.beta;
+    p.seqs = Seqs{a.cu_seqlens, a.cu_seqlens ? a.n_seqs : a.B, a.T, (long long)a.B * a.T};
+    p.hk = a.k_heads;
+    p.hv = a.v_heads;
+    p.per = a.v_heads / a.k_heads;
+    p.dk = a.dk;
+    p.dv = a.dv;
+    p.init = a.initial_state;
+    p.init_idx = a.initial_state_indices;
+    p.fin_idx = a.final_state_indices;
+    p.pool = a.state_pool_size;
+    p.o = o;
+    p.fin = final_state;
+    p.err = err;
+    return p;
+}
+
+cudaError_t launch_delta_rows(kda_dtype dtype, const DeltaParams &p, float *kept, int kept_rows, cudaStream_t s) {
+    const Rows f{p, kept, kept_rows, s};
+    return dtype == KDA_BF16 ? by_size<__nv_bfloat16>(p, f) : by_size<float>(p, f);
+}
+
+cudaError_t launch_delta_decode(const kda_delta_args &a, float *state, void *o, unsigned *err, cudaStream_t s) {
+    DeltaParams p = delta_params(a, o, state, err);
+    p.init = state;
+    const Token f{p, s};
+    return a.dtype == KDA_BF16 ? by_size<__nv_bfloat16>(p, f) : by_size<float>(p, f);
+}
+
+size_t delta_prefill_workspace_bytes(const kda_delta_args &, int) { return 0; }
+
+cudaError_t launch_delta_prefill(const kda_delta_args &a, void *o, float *final_state, void *, int, unsigned *err, cudaStream_t s) {
+    return launch_delta_rows(a.dtype, delta_params(a, o, final_state, err), nullptr, 0, s);
+}
+
+}  // namespace kda

@@ -169,6 +169,49 @@ kda_status check_rotary(const kda_rotary_args &a) {
     return KDA_OK;
 }
 
+kda_status check_delta(const kda_delta_args &a, bool decode, bool pools) {
+    kda_status st;
+    if ((st = check_dtype(a.dtype)) || (st = check_sequences(a, decode, pools))) return st;
+    if (a.k_heads < 0 || a.v_heads < 0) return fail(KDA_ERR_INVALID_ARG, "negative size k_heads=%d v_heads=%d", a.k_heads, a.v_heads);
+    if (a.dk <= 0 || a.dv <= 0) return fail(KDA_ERR_INVALID_ARG, "head sizes dk=%d dv=%d must be positive", a.dk, a.dv);
+    for (int d : {a.dk, a.dv})
+        if (d != 32 && d != 64 && d != 128) return fail(KDA_ERR_UNSUPPORTED, "head sizes dk=%d dv=%d: supported 32, 64, 128", a.dk, a.dv);
+    if (a.v_heads == 0) return KDA_OK;
+    if (a.k_heads == 0 || a.v_heads % a.k_heads != 0)
+        return fail(KDA_ERR_INVALID_ARG, "v_heads=%d is not a multiple of k_heads=%d", a.v_heads, a.k_heads);
+    if (a.v_heads > 65536) return fail(KDA_ERR_UNSUPPORTED, "v_heads=%d: at most 65536", a.v_heads);
+    const long long n = a.cu_seqlens ? a.n_seqs : a.B, rows = (long long)a.B * a.T;
+    if (n * a.v_heads > (1 << 28)) return fail(KDA_ERR_UNSUPPORTED, "%lld sequences of %d heads: at most 2^28 states", n, a.v_heads);
+    if (rows * a.v_heads > (1LL << 36)) return fail(KDA_ERR_UNSUPPORTED, "%lld rows of %d heads: at most 2^36 in all", rows, a.v_heads);
+    if (rows > 0 && ((st = check_rows(a.q, "q", a.dtype, a.q_stride, (long long)a.k_heads * a.dk)) ||
+                     (st = check_rows(a.k, "k", a.dtype, a.k_stride, (long long)a.k_heads * a.dk)) ||
+                     (st = check_rows(a.v, "v", a.dtype, a.v_stride, (long long)a.v_heads * a.dv)) ||
+                     (st = check_given(a.g, "g", 4)) || (st = check_given(a.beta, "beta", 4))))
+        return st;
+    return check_optional(a.initial_state, "initial_state", 16);
+}
+
+kda_status check_norm(const kda_layer_norm_args &a) {
+    kda_status st;
+    if ((st = check_dtype(a.dtype))) return st;
+    if (a.rows < 0 || a.heads < 0) return fail(KDA_ERR_INVALID_ARG, "negative size rows=%lld heads=%d", (long long)a.rows, a.heads);
+    if (a.width <= 0) return fail(KDA_ERR_INVALID_ARG, "width=%d must be positive", a.width);
+    if (a.width > 32768) return fail(KDA_ERR_UNSUPPORTED, "width=%d: at most 32768", a.width);
+    if (a.rows > 0x7fffffffLL || (a.heads && a.rows > 0x7fffffffLL / a.heads))
+        return fail(KDA_ERR_INVALID_ARG, "too many rows: rows=%lld heads=%d", (long long)a.rows, a.heads);
+    if (a.norm != 0 && a.norm != 1) return fail(KDA_ERR_INVALID_ARG, "unknown norm %d", a.norm);
+    if (a.activation != 0 && a.activation != 1) return fail(KDA_ERR_INVALID_ARG, "unknown activation %d", a.activation);
+    if (!(a.eps >= 0.f) || std::isinf(a.eps)) return fail(KDA_ERR_INVALID_ARG, "eps=%g must be finite and not negative", (double)a.eps);
+    const size_t e = esize(a.dtype);
+    if ((st = check_optional(a.weight, "weight", e)) || (st = check_optional(a.bias, "bias", e))) return st;
+    if (a.rows == 0 || a.heads == 0) return KDA_OK;
+    const long long width = (long long)a.heads * a.width;
+    if ((st = check_rows(a.x, "x", a.dtype, a.x_stride, width))) return st;
+    if (a.residual && (st = check_rows(a.residual, "residual", a.dtype, a.residual_stride, width))) return st;
+    if (a.z && (st = check_rows(a.z, "z", a.dtype, a.z_stride, width))) return st;
+    return KDA_OK;
+}
+
 // Without rows no kernel goes over them and looks at cu_seqlens: this call does.
 template <typename A>
 kda_status check_no_rows(const A &a, unsigned *err, cudaStream_t s) {
@@ -355,6 +398,117 @@ kda_status kda_qk_norm_rotary_backward(const kda_rotary_args *args, const void *
     if (!err) return no_error_word();
     return launched(launch_rotary_backward(a, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace, sms, err, as_stream(stream)),
                     "norm and rotation backward");
+}
+
+size_t kda_delta_prefill_workspace_size(const kda_delta_args *args) {
+    kda_delta_args a;
+    if (read_args(args, a, "kda_delta_args") || check_delta(a, false, true) || a.v_heads == 0) return 0;
+    return delta_prefill_workspace_bytes(a, current_sms());
+}
+
+kda_status kda_delta_prefill(const kda_delta_args *args, void *o, float *final_state, void *workspace, size_t workspace_bytes,
+                             kda_stream_t stream) {
+    kda_delta_args a;
+    kda_status st;
+    if ((st = read_args(args, a, "kda_delta_args")) || (st = check_delta(a, false, true))) return st;
+    if (a.final_state_indices && !final_state)
+        return fail(KDA_ERR_INVALID_ARG, "final_state_indices given without final_state (the pool)");
+    if ((st = check_optional(final_state, "final_state", 16))) return st;
+    if (a.v_heads == 0) return ok();
+    if ((st = check_some_sequence(a))) return st;
+    if (sequences(a) == 0 && !a.cu_seqlens) return ok();
+    if ((long long)a.B * a.T > 0 && (st = check_ptr(o, "o", true))) return st;
+    const int sms = current_sms();
+    if ((st = check_workspace(workspace, workspace_bytes, delta_prefill_workspace_bytes(a, sms)))) return st;
+    unsigned *err = device_error_word();
+    if (!err) return no_error_word();
+    if ((st = check_no_rows(a, err, as_stream(stream))) || sequences(a) == 0) return st;
+    return launched(launch_delta_prefill(a, o, final_state, workspace, sms, err, as_stream(stream)), "delta rule");
+}
+
+kda_status kda_delta_decode_step(const kda_delta_args *args, float *state, void *o, kda_stream_t stream) {
+    kda_delta_args a;
+    kda_status st;
+    if ((st = read_args(args, a, "kda_delta_args")) || (st = check_delta(a, true, true))) return st;
+    if (a.v_heads == 0 || a.B == 0) return ok();
+    if ((st = check_ptr(state, "state", true)) || (st = check_ptr(o, "o", true))) return st;
+    unsigned *err = device_error_word();
+    if (!err) return no_error_word();
+    return launched(launch_delta_decode(a, state, o, err, as_stream(stream)), "delta rule decode step");
+}
+
+size_t kda_delta_backward_workspace_size(const kda_delta_args *args) {
+    kda_delta_args a;
+    if (read_args(args, a, "kda_delta_args") || check_delta(a, false, false) || a.v_heads == 0) return 0;
+    return delta_backward_workspace_bytes(a, current_sms());
+}
+
+kda_status kda_delta_backward(const kda_delta_args *args, const kda_delta_grads *grads, void *workspace, size_t workspace_bytes,
+                              kda_stream_t stream) {
+    kda_delta_args a;
+    kda_delta_grads g;
+    kda_status st;
+    if ((st = read_args(args, a, "kda_delta_args")) || (st = read_args(grads, g, "kda_delta_grads")) ||
+        (st = check_delta(a, false, false)))
+        return st;
+    if (a.v_heads == 0) {  // no value head to sum over: dq and dk of key heads without any are zeros
+        const size_t bytes = (size_t)a.B * a.T * a.k_heads * a.dk * 4;
+        if (!bytes) return ok();
+        if ((st = check_ptr(g.dq, "dq", true)) || (st = check_ptr(g.dk, "dk", true))) return st;
+        cudaError_t e = cudaMemsetAsync(g.dq, 0, bytes, as_stream(stream));
+        if (e == cudaSuccess) e = cudaMemsetAsync(g.dk, 0, bytes, as_stream(stream));
+        return launched(e, "delta rule backward");
+    }
+    if ((long long)a.B * a.T > 0 &&
+        ((st = check_ptr(g.d_o, "d_o", true)) || (st = check_ptr(g.dq, "dq", true)) || (st = check_ptr(g.dk, "dk", true)) ||
+         (st = check_ptr(g.dv, "dv", true)) || (st = check_given(g.dg, "dg", 4)) || (st = check_given(g.dbeta, "dbeta", 4))))
+        return st;
+    if ((st = check_optional(g.d_final_state, "d_final_state", 16)) || (st = check_optional(g.d_initial_state, "d_initial_state", 16)))
+        return st;
+    if ((st = check_some_sequence(a))) return st;
+    const int sms = current_sms();
+    if ((st = check_workspace(workspace, workspace_bytes, delta_backward_workspace_bytes(a, sms)))) return st;
+    unsigned *err = device_error_word();
+    if (!err) return no_error_word();
+    if ((st = check_no_rows(a, err, as_stream(stream))) || sequences(a) == 0) return st;
+    return launched(launch_delta_backward(a, g, workspace, sms, err, as_stream(stream)), "delta rule backward");
+}
+
+kda_status kda_layer_norm(const kda_layer_norm_args *args, void *y, void *sum, kda_stream_t stream) {
+    kda_layer_norm_args a;
+    kda_status st;
+    if ((st = read_args(args, a, "kda_layer_norm_args")) || (st = check_norm(a))) return st;
+    if (sum && !a.residual) return fail(KDA_ERR_INVALID_ARG, "the sum is asked for without a residual");
+    if (a.rows == 0 || a.heads == 0) return ok();
+    const size_t e = esize(a.dtype);
+    if ((st = check_given(y, "y", e)) || (st = check_optional(sum, "sum", e))) return st;
+    return launched(launch_layer_norm(a, y, sum, current_sms(), as_stream(stream)), "layer norm");
+}
+
+size_t kda_layer_norm_backward_workspace_size(const kda_layer_norm_args *args) {
+    kda_layer_norm_args a;
+    if (read_args(args, a, "kda_layer_norm_args") || check_norm(a)) return 0;
+    return layer_norm_backward_workspace_bytes(a, current_sms());
+}
+
+kda_status kda_layer_norm_backward(const kda_layer_norm_args *args, const void *dy, const void *d_sum, float *dx, float *dz,
+                                   float *dweight, float *dbias, void *workspace, size_t workspace_bytes, kda_stream_t stream) {
+    kda_layer_norm_args a;
+    kda_status st;
+    if ((st = read_args(args, a, "kda_layer_norm_args")) || (st = check_norm(a))) return st;
+    if (a.residual) return fail(KDA_ERR_INVALID_ARG, "the gradients take the sum as x, and no residual");
+    const size_t e = esize(a.dtype);
+    if (a.rows > 0 && a.heads > 0) {
+        if ((st = check_given(dy, "dy", e)) || (st = check_given(dx, "dx", 4)) || (st = check_optional(d_sum, "d_sum", e))) return st;
+        if (a.z && (st = check_given(dz, "dz", 4))) return st;
+    }
+    if ((a.weight && (st = check_given(dweight, "dweight", 4))) || (a.bias && (st = check_given(dbias, "dbias", 4)))) return st;
+    if ((!a.z && dz) || (!a.weight && dweight) || (!a.bias && dbias))
+        return fail(KDA_ERR_INVALID_ARG, "a gradient is asked for an input that is not given");
+    const int sms = current_sms();
+    if ((st = check_workspace(workspace, workspace_bytes, layer_norm_backward_workspace_bytes(a, sms)))) return st;
+    return launched(launch_layer_norm_backward(a, dy, d_sum, dx, dz, dweight, dbias, workspace, sms, as_stream(stream)),
+                    "layer norm backward");
 }
 
 }  // extern "C"

@@ -1,7 +1,8 @@
 """ctypes binding of the operators around the mixer: the short causal convolution, the selective
-state space scan and the norm of q and k with the position rotation.
+state space scan, the norm of q and k with the position rotation, the delta rule with one decay per
+value head, and the layer norm with its residual and gate.
 
-As in ``_lib``: argument marshalling only. Inputs named as row inputs (x, dt, z, B, C, q, k) may be
+As in ``_lib``: argument marshalling only. Inputs named as row inputs (x, dt, z, B, C, q, k, v, residual, gate) may be
 slices of a wider projection: their innermost dimensions are dense and their rows lie at one
 uniform distance; everything else is contiguous. There is no fallback without the library.
 """
@@ -40,6 +41,17 @@ RotaryArgs = _struct("kda_rotary_args", [
     ("interleaved", _i), ("eps", ctypes.c_float), ("q", _vp), ("k", _vp), ("q_stride", _i64), ("k_stride", _i64),
     ("q_weight", _vp), ("k_weight", _vp), ("cos_table", _vp), ("sin_table", _vp), ("positions", _vp),
     ("table_rows", _i64)])
+DeltaArgs = _struct("kda_delta_args", [
+    ("dtype", _i), ("B", _i), ("T", _i), ("k_heads", _i), ("v_heads", _i), ("dk", _i), ("dv", _i), ("q", _vp), ("k", _vp),
+    ("v", _vp), ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64), ("g", _vp), ("beta", _vp), ("cu_seqlens", _vp),
+    ("n_seqs", _i), ("initial_state", _vp), ("initial_state_indices", _vp), ("final_state_indices", _vp),
+    ("state_pool_size", _i)])
+DeltaGrads = _struct("kda_delta_grads", [(n, _vp) for n in (
+    "d_o", "d_final_state", "dq", "dk", "dv", "dg", "dbeta", "d_initial_state")])
+LayerNormArgs = _struct("kda_layer_norm_args", [
+    ("dtype", _i), ("rows", _i64), ("heads", _i), ("width", _i), ("norm", _i), ("activation", _i), ("eps", ctypes.c_float),
+    ("x", _vp), ("residual", _vp), ("z", _vp), ("x_stride", _i64), ("residual_stride", _i64), ("z_stride", _i64),
+    ("weight", _vp), ("bias", _vp)])
 
 _CODES = {_i: "i", _i64: "q", _sz: "N", _vp: "P", ctypes.c_float: "f"}
 
@@ -58,6 +70,7 @@ def _packer(cls):
 
 _conv_struct, _scan_struct, _rotary_struct = _packer(ConvArgs), _packer(ScanArgs), _packer(RotaryArgs)
 _grads_struct = _packer(ScanGrads)
+_delta_struct, _delta_grads_struct, _norm_struct = _packer(DeltaArgs), _packer(DeltaGrads), _packer(LayerNormArgs)
 
 _typed = None
 
@@ -74,12 +87,19 @@ def _library():
                            ("kda_scan_decode_step", [_vp, _vp, _vp, _vp]),
                            ("kda_scan_backward", [_vp, _vp, _vp, _sz, _vp]),
                            ("kda_qk_norm_rotary", [_vp, _vp, _vp, _vp]),
-                           ("kda_qk_norm_rotary_backward", [_vp] + [_vp] * 7 + [_sz, _vp])):
+                           ("kda_qk_norm_rotary_backward", [_vp] + [_vp] * 7 + [_sz, _vp]),
+                           ("kda_delta_prefill", [_vp, _vp, _vp, _vp, _sz, _vp]),
+                           ("kda_delta_decode_step", [_vp, _vp, _vp, _vp]),
+                           ("kda_delta_backward", [_vp, _vp, _vp, _sz, _vp]),
+                           ("kda_layer_norm", [_vp, _vp, _vp, _vp]),
+                           ("kda_layer_norm_backward", [_vp] + [_vp] * 7 + [_sz, _vp])):
             f = getattr(lib, name)
             f.argtypes, f.restype = args, _i
         for name, arg in (("kda_conv_backward_workspace_size", ConvArgs), ("kda_scan_prefill_workspace_size", ScanArgs),
                           ("kda_scan_backward_workspace_size", ScanArgs),
-                          ("kda_qk_norm_rotary_backward_workspace_size", RotaryArgs)):
+                          ("kda_qk_norm_rotary_backward_workspace_size", RotaryArgs),
+                          ("kda_delta_prefill_workspace_size", DeltaArgs), ("kda_delta_backward_workspace_size", DeltaArgs),
+                          ("kda_layer_norm_backward_workspace_size", LayerNormArgs)):
             f = getattr(lib, name)
             f.argtypes, f.restype = [_vp], _sz
         _typed = lib
@@ -470,4 +490,168 @@ def qk_norm_rotary_backward(q, k, cos, sin, positions, dq_out, dk_out, q_weight=
     ws = _workspace(ws_bytes, dev)
     _call(dev, lib.kda_qk_norm_rotary_backward, a, dq_out.data_ptr(), dk_out.data_ptr(),
           *(_address(out[n]) for n in ("dq", "dk", "dq_weight", "dk_weight")), _address(ws), ws_bytes)
+    return out
+
+
+# ------------------------------------------- delta rule with one decay per value head ---
+
+
+def _delta_front(q, k, v, g, beta, lead):
+    """Checks the inputs that all calls share; returns the leading fields of their struct, the device and the shapes of o and of a state."""
+    dev = _device(q)
+    if q.dim() != lead + 2:
+        raise ValueError(f"q must have {lead + 2} dimensions")
+    shape, dtype = q.shape, q.dtype
+    if not isinstance(v, torch.Tensor) or v.dim() != lead + 2:
+        raise ValueError(f"v must be a tensor of {lead + 2} dimensions")
+    hk, dk = shape[-2:]
+    hv, dv = v.shape[-2:]
+    rows = shape[:lead]
+    o_shape = (*rows, hv, dv)
+    qs = _row_stride("q", q, dtype, shape, lead, dev)
+    ks = _row_stride("k", k, dtype, shape, lead, dev)
+    vs = _row_stride("v", v, dtype, o_shape, lead, dev)
+    _dense("g", g, torch.float32, (*rows, hv), dev)
+    _dense("beta", beta, torch.float32, (*rows, hv), dev)
+    return (_DTYPES[dtype], rows[0], rows[1] if lead == 2 else 1, hk, hv, dk, dv, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            qs, ks, vs, g.data_ptr(), beta.data_ptr()), dev, o_shape, (hv, dk, dv)
+
+
+def delta_prefill(q, k, v, g, beta, cu_seqlens=None, initial_state=None, output_final_state=True, o=None, final_state=None,
+                  initial_state_indices=None, final_state_indices=None):
+    """The delta rule with one decay per value head over whole sequences.
+
+    q, k [B, T, Hk, dk], v [B, T, Hv, dv] (bf16 or fp32; rows may be strided; dk, dv 32, 64 or 128), g (log-decay, <= 0), beta fp32
+    [B, T, Hv]. Hv is a multiple of Hk: value head h uses key head h // (Hv // Hk). Per value head
+    S_t = exp(g_t) (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T, o_t = S_t^T q_t; the rows of k are unit rows, q is not scaled. Sequences,
+    states (fp32 [N, Hv, dk, dv]) and pools as in ``prefill``. Returns (o [B, T, Hv, dv], final_state or None)."""
+    lib = _library()
+    front, dev, o_shape, one = _delta_front(q, k, v, g, beta, 2)
+    n = _sequences(cu_seqlens, o_shape[0], dev)
+    pool = _states(initial_state, final_state, initial_state_indices, final_state_indices, n, one, torch.float32, dev)
+    o = _output("o", o, q, o_shape)
+    if final_state is None and output_final_state:
+        final_state = torch.empty(n, *one, dtype=torch.float32, device=dev)
+    a = _delta_struct(*front, _address(cu_seqlens), n, _address(initial_state), _address(initial_state_indices),
+                      _address(final_state_indices), pool)
+    ws_bytes = _on_device(dev, lib.kda_delta_prefill_workspace_size, a)
+    ws = _workspace(ws_bytes, dev)
+    _call(dev, lib.kda_delta_prefill, a, o.data_ptr(), _address(final_state), _address(ws), ws_bytes)
+    return o, final_state
+
+
+def delta_decode_step(q, k, v, g, beta, state, state_indices=None, final_state_indices=None, o=None):
+    """One token of ``delta_prefill`` for N sequences: q, k [N, Hk, dk], v [N, Hv, dv], g, beta fp32 [N, Hv]; ``state`` fp32
+    [N, Hv, dk, dv] (or a pool with ``state_indices`` int32 [N], as in ``decode_step``) is updated in place. Returns o [N, Hv, dv]."""
+    lib = _library()
+    front, dev, o_shape, one = _delta_front(q, k, v, g, beta, 1)
+    n = o_shape[0]
+    pool = _decode_slots(state, state_indices, final_state_indices, n, dev)
+    _dense("state", state, torch.float32, (n if state_indices is None else pool, *one), dev)
+    o = _output("o", o, q, o_shape)
+    a = _delta_struct(*front, 0, 0, 0, _address(state_indices), _address(final_state_indices), pool)
+    _call(dev, lib.kda_delta_decode_step, a, state.data_ptr(), o.data_ptr())
+    return o
+
+
+def delta_backward(q, k, v, g, beta, d_o, cu_seqlens=None, initial_state=None, d_final_state=None, want_d_initial_state=True):
+    """Gradients of sum(d_o * o) + sum(d_final_state * final_state) through ``delta_prefill`` (no pools). d_o has o's layout and
+    dtype; d_final_state fp32 [N, Hv, dk, dv] or None. Returns a dict of fp32 tensors: dq, dk [B, T, Hk, dk] (summed over the value heads
+    of a key head), dv [B, T, Hv, dv], dg, dbeta [B, T, Hv], d_initial_state [N, Hv, dk, dv] (or None)."""
+    lib = _library()
+    front, dev, o_shape, one = _delta_front(q, k, v, g, beta, 2)
+    n = _sequences(cu_seqlens, o_shape[0], dev)
+    _dense("d_o", d_o, q.dtype, o_shape, dev)
+    _states(initial_state, None, None, None, n, one, torch.float32, dev)
+    if d_final_state is not None:
+        _dense("d_final_state", d_final_state, torch.float32, (n, *one), dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    out = dict(dq=torch.empty(q.shape, **f32), dk=torch.empty(q.shape, **f32), dv=torch.empty(o_shape, **f32),
+               dg=torch.empty(o_shape[:-1], **f32), dbeta=torch.empty(o_shape[:-1], **f32),
+               d_initial_state=torch.empty(n, *one, **f32) if want_d_initial_state else None)
+    a = _delta_struct(*front, _address(cu_seqlens), n, _address(initial_state), 0, 0, 0)
+    grads = _delta_grads_struct(d_o.data_ptr(), _address(d_final_state), *(_address(out[name]) for name in (
+        "dq", "dk", "dv", "dg", "dbeta", "d_initial_state")))
+    ws_bytes = _on_device(dev, lib.kda_delta_backward_workspace_size, a)
+    ws = _workspace(ws_bytes, dev)
+    _call(dev, lib.kda_delta_backward, a, grads, _address(ws), ws_bytes)
+    return out
+
+
+# ------------------------------------------------------------------------- layer norm ---
+
+
+def _norm_args(x, weight, bias, residual, gate, activation, norm, eps):
+    dev = _device(x)
+    if norm not in ("layer", "rms"):
+        raise ValueError(f"unknown norm {norm!r}: 'layer' or 'rms'")
+    if activation not in ("silu", "sigmoid"):
+        raise ValueError(f"unknown activation {activation!r}: 'silu' or 'sigmoid'")
+    if x.dim() == 0:
+        raise ValueError("x must have at least one dimension")
+    shape, dtype = x.shape, x.dtype
+    D = shape[-1]
+    if weight is not None:
+        _dense("weight", weight, dtype, (D,), dev)
+    if bias is not None:
+        _dense("bias", bias, dtype, (D,), dev)
+    others = [("residual", residual), ("gate", gate)]
+    # The rows of each input: all leading dimensions where they lie at one distance, else all but the last of them, which is then heads.
+    heads, lead = 1, len(shape) - 1
+    strides = None
+    if x.is_contiguous() and all(t is None or (isinstance(t, torch.Tensor) and t.is_contiguous()) for _, t in others):
+        strides = (D, D, D)
+        for name, t in others:
+            if t is not None:
+                _dense(name, t, dtype, shape, dev)
+    elif lead >= 2:
+        # Heads side by side in a row are dense, so the rows are the dimensions before them.
+        try:
+            strides = tuple(0 if t is None else _row_stride(name, t, dtype, shape, lead - 1, dev) for name, t in (("x", x), *others))
+            heads, lead = shape[-2], lead - 1
+        except ValueError:
+            strides = None
+    if strides is None:
+        strides = tuple(0 if t is None else _row_stride(name, t, dtype, shape, lead, dev) for name, t in (("x", x), *others))
+    rows = 1
+    for d in shape[:lead]:
+        rows *= d
+    return _norm_struct(_DTYPES[dtype], rows, heads, D, 1 if norm == "rms" else 0, 1 if activation == "sigmoid" else 0, eps,
+                        x.data_ptr(), _address(residual), _address(gate), *strides, _address(weight), _address(bias)), dev
+
+
+def layer_norm(x, weight=None, bias=None, residual=None, gate=None, activation="silu", norm="layer", eps=1e-6, y=None, sum_out=None):
+    """Layer norm (or RMS norm) over the last dimension, with the sum with a residual before it and a gate behind it.
+
+    s = x + residual; n = (s - mean) / sqrt(var + eps), or s / sqrt(mean(s^2) + eps) with norm "rms"; y = (n weight + bias) act(gate), act
+    "silu" or "sigmoid". x, residual, gate [..., D] (bf16 or fp32, D up to 32768; their rows may be strided: [rows, heads, D] slices of a
+    wider projection, or rows of D), weight, bias [D] or None. The norm is taken of the sum before its rounding. ``sum_out`` may be x or the
+    residual itself. Returns (y, s in x's dtype, or None without a residual), dense."""
+    lib = _library()
+    a, dev = _norm_args(x, weight, bias, residual, gate, activation, norm, eps)
+    y = _output("y", y, x, x.shape)
+    if residual is not None:
+        sum_out = _output("sum_out", sum_out, x, x.shape)
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    _call(dev, lib.kda_layer_norm, a, y.data_ptr(), _address(sum_out))
+    return y, sum_out
+
+
+def layer_norm_backward(x, weight, dy, bias=None, gate=None, activation="silu", norm="layer", eps=1e-6, d_sum=None):
+    """Gradients of sum(dy * y) + sum(d_sum * s) through ``layer_norm``; x is the sum that it returned (or its x without a residual). dy and
+    d_sum (or None) are dense, in x's dtype. Returns a dict of fp32 tensors: dx (also the residual's gradient), dweight, dbias, dgate (None
+    without the input)."""
+    lib = _library()
+    a, dev = _norm_args(x, weight, bias, None, gate, activation, norm, eps)
+    _dense("dy", dy, x.dtype, x.shape, dev)
+    if d_sum is not None:
+        _dense("d_sum", d_sum, x.dtype, x.shape, dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    out = dict(dx=torch.empty(x.shape, **f32), dweight=None if weight is None else torch.empty(x.shape[-1], **f32),
+               dbias=None if bias is None else torch.empty(x.shape[-1], **f32), dgate=None if gate is None else torch.empty(x.shape, **f32))
+    ws_bytes = _on_device(dev, lib.kda_layer_norm_backward_workspace_size, a)
+    ws = _workspace(ws_bytes, dev)
+    _call(dev, lib.kda_layer_norm_backward, a, dy.data_ptr(), _address(d_sum), out["dx"].data_ptr(), _address(out["dgate"]),
+          _address(out["dweight"]), _address(out["dbias"]), _address(ws), ws_bytes)
     return out

@@ -447,6 +447,89 @@ KDA_API kda_status kda_qk_norm_rotary_backward(const kda_rotary_args *args, cons
 KDA_API size_t kda_qk_norm_rotary_backward_workspace_size(const kda_rotary_args *args);
 
 /*
+ * Gated delta rule with one decay per value head (linear attention whose value heads share key heads). Value head h
+ * uses key head h / (v_heads / k_heads); per value head, with a = exp(g_t), b = beta_t and the state S (dk x dv, fp32):
+ *     S' = a S_{t-1};   u = b (v_t - S'^T k_t);   S_t = S' + k_t u^T;   o_t = S_t^T q_t      (no scale is applied to q)
+ * g <= 0 is the log-decay (-inf clears the state; below -128 is computed as -128, whose exponential is 0 in fp32). The rows of k are taken
+ * as unit rows (kda_qk_norm_rotary with norm 1) and b in [0, 1] (up to 2 is computed as well): with |k|^2 b > 2 the recurrence itself grows.
+ */
+typedef struct kda_delta_args {
+    size_t struct_size;
+    kda_dtype dtype;         /* of q, k, v and o */
+    int B, T;                /* decode: B sequences, T == 1 */
+    int k_heads, v_heads;    /* v_heads a multiple of k_heads, at most 65536 */
+    int dk, dv;              /* 32, 64 or 128 each */
+    const void *q, *k;       /* [B, T, k_heads, dk] */
+    const void *v;           /* [B, T, v_heads, dv] */
+    int64_t q_stride, k_stride, v_stride;
+    const float *g, *beta;   /* fp32 [B, T, v_heads] */
+    const int32_t *cu_seqlens;
+    int n_seqs;
+    const float *initial_state; /* fp32 [N, v_heads, dk, dv], a pool of such slots with indices, or NULL; not for decode */
+    const int32_t *initial_state_indices, *final_state_indices; /* as kda_conv_args */
+    int state_pool_size;
+} kda_delta_args;
+
+/* o [B, T, v_heads, dv]; final_state fp32 [N, v_heads, dk, dv] (or the pool) or NULL; may be initial_state's memory. States are 16-byte
+ * aligned. workspace: kda_delta_prefill_workspace_size() bytes (may be 0), 16-byte aligned. */
+KDA_API kda_status kda_delta_prefill(const kda_delta_args *args, void *o, float *final_state, void *workspace,
+                                     size_t workspace_bytes, kda_stream_t stream);
+KDA_API size_t kda_delta_prefill_workspace_size(const kda_delta_args *args);
+
+/* One token for each of B sequences (T == 1): state fp32 [B, v_heads, dk, dv] (or the pool) is updated in place. */
+KDA_API kda_status kda_delta_decode_step(const kda_delta_args *args, float *state, void *o, kda_stream_t stream);
+
+/* Gradients of sum(d_o * o) + sum(d_final_state * final_state), all fp32 and written in full. No state pools.
+ * workspace: kda_delta_backward_workspace_size() bytes, 16-byte aligned. */
+typedef struct kda_delta_grads {
+    size_t struct_size;
+    const void *d_o;            /* [B, T, v_heads, dv] in `dtype`, dense */
+    const float *d_final_state; /* fp32 [N, v_heads, dk, dv] or NULL (zero) */
+    float *dq, *dk;             /* [B, T, k_heads, dk]: summed over the value heads of a key head */
+    float *dv;                  /* [B, T, v_heads, dv] */
+    float *dg, *dbeta;          /* [B, T, v_heads] (dg: with respect to the log-decay) */
+    float *d_initial_state;     /* [N, v_heads, dk, dv] or NULL */
+} kda_delta_grads;
+KDA_API kda_status kda_delta_backward(const kda_delta_args *args, const kda_delta_grads *grads, void *workspace,
+                                      size_t workspace_bytes, kda_stream_t stream);
+KDA_API size_t kda_delta_backward_workspace_size(const kda_delta_args *args);
+
+/*
+ * Layer norm and RMS norm, with the sum with a residual before them and a gate behind them:
+ *     s = x + residual;   n = (s - mean(s)) / sqrt(mean((s - mean(s))^2) + eps)  (norm 0, layer)   or
+ *     n = s / sqrt(mean(s^2) + eps)  (norm 1, RMS);   y = (n weight + bias) act(z)
+ * over the last `width` values. A row of x holds `heads` of them (a mixer's output per head), with one weight and bias
+ * for all heads. The norm is taken of the sum before its rounding to `dtype`.
+ */
+typedef struct kda_layer_norm_args {
+    size_t struct_size;
+    kda_dtype dtype;         /* of x, residual, weight, bias, z, y and the sum */
+    int64_t rows;            /* at most 2^31 - 1 */
+    int heads, width;        /* width 1 to 32768; heads * rows at most 2^31 - 1 */
+    int norm;                /* 0 layer, 1 RMS */
+    int activation;          /* of the gate: 0 z sigmoid(z) (SiLU), 1 sigmoid(z) */
+    float eps;               /* >= 0, finite */
+    const void *x;           /* [rows, heads, width] */
+    const void *residual;    /* [rows, heads, width] or NULL; not for the gradients */
+    const void *z;           /* [rows, heads, width] or NULL (no gate) */
+    int64_t x_stride, residual_stride, z_stride;
+    const void *weight, *bias; /* [width] or NULL (ones, zeros) */
+} kda_layer_norm_args;
+
+/* y [rows, heads, width]; sum [rows, heads, width] or NULL: s in `dtype`, given only with a residual; both dense. `sum` may be the memory of
+ * x or of the residual, and y that of x, residual or z, where that input is dense. */
+KDA_API kda_status kda_layer_norm(const kda_layer_norm_args *args, void *y, void *sum, kda_stream_t stream);
+
+/* Gradients of sum(dy * y) + sum(d_sum * s), with x the sum that the forward pass returned (or its x without a residual): dx
+ * [rows, heads, width], which is also the residual's gradient; dz like dx; dweight, dbias [width]; given exactly when z, the weight and the
+ * bias are (NULL otherwise); all fp32, dense. dy and d_sum (or NULL) are dense, in `dtype`. workspace:
+ * kda_layer_norm_backward_workspace_size() bytes, 16-byte aligned. */
+KDA_API kda_status kda_layer_norm_backward(const kda_layer_norm_args *args, const void *dy, const void *d_sum, float *dx,
+                                           float *dz, float *dweight, float *dbias, void *workspace, size_t workspace_bytes,
+                                           kda_stream_t stream);
+KDA_API size_t kda_layer_norm_backward_workspace_size(const kda_layer_norm_args *args);
+
+/*
  * kda_check_status -- synchronise `stream`, then read and clear the device error word of the
  * current device. Returns KDA_OK, KDA_ERR_INVALID_ARG (bad cu_seqlens, a state slot past the pool
  * end or a position past the rotation tables seen by a kernel), KDA_ERR_TIMEOUT (a bounded pipeline wait gave up; that
@@ -473,7 +556,8 @@ KDA_API const char *kda_status_string(kda_status status);
 KDA_API const char *kda_last_error(void);
 
 /* Library ABI version: major * 10000 + minor * 100 + patch. Version 2 made packed calls to
- * kda_prefill_workspace_size explicit (the cu_seqlens argument); 2.1 added the operators around the mixer. */
+ * kda_prefill_workspace_size explicit (the cu_seqlens argument); 2.1 added the operators around the mixer; 2.2 the delta rule with one decay per
+ * value head and the layer norm. */
 KDA_API int kda_version(void);
 
 #ifdef __cplusplus
