@@ -11,6 +11,7 @@
 // Single token: bound by HBM, the fp32 state is read once and written once (16-byte accesses, all of a lane's loads in flight together).
 // Prompts: bound by a token's latency (the sums' shuffles between two dependent passes over the registers).
 #include "kda_delta.cuh"
+#include "kda_delta_tc.h"
 #include "kda_layers.h"
 
 namespace kda {
@@ -340,7 +341,9 @@ cudaError_t launch_delta_decode(const kda_delta_args &a, float *state, void *o, 
 size_t delta_prefill_workspace_bytes(const kda_delta_args &, int) { return 0; }
 
 cudaError_t launch_delta_prefill(const kda_delta_args &a, void *o, float *final_state, void *, int, unsigned *err, cudaStream_t s) {
-    return launch_delta_rows(a.dtype, delta_params(a, o, final_state, err), nullptr, 0, s);
+    const DeltaParams p = delta_params(a, o, final_state, err);
+    if (p.seqs.rows >= 32ll * p.seqs.n_seqs && delta_tc_supported(a.dtype, p)) return launch_delta_tc(p, s);
+    return launch_delta_rows(a.dtype, p, nullptr, 0, s);
 }
 
 }  // namespace kda
