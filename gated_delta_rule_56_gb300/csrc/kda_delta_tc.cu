@@ -15,9 +15,9 @@
 // as several bf16 values: S and R as two (their rounding, 2^-17, meets products that are smaller than the sums they go into), U with its
 // decay as three in the state's update, where its rounding would be the state's. U = R + (T - I) R adds R itself in fp32. T and P as two each.
 //
-// Roles (16 warps, one block per SM): warps 0-7 the chain (two per lane quarter, half of the columns each), 8 issues the MMAs, 9 the TMA
-// loads, 12-15 prepare the next chunk: decays, A and P from the K K^T and Q K^T accumulators (thread = TMEM lane = row), the inverse of I + A by
-// 16 x 16 blocks in fp32, T - I and P as operands. Tiles of K and Q have three stages, V, T and P two.
+// Roles (one block per SM): warps 0-15 the chain (four per lane quarter, a quarter of the rows and key channels each), 16-23 prepare the next
+// chunk: decays, A and P from the K K^T and Q K^T accumulators (thread = TMEM lane = row), the inverse of I + A by 16 x 16 blocks, T - I
+// and P as operands; 24 issues the MMAs, 25 the TMA loads. Tiles of K and Q have three stages, V, T and P two.
 //
 // Bound by the chain's latency (three dependent MMA groups and the conversions between them), not by HBM.
 #include <cudaTypedefs.h>
@@ -34,19 +34,19 @@ namespace {
 using namespace tc;
 
 constexpr int C = 64;
-constexpr int kThreads = 512;
+constexpr int kChainWarps = 16, kPrepWarps = 8, kIssuer = 24, kLoader = 25;
+constexpr int kThreads = 28 * 32, kPrep = kPrepWarps * 32;
 constexpr uint64_t kWaitNs = 1000000000ull;  // 1 s per wait
-constexpr int kPrep = 128;
 
 // TMEM columns
 constexpr uint32_t TM_S = 0;      // S^T: first bf16 values in 0..63, second in 64..127; then U with its decay, three times 32
 constexpr uint32_t TM_KS = 128;   // KS, then (T - I) R
 constexpr uint32_t TM_R = 192;    // R, then U: two times 32
-constexpr uint32_t TM_DS = 256;   // QS, then the update of the state
-constexpr uint32_t TM_PU = 384;
+constexpr uint32_t TM_SF = 256;   // S^T in fp32: scaled by a chunk's decay before the MMAs add the chunk's rows
+constexpr uint32_t TM_O = 384;    // QS, scaled, then with P U added
 constexpr uint32_t TM_KK = 448;   // [K; Q] K^T
 
-constexpr int kKqStages = 3, kVStages = 2, kTpStages = 2;
+constexpr int kKqStages = 3, kVStages = 2, kTpStages = 2, kVecs = 3;
 constexpr uint32_t kKqBytes = 32768, kVBytes = 16384, kTpBytes = 32768;
 
 struct Vec {
@@ -60,12 +60,12 @@ struct Shared {
     uint8_t tp[kTpStages][kTpBytes];  // T - I (two bf16 values), P (two)
     float A[C][C + 4];
     float Y[32][36];
-    Vec vec[kTpStages];
-    float Gh[C], Gl[C], f[C];
+    Vec vec[kVecs];
+    float a[2][C], pre[2][C], f[2][C];  // decays: of a row; within its block of 16, up to the row; from the row to the block's end
     uint64_t full_kq[kKqStages], free_kq[kKqStages], ready_kq[kKqStages];
     uint64_t full_v[kVStages], free_v[kVStages], ready_v[kVStages];
     uint64_t free_tp[kTpStages], ready_tp[kTpStages];
-    uint64_t kk, kk_free, s, ks, qs, r, u, u2, up, ds, pu, drain;
+    uint64_t kk, kk_free, s, ks, qs, r, u, u2, up, ds, pu, o_free, drain;
     uint32_t tmem;
 };
 
@@ -73,18 +73,26 @@ struct Maps {
     CUtensorMap q, k, v;
 };
 
+// a, b as hi + lo, each a pair of bf16 values: 2^-16 at most is left.
+__device__ __forceinline__ void rest_of(float a, float b, uint32_t hi, float &c, float &d) {
+    unpair(add2(pair(a, b), pair(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xffff0000u))), c, d);
+}
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    float c, d;
     hi = pack_bf16(a, b);
-    lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+    rest_of(a, b, hi, c, d);
+    lo = pack_bf16(c, d);
 }
 __device__ __forceinline__ void split3(float a, float b, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+    float c, d, e, f;
     hi = pack_bf16(a, b);
-    const float c = a - __uint_as_float(hi << 16), d = b - __uint_as_float(hi & 0xffff0000u);
+    rest_of(a, b, hi, c, d);
     mid = pack_bf16(c, d);
-    lo = pack_bf16(c - __uint_as_float(mid << 16), d - __uint_as_float(mid & 0xffff0000u));
+    rest_of(c, d, mid, e, f);
+    lo = pack_bf16(e, f);
 }
 
-__device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 // All prep threads wait, and leave together when a wait runs out.
 __device__ __forceinline__ bool prep_wait(uint64_t *bar, uint32_t parity) {
     const uint32_t bad = mbar_wait(bar, parity, kWaitNs) ? 0u : 1u;
@@ -92,7 +100,7 @@ __device__ __forceinline__ bool prep_wait(uint64_t *bar, uint32_t parity) {
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 1, 128, p;\n\t"
+        "bar.red.or.pred q, 1, 256, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(any)
         : "r"(bad)
@@ -115,27 +123,36 @@ __device__ __forceinline__ uint64_t kstep(int st, uint32_t tile) {
 
 // ------------------------------------------------------------------------ prep -----------
 
-// x[j] = D_ij x[j] (times b): decays of row i against the rows of its own and earlier blocks of 16; zero behind the diagonal.
-__device__ __forceinline__ void decay_row(float (&x)[C], const Shared &s, int i, bool q_row, float Gh, float Gl, float scale) {
-    const int bi = i >> 4;
+// x[j] = D_ij x[j] (times `scale`) for 32 columns from c0: decays of row i against the rows of its own and earlier blocks of 16; zero behind
+// the diagonal. Only products of decays, so nothing cancels and nothing overflows.
+__device__ __forceinline__ void decay_row(float (&x)[32], const float *a, const float *pre, const float *f, int i, int c0, bool q_row,
+                                          float scale) {
+    const int bi = i >> 4, in = i & 15;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        if (b < bi) {  // through the block's last row: both exponents are differences, at most 0
-            const float e = scale * expf(__fadd_rn(__fsub_rn(Gh, s.Gh[16 * b + 15]), __fsub_rn(Gl, s.Gl[16 * b + 15])));
+    for (int b = 0; b < 2; ++b) {
+        const int o = c0 + 16 * b;
+        if (o < 16 * bi) {  // row -> end of the block, the blocks between, start of this block -> row
+            float e = scale * pre[i];
+            for (int m = (o >> 4) + 1; m < bi; ++m) e *= pre[16 * m + 15];
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(&s.f[16 * b + j]);
-                x[16 * b + j] *= e * f.x;
-                x[16 * b + j + 1] *= e * f.y;
-                x[16 * b + j + 2] *= e * f.z;
-                x[16 * b + j + 3] *= e * f.w;
+                const ulonglong2 f4 = *reinterpret_cast<const ulonglong2 *>(f + o + j);
+                float *y = &x[16 * b + j];
+                unpair(mul2(pair(y[0], y[1]), mul2(both(e), f4.x)), y[0], y[1]);
+                unpair(mul2(pair(y[2], y[3]), mul2(both(e), f4.y)), y[2], y[3]);
             }
-        } else if (b == bi) {
+        } else if (o == 16 * bi) {
+            float D = scale;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int at = 16 * b + j;
-                const float D = expf(__fadd_rn(__fsub_rn(Gh, s.Gh[at]), __fsub_rn(Gl, s.Gl[at])));
-                x[at] = at < i || (q_row && at == i) ? scale * D * x[at] : 0.f;
+            for (int j = 12; j >= 0; j -= 4) {
+                const float4 a4 = *reinterpret_cast<const float4 *>(a + o + j);
+                const float av[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+                for (int m = 3; m >= 0; --m) {
+                    const int at = j + m;  // D is that of column `at` when its turn comes
+                    x[16 * b + at] = at < in || (q_row && at == in) ? D * x[16 * b + at] : 0.f;
+                    D = at <= in ? D * av[m] : D;
+                }
             }
         } else {
 #pragma unroll
@@ -144,18 +161,63 @@ __device__ __forceinline__ void decay_row(float (&x)[C], const Shared &s, int i,
     }
 }
 
-// (I + A)^-1 in place of A (strictly lower, zeros above), 128 threads: 16 x 16 blocks by substitution, then joined twice.
+// acc += A (16 x K) B (K x 8), fp32 in shared memory, one warp: tf32 MMAs over two values per operand (2^-21 of a product is left).
+__device__ __forceinline__ void two_tf32(float x, uint32_t &hi, uint32_t &lo) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+template <int K>
+__device__ __forceinline__ void warp_product(float (&acc)[4], const float *A, int as, const float *B, int bs, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    float more[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < K; k += 8) {
+        uint32_t ah[4], al[4], bh[2], bl[2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) two_tf32(A[(g + 8 * (e & 1)) * as + k + t + 4 * (e >> 1)], ah[e], al[e]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) two_tf32(B[(k + t + 4 * e) * bs + g], bh[e], bl[e]);
+        mma_tf32(acc, ah, bh);
+        mma_tf32(more, ah, bl);
+        mma_tf32(more, al, bh);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += more[e];
+}
+__device__ __forceinline__ void warp_store(float *out, int os, const float (&acc)[4], float sign, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    *reinterpret_cast<float2 *>(out + g * os + 2 * t) = make_float2(sign * acc[0], sign * acc[1]);
+    *reinterpret_cast<float2 *>(out + (g + 8) * os + 2 * t) = make_float2(sign * acc[2], sign * acc[3]);
+}
+
+// (I + A)^-1 in place of A (strictly lower; the blocks right of the diagonal ones are not read), 8 warps: 16 x 16 blocks by
+// substitution, then joined twice: the block below the diagonal is -X22 A21 X11.
 __device__ __forceinline__ void invert(Shared &s, int pt) {
+    constexpr int L = C + 4;
     const int w = pt >> 5, lane = pt & 31;
-    {
+    if (w < 4) {
         const int j = lane & 15, o = 16 * w;
         float x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float a = i == j ? 1.f : 0.f;
+        for (int i = 0; i < 16; ++i) x[i] = i == j ? 1.f : 0.f;
 #pragma unroll
-            for (int m = 0; m < i; ++m) a = fmaf(-s.A[o + i][o + m], x[m], a);
-            x[i] = a;
+        for (int m = 0; m < 16; m += 4) {  // four columns of A at a time
+            float4 own[4];
+#pragma unroll
+            for (int i = 1; i < 4; ++i) own[i] = *reinterpret_cast<const float4 *>(&s.A[o + m + i][o + m]);
+            x[m + 1] = fmaf(-own[1].x, x[m], x[m + 1]);
+            x[m + 2] = fmaf(-own[2].y, x[m + 1], fmaf(-own[2].x, x[m], x[m + 2]));
+            x[m + 3] = fmaf(-own[3].z, x[m + 2], fmaf(-own[3].y, x[m + 1], fmaf(-own[3].x, x[m], x[m + 3])));
+#pragma unroll
+            for (int i = m + 4; i < 16; ++i) {
+                const float4 a = *reinterpret_cast<const float4 *>(&s.A[o + i][o + m]);
+                x[i] = fmaf(-a.w, x[m + 3], fmaf(-a.z, x[m + 2], fmaf(-a.y, x[m + 1], fmaf(-a.x, x[m], x[i]))));
+            }
         }
         __syncwarp();
         if (lane < 16)
@@ -164,58 +226,31 @@ __device__ __forceinline__ void invert(Shared &s, int pt) {
     }
     prep_sync();
     {
-        const int o = 32 * (pt >> 6), t = pt & 63, r = t >> 2, c = (t & 3) * 4;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float a = s.A[o + 16 + r][o + j];
-            const float4 x = *reinterpret_cast<const float4 *>(&s.A[o + j][o + c]);
-            y = make_float4(fmaf(a, x.x, y.x), fmaf(a, x.y, y.y), fmaf(a, x.z, y.z), fmaf(a, x.w, y.w));
+        const int o = 32 * (w >> 1), n = 8 * (w & 1);
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        if (w < 4) {
+            warp_product<16>(acc, &s.A[o + 16][o], L, &s.A[o][o + n], L, lane);
+            warp_store(&s.Y[o >> 1][n], 36, acc, 1.f, lane);
         }
-        *reinterpret_cast<float4 *>(&s.Y[(o >> 1) + r][c]) = y;
         prep_sync();
-        y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float a = -s.A[o + 16 + r][o + 16 + j];
-            const float4 x = *reinterpret_cast<const float4 *>(&s.Y[(o >> 1) + j][c]);
-            y = make_float4(fmaf(a, x.x, y.x), fmaf(a, x.y, y.y), fmaf(a, x.z, y.z), fmaf(a, x.w, y.w));
+        if (w < 4) {
+            acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+            warp_product<16>(acc, &s.A[o + 16][o + 16], L, &s.Y[o >> 1][n], 36, lane);
+            warp_store(&s.A[o + 16][o + n], L, acc, -1.f, lane);
         }
-        *reinterpret_cast<float4 *>(&s.A[o + 16 + r][o + c]) = y;
     }
     prep_sync();
     {
-        const int r = pt >> 2, c = (pt & 3) * 8;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = 0.f;
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(half ? &s.A[32 + r][32 + j] : &s.A[32 + r][j]);
-                const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const float *line = half ? &s.Y[j + m][c] : &s.A[j + m][c];
-                    const float4 lo = *reinterpret_cast<const float4 *>(line), hi = *reinterpret_cast<const float4 *>(line + 4);
-                    y[0] = fmaf(av[m], lo.x, y[0]);
-                    y[1] = fmaf(av[m], lo.y, y[1]);
-                    y[2] = fmaf(av[m], lo.z, y[2]);
-                    y[3] = fmaf(av[m], lo.w, y[3]);
-                    y[4] = fmaf(av[m], hi.x, y[4]);
-                    y[5] = fmaf(av[m], hi.y, y[5]);
-                    y[6] = fmaf(av[m], hi.z, y[6]);
-                    y[7] = fmaf(av[m], hi.w, y[7]);
-                }
-            }
-            float *to = half ? &s.A[32 + r][c] : &s.Y[r][c];
-            const float sign = half ? -1.f : 1.f;
-            *reinterpret_cast<float4 *>(to) = make_float4(sign * y[0], sign * y[1], sign * y[2], sign * y[3]);
-            *reinterpret_cast<float4 *>(to + 4) = make_float4(sign * y[4], sign * y[5], sign * y[6], sign * y[7]);
-            prep_sync();
-        }
+        const int o = 16 * (w & 1), n = 8 * (w >> 1);
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        warp_product<32>(acc, &s.A[32 + o][0], L, &s.A[0][n], L, lane);
+        warp_store(&s.Y[o][n], 36, acc, 1.f, lane);
+        prep_sync();
+        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+        warp_product<32>(acc, &s.A[32 + o][32], L, &s.Y[0][n], 36, lane);
+        warp_store(&s.A[32 + o][n], L, acc, -1.f, lane);
     }
+    prep_sync();
 }
 
 // 8 values of row i, channels 8 chunk .. 8 chunk + 7, as two bf16 operands of 64 x 64 (128-byte swizzle).
@@ -228,21 +263,71 @@ __device__ __forceinline__ void store_operand(uint8_t *hi, uint8_t *lo, int i, i
     *reinterpret_cast<uint4 *>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+// A chunk's decays, by one warp: lane = rows lane and lane + 32. Each is the exponential of a sum of its own log-decays alone (prefix or
+// suffix sums, never differences): neighbours behind a strong decay keep their small ones.
+__device__ __forceinline__ void decays(Shared &s, int c, int lane, float g0, float g1, float b0, float b1) {
+    Vec &v = s.vec[c % kVecs];
+    g0 = log_decay(g0);
+    g1 = log_decay(g1);
+    float up[2] = {g0, g1}, down[2] = {g0, g1}, total[4];
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const float x = __shfl_up_sync(0xffffffffu, up[half], d, 16), y = __shfl_down_sync(0xffffffffu, down[half], d, 16);
+            if ((lane & 15) >= d) up[half] += x;
+            if ((lane & 15) + d < 16) down[half] += y;
+        }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) total[b] = __shfl_sync(0xffffffffu, up[b >> 1], 16 * (b & 1) + 15);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const float next = __shfl_down_sync(0xffffffffu, down[half], 1, 16), behind = (lane & 15) == 15 ? 0.f : next;
+        const int i = lane + 32 * half;
+        const bool second = lane & 16;
+        float before = half ? total[0] + total[1] : 0.f, after = half ? 0.f : total[2] + total[3];
+        if (second) before += total[2 * half]; else after += total[2 * half + 1];
+        const float E = expf(up[half] + before), b = half ? b1 : b0;
+        s.a[c & 1][i] = expf(half ? g1 : g0);
+        s.pre[c & 1][i] = expf(up[half]);
+        s.f[c & 1][i] = expf(behind);
+        v.E[i] = E;
+        v.F[i] = expf(behind + after);
+        v.b[i] = b;
+        v.be[i] = b * E;
+    }
+    if (lane == 0) v.whole = expf((total[0] + total[1]) + (total[2] + total[3]));
+}
+
 template <int DK>
 __device__ __forceinline__ bool prep(Shared &s, const DeltaParams &p, int h, long long begin, long long end, int chunks, uint32_t tmem) {
-    const int pt = threadIdx.x - (kThreads - kPrep), lane = pt & 31, w = pt >> 5;
-    const int i = pt & 63;  // this thread's row
-    const bool q_row = pt >= 64;
-    const uint32_t tq = (uint32_t)(32 * w) << 16;
+    const int pt = threadIdx.x - kChainWarps * 32, lane = pt & 31, w = pt >> 5;
+    // A warp's rows: quarter w % 4 of [K; Q], columns of half w / 4. Rows 0..31 have nothing in the second half: those two warps have time, and
+    // the first of them does the decays.
+    const int i = pt & 63, c0 = 32 * (w >> 2);
+    const bool q_row = w & 2, live = (w & 1) || w < 4;
+    const bool scalar = w == 4;
+    const uint32_t tq = (uint32_t)(32 * (w & 3)) << 16;
     const int vtiles = p.dv > 64 ? 2 : 1;
+    float g0 = 0.f, g1 = 0.f, b0 = 0.f, b1 = 0.f;
+    auto fetch = [&](int c) {
+        const long long at = (begin + (long long)c * C + lane) * p.hv + h, left = end - begin - (long long)c * C - lane;
+        g0 = left > 0 ? p.g[at] : 0.f;
+        b0 = left > 0 ? p.beta[at] : 0.f;
+        g1 = left > 32 ? p.g[at + 32 * p.hv] : 0.f;
+        b1 = left > 32 ? p.beta[at + 32 * p.hv] : 0.f;
+    };
+    if (scalar && chunks > 0) {
+        fetch(0);
+        decays(s, 0, lane, g0, g1, b0, b1);
+        if (chunks > 1) fetch(1);
+    }
+    // What the operands have right of the diagonal blocks is never written again.
+    for (int e = pt; e < kTpStages * (int)kTpBytes / 16; e += kPrep) reinterpret_cast<uint4 *>(s.tp[0])[e] = make_uint4(0u, 0u, 0u, 0u);
+    prep_sync();
     for (int c = 0; c < chunks; ++c) {
         const int ks = c % kKqStages, vs = c % kVStages, ts = c % kTpStages;
-        const long long row0 = begin + (long long)c * C;
-        const int m = (int)min((long long)C, end - row0);
-        // Both halves of the rows, for the sums.
-        float g0 = lane < m ? log_decay(p.g[(row0 + lane) * p.hv + h]) : 0.f;
-        float g1 = lane + 32 < m ? log_decay(p.g[(row0 + lane + 32) * p.hv + h]) : 0.f;
-        const float beta = i < m ? p.beta[(row0 + i) * p.hv + h] : 0.f;
+        const int m = (int)min((long long)C, end - begin - (long long)c * C);
         if (!prep_wait(&s.full_kq[ks], (uint32_t)(c / kKqStages) & 1u) || !prep_wait(&s.full_v[vs], (uint32_t)(c / kVStages) & 1u)) return false;
         if (m < C) {  // the rows behind the sequence are another one's: zeros, so that nothing of theirs meets a product
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -257,84 +342,45 @@ __device__ __forceinline__ bool prep(Shared &s, const DeltaParams &p, int h, lon
         warp_arrive(&s.ready_kq[ks]);
         warp_arrive(&s.ready_v[vs]);
         if (c >= kTpStages && !prep_wait(&s.free_tp[ts], (uint32_t)(c / kTpStages - 1) & 1u)) return false;
-        // Sums of up to 64 decays in two fp32 values, so that differences of neighbours behind strong decays stay exact (the error of a
-        // two-term sum, by D. E. Knuth's branch-free formula).
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const float x0 = __shfl_up_sync(0xffffffffu, g0, d), y0 = __shfl_up_sync(0xffffffffu, l0, d);
-            const float x1 = __shfl_up_sync(0xffffffffu, g1, d), y1 = __shfl_up_sync(0xffffffffu, l1, d);
-            if (lane >= d) {
-                float t = __fadd_rn(g0, x0), z = __fsub_rn(t, g0);
-                l0 = __fadd_rn(__fadd_rn(l0, y0), __fadd_rn(__fsub_rn(g0, __fsub_rn(t, z)), __fsub_rn(x0, z)));
-                g0 = t;
-                t = __fadd_rn(g1, x1), z = __fsub_rn(t, g1);
-                l1 = __fadd_rn(__fadd_rn(l1, y1), __fadd_rn(__fsub_rn(g1, __fsub_rn(t, z)), __fsub_rn(x1, z)));
-                g1 = t;
-            }
-        }
-        {
-            const float x = __shfl_sync(0xffffffffu, g0, 31), y = __shfl_sync(0xffffffffu, l0, 31);
-            const float t = __fadd_rn(g1, x), z = __fsub_rn(t, g1);
-            l1 = __fadd_rn(__fadd_rn(l1, y), __fadd_rn(__fsub_rn(g1, __fsub_rn(t, z)), __fsub_rn(x, z)));
-            g1 = t;
-        }
-        const float Gc = __shfl_sync(0xffffffffu, g1, 31), Lc = __shfl_sync(0xffffffffu, l1, 31);
-        const float Gh = w & 1 ? g1 : g0, Gl = w & 1 ? l1 : l0;  // of row i
-        {
-            const float eh = __shfl_sync(0xffffffffu, Gh, lane | 15), el = __shfl_sync(0xffffffffu, Gl, lane | 15);
-            if (!q_row) {
-                Vec &v = s.vec[ts];
-                const float E = expf(__fadd_rn(Gh, Gl));
-                s.Gh[i] = Gh;
-                s.Gl[i] = Gl;
-                s.f[i] = expf(__fadd_rn(__fsub_rn(eh, Gh), __fsub_rn(el, Gl)));
-                v.E[i] = E;
-                v.F[i] = expf(__fadd_rn(__fsub_rn(Gc, Gh), __fsub_rn(Lc, Gl)));
-                v.b[i] = beta;
-                v.be[i] = beta * E;
-                if (i == 0) v.whole = expf(__fadd_rn(Gc, Lc));
-            }
-        }
-        if (!prep_wait(&s.kk, (uint32_t)c & 1u)) return false;  // also: the sums are in shared memory
+        if (!prep_wait(&s.kk, (uint32_t)c & 1u)) return false;
         tc_fence_after();
-        float x[C];
-        {
-            float a[32], b[32];
-            tmem_ld32(tmem + tq + TM_KK, a);
-            tmem_ld32(tmem + tq + TM_KK + 32, b);
+        uint8_t *tp = s.tp[ts];
+        if (live) {
+            float x[32];
+            tmem_ld32(tmem + tq + TM_KK + c0, x);
             tmem_ld_wait();
             tc_fence_before();
             warp_arrive(&s.kk_free);
+            decay_row(x, s.a[c & 1], s.pre[c & 1], s.f[c & 1], i, c0, q_row, q_row ? 1.f : s.vec[c % kVecs].b[i]);
+            if (q_row) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = a[e], x[32 + e] = b[e];
-        }
-        decay_row(x, s, i, q_row, Gh, Gl, q_row ? 1.f : beta);
-        uint8_t *tp = s.tp[ts];
-        if (q_row) {
+                for (int e = 0; e < 4; ++e) store_operand(tp + 16384, tp + 24576, i, c0 / 8 + e, &x[8 * e]);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) store_operand(tp + 16384, tp + 24576, i, e, &x[8 * e]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < C; e += 4) *reinterpret_cast<float4 *>(&s.A[i][e]) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4 *>(&s.A[i][c0 + e]) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            }
+        } else if (scalar && c + 1 < chunks) {  // chunk c - 2, which used this Vec, is done: its T and P are free
+            decays(s, c + 1, lane, g0, g1, b0, b1);
+            if (c + 2 < chunks) fetch(c + 2);
         }
         prep_sync();
         invert(s, pt);
         {
-            const int r = pt >> 1, c0 = (pt & 1) * 32;
+            const int r = pt >> 2, e0 = (pt & 3) * 16;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2; ++e) {
+                const int at0 = e0 + 8 * e;
+                if (at0 > (r | 15)) continue;
                 float y[8];
 #pragma unroll
                 for (int j = 0; j < 8; j += 4) {
-                    const int at = c0 + 8 * e + j;
-                    const float4 t = *reinterpret_cast<const float4 *>(&s.A[r][at]);
-                    y[j] = at < r ? t.x : 0.f;
-                    y[j + 1] = at + 1 < r ? t.y : 0.f;
-                    y[j + 2] = at + 2 < r ? t.z : 0.f;
-                    y[j + 3] = at + 3 < r ? t.w : 0.f;
+                    const float4 t = *reinterpret_cast<const float4 *>(&s.A[r][at0 + j]);
+                    y[j] = t.x, y[j + 1] = t.y, y[j + 2] = t.z, y[j + 3] = t.w;
                 }
-                store_operand(tp, tp + 8192, r, c0 / 8 + e, y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = at0 + j < r ? y[j] : 0.f;  // T - I
+                store_operand(tp, tp + 8192, r, at0 / 8, y);
             }
         }
         fence_async_smem();
@@ -365,6 +411,7 @@ __device__ __forceinline__ bool issue(Shared &s, int chunks) {
     if (chunks > 0 && !gram(0)) return false;
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
+        if (c + 1 < chunks && !gram(c + 1)) return false;
         const uint32_t par = (uint32_t)c & 1u;
         const uint32_t kqc = kq + (uint32_t)(c % kKqStages) * kKqBytes, tpc = tp + (uint32_t)(c % kTpStages) * kTpBytes;
         const uint64_t d_k = sdesc_sw128(kqc, 16u, 1024u), d_q = sdesc_sw128(kqc + 8192u, 16u, 1024u);
@@ -377,13 +424,14 @@ __device__ __forceinline__ bool issue(Shared &s, int chunks) {
             for (int st = 0; st < DK / 16; ++st)
                 mma_bf16_tmem_a_warp(tmem + TM_KS, tmem + TM_S + 64 * e + 8 * st, d_k + kstep(st, 16384u), idesc_bf16(128, 64), e + st > 0);
         mma_commit_warp(&s.ks);
+        if (c > 0 && !warp_wait(&s.o_free, par ^ 1u)) return false;
+        tc_fence_after();
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int st = 0; st < DK / 16; ++st)
-                mma_bf16_tmem_a_warp(tmem + TM_DS, tmem + TM_S + 64 * e + 8 * st, d_q + kstep(st, 16384u), idesc_bf16(128, 64), e + st > 0);
+                mma_bf16_tmem_a_warp(tmem + TM_O, tmem + TM_S + 64 * e + 8 * st, d_q + kstep(st, 16384u), idesc_bf16(128, 64), e + st > 0);
         mma_commit_warp(&s.qs);
-        if (c + 1 < chunks && !gram(c + 1)) return false;
         if (!warp_wait(&s.ready_tp[c % kTpStages], (uint32_t)(c / kTpStages) & 1u) || !warp_wait(&s.r, par)) return false;
         tc_fence_after();
         const uint64_t d_t = sdesc_sw128(tpc, 16u, 1024u), d_p = sdesc_sw128(tpc + 16384u, 16u, 1024u);
@@ -400,8 +448,8 @@ __device__ __forceinline__ bool issue(Shared &s, int chunks) {
         for (int e = 0; e < 3; ++e)
 #pragma unroll
             for (int st = 0; st < C / 16; ++st)
-                mma_bf16_tmem_a_warp(tmem + TM_DS, tmem + TM_S + 32 * e + 8 * st, d_kn + kDescStepMN128 * st,
-                                     idesc_bf16(128, DK) | kIdescBMajorMN, e + st > 0);
+                mma_bf16_tmem_a_warp(tmem + TM_SF, tmem + TM_S + 32 * e + 8 * st, d_kn + kDescStepMN128 * st,
+                                     idesc_bf16(128, DK) | kIdescBMajorMN, 1u);
         mma_commit_warp(&s.ds);
         if (!warp_wait(&s.up, par)) return false;
         tc_fence_after();
@@ -409,8 +457,8 @@ __device__ __forceinline__ bool issue(Shared &s, int chunks) {
         for (int e = 0; e < 3; ++e)
 #pragma unroll
             for (int st = 0; st < C / 16; ++st)
-                mma_bf16_tmem_a_warp(tmem + TM_PU, tmem + TM_R + (e == 2 ? 32 : 0) + 8 * st, d_p + (e == 1 ? 512u : 0u) + kstep(st, 0u),
-                                     idesc_bf16(128, 64), e + st > 0);
+                mma_bf16_tmem_a_warp(tmem + TM_O, tmem + TM_R + (e == 2 ? 32 : 0) + 8 * st, d_p + (e == 1 ? 512u : 0u) + kstep(st, 0u),
+                                     idesc_bf16(128, 64), 1u);
         mma_commit_warp(&s.pu);
         mma_commit_warp(&s.free_tp[c % kTpStages]);
         mma_commit_warp(&s.free_kq[c % kKqStages]);
@@ -456,150 +504,182 @@ __device__ __forceinline__ bool load(Shared &s, const Maps &maps, const DeltaPar
 
 // ------------------------------------------------------------------------ chain ----------
 
-template <int DK>
-__device__ __forceinline__ void publish_state(const float (&S)[DK / 2], uint32_t at) {
+// The state's operands from its fp32 values, N of a thread.
+template <int N>
+__device__ __forceinline__ void publish_state(const float (&S)[N], uint32_t at) {
+    uint32_t hi[N / 2], lo[N / 2];
 #pragma unroll
-    for (int g = 0; g < DK / 64; ++g) {
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) split2(S[32 * g + 2 * e], S[32 * g + 2 * e + 1], hi[e], lo[e]);
-        tmem_st16(at + 16 * g, hi);
-        tmem_st16(at + 64 + 16 * g, lo);
-    }
+    for (int e = 0; e < N / 2; ++e) split2(S[2 * e], S[2 * e + 1], hi[e], lo[e]);
+    tmem_st(at, hi);
+    tmem_st(at + 64, lo);
     tmem_st_wait();
     tc_fence_before();
 }
 
+// 16 values times 16 of shared memory.
+__device__ __forceinline__ void scale16(float (&x)[16], const float *by) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+        const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(by + e);
+        unpair(mul2(pair(x[e], x[e + 1]), f.x), x[e], x[e + 1]);
+        unpair(mul2(pair(x[e + 2], x[e + 3]), f.y), x[e + 2], x[e + 3]);
+    }
+}
+
 template <int DK>
 __device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, int n, int h, long long begin, long long end, int chunks, uint32_t tmem) {
-    constexpr int H = DK / 2;  // key channels of a thread
-    const int wg = threadIdx.x >> 7, col = threadIdx.x & 127;  // half, value column
+    constexpr int H = DK / 4;  // key channels of a thread
+    const int part = threadIdx.x >> 7, col = threadIdx.x & 127;  // quarter of the rows and of the key channels; value column
+    const int t0 = 16 * part;
     const uint32_t at = tmem + ((uint32_t)(col & 96) << 16);
     const bool live = col < p.dv;
-    const size_t one = (size_t)p.hv * p.dk * p.dv, in = (size_t)h * p.dk * p.dv + (size_t)wg * H * p.dv + col;
-    const int keys = min(max(p.dk - wg * H, 0), H);  // of this half that the state has
-    const long long from = p.init ? state_slot(p.init_idx, p.pool, n, p.err) : -1;
-    float S[H];
-#pragma unroll
-    for (int e = 0; e < H; ++e) S[e] = from >= 0 && live && e < keys ? p.init[from * one + in + (size_t)e * p.dv] : 0.f;
+    const size_t one = (size_t)p.hv * p.dk * p.dv, in = (size_t)h * p.dk * p.dv + (size_t)part * H * p.dv + col;
+    const int keys = min(max(p.dk - part * H, 0), H);  // of this quarter that the state has
     // This column's place in a row of a V tile: 16-byte piece ^ (row % 8).
-    const uint32_t v_in = (uint32_t)(col >> 6) * 8192u + (uint32_t)(col & 7) * 2u, piece = (uint32_t)(col & 63) >> 3;
+    const uint32_t v_in = (uint32_t)(col >> 6) * 8192u + (uint32_t)(col & 7) * 2u + (uint32_t)t0 * 128u, piece = (uint32_t)(col & 63) >> 3;
     const bool loaded = col < (p.dv > 64 ? 128 : 64);
-    if (chunks > 0) {
-        publish_state<DK>(S, at + TM_S + wg * (H / 2));
-        warp_arrive(&s.s);
+    // Scaled by the next chunk's decay, the state goes back for the MMAs to add to.
+    auto scaled = [&](float (&S)[H], int c) -> bool {
+        if (!warp_wait(&s.ready_tp[c % kTpStages], (uint32_t)(c / kTpStages) & 1u)) return false;
+        const float whole = s.vec[c % kVecs].whole;
+#pragma unroll
+        for (int e = 0; e < H; ++e) S[e] *= whole;
+        tmem_st(at + TM_SF + part * H, S);
+        return true;
+    };
+    auto finish = [&](const float (&S)[H]) {
+        const long long to = p.fin ? state_slot(p.fin_idx, p.pool, n, p.err) : -1;
+        if (to >= 0 && live)
+#pragma unroll
+            for (int e = 0; e < H; ++e)
+                if (e < keys) p.fin[to * one + in + (size_t)e * p.dv] = S[e];
+    };
+    {
+        const long long from = p.init ? state_slot(p.init_idx, p.pool, n, p.err) : -1;
+        float S[H];
+#pragma unroll
+        for (int e = 0; e < H; ++e) S[e] = from >= 0 && live && e < keys ? p.init[from * one + in + (size_t)e * p.dv] : 0.f;
+        if (chunks > 0) {
+            publish_state(S, at + TM_S + part * (H / 2));
+            warp_arrive(&s.s);
+            if (!scaled(S, 0)) return false;
+        } else {
+            finish(S);
+        }
     }
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + (begin * p.hv + h) * p.dv + col;
-    const long long o_row = (long long)p.hv * p.dv;
+    const uint32_t o_step = (uint32_t)p.hv * p.dv * 2;  // bytes between rows of o
+    char *o = reinterpret_cast<char *>(static_cast<__nv_bfloat16 *>(p.o) + (begin * p.hv + h) * p.dv);
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
         const uint32_t par = (uint32_t)c & 1u;
-        const int vs = c % kVStages, t0 = 32 * wg;
-        const Vec &vec = s.vec[c % kTpStages];
-        float R[32], acc[32];
+        const int vs = c % kVStages;
+        const Vec &vec = s.vec[c % kVecs];  // there: the state was scaled by it
+        float R[16];
         // R = b v - b E KS
-        if (!warp_wait(&s.ready_v[vs], (uint32_t)(c / kVStages) & 1u) ||
-            !warp_wait(&s.ready_tp[c % kTpStages], (uint32_t)(c / kTpStages) & 1u))
-            return false;
-        const uint8_t *v = s.v[vs] + v_in + (size_t)t0 * 128;
+        if (!warp_wait(&s.ready_v[vs], (uint32_t)(c / kVStages) & 1u)) return false;
+        const uint8_t *v = s.v[vs] + v_in;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
+        for (int e = 0; e < 16; ++e) {
             const uint32_t x = loaded ? *reinterpret_cast<const uint16_t *>(v + e * 128 + ((piece ^ (uint32_t)(e & 7)) << 4)) : 0u;
-            R[e] = vec.b[t0 + e] * __uint_as_float(x << 16);
+            R[e] = __uint_as_float(x << 16);
         }
         warp_arrive(&s.free_v[vs]);
+        scale16(R, vec.b + t0);
         if (!warp_wait(&s.ks, par)) return false;
         tc_fence_after();
-        tmem_ld32(at + TM_KS + t0, acc);
-        tmem_ld_wait();
         {
-            uint32_t hi[16], lo[16];
+            float x[16];
+            tmem_ld(at + TM_KS + t0, x);
+            tmem_ld_wait();
+            scale16(x, vec.be + t0);
+            uint32_t hi[8], lo[8];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                R[e] = fmaf(-vec.be[t0 + e], acc[e], R[e]);
-                R[e + 1] = fmaf(-vec.be[t0 + e + 1], acc[e + 1], R[e + 1]);
+            for (int e = 0; e < 16; e += 2) {
+                R[e] -= x[e];
+                R[e + 1] -= x[e + 1];
                 split2(R[e], R[e + 1], hi[e / 2], lo[e / 2]);
             }
-            tmem_st16(at + TM_R + 16 * wg, hi);
-            tmem_st16(at + TM_R + 32 + 16 * wg, lo);
+            tmem_st(at + TM_R + 8 * part, hi);
+            tmem_st(at + TM_R + 32 + 8 * part, lo);
             tmem_st_wait();
             tc_fence_before();
             warp_arrive(&s.r);
         }
-        // Beside (T - I) R: the reading of the state
+        // Beside (T - I) R: the reading of the state, with its decay
         if (!warp_wait(&s.qs, par)) return false;
         tc_fence_after();
-        tmem_ld32(at + TM_DS + t0, acc);
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 32; ++e) acc[e] *= vec.E[t0 + e];
+        {
+            float x[16];
+            tmem_ld(at + TM_O + t0, x);
+            tmem_ld_wait();
+            scale16(x, vec.E + t0);
+            tmem_st(at + TM_O + t0, x);
+        }
         if (!warp_wait(&s.u, par)) return false;
         tc_fence_after();
         {
-            float x[32];
-            tmem_ld32(at + TM_KS + t0, x);
+            float x[16];
+            tmem_ld(at + TM_KS + t0, x);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) R[e] += x[e];  // U
-            uint32_t hi[16], mid[16], lo[16];
+            for (int e = 0; e < 16; ++e) x[e] = R[e] += x[e];  // U
+            scale16(x, vec.F + t0);
+            uint32_t hi[8], lo[8];
+            {
+                uint32_t mid[8];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2)
-                split3(vec.F[t0 + e] * R[e], vec.F[t0 + e + 1] * R[e + 1], hi[e / 2], mid[e / 2], lo[e / 2]);
-            tmem_st16(at + TM_S + 16 * wg, hi);
-            tmem_st16(at + TM_S + 32 + 16 * wg, mid);
-            tmem_st16(at + TM_S + 64 + 16 * wg, lo);
+                for (int e = 0; e < 8; ++e) split3(x[2 * e], x[2 * e + 1], hi[e], mid[e], lo[e]);
+                tmem_st(at + TM_S + 8 * part, hi);
+                tmem_st(at + TM_S + 32 + 8 * part, mid);
+                tmem_st(at + TM_S + 64 + 8 * part, lo);
+            }
             tmem_st_wait();
             tc_fence_before();
             warp_arrive(&s.u2);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) split2(R[e], R[e + 1], hi[e / 2], lo[e / 2]);
-            tmem_st16(at + TM_R + 16 * wg, hi);
-            tmem_st16(at + TM_R + 32 + 16 * wg, lo);
+            for (int e = 0; e < 8; ++e) split2(R[2 * e], R[2 * e + 1], hi[e], lo[e]);
+            tmem_st(at + TM_R + 8 * part, hi);
+            tmem_st(at + TM_R + 32 + 8 * part, lo);
+            tmem_st_wait();
+            tc_fence_before();
+            warp_arrive(&s.up);
         }
-        const float whole = vec.whole;
-        tmem_st_wait();
-        tc_fence_before();
-        warp_arrive(&s.up);
         if (!warp_wait(&s.ds, par)) return false;
         tc_fence_after();
-#pragma unroll
-        for (int g = 0; g < H / 32; ++g) {
-            float x[32];
-            tmem_ld32(at + TM_DS + wg * H + 32 * g, x);
+        {
+            float S[H];
+            tmem_ld(at + TM_SF + part * H, S);
             tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) S[32 * g + e] = fmaf(whole, S[32 * g + e], x[e]);
-        }
-        if (c + 1 < chunks) {
-            publish_state<DK>(S, at + TM_S + wg * (H / 2));
-            warp_arrive(&s.s);
+            if (c + 1 < chunks) {
+                publish_state(S, at + TM_S + part * (H / 2));
+                warp_arrive(&s.s);
+                if (!scaled(S, c + 1)) return false;
+            } else {
+                finish(S);
+            }
         }
         // Beside the next chunk's KS: the outputs
         if (!warp_wait(&s.pu, par)) return false;
         tc_fence_after();
         {
-            float x[32];
-            tmem_ld32(at + TM_PU + t0, x);
+            float x[16];
+            tmem_ld(at + TM_O + t0, x);
             tmem_ld_wait();
-            const int m = (int)min((long long)32, end - (begin + (long long)c * C + t0));
-            __nv_bfloat16 *to = o + ((long long)c * C + t0) * o_row;
-            if (live) {
-                if (m == 32) {
+            tc_fence_before();
+            warp_arrive(&s.o_free);
+            const int m = (int)min((long long)16, end - (begin + (long long)c * C + t0));
+            char *to = o + (size_t)((long long)c * C + t0) * o_step;
+            uint32_t off = (uint32_t)col * 2u;
+            if (live)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) to[e * o_row] = __float2bfloat16_rn(acc[e] + x[e]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (e < m) to[e * o_row] = __float2bfloat16_rn(acc[e] + x[e]);
+                for (int e = 0; e < 16; e += 2) {
+                    const uint32_t two = pack_bf16(x[e], x[e + 1]);
+                    if (e < m) *reinterpret_cast<uint16_t *>(to + off) = (uint16_t)two;
+                    if (e + 1 < m) *reinterpret_cast<uint16_t *>(to + (off + o_step)) = (uint16_t)(two >> 16);
+                    off += 2u * o_step;
                 }
-            }
         }
     }
-    const long long to = p.fin ? state_slot(p.fin_idx, p.pool, n, p.err) : -1;
-    if (to >= 0 && live)
-#pragma unroll
-        for (int e = 0; e < H; ++e)
-            if (e < keys) p.fin[to * one + in + (size_t)e * p.dv] = S[e];
     return true;
 }
 
@@ -620,19 +700,19 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_kernel(const __grid_cons
         for (int i = 0; i < kKqStages; ++i) {
             mbar_init(&s.full_kq[i], 1);
             mbar_init(&s.free_kq[i], 1);
-            mbar_init(&s.ready_kq[i], 4);
+            mbar_init(&s.ready_kq[i], kPrepWarps);
         }
         for (int i = 0; i < kVStages; ++i) {
             mbar_init(&s.full_v[i], 1);
-            mbar_init(&s.free_v[i], 8);
-            mbar_init(&s.ready_v[i], 4);
+            mbar_init(&s.free_v[i], kChainWarps);
+            mbar_init(&s.ready_v[i], kPrepWarps);
         }
         for (int i = 0; i < kTpStages; ++i) {
             mbar_init(&s.free_tp[i], 1);
-            mbar_init(&s.ready_tp[i], 4);
+            mbar_init(&s.ready_tp[i], kPrepWarps);
         }
-        mbar_init(&s.kk_free, 4);
-        for (uint64_t *b : {&s.s, &s.r, &s.u2, &s.up}) mbar_init(b, 8);
+        mbar_init(&s.kk_free, 6);  // the warps that have rows there
+        for (uint64_t *b : {&s.s, &s.r, &s.u2, &s.up, &s.o_free}) mbar_init(b, kChainWarps);
         for (uint64_t *b : {&s.kk, &s.ks, &s.qs, &s.u, &s.ds, &s.pu, &s.drain}) mbar_init(b, 1);
         fence_mbar_init();
     }
@@ -646,26 +726,26 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     bool ok = true;
-    // 2 x 128 x 176 + 128 x 40 + 128 x 120 = 512 x 128 registers, what the block was launched with.
-    if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    // The block was launched with 896 x 72 registers: 512 x 80 + 256 x 72 + 128 x 40.
+    if (warp < kChainWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
         ok = chain<DK>(s, p, n, h, begin, end, chunks, tmem);
-    } else if (warp < 12) {
+    } else if (warp < kChainWarps + kPrepWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        ok = prep<DK>(s, p, h, begin, end, chunks, tmem);
+    } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 8) {
+        if (warp == kIssuer) {
             ok = issue<DK>(s, chunks);
             if (!ok) {  // nothing may be in flight at the end
                 mma_commit_warp(&s.drain);
                 (void)mbar_wait(&s.drain, 0, kWaitNs);
             }
             __syncwarp();
-        } else if (warp == 9) {
+        } else if (warp == kLoader) {
             ok = load<DK>(s, maps, p, h, begin, chunks);
             __syncwarp();
         }
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-        ok = prep<DK>(s, p, h, begin, end, chunks, tmem);
     }
     if (!ok) atomicOr(p.err, kErrTimeout);
     tc_fence_before();
