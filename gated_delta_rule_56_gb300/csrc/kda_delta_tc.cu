@@ -17,7 +17,7 @@
 //
 // Roles (one block per SM): warps 0-15 the chain (four per lane quarter, a quarter of the rows and key channels each), 16-23 prepare the next
 // chunk: decays, A and P from the K K^T and Q K^T accumulators (thread = TMEM lane = row), the inverse of I + A by 16 x 16 blocks, T - I
-// and P as operands; 24 issues the MMAs, 25 the TMA loads. Tiles of K and Q have three stages, V, T and P two.
+// and P as operands; 24 issues the MMAs, 25 the TMA loads, 26 makes the decays. Tiles of K and Q have three stages, V, T and P two.
 //
 // Bound by the chain's latency (three dependent MMA groups and the conversions between them), not by HBM.
 #include <cudaTypedefs.h>
@@ -34,7 +34,7 @@ namespace {
 using namespace tc;
 
 constexpr int C = 64;
-constexpr int kChainWarps = 16, kPrepWarps = 8, kIssuer = 24, kLoader = 25;
+constexpr int kChainWarps = 16, kPrepWarps = 8, kIssuer = 24, kLoader = 25, kDecays = 26;
 constexpr int kThreads = 28 * 32, kPrep = kPrepWarps * 32;
 constexpr uint64_t kWaitNs = 1000000000ull;  // 1 s per wait
 
@@ -65,6 +65,7 @@ struct Shared {
     uint64_t full_kq[kKqStages], free_kq[kKqStages], ready_kq[kKqStages];
     uint64_t full_v[kVStages], free_v[kVStages], ready_v[kVStages];
     uint64_t free_tp[kTpStages], ready_tp[kTpStages];
+    uint64_t free_vec[kVecs], ready_decays[2];
     uint64_t kk, kk_free, s, ks, qs, r, u, u2, up, ds, pu, o_free, drain;
     uint32_t tmem;
 };
@@ -93,9 +94,9 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t &hi, uint32_t 
 }
 
 __device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-// All prep threads wait, and leave together when a wait runs out.
-__device__ __forceinline__ bool prep_wait(uint64_t *bar, uint32_t parity) {
-    const uint32_t bad = mbar_wait(bar, parity, kWaitNs) ? 0u : 1u;
+// prep_sync; true if `ok` in all of them, so that they leave together when a wait runs out.
+__device__ __forceinline__ bool prep_all(bool ok) {
+    const uint32_t bad = ok ? 0u : 1u;
     uint32_t any;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
@@ -174,7 +175,7 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
 template <int K>
 __device__ __forceinline__ void warp_product(float (&acc)[4], const float *A, int as, const float *B, int bs, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    float more[4] = {0.f, 0.f, 0.f, 0.f};
+    float more[2][4] = {};  // three chains of MMAs
 #pragma unroll
     for (int k = 0; k < K; k += 8) {
         uint32_t ah[4], al[4], bh[2], bl[2];
@@ -183,11 +184,11 @@ __device__ __forceinline__ void warp_product(float (&acc)[4], const float *A, in
 #pragma unroll
         for (int e = 0; e < 2; ++e) two_tf32(B[(k + t + 4 * e) * bs + g], bh[e], bl[e]);
         mma_tf32(acc, ah, bh);
-        mma_tf32(more, ah, bl);
-        mma_tf32(more, al, bh);
+        mma_tf32(more[0], ah, bl);
+        mma_tf32(more[1], al, bh);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] += more[e];
+    for (int e = 0; e < 4; ++e) acc[e] += more[0][e] + more[1][e];
 }
 __device__ __forceinline__ void warp_store(float *out, int os, const float (&acc)[4], float sign, int lane) {
     const int g = lane >> 2, t = lane & 3;
@@ -263,73 +264,74 @@ __device__ __forceinline__ void store_operand(uint8_t *hi, uint8_t *lo, int i, i
     *reinterpret_cast<uint4 *>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// A chunk's decays, by one warp: lane = rows lane and lane + 32. Each is the exponential of a sum of its own log-decays alone (prefix or
+// The chunks' decays, by one warp: lane = rows lane and lane + 32. Each is the exponential of a sum of its own log-decays alone (prefix or
 // suffix sums, never differences): neighbours behind a strong decay keep their small ones.
-__device__ __forceinline__ void decays(Shared &s, int c, int lane, float g0, float g1, float b0, float b1) {
-    Vec &v = s.vec[c % kVecs];
-    g0 = log_decay(g0);
-    g1 = log_decay(g1);
-    float up[2] = {g0, g1}, down[2] = {g0, g1}, total[4];
-#pragma unroll
-    for (int d = 1; d < 16; d *= 2)
+__device__ __forceinline__ bool decays(Shared &s, const DeltaParams &p, int h, long long begin, long long end, int chunks) {
+    const int lane = threadIdx.x & 31;
+    const bool second = lane & 16, last = (lane & 15) == 15;
+    const float *g = p.g + (begin + lane) * p.hv + h, *beta = p.beta + (begin + lane) * p.hv + h;
+    const long long half_rows = 32ll * p.hv;
+    for (int c = 0; c < chunks; ++c) {
+        const long long left = end - begin - (long long)c * C - lane;
+        float up[2], down[2], total[4], b[2], own[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const float x = __shfl_up_sync(0xffffffffu, up[half], d, 16), y = __shfl_down_sync(0xffffffffu, down[half], d, 16);
-            if ((lane & 15) >= d) up[half] += x;
-            if ((lane & 15) + d < 16) down[half] += y;
+            own[half] = left > 32 * half ? log_decay(g[half * half_rows]) : 0.f;
+            b[half] = left > 32 * half ? beta[half * half_rows] : 0.f;
+            up[half] = down[half] = own[half];
         }
+        g += 2 * half_rows;
+        beta += 2 * half_rows;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) total[b] = __shfl_sync(0xffffffffu, up[b >> 1], 16 * (b & 1) + 15);
+        for (int d = 1; d < 16; d *= 2)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const float next = __shfl_down_sync(0xffffffffu, down[half], 1, 16), behind = (lane & 15) == 15 ? 0.f : next;
-        const int i = lane + 32 * half;
-        const bool second = lane & 16;
-        float before = half ? total[0] + total[1] : 0.f, after = half ? 0.f : total[2] + total[3];
-        if (second) before += total[2 * half]; else after += total[2 * half + 1];
-        const float E = expf(up[half] + before), b = half ? b1 : b0;
-        s.a[c & 1][i] = expf(half ? g1 : g0);
-        s.pre[c & 1][i] = expf(up[half]);
-        s.f[c & 1][i] = expf(behind);
-        v.E[i] = E;
-        v.F[i] = expf(behind + after);
-        v.b[i] = b;
-        v.be[i] = b * E;
+            for (int half = 0; half < 2; ++half) {
+                const float x = __shfl_up_sync(0xffffffffu, up[half], d, 16), y = __shfl_down_sync(0xffffffffu, down[half], d, 16);
+                if ((lane & 15) >= d) up[half] += x;
+                if ((lane & 15) + d < 16) down[half] += y;
+            }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) total[e] = __shfl_sync(0xffffffffu, up[e >> 1], 16 * (e & 1) + 15);
+        if (c >= kVecs && !warp_wait(&s.free_vec[c % kVecs], (uint32_t)(c / kVecs - 1) & 1u)) return false;
+        if (c >= 2 && !warp_wait(&s.ready_tp[c & 1], (uint32_t)(c / 2 - 1) & 1u)) return false;  // chunk c - 2 is prepared
+        Vec &v = s.vec[c % kVecs];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const float next = __shfl_down_sync(0xffffffffu, down[half], 1, 16), behind = last ? 0.f : next;
+            const int i = lane + 32 * half;
+            float before = half ? total[0] + total[1] : 0.f, after = half ? 0.f : total[2] + total[3];
+            if (second) before += total[2 * half]; else after += total[2 * half + 1];
+            const float E = expf(up[half] + before);
+            s.a[c & 1][i] = expf(own[half]);
+            s.pre[c & 1][i] = expf(up[half]);
+            s.f[c & 1][i] = expf(behind);
+            v.E[i] = E;
+            v.F[i] = expf(behind + after);
+            v.b[i] = b[half];
+            v.be[i] = b[half] * E;
+        }
+        if (lane == 0) v.whole = expf((total[0] + total[1]) + (total[2] + total[3]));
+        warp_arrive(&s.ready_decays[c & 1]);
     }
-    if (lane == 0) v.whole = expf((total[0] + total[1]) + (total[2] + total[3]));
+    return true;
 }
 
 template <int DK>
 __device__ __forceinline__ bool prep(Shared &s, const DeltaParams &p, int h, long long begin, long long end, int chunks, uint32_t tmem) {
     const int pt = threadIdx.x - kChainWarps * 32, lane = pt & 31, w = pt >> 5;
-    // A warp's rows: quarter w % 4 of [K; Q], columns of half w / 4. Rows 0..31 have nothing in the second half: those two warps have time, and
-    // the first of them does the decays.
+    // A warp's rows: quarter w % 4 of [K; Q], columns of half w / 4. Rows 0..31 have nothing in the second half.
     const int i = pt & 63, c0 = 32 * (w >> 2);
     const bool q_row = w & 2, live = (w & 1) || w < 4;
-    const bool scalar = w == 4;
     const uint32_t tq = (uint32_t)(32 * (w & 3)) << 16;
     const int vtiles = p.dv > 64 ? 2 : 1;
-    float g0 = 0.f, g1 = 0.f, b0 = 0.f, b1 = 0.f;
-    auto fetch = [&](int c) {
-        const long long at = (begin + (long long)c * C + lane) * p.hv + h, left = end - begin - (long long)c * C - lane;
-        g0 = left > 0 ? p.g[at] : 0.f;
-        b0 = left > 0 ? p.beta[at] : 0.f;
-        g1 = left > 32 ? p.g[at + 32 * p.hv] : 0.f;
-        b1 = left > 32 ? p.beta[at + 32 * p.hv] : 0.f;
-    };
-    if (scalar && chunks > 0) {
-        fetch(0);
-        decays(s, 0, lane, g0, g1, b0, b1);
-        if (chunks > 1) fetch(1);
-    }
     // What the operands have right of the diagonal blocks is never written again.
     for (int e = pt; e < kTpStages * (int)kTpBytes / 16; e += kPrep) reinterpret_cast<uint4 *>(s.tp[0])[e] = make_uint4(0u, 0u, 0u, 0u);
     prep_sync();
     for (int c = 0; c < chunks; ++c) {
         const int ks = c % kKqStages, vs = c % kVStages, ts = c % kTpStages;
         const int m = (int)min((long long)C, end - begin - (long long)c * C);
-        if (!prep_wait(&s.full_kq[ks], (uint32_t)(c / kKqStages) & 1u) || !prep_wait(&s.full_v[vs], (uint32_t)(c / kVStages) & 1u)) return false;
-        if (m < C) {  // the rows behind the sequence are another one's: zeros, so that nothing of theirs meets a product
+        bool ok = mbar_wait(&s.full_kq[ks], (uint32_t)(c / kKqStages) & 1u, kWaitNs) && mbar_wait(&s.full_v[vs], (uint32_t)(c / kVStages) & 1u, kWaitNs);
+        if (ok && m < C) {  // the rows behind the sequence are another one's: zeros, so that nothing of theirs meets a product
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
             for (int e = pt; e < (C - m) * 8; e += kPrep) {
                 const uint32_t at = (uint32_t)m * 128u + (uint32_t)e * 16u;
@@ -341,8 +343,9 @@ __device__ __forceinline__ bool prep(Shared &s, const DeltaParams &p, int h, lon
         }
         warp_arrive(&s.ready_kq[ks]);
         warp_arrive(&s.ready_v[vs]);
-        if (c >= kTpStages && !prep_wait(&s.free_tp[ts], (uint32_t)(c / kTpStages - 1) & 1u)) return false;
-        if (!prep_wait(&s.kk, (uint32_t)c & 1u)) return false;
+        if (c >= kTpStages) ok = ok && mbar_wait(&s.free_tp[ts], (uint32_t)(c / kTpStages - 1) & 1u, kWaitNs);
+        if (!prep_all(ok && mbar_wait(&s.ready_decays[c & 1], (uint32_t)(c >> 1) & 1u, kWaitNs) && mbar_wait(&s.kk, (uint32_t)c & 1u, kWaitNs)))
+            return false;
         tc_fence_after();
         uint8_t *tp = s.tp[ts];
         if (live) {
@@ -360,9 +363,6 @@ __device__ __forceinline__ bool prep(Shared &s, const DeltaParams &p, int h, lon
                 for (int e = 0; e < 32; e += 4)
                     *reinterpret_cast<float4 *>(&s.A[i][c0 + e]) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
             }
-        } else if (scalar && c + 1 < chunks) {  // chunk c - 2, which used this Vec, is done: its T and P are free
-            decays(s, c + 1, lane, g0, g1, b0, b1);
-            if (c + 2 < chunks) fetch(c + 2);
         }
         prep_sync();
         invert(s, pt);
@@ -384,8 +384,7 @@ __device__ __forceinline__ bool prep(Shared &s, const DeltaParams &p, int h, lon
             }
         }
         fence_async_smem();
-        warp_arrive(&s.ready_tp[ts]);
-        prep_sync();  // A is read out before the next chunk's
+        warp_arrive(&s.ready_tp[ts]);  // A is read out: the next chunk's comes behind another prep_all
     }
     return true;
 }
@@ -462,6 +461,7 @@ __device__ __forceinline__ bool issue(Shared &s, int chunks) {
         mma_commit_warp(&s.pu);
         mma_commit_warp(&s.free_tp[c % kTpStages]);
         mma_commit_warp(&s.free_kq[c % kKqStages]);
+        mma_commit_warp(&s.free_vec[c % kVecs]);
     }
     return true;
 }
@@ -535,9 +535,9 @@ __device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, int n, in
     const bool live = col < p.dv;
     const size_t one = (size_t)p.hv * p.dk * p.dv, in = (size_t)h * p.dk * p.dv + (size_t)part * H * p.dv + col;
     const int keys = min(max(p.dk - part * H, 0), H);  // of this quarter that the state has
-    // This column's place in a row of a V tile: 16-byte piece ^ (row % 8).
+    // This column's place in a row of a V tile: 16-byte piece ^ (row % 8). Columns past dv read what is there; lanes do not meet, and those are
+    // not stored.
     const uint32_t v_in = (uint32_t)(col >> 6) * 8192u + (uint32_t)(col & 7) * 2u + (uint32_t)t0 * 128u, piece = (uint32_t)(col & 63) >> 3;
-    const bool loaded = col < (p.dv > 64 ? 128 : 64);
     // Scaled by the next chunk's decay, the state goes back for the MMAs to add to.
     auto scaled = [&](float (&S)[H], int c) -> bool {
         if (!warp_wait(&s.ready_tp[c % kTpStages], (uint32_t)(c / kTpStages) & 1u)) return false;
@@ -580,7 +580,7 @@ __device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, int n, in
         const uint8_t *v = s.v[vs] + v_in;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            const uint32_t x = loaded ? *reinterpret_cast<const uint16_t *>(v + e * 128 + ((piece ^ (uint32_t)(e & 7)) << 4)) : 0u;
+            const uint32_t x = *reinterpret_cast<const uint16_t *>(v + e * 128 + ((piece ^ (uint32_t)(e & 7)) << 4));
             R[e] = __uint_as_float(x << 16);
         }
         warp_arrive(&s.free_v[vs]);
@@ -669,15 +669,19 @@ __device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, int n, in
             warp_arrive(&s.o_free);
             const int m = (int)min((long long)16, end - (begin + (long long)c * C + t0));
             char *to = o + (size_t)((long long)c * C + t0) * o_step;
-            uint32_t off = (uint32_t)col * 2u;
-            if (live)
+            const uint32_t off = (uint32_t)col * 2u;
+            if (live && m == 16) {
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
                     const uint32_t two = pack_bf16(x[e], x[e + 1]);
-                    if (e < m) *reinterpret_cast<uint16_t *>(to + off) = (uint16_t)two;
-                    if (e + 1 < m) *reinterpret_cast<uint16_t *>(to + (off + o_step)) = (uint16_t)(two >> 16);
-                    off += 2u * o_step;
+                    *reinterpret_cast<uint16_t *>(to + (off + e * o_step)) = (uint16_t)two;
+                    *reinterpret_cast<uint16_t *>(to + (off + (e + 1) * o_step)) = (uint16_t)(two >> 16);
                 }
+            } else if (live) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (e < m) *reinterpret_cast<__nv_bfloat16 *>(to + (off + e * o_step)) = __float2bfloat16_rn(x[e]);
+            }
         }
     }
     return true;
@@ -711,6 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_kernel(const __grid_cons
             mbar_init(&s.free_tp[i], 1);
             mbar_init(&s.ready_tp[i], kPrepWarps);
         }
+        for (int i = 0; i < kVecs; ++i) mbar_init(&s.free_vec[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&s.ready_decays[i], 1);
         mbar_init(&s.kk_free, 6);  // the warps that have rows there
         for (uint64_t *b : {&s.s, &s.r, &s.u2, &s.up, &s.o_free}) mbar_init(b, kChainWarps);
         for (uint64_t *b : {&s.kk, &s.ks, &s.qs, &s.u, &s.ds, &s.pu, &s.drain}) mbar_init(b, 1);
@@ -726,15 +732,15 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     bool ok = true;
-    // The block was launched with 896 x 72 registers: 512 x 80 + 256 x 72 + 128 x 40.
+    // 896 x 72 registers, the same for all: each role is held to them by itself (0 to 12 bytes spill; without the word 48 to 136 do).
     if (warp < kChainWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         ok = chain<DK>(s, p, n, h, begin, end, chunks, tmem);
     } else if (warp < kChainWarps + kPrepWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         ok = prep<DK>(s, p, h, begin, end, chunks, tmem);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kIssuer) {
             ok = issue<DK>(s, chunks);
             if (!ok) {  // nothing may be in flight at the end
@@ -745,6 +751,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_kernel(const __grid_cons
         } else if (warp == kLoader) {
             ok = load<DK>(s, maps, p, h, begin, chunks);
             __syncwarp();
+        } else if (warp == kDecays) {
+            ok = decays(s, p, h, begin, end, chunks);
         }
     }
     if (!ok) atomicOr(p.err, kErrTimeout);
