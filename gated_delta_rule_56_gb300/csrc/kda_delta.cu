@@ -342,7 +342,7 @@ size_t delta_prefill_workspace_bytes(const kda_delta_args &, int) { return 0; }
 
 cudaError_t launch_delta_prefill(const kda_delta_args &a, void *o, float *final_state, void *, int, unsigned *err, cudaStream_t s) {
     const DeltaParams p = delta_params(a, o, final_state, err);
-    if (p.seqs.rows >= 32ll * p.seqs.n_seqs && delta_tc_supported(a.dtype, p)) return launch_delta_tc(p, s);
+    if (delta_tc_supported(a.dtype, p)) return launch_delta_tc(p, s);
     return launch_delta_rows(a.dtype, p, nullptr, 0, s);
 }
 

@@ -17,6 +17,7 @@
 // One block per (sequence, value head), the chunks from the last to the first with S0 and dS in shared memory. Bound by the
 // multiply-adds (6 products of 16 rows with a state) and their reads of shared memory; a path for few, small or fp32 calls.
 #include "kda_delta.cuh"
+#include "kda_delta_tc.h"
 #include "kda_layers.h"
 
 namespace kda {
@@ -342,32 +343,33 @@ size_t head_floats(const kda_delta_args &a) {  // one of dq, dk per value head
 
 }  // namespace
 
-size_t delta_backward_workspace_bytes(const kda_delta_args &a, int) { return (kept_floats(a) + 2 * head_floats(a)) * 4; }
+size_t delta_backward_workspace_bytes(const kda_delta_args &a, int) {
+    const DeltaParams p = delta_params(a, nullptr, nullptr, nullptr);
+    return (delta_tc_supported(a.dtype, p) ? delta_tc_backward_bytes(p) : kept_floats(a) * 4) + 2 * head_floats(a) * 4;
+}
 
 cudaError_t launch_delta_backward(const kda_delta_args &a, const kda_delta_grads &g, void *ws, int, unsigned *err, cudaStream_t s) {
-    BackParams p{};
-    p.f = delta_params(a, nullptr, nullptr, err);
-    p.d_o = g.d_o;
-    p.d_fin = g.d_final_state;
-    float *kept = static_cast<float *>(ws);
-    p.kept = kept;
-    const bool apart = head_floats(a) > 0;
-    p.dq = apart ? kept + kept_floats(a) : g.dq;
-    p.dk = apart ? p.dq + head_floats(a) : g.dk;
-    p.dv = g.dv;
-    p.dg = g.dg;
-    p.db = g.dbeta;
-    p.d_init = g.d_initial_state;
-    if (p.f.seqs.n_seqs == 0) return cudaSuccess;
-    cudaError_t e = launch_delta_rows(a.dtype, p.f, kept, kC, s);
-    if (e != cudaSuccess) return e;
-    e = a.dtype == KDA_BF16 ? launch_back_typed<__nv_bfloat16>(p, s) : launch_back_typed<float>(p, s);
+    const DeltaParams f = delta_params(a, nullptr, nullptr, err);
+    if (f.seqs.n_seqs == 0) return cudaSuccess;
+    const bool apart = head_floats(a) > 0, tc = delta_tc_supported(a.dtype, f);
+    float *heads = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + (tc ? delta_tc_backward_bytes(f) : kept_floats(a) * 4));
+    float *dq = apart ? heads : g.dq, *dk = apart ? heads + head_floats(a) : g.dk;
+    cudaError_t e;
+    if (tc) {
+        e = launch_delta_tc_backward(f, DeltaGradients{g.d_o, g.d_final_state, dq, dk, g.dv, g.dg, g.dbeta, g.d_initial_state}, ws, s);
+    } else {
+        float *kept = static_cast<float *>(ws);
+        const BackParams p{f, g.d_o, g.d_final_state, kept, dq, dk, g.dv, g.dg, g.dbeta, g.d_initial_state};
+        e = launch_delta_rows(a.dtype, f, kept, kC, s);
+        if (e != cudaSuccess) return e;
+        e = a.dtype == KDA_BF16 ? launch_back_typed<__nv_bfloat16>(p, s) : launch_back_typed<float>(p, s);
+    }
     if (e != cudaSuccess || !apart) return e;
-    const long long n = p.f.seqs.rows * a.k_heads * (a.dk / 4);
+    const long long n = f.seqs.rows * a.k_heads * (a.dk / 4);
     if (n == 0) return cudaSuccess;
     delta_shared_kernel<<<dim3((unsigned)((n + 255) / 256), 2), 256, 0, s>>>(
-        reinterpret_cast<const float4 *>(p.dq), reinterpret_cast<const float4 *>(p.dk), reinterpret_cast<float4 *>(g.dq),
-        reinterpret_cast<float4 *>(g.dk), n, a.dk / 4, p.f.per);
+        reinterpret_cast<const float4 *>(dq), reinterpret_cast<const float4 *>(dk), reinterpret_cast<float4 *>(g.dq),
+        reinterpret_cast<float4 *>(g.dk), n, a.dk / 4, f.per);
     return cudaGetLastError();
 }
 

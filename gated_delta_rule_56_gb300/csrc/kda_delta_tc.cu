@@ -20,23 +20,17 @@
 // and P as operands; 24 issues the MMAs, 25 the TMA loads, 26 makes the decays. Tiles of K and Q have three stages, V, T and P two.
 //
 // Bound by the chain's latency (three dependent MMA groups and the conversions between them), not by HBM.
-#include <cudaTypedefs.h>
-
 #include <mutex>
 
-#include "kda_delta.cuh"
-#include "kda_delta_tc.h"
-#include "kda_tc.cuh"
+#include "kda_delta_tc.cuh"
 
 namespace kda {
 namespace {
 
-using namespace tc;
+using namespace delta_tc;
 
-constexpr int C = 64;
-constexpr int kChainWarps = 16, kPrepWarps = 8, kIssuer = 24, kLoader = 25, kDecays = 26;
+constexpr int kChainWarps = 16, kPrepWarps = 8, kIssuer = 24, kLoader = 25, kDecays = 26, kKeeper = 27;
 constexpr int kThreads = 28 * 32, kPrep = kPrepWarps * 32;
-constexpr uint64_t kWaitNs = 1000000000ull;  // 1 s per wait
 
 // TMEM columns
 constexpr uint32_t TM_S = 0;      // S^T: first bf16 values in 0..63, second in 64..127; then U with its decay, three times 32
@@ -48,11 +42,6 @@ constexpr uint32_t TM_KK = 448;   // [K; Q] K^T
 
 constexpr int kKqStages = 3, kVStages = 2, kTpStages = 2, kVecs = 3;
 constexpr uint32_t kKqBytes = 32768, kVBytes = 16384, kTpBytes = 32768;
-
-struct Vec {
-    float E[C], F[C], b[C], be[C];  // exp(G_i), exp(G_C - G_i), beta_i, beta_i exp(G_i)
-    float whole, pad[3];            // exp(G_C)
-};
 
 struct Shared {
     uint8_t kq[kKqStages][kKqBytes];  // per 64 key channels: 64 rows of K, 64 rows of Q
@@ -74,25 +63,6 @@ struct Maps {
     CUtensorMap q, k, v;
 };
 
-// a, b as hi + lo, each a pair of bf16 values: 2^-16 at most is left.
-__device__ __forceinline__ void rest_of(float a, float b, uint32_t hi, float &c, float &d) {
-    unpair(add2(pair(a, b), pair(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xffff0000u))), c, d);
-}
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-    float c, d;
-    hi = pack_bf16(a, b);
-    rest_of(a, b, hi, c, d);
-    lo = pack_bf16(c, d);
-}
-__device__ __forceinline__ void split3(float a, float b, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-    float c, d, e, f;
-    hi = pack_bf16(a, b);
-    rest_of(a, b, hi, c, d);
-    mid = pack_bf16(c, d);
-    rest_of(c, d, mid, e, f);
-    lo = pack_bf16(e, f);
-}
-
 __device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 // prep_sync; true if `ok` in all of them, so that they leave together when a wait runs out.
 __device__ __forceinline__ bool prep_all(bool ok) {
@@ -108,59 +78,7 @@ __device__ __forceinline__ bool prep_all(bool ok) {
         : "memory");
     return any == 0;
 }
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs));
-}
-// One arrival per warp, behind everything its lanes did.
-__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
-
-// K step st (16 channels) of a K-major operand in 128-byte swizzled tiles of 64 channels, `tile` bytes apart.
-__device__ __forceinline__ uint64_t kstep(int st, uint32_t tile) {
-    return (uint64_t)(((uint32_t)(st >> 2) * tile + (uint32_t)(st & 3) * 32u) >> 4);
-}
-
 // ------------------------------------------------------------------------ prep -----------
-
-// x[j] = D_ij x[j] (times `scale`) for 32 columns from c0: decays of row i against the rows of its own and earlier blocks of 16; zero behind
-// the diagonal. Only products of decays, so nothing cancels and nothing overflows.
-__device__ __forceinline__ void decay_row(float (&x)[32], const float *a, const float *pre, const float *f, int i, int c0, bool q_row,
-                                          float scale) {
-    const int bi = i >> 4, in = i & 15;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        const int o = c0 + 16 * b;
-        if (o < 16 * bi) {  // row -> end of the block, the blocks between, start of this block -> row
-            float e = scale * pre[i];
-            for (int m = (o >> 4) + 1; m < bi; ++m) e *= pre[16 * m + 15];
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-                const ulonglong2 f4 = *reinterpret_cast<const ulonglong2 *>(f + o + j);
-                float *y = &x[16 * b + j];
-                unpair(mul2(pair(y[0], y[1]), mul2(both(e), f4.x)), y[0], y[1]);
-                unpair(mul2(pair(y[2], y[3]), mul2(both(e), f4.y)), y[2], y[3]);
-            }
-        } else if (o == 16 * bi) {
-            float D = scale;
-#pragma unroll
-            for (int j = 12; j >= 0; j -= 4) {
-                const float4 a4 = *reinterpret_cast<const float4 *>(a + o + j);
-                const float av[4] = {a4.x, a4.y, a4.z, a4.w};
-#pragma unroll
-                for (int m = 3; m >= 0; --m) {
-                    const int at = j + m;  // D is that of column `at` when its turn comes
-                    x[16 * b + at] = at < in || (q_row && at == in) ? D * x[16 * b + at] : 0.f;
-                    D = at <= in ? D * av[m] : D;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[16 * b + j] = 0.f;
-        }
-    }
-}
 
 // acc += A (16 x K) B (K x 8), fp32 in shared memory, one warp: tf32 MMAs over two values per operand (2^-21 of a product is left).
 __device__ __forceinline__ void two_tf32(float x, uint32_t &hi, uint32_t &lo) {
@@ -254,63 +172,26 @@ __device__ __forceinline__ void invert(Shared &s, int pt) {
     prep_sync();
 }
 
-// 8 values of row i, channels 8 chunk .. 8 chunk + 7, as two bf16 operands of 64 x 64 (128-byte swizzle).
-__device__ __forceinline__ void store_operand(uint8_t *hi, uint8_t *lo, int i, int chunk, const float *x) {
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) split2(x[2 * e], x[2 * e + 1], h[e], l[e]);
-    const uint32_t at = (uint32_t)i * 128u + (uint32_t)((chunk ^ (i & 7)) << 4);
-    *reinterpret_cast<uint4 *>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4 *>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
-}
-
-// The chunks' decays, by one warp: lane = rows lane and lane + 32. Each is the exponential of a sum of its own log-decays alone (prefix or
-// suffix sums, never differences): neighbours behind a strong decay keep their small ones.
+// The chunks' decays, by one warp, up to two chunks ahead of the chain.
 __device__ __forceinline__ bool decays(Shared &s, const DeltaParams &p, int h, long long begin, long long end, int chunks) {
     const int lane = threadIdx.x & 31;
-    const bool second = lane & 16, last = (lane & 15) == 15;
     const float *g = p.g + (begin + lane) * p.hv + h, *beta = p.beta + (begin + lane) * p.hv + h;
     const long long half_rows = 32ll * p.hv;
     for (int c = 0; c < chunks; ++c) {
         const long long left = end - begin - (long long)c * C - lane;
-        float up[2], down[2], total[4], b[2], own[2];
+        float own[2], b[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             own[half] = left > 32 * half ? log_decay(g[half * half_rows]) : 0.f;
             b[half] = left > 32 * half ? beta[half * half_rows] : 0.f;
-            up[half] = down[half] = own[half];
         }
         g += 2 * half_rows;
         beta += 2 * half_rows;
-#pragma unroll
-        for (int d = 1; d < 16; d *= 2)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const float x = __shfl_up_sync(0xffffffffu, up[half], d, 16), y = __shfl_down_sync(0xffffffffu, down[half], d, 16);
-                if ((lane & 15) >= d) up[half] += x;
-                if ((lane & 15) + d < 16) down[half] += y;
-            }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) total[e] = __shfl_sync(0xffffffffu, up[e >> 1], 16 * (e & 1) + 15);
-        if (c >= kVecs && !warp_wait(&s.free_vec[c % kVecs], (uint32_t)(c / kVecs - 1) & 1u)) return false;
-        if (c >= 2 && !warp_wait(&s.ready_tp[c & 1], (uint32_t)(c / 2 - 1) & 1u)) return false;  // chunk c - 2 is prepared
-        Vec &v = s.vec[c % kVecs];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const float next = __shfl_down_sync(0xffffffffu, down[half], 1, 16), behind = last ? 0.f : next;
-            const int i = lane + 32 * half;
-            float before = half ? total[0] + total[1] : 0.f, after = half ? 0.f : total[2] + total[3];
-            if (second) before += total[2 * half]; else after += total[2 * half + 1];
-            const float E = expf(up[half] + before);
-            s.a[c & 1][i] = expf(own[half]);
-            s.pre[c & 1][i] = expf(up[half]);
-            s.f[c & 1][i] = expf(behind);
-            v.E[i] = E;
-            v.F[i] = expf(behind + after);
-            v.b[i] = b[half];
-            v.be[i] = b[half] * E;
-        }
-        if (lane == 0) v.whole = expf((total[0] + total[1]) + (total[2] + total[3]));
+        const bool ok = chunk_decays(s.vec[c % kVecs], s.a[c & 1], s.pre[c & 1], s.f[c & 1], lane, own, b, [&] {
+            if (c >= kVecs && !warp_wait(&s.free_vec[c % kVecs], (uint32_t)(c / kVecs - 1) & 1u)) return false;
+            return c < 2 || warp_wait(&s.ready_tp[c & 1], (uint32_t)(c / 2 - 1) & 1u);  // chunk c - 2 is prepared
+        });
+        if (!ok) return false;
         warp_arrive(&s.ready_decays[c & 1]);
     }
     return true;
@@ -354,7 +235,9 @@ __device__ __forceinline__ bool prep(Shared &s, const DeltaParams &p, int h, lon
             tmem_ld_wait();
             tc_fence_before();
             warp_arrive(&s.kk_free);
-            decay_row(x, s.a[c & 1], s.pre[c & 1], s.f[c & 1], i, c0, q_row, q_row ? 1.f : s.vec[c % kVecs].b[i]);
+            const float scale = q_row ? 1.f : s.vec[c % kVecs].b[i];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) decay_block(x + 16 * b, s.a[c & 1], s.pre[c & 1], s.f[c & 1], i, c0 + 16 * b, q_row, scale);
             if (q_row) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) store_operand(tp + 16384, tp + 24576, i, c0 / 8 + e, &x[8 * e]);
@@ -391,7 +274,7 @@ __device__ __forceinline__ bool prep(Shared &s, const DeltaParams &p, int h, lon
 
 // ------------------------------------------------------------------------ issuer ---------
 
-template <int DK>
+template <int DK, bool KEEP>
 __device__ __forceinline__ bool issue(Shared &s, int chunks) {
     const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
     const uint32_t kq = smem_u32(s.kq[0]), tp = smem_u32(s.tp[0]);
@@ -423,14 +306,16 @@ __device__ __forceinline__ bool issue(Shared &s, int chunks) {
             for (int st = 0; st < DK / 16; ++st)
                 mma_bf16_tmem_a_warp(tmem + TM_KS, tmem + TM_S + 64 * e + 8 * st, d_k + kstep(st, 16384u), idesc_bf16(128, 64), e + st > 0);
         mma_commit_warp(&s.ks);
-        if (c > 0 && !warp_wait(&s.o_free, par ^ 1u)) return false;
-        tc_fence_after();
+        if constexpr (!KEEP) {
+            if (c > 0 && !warp_wait(&s.o_free, par ^ 1u)) return false;
+            tc_fence_after();
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int st = 0; st < DK / 16; ++st)
-                mma_bf16_tmem_a_warp(tmem + TM_O, tmem + TM_S + 64 * e + 8 * st, d_q + kstep(st, 16384u), idesc_bf16(128, 64), e + st > 0);
-        mma_commit_warp(&s.qs);
+                for (int st = 0; st < DK / 16; ++st)
+                    mma_bf16_tmem_a_warp(tmem + TM_O, tmem + TM_S + 64 * e + 8 * st, d_q + kstep(st, 16384u), idesc_bf16(128, 64), e + st > 0);
+            mma_commit_warp(&s.qs);
+        }
         if (!warp_wait(&s.ready_tp[c % kTpStages], (uint32_t)(c / kTpStages) & 1u) || !warp_wait(&s.r, par)) return false;
         tc_fence_after();
         const uint64_t d_t = sdesc_sw128(tpc, 16u, 1024u), d_p = sdesc_sw128(tpc + 16384u, 16u, 1024u);
@@ -450,15 +335,17 @@ __device__ __forceinline__ bool issue(Shared &s, int chunks) {
                 mma_bf16_tmem_a_warp(tmem + TM_SF, tmem + TM_S + 32 * e + 8 * st, d_kn + kDescStepMN128 * st,
                                      idesc_bf16(128, DK) | kIdescBMajorMN, 1u);
         mma_commit_warp(&s.ds);
-        if (!warp_wait(&s.up, par)) return false;
-        tc_fence_after();
+        if constexpr (!KEEP) {
+            if (!warp_wait(&s.up, par)) return false;
+            tc_fence_after();
 #pragma unroll
-        for (int e = 0; e < 3; ++e)
+            for (int e = 0; e < 3; ++e)
 #pragma unroll
-            for (int st = 0; st < C / 16; ++st)
-                mma_bf16_tmem_a_warp(tmem + TM_O, tmem + TM_R + (e == 2 ? 32 : 0) + 8 * st, d_p + (e == 1 ? 512u : 0u) + kstep(st, 0u),
-                                     idesc_bf16(128, 64), 1u);
-        mma_commit_warp(&s.pu);
+                for (int st = 0; st < C / 16; ++st)
+                    mma_bf16_tmem_a_warp(tmem + TM_O, tmem + TM_R + (e == 2 ? 32 : 0) + 8 * st, d_p + (e == 1 ? 512u : 0u) + kstep(st, 0u),
+                                         idesc_bf16(128, 64), 1u);
+            mma_commit_warp(&s.pu);
+        }
         mma_commit_warp(&s.free_tp[c % kTpStages]);
         mma_commit_warp(&s.free_kq[c % kKqStages]);
         mma_commit_warp(&s.free_vec[c % kVecs]);
@@ -504,30 +391,8 @@ __device__ __forceinline__ bool load(Shared &s, const Maps &maps, const DeltaPar
 
 // ------------------------------------------------------------------------ chain ----------
 
-// The state's operands from its fp32 values, N of a thread.
-template <int N>
-__device__ __forceinline__ void publish_state(const float (&S)[N], uint32_t at) {
-    uint32_t hi[N / 2], lo[N / 2];
-#pragma unroll
-    for (int e = 0; e < N / 2; ++e) split2(S[2 * e], S[2 * e + 1], hi[e], lo[e]);
-    tmem_st(at, hi);
-    tmem_st(at + 64, lo);
-    tmem_st_wait();
-    tc_fence_before();
-}
-
-// 16 values times 16 of shared memory.
-__device__ __forceinline__ void scale16(float (&x)[16], const float *by) {
-#pragma unroll
-    for (int e = 0; e < 16; e += 4) {
-        const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(by + e);
-        unpair(mul2(pair(x[e], x[e + 1]), f.x), x[e], x[e + 1]);
-        unpair(mul2(pair(x[e + 2], x[e + 3]), f.y), x[e + 2], x[e + 3]);
-    }
-}
-
-template <int DK>
-__device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, int n, int h, long long begin, long long end, int chunks, uint32_t tmem) {
+template <int DK, bool KEEP>
+__device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, const DeltaKept &kept, int n, int h, long long begin, long long end, int chunks, uint32_t tmem) {
     constexpr int H = DK / 4;  // key channels of a thread
     const int part = threadIdx.x >> 7, col = threadIdx.x & 127;  // quarter of the rows and of the key channels; value column
     const int t0 = 16 * part;
@@ -547,6 +412,15 @@ __device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, int n, in
         tmem_st(at + TM_SF + part * H, S);
         return true;
     };
+    // Kept for the gradients: the state before chunk c.
+    float *kept_S = KEEP ? kept.S + (size_t)first_chunk(begin, n, C) * one + in : nullptr;
+    auto keep = [&](const float (&S)[H], int c) {
+        if constexpr (KEEP)
+            if (live)
+#pragma unroll
+                for (int e = 0; e < H; ++e)
+                    if (e < keys) kept_S[(size_t)c * one + (size_t)e * p.dv] = S[e];
+    };
     auto finish = [&](const float (&S)[H]) {
         const long long to = p.fin ? state_slot(p.fin_idx, p.pool, n, p.err) : -1;
         if (to >= 0 && live)
@@ -562,6 +436,7 @@ __device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, int n, in
         if (chunks > 0) {
             publish_state(S, at + TM_S + part * (H / 2));
             warp_arrive(&s.s);
+            keep(S, 0);
             if (!scaled(S, 0)) return false;
         } else {
             finish(S);
@@ -605,15 +480,17 @@ __device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, int n, in
             tc_fence_before();
             warp_arrive(&s.r);
         }
-        // Beside (T - I) R: the reading of the state, with its decay
-        if (!warp_wait(&s.qs, par)) return false;
-        tc_fence_after();
-        {
-            float x[16];
-            tmem_ld(at + TM_O + t0, x);
-            tmem_ld_wait();
-            scale16(x, vec.E + t0);
-            tmem_st(at + TM_O + t0, x);
+        if constexpr (!KEEP) {
+            // Beside (T - I) R: the reading of the state, with its decay
+            if (!warp_wait(&s.qs, par)) return false;
+            tc_fence_after();
+            {
+                float x[16];
+                tmem_ld(at + TM_O + t0, x);
+                tmem_ld_wait();
+                scale16(x, vec.E + t0);
+                tmem_st(at + TM_O + t0, x);
+            }
         }
         if (!warp_wait(&s.u, par)) return false;
         tc_fence_after();
@@ -636,13 +513,21 @@ __device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, int n, in
             tmem_st_wait();
             tc_fence_before();
             warp_arrive(&s.u2);
+            if constexpr (KEEP) {
+                if (live) {
+                    float *to = kept.U + (((size_t)(first_chunk(begin, n, C) + c) * p.hv + h) * C + t0) * p.dv + col;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) split2(R[2 * e], R[2 * e + 1], hi[e], lo[e]);
-            tmem_st(at + TM_R + 8 * part, hi);
-            tmem_st(at + TM_R + 32 + 8 * part, lo);
-            tmem_st_wait();
-            tc_fence_before();
-            warp_arrive(&s.up);
+                    for (int e = 0; e < 16; ++e) to[(size_t)e * p.dv] = R[e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) split2(R[2 * e], R[2 * e + 1], hi[e], lo[e]);
+                tmem_st(at + TM_R + 8 * part, hi);
+                tmem_st(at + TM_R + 32 + 8 * part, lo);
+                tmem_st_wait();
+                tc_fence_before();
+                warp_arrive(&s.up);
+            }
         }
         if (!warp_wait(&s.ds, par)) return false;
         tc_fence_after();
@@ -653,11 +538,13 @@ __device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, int n, in
             if (c + 1 < chunks) {
                 publish_state(S, at + TM_S + part * (H / 2));
                 warp_arrive(&s.s);
+                keep(S, c + 1);
                 if (!scaled(S, c + 1)) return false;
             } else {
                 finish(S);
             }
         }
+        if constexpr (KEEP) continue;
         // Beside the next chunk's KS: the outputs
         if (!warp_wait(&s.pu, par)) return false;
         tc_fence_after();
@@ -687,8 +574,26 @@ __device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, int n, in
     return true;
 }
 
-template <int DK>
-__global__ void __launch_bounds__(kThreads, 1) delta_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ DeltaParams p) {
+// For the gradients: T and P of every chunk go out as they are, from shared memory.
+__device__ __forceinline__ bool keep_operands(Shared &s, uint8_t *to, long long step, int chunks) {
+    for (int c = 0; c < chunks; ++c) {
+        if (!warp_wait(&s.ready_tp[c % kTpStages], (uint32_t)(c / kTpStages) & 1u)) return false;
+        if ((threadIdx.x & 31) == 0) {
+            bulk_store(to + c * step, s.tp[c % kTpStages], kTpBytes);
+            bulk_commit();
+            bulk_wait_read_all();
+            mbar_arrive(&s.free_tp[c % kTpStages]);
+        }
+        __syncwarp();
+    }
+    if ((threadIdx.x & 31) == 0) bulk_wait_all();
+    __syncwarp();
+    return true;
+}
+
+template <int DK, bool KEEP>
+__global__ void __launch_bounds__(kThreads, 1)
+    delta_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ DeltaParams p, const __grid_constant__ DeltaKept kept) {
     extern __shared__ uint8_t raw[];
     Shared &s = *reinterpret_cast<Shared *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5;
@@ -712,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_kernel(const __grid_cons
             mbar_init(&s.ready_v[i], kPrepWarps);
         }
         for (int i = 0; i < kTpStages; ++i) {
-            mbar_init(&s.free_tp[i], 1);
+            mbar_init(&s.free_tp[i], KEEP ? 2 : 1);
             mbar_init(&s.ready_tp[i], kPrepWarps);
         }
         for (int i = 0; i < kVecs; ++i) mbar_init(&s.free_vec[i], 1);
@@ -735,14 +640,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_kernel(const __grid_cons
     // 896 x 72 registers, the same for all: each role is held to them by itself (0 to 12 bytes spill; without the word 48 to 136 do).
     if (warp < kChainWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        ok = chain<DK>(s, p, n, h, begin, end, chunks, tmem);
+        ok = chain<DK, KEEP>(s, p, kept, n, h, begin, end, chunks, tmem);
     } else if (warp < kChainWarps + kPrepWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         ok = prep<DK>(s, p, h, begin, end, chunks, tmem);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kIssuer) {
-            ok = issue<DK>(s, chunks);
+            ok = issue<DK, KEEP>(s, chunks);
             if (!ok) {  // nothing may be in flight at the end
                 mma_commit_warp(&s.drain);
                 (void)mbar_wait(&s.drain, 0, kWaitNs);
@@ -753,6 +658,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_kernel(const __grid_cons
             __syncwarp();
         } else if (warp == kDecays) {
             ok = decays(s, p, h, begin, end, chunks);
+        } else if (KEEP && warp == kKeeper) {
+            ok = keep_operands(s, kept.tp + ((size_t)first_chunk(begin, n, C) * p.hv + h) * kTpBytes, (long long)p.hv * kTpBytes, chunks);
         }
     }
     if (!ok) atomicOr(p.err, kErrTimeout);
@@ -762,7 +669,34 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_kernel(const __grid_cons
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+// Sequences of fewer rows on average go token by token.
+constexpr long long kFewestRows = 32;
+
+constexpr size_t kSharedBytes = sizeof(Shared) + 1024;
+
+template <int DK, bool KEEP>
+cudaError_t launch(const Maps &maps, const DeltaParams &p, const DeltaKept &kept, cudaStream_t s) {
+    auto *f = &delta_tc_kernel<DK, KEEP>;
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSharedBytes);
+    if (e != cudaSuccess) return e;
+    f<<<(unsigned)((long long)p.seqs.n_seqs * p.hv), kThreads, kSharedBytes, s>>>(maps, p, kept);
+    return cudaGetLastError();
+}
+
+template <bool KEEP>
+cudaError_t launch_any(const DeltaParams &p, const DeltaKept &kept, cudaStream_t s) {
+    Maps maps;
+    if (!encode(&maps.q, p.q, p.seqs.rows, p.hk, p.dk, p.qs) || !encode(&maps.k, p.k, p.seqs.rows, p.hk, p.dk, p.ks) ||
+        !encode(&maps.v, p.v, p.seqs.rows, p.hv, p.dv, p.vs))
+        return cudaErrorInvalidValue;
+    return p.dk == 128 ? launch<128, KEEP>(maps, p, kept, s) : launch<64, KEEP>(maps, p, kept, s);
+}
+
+}  // namespace
+
+namespace delta_tc {
+
+static PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -775,8 +709,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-// Rows of `heads` heads of d channels, `stride` elements apart, in boxes of 64 rows x 64 channels (128-byte swizzle); what lies past the
-// channels and the rows reads as zeros.
 bool encode(CUtensorMap *map, const void *base, long long rows, int heads, int d, long long stride) {
     auto enc = encoder();
     if (!enc) return false;
@@ -787,30 +719,14 @@ bool encode(CUtensorMap *map, const void *base, long long rows, int heads, int d
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr size_t kSharedBytes = sizeof(Shared) + 1024;
-
-template <int DK>
-cudaError_t launch(const Maps &maps, const DeltaParams &p, cudaStream_t s) {
-    auto *f = &delta_tc_kernel<DK>;
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSharedBytes);
-    if (e != cudaSuccess) return e;
-    f<<<(unsigned)((long long)p.seqs.n_seqs * p.hv), kThreads, kSharedBytes, s>>>(maps, p);
-    return cudaGetLastError();
-}
-
-}  // namespace
+}  // namespace delta_tc
 
 bool delta_tc_supported(kda_dtype dtype, const DeltaParams &p) {
     auto ok = [](const void *x, long long stride) { return aligned16(x) && stride % 8 == 0; };
-    return dtype == KDA_BF16 && p.seqs.rows > 0 && ok(p.q, p.qs) && ok(p.k, p.ks) && ok(p.v, p.vs) && encoder();
+    return dtype == KDA_BF16 && p.seqs.rows > 0 && p.seqs.rows >= kFewestRows * p.seqs.n_seqs && ok(p.q, p.qs) && ok(p.k, p.ks) && ok(p.v, p.vs) && delta_tc::encoder();
 }
 
-cudaError_t launch_delta_tc(const DeltaParams &p, cudaStream_t s) {
-    Maps maps;
-    if (!encode(&maps.q, p.q, p.seqs.rows, p.hk, p.dk, p.qs) || !encode(&maps.k, p.k, p.seqs.rows, p.hk, p.dk, p.ks) ||
-        !encode(&maps.v, p.v, p.seqs.rows, p.hv, p.dv, p.vs))
-        return cudaErrorInvalidValue;
-    return p.dk == 128 ? launch<128>(maps, p, s) : launch<64>(maps, p, s);
-}
+cudaError_t launch_delta_tc(const DeltaParams &p, cudaStream_t s) { return launch_any<false>(p, DeltaKept{}, s); }
+cudaError_t launch_delta_tc_kept(const DeltaParams &p, const DeltaKept &kept, cudaStream_t s) { return launch_any<true>(p, kept, s); }
 
 }  // namespace kda

@@ -5,8 +5,26 @@
 
 namespace kda {
 
-// bf16 rows that TMA can load (16-byte aligned).
+// bf16 rows that TMA can load (16-byte aligned), sequences long enough for chunks of 64 rows.
 bool delta_tc_supported(kda_dtype dtype, const DeltaParams &p);
 cudaError_t launch_delta_tc(const DeltaParams &p, cudaStream_t s);
+
+// What the gradients keep of the forward pass, per chunk (number of first_chunk) and value head.
+struct DeltaKept {
+    uint8_t *tp;  // operands T - I and P, two bf16 values each: 32768 bytes
+    float *S;     // the state before the chunk [dk, dv]
+    float *U;     // its written values [64, dv]
+};
+constexpr size_t kDeltaTpBytes = 32768;
+cudaError_t launch_delta_tc_kept(const DeltaParams &p, const DeltaKept &kept, cudaStream_t s);
+
+// Gradients: workspace bytes, and the launches. dq, dk: per value head where value heads share a key head (p.per > 1).
+struct DeltaGradients {
+    const void *d_o;
+    const float *d_fin;
+    float *dq, *dk, *dv, *dg, *db, *d_init;
+};
+size_t delta_tc_backward_bytes(const DeltaParams &p);
+cudaError_t launch_delta_tc_backward(const DeltaParams &p, const DeltaGradients &g, void *ws, cudaStream_t s);
 
 }  // namespace kda

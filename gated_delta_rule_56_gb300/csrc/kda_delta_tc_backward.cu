@@ -1,0 +1,800 @@
+// kda_delta_tc_backward.cu -- gradients of the delta rule with one decay per value head on the sm_103a tensor cores (bf16 inputs).
+//
+// The formulas are those of kda_delta_backward.cu, on chunks of 64 rows, in three launches:
+//   1. the forward kernel (kda_delta_tc.cu) without its outputs: it keeps, per chunk, the state S0 before it, the values U, and T - I and P as
+//      the operands that they are;
+//   2. the chain of the state's gradient, chunks from the last to the first. One block per (sequence, value head), all transposed
+//      (TMEM lane = value column) as in the forward chain, the same three dependent MMA groups per chunk:
+//          dS^T K^T -> dU^T = F (dS^T K^T) + dO^T P -> dR^T = dU^T + dU^T (T - I) -> dS^T <- e^{G_C} dS^T + (E dO)^T Q - (b E dR)^T K
+//      T - I, P, K and Q are the operands of the forward pass read with the other index as the long one. It keeps dS and dR per chunk;
+//   3. everything else, which needs no other chunk: one block per (chunk, value head), [dO; dR] as the 128 rows of the accumulators:
+//          [dO; dR] U^T -> Gp, Ga;   [dO; dR] S0^T, scaled by +-E, + [Gp; Ga] K = [dq; row];   F (U dS^T) + Gp^T Q + (b Ga)^T K = col.
+// Where value heads share key heads, dq and dk go per value head to the workspace and are added up in a fixed order.
+//
+// Operands that are not exact in bf16 go in as two values (2^-17 of them is left, the products of both rests are left out), those that are
+// added to the gradient of the state as three; sums, states and outputs are fp32.
+//
+// Bound by latency: the chains have one block per SM and sequence and value head, the third kernel runs its phases one after the other.
+#include "kda_delta_tc.cuh"
+
+namespace kda {
+namespace {
+
+using namespace delta_tc;
+
+// ------------------------------------------------------------------ the chain backward ---
+
+constexpr int kChainWarps = 16, kIssuer = 16, kLoader = 17, kDecays = 18;
+constexpr int kThreads = 20 * 32;
+constexpr int kStages = 2, kVecs = 3;
+
+// TMEM columns
+constexpr uint32_t TM_D = 0;      // dS^T: first bf16 values in 0..63, second in 64..127; then b E dR, three times 32
+constexpr uint32_t TM_KD = 128;   // dS^T K^T, then dU^T (T - I)
+constexpr uint32_t TM_U = 192;    // dU: two times 32
+constexpr uint32_t TM_DF = 256;   // dS^T in fp32
+constexpr uint32_t TM_O = 384;    // dO^T (exact), 32; then E dO, three times 32
+constexpr uint32_t TM_PD = 416;   // dO^T P
+
+struct ChainShared {
+    uint8_t kq[kStages][32768];  // as in the forward kernel: per 64 key channels, 64 rows of K, 64 rows of Q
+    uint8_t d_o[kStages][16384];
+    uint8_t tp[kStages][kDeltaTpBytes];
+    Vec vec[kVecs];
+    uint64_t full[kStages], free[kStages], ready[kStages];
+    uint64_t ready_vec[kVecs], free_vec[kVecs];
+    uint64_t s, o, pd, pd_read, kd, r, u, h, u2, ds, drain;
+    uint32_t tmem;
+};
+
+struct ChainMaps {
+    CUtensorMap q, k, d_o;
+};
+struct ChainParams {
+    DeltaParams f;
+    const uint8_t *tp;
+    const float *d_fin;
+    float *dS, *dR, *d_init;  // dS: of the state behind a chunk [chunk, value head, dk, dv]; dR [chunk, value head, 64, dv]
+};
+
+template <int DK>
+__device__ __forceinline__ bool chain_issue(ChainShared &s, int chunks) {
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
+#pragma unroll 1
+    for (int k = 0; k < chunks; ++k) {
+        const uint32_t par = (uint32_t)k & 1u;
+        const int st = k % kStages;
+        const uint32_t kq = smem_u32(s.kq[st]), tp = smem_u32(s.tp[st]);
+        const uint64_t d_k = sdesc_sw128(kq, 16u, 1024u), d_kn = sdesc_sw128(kq, 16384u, 1024u), d_qn = sdesc_sw128(kq + 8192u, 16384u, 1024u);
+        const uint64_t d_t = sdesc_sw128(tp, 8192u, 1024u), d_p = sdesc_sw128(tp + 16384u, 8192u, 1024u);  // MN-major: the column is the N index
+        if (!warp_wait(&s.ready[st], (uint32_t)(k / kStages) & 1u) || !warp_wait(&s.o, par)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < C / 16; ++i)
+                mma_bf16_tmem_a_warp(tmem + TM_PD, tmem + TM_O + 8 * i, d_p + 512u * e + kDescStepMN128 * i, idesc_bf16(128, 64) | kIdescBMajorMN,
+                                     e + i > 0);
+        mma_commit_warp(&s.pd);
+        if (!warp_wait(&s.s, par)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < DK / 16; ++i)
+                mma_bf16_tmem_a_warp(tmem + TM_KD, tmem + TM_D + 64 * e + 8 * i, d_k + kstep(i, 16384u), idesc_bf16(128, 64), e + i > 0);
+        mma_commit_warp(&s.kd);
+        if (!warp_wait(&s.r, par)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+#pragma unroll
+            for (int i = 0; i < C / 16; ++i)
+                mma_bf16_tmem_a_warp(tmem + TM_KD, tmem + TM_U + (e == 2 ? 32 : 0) + 8 * i, d_t + (e == 1 ? 512u : 0u) + kDescStepMN128 * i,
+                                     idesc_bf16(128, 64) | kIdescBMajorMN, e + i > 0);
+        mma_commit_warp(&s.u);
+        if (!warp_wait(&s.h, par)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+#pragma unroll
+            for (int i = 0; i < C / 16; ++i)
+                mma_bf16_tmem_a_warp(tmem + TM_DF, tmem + TM_O + 32 * e + 8 * i, d_qn + kDescStepMN128 * i, idesc_bf16(128, DK) | kIdescBMajorMN, 1u);
+        if (!warp_wait(&s.u2, par)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+#pragma unroll
+            for (int i = 0; i < C / 16; ++i)
+                mma_bf16_tmem_a_warp(tmem + TM_DF, tmem + TM_D + 32 * e + 8 * i, d_kn + kDescStepMN128 * i, idesc_bf16(128, DK) | kIdescBMajorMN, 1u);
+        mma_commit_warp(&s.ds);
+        mma_commit_warp(&s.free[st]);
+        mma_commit_warp(&s.free_vec[k % kVecs]);
+    }
+    return true;
+}
+
+template <int DK>
+__device__ __forceinline__ bool chain_load(ChainShared &s, const ChainMaps &maps, const ChainParams &p, int n, int h, long long begin, int chunks) {
+    const int hk = h / p.f.per, vtiles = p.f.dv > 64 ? 2 : 1;
+    int k = 0;
+    bool ok = true;
+    for (; k < chunks; ++k) {
+        const int st = k % kStages, c = chunks - 1 - k, row = (int)(begin + (long long)c * C);
+        if (k >= kStages && !(ok = warp_wait(&s.free[st], (uint32_t)(k / kStages - 1) & 1u))) break;
+        if (elect_one()) {
+            mbar_arrive_expect_tx(&s.full[st], DK / 64 * 16384 + vtiles * 8192 + (uint32_t)kDeltaTpBytes);
+            for (int a = 0; a < DK / 64; ++a) {
+                tma_load_3d(s.kq[st] + a * 16384, &maps.k, &s.full[st], 64 * a, hk, row);
+                tma_load_3d(s.kq[st] + a * 16384 + 8192, &maps.q, &s.full[st], 64 * a, hk, row);
+            }
+            for (int a = 0; a < vtiles; ++a) tma_load_3d(s.d_o[st] + a * 8192, &maps.d_o, &s.full[st], 64 * a, h, row);
+            bulk_load(s.tp[st], p.tp + ((size_t)(first_chunk(begin, n, C) + c) * p.f.hv + h) * kDeltaTpBytes, (uint32_t)kDeltaTpBytes, &s.full[st]);
+        }
+        __syncwarp();
+    }
+    if (!ok)  // the copies in flight, before the block's shared memory goes
+        for (int b = k > kStages ? k - kStages : 0; b < k; ++b) (void)mbar_wait(&s.full[b % kStages], (uint32_t)(b / kStages) & 1u, kWaitNs);
+    return ok;
+}
+
+__device__ __forceinline__ bool chain_decays(ChainShared &s, const ChainParams &p, int h, long long begin, long long end, int chunks) {
+    const int lane = threadIdx.x & 31;
+    for (int k = 0; k < chunks; ++k) {
+        const long long row = begin + (long long)(chunks - 1 - k) * C + lane;
+        float own[2], b[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const long long r = row + 32 * half;
+            own[half] = r < end ? log_decay(p.f.g[r * p.f.hv + h]) : 0.f;
+            b[half] = r < end ? p.f.beta[r * p.f.hv + h] : 0.f;
+        }
+        const bool ok = chunk_decays(s.vec[k % kVecs], nullptr, nullptr, nullptr, lane, own, b, [&] {
+            return k < kVecs || warp_wait(&s.free_vec[k % kVecs], (uint32_t)(k / kVecs - 1) & 1u);
+        });
+        if (!ok) return false;
+        warp_arrive(&s.ready_vec[k % kVecs]);
+    }
+    return true;
+}
+
+template <int DK>
+__device__ __forceinline__ bool chain(ChainShared &s, const ChainParams &p, int n, int h, long long begin, long long end, int chunks, uint32_t tmem) {
+    constexpr int H = DK / 4;  // key channels of a thread
+    const int part = threadIdx.x >> 7, col = threadIdx.x & 127;  // quarter of the rows and of the key channels; value column
+    const int t0 = 16 * part, dk = p.f.dk, dv = p.f.dv;
+    const uint32_t at = tmem + ((uint32_t)(col & 96) << 16);
+    const bool live = col < dv;
+    const size_t one = (size_t)p.f.hv * dk * dv, in = (size_t)h * dk * dv + (size_t)part * H * dv + col;
+    const int keys = min(max(dk - part * H, 0), H);
+    const uint32_t o_in = (uint32_t)(col >> 6) * 8192u + (uint32_t)(col & 7) * 2u + (uint32_t)t0 * 128u, piece = (uint32_t)(col & 63) >> 3;
+    const long long chunk0 = first_chunk(begin, n, C);
+    auto scaled = [&](float (&S)[H], int k) -> bool {
+        if (!warp_wait(&s.ready_vec[k % kVecs], (uint32_t)(k / kVecs) & 1u)) return false;
+        const float whole = s.vec[k % kVecs].whole;
+#pragma unroll
+        for (int e = 0; e < H; ++e) S[e] *= whole;
+        tmem_st(at + TM_DF + part * H, S);
+        return true;
+    };
+    auto store = [&](const float (&S)[H], float *to) {
+        if (live)
+#pragma unroll
+            for (int e = 0; e < H; ++e)
+                if (e < keys) to[in + (size_t)e * dv] = S[e];
+    };
+    {
+        float S[H];
+#pragma unroll
+        for (int e = 0; e < H; ++e) S[e] = p.d_fin && live && e < keys ? p.d_fin[(size_t)n * one + in + (size_t)e * dv] : 0.f;
+        if (chunks == 0) {
+            if (p.d_init) store(S, p.d_init + (size_t)n * one);
+            return true;
+        }
+        publish_state(S, at + TM_D + part * (H / 2));
+        warp_arrive(&s.s);
+        store(S, p.dS + (size_t)(chunk0 + chunks - 1) * one);
+        if (!scaled(S, 0)) return false;
+    }
+#pragma unroll 1
+    for (int k = 0; k < chunks; ++k) {
+        const uint32_t par = (uint32_t)k & 1u;
+        const int st = k % kStages, c = chunks - 1 - k, m = (int)min((long long)C, end - begin - (long long)c * C);
+        const Vec &vec = s.vec[k % kVecs];
+        if (!warp_wait(&s.full[st], (uint32_t)(k / kStages) & 1u)) return false;
+        if (m < C) {  // K and Q behind the sequence are another one's: zeros
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            for (int e = threadIdx.x; e < (C - m) * 8; e += kChainWarps * 32)
+#pragma unroll
+                for (int a = 0; a < DK / 32; ++a) *reinterpret_cast<uint4 *>(&s.kq[st][a * 8192 + m * 128 + e * 16]) = zero;
+            fence_async_smem();
+        }
+        warp_arrive(&s.ready[st]);
+        // dO^T: exact for P, with its decay for Q
+        float d_o[16];
+        {
+            const uint8_t *v = s.d_o[st] + o_in;
+            uint32_t word[8];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                uint32_t x = *reinterpret_cast<const uint16_t *>(v + e * 128 + ((piece ^ (uint32_t)(e & 7)) << 4));
+                if (t0 + e >= m) x = 0u;
+                d_o[e] = __uint_as_float(x << 16);
+                word[e / 2] = e & 1 ? word[e / 2] | (x << 16) : x;
+            }
+            tmem_st(at + TM_O + 8 * part, word);
+            tmem_st_wait();
+            tc_fence_before();
+            warp_arrive(&s.o);
+        }
+        float dU[16];
+        if (!warp_wait(&s.pd, par)) return false;
+        tc_fence_after();
+        tmem_ld(at + TM_PD + t0, dU);
+        tmem_ld_wait();
+        tc_fence_before();
+        warp_arrive(&s.pd_read);
+        if (!warp_wait(&s.kd, par)) return false;
+        tc_fence_after();
+        {
+            float x[16];
+            tmem_ld(at + TM_KD + t0, x);
+            tmem_ld_wait();
+            scale16(x, vec.F + t0);
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) dU[e] += x[e];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) split2(dU[2 * e], dU[2 * e + 1], hi[e], lo[e]);
+            tmem_st(at + TM_U + 8 * part, hi);
+            tmem_st(at + TM_U + 32 + 8 * part, lo);
+            tmem_st_wait();
+            tc_fence_before();
+            warp_arrive(&s.r);
+        }
+        // Beside dU (T - I): E dO, in the place of dO and of dO^T P, which everyone has read
+        if (!warp_wait(&s.pd_read, par)) return false;
+        tc_fence_after();
+        {
+            scale16(d_o, vec.E + t0);
+            uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) split3(d_o[2 * e], d_o[2 * e + 1], hi[e], mid[e], lo[e]);
+            tmem_st(at + TM_O + 8 * part, hi);
+            tmem_st(at + TM_O + 32 + 8 * part, mid);
+            tmem_st(at + TM_O + 64 + 8 * part, lo);
+            tmem_st_wait();
+            tc_fence_before();
+            warp_arrive(&s.h);
+        }
+        if (!warp_wait(&s.u, par)) return false;
+        tc_fence_after();
+        {
+            float x[16];
+            tmem_ld(at + TM_KD + t0, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = dU[e] += x[e];  // dR
+            scale16(x, vec.be + t0);
+            uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) split3(-x[2 * e], -x[2 * e + 1], hi[e], mid[e], lo[e]);
+            tmem_st(at + TM_D + 8 * part, hi);
+            tmem_st(at + TM_D + 32 + 8 * part, mid);
+            tmem_st(at + TM_D + 64 + 8 * part, lo);
+            tmem_st_wait();
+            tc_fence_before();
+            warp_arrive(&s.u2);
+            if (live) {
+                float *to = p.dR + (((size_t)(chunk0 + c) * p.f.hv + h) * C + t0) * dv + col;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) to[(size_t)e * dv] = dU[e];
+            }
+        }
+        if (!warp_wait(&s.ds, par)) return false;
+        tc_fence_after();
+        float S[H];
+        tmem_ld(at + TM_DF + part * H, S);
+        tmem_ld_wait();
+        if (k + 1 < chunks) {
+            publish_state(S, at + TM_D + part * (H / 2));
+            warp_arrive(&s.s);
+            store(S, p.dS + (size_t)(chunk0 + c - 1) * one);
+            if (!scaled(S, k + 1)) return false;
+        } else if (p.d_init) {
+            store(S, p.d_init + (size_t)n * one);
+        }
+    }
+    return true;
+}
+
+template <int DK>
+__global__ void __launch_bounds__(kThreads, 1) delta_chain_back_kernel(const __grid_constant__ ChainMaps maps, const __grid_constant__ ChainParams p) {
+    extern __shared__ uint8_t raw[];
+    ChainShared &s = *reinterpret_cast<ChainShared *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5;
+    const int h = blockIdx.x % p.f.hv, n = blockIdx.x / p.f.hv;
+    long long begin, end;
+    if (!rows_of(p.f, n, begin, end)) return;
+    const int chunks = (int)((end - begin + C - 1) / C);
+    if (warp == 0) {
+        tmem_alloc(&s.tmem, 512);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.free[i], 1);
+            mbar_init(&s.ready[i], kChainWarps);
+        }
+        for (int i = 0; i < kVecs; ++i) {
+            mbar_init(&s.ready_vec[i], 1);
+            mbar_init(&s.free_vec[i], 1);
+        }
+        for (uint64_t *b : {&s.s, &s.o, &s.pd_read, &s.r, &s.h, &s.u2}) mbar_init(b, kChainWarps);
+        for (uint64_t *b : {&s.pd, &s.kd, &s.u, &s.ds, &s.drain}) mbar_init(b, 1);
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    bool ok = true;
+    if (warp < kChainWarps) {
+        ok = chain<DK>(s, p, n, h, begin, end, chunks, tmem);
+    } else if (warp == kIssuer) {
+        ok = chain_issue<DK>(s, chunks);
+        if (!ok) {  // nothing may be in flight at the end
+            mma_commit_warp(&s.drain);
+            (void)mbar_wait(&s.drain, 0, kWaitNs);
+        }
+    } else if (warp == kLoader) {
+        ok = chain_load<DK>(s, maps, p, n, h, begin, chunks);
+    } else if (warp == kDecays) {
+        ok = chain_decays(s, p, h, begin, end, chunks);
+    }
+    __syncwarp();
+    if (!ok) atomicOr(p.f.err, kErrTimeout);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------- everything of a chunk -----
+
+constexpr int kGradThreads = 512;
+constexpr uint32_t TG_1 = 0;     // [dO; dR] S0^T, scaled, then with [Gp; Ga] K: [dq; row]
+constexpr uint32_t TG_2 = 128;   // U dS^T, scaled, then with Gp^T Q + (b Ga)^T K: col in lanes 0..63
+constexpr uint32_t TG_P = 256;   // [dO; dR] U^T
+constexpr uint32_t TG_A = 320;   // [dO; dR]: two times 64
+
+struct GradShared {
+    uint8_t kq[32768];
+    uint8_t u_hi[16384], u_lo[16384];    // U, per 64 value channels 64 rows
+    uint8_t s_hi[32768], s_lo[32768];    // S0, then dS, per 64 value channels 128 rows (key channels); then rows of b row
+    uint8_t g_hi[16384], g_lo[16384];    // [Gp; Ga], 128 rows
+    uint8_t bg_hi[8192], bg_lo[8192];    // b Ga
+    Vec vec;
+    float a[C], pre[C], f[C];
+    float sums[4][5][C];                 // per quarter of the columns: q.dq, k.row, k.col, k.(the part of col from dS), dR.v
+    float joined[kGradThreads / 32];
+    uint64_t full, b0, b1, b2, b3, b4;
+    uint32_t tmem;
+};
+static_assert(2 * 32768 >= C * (128 + 4) * 4, "b row in the state's place");
+
+struct GradMaps {
+    CUtensorMap q, k;
+};
+struct GradParams {
+    DeltaParams f;
+    const void *d_o;
+    const float *S, *U, *dS, *dR;
+    float *dq, *dk, *dv, *dg, *db;  // dq, dk [rows, value heads, dk]
+};
+
+// N consecutive fp32 values from column c of a row of `width`, zeros past it (width is a multiple of 32, c of 8).
+template <int N>
+__device__ __forceinline__ void load_row(float (&x)[N], const float *row, int c, int width) {
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+        const float4 v = c + e < width ? *reinterpret_cast<const float4 *>(row + c + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[e] = v.x, x[e + 1] = v.y, x[e + 2] = v.z, x[e + 3] = v.w;
+    }
+}
+__device__ __forceinline__ void bf16_pairs(const uint4 &v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[2 * e] = __uint_as_float(w[e] << 16), x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+}
+
+// A state [dk, dv] as the operand of s_hi, s_lo: thread = row and quarter of its columns. With `other`, also the products with that state.
+template <int DK>
+__device__ __forceinline__ float state_operand(GradShared &s, const float *S, const float *other, int dk, int dv) {
+    const int r = threadIdx.x >> 2, c0 = (threadIdx.x & 3) * 32;
+    float sum = 0.f;
+    if (r < DK) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int c = c0 + 8 * e;
+            float x[8];
+            load_row(x, S + (size_t)r * dv, c, r < dk ? dv : 0);
+            if (other) {
+                float y[8];
+                load_row(y, other + (size_t)r * dv, c, r < dk ? dv : 0);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum = fmaf(x[j], y[j], sum);
+            }
+            store_operand(s.s_hi + (c >> 6) * 16384, s.s_lo + (c >> 6) * 16384, r, (c & 63) >> 3, x);
+        }
+    }
+    return sum;
+}
+
+// D = A B^T over the value channels, A and B in two bf16 values each without the product of the rests; one warp.
+template <int DK>
+__global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradParams p) {
+    extern __shared__ uint8_t raw[];
+    GradShared &s = *reinterpret_cast<GradShared *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    constexpr int W = DK / 4;  // key columns of a thread
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hv = p.f.hv, dk = p.f.dk, dv = p.f.dv;
+    const int h = blockIdx.x % hv;
+    const long long slot = blockIdx.x / hv;
+    // The sequence whose chunk has this number, if any: the last one that starts at or before it.
+    int n = 0;
+    for (int hi = p.f.seqs.n_seqs; hi - n > 1;) {
+        const int mid = (n + hi) >> 1;
+        if (first_chunk(p.f.seqs.begin(mid), mid, C) <= slot) n = mid; else hi = mid;
+    }
+    const long long begin = p.f.seqs.begin(n), end = p.f.seqs.end(n), c = slot - first_chunk(begin, n, C);
+    if (begin < 0 || end < begin || end > p.f.seqs.rows || c < 0 || c * C >= end - begin) return;
+    const long long row0 = begin + c * C;
+    const int m = (int)min((long long)C, end - row0);
+    const size_t at_chunk = (size_t)slot * hv + h;
+
+    if (warp == 0) {
+        tmem_alloc(&s.tmem, 512);
+        tmem_relinquish();
+    }
+    if (tid == 32) {
+        for (uint64_t *b : {&s.full, &s.b0, &s.b1, &s.b2, &s.b3, &s.b4}) mbar_init(b, 1);
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
+    const int L = tid & 127, part = tid >> 7, i = L & 63;  // TMEM lane, quarter of the columns, row of the chunk
+    const bool second = L >= 64;                           // a row of dR
+    const uint32_t at = tmem + ((uint32_t)(L & 96) << 16);
+    bool ok = true;
+    if (tid == 0) {
+        mbar_arrive_expect_tx(&s.full, DK / 64 * 16384);
+        for (int a = 0; a < DK / 64; ++a) {
+            tma_load_3d(s.kq + a * 16384, &maps.k, &s.full, 64 * a, h / p.f.per, (int)row0);
+            tma_load_3d(s.kq + a * 16384 + 8192, &maps.q, &s.full, 64 * a, h / p.f.per, (int)row0);
+        }
+    }
+    if (warp == 1) {
+        float own[2], b[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int r = lane + 32 * half;
+            own[half] = r < m ? log_decay(p.f.g[(row0 + r) * hv + h]) : 0.f;
+            b[half] = r < m ? p.f.beta[(row0 + r) * hv + h] : 0.f;
+        }
+        chunk_decays(s.vec, s.a, s.pre, s.f, lane, own, b, [] { return true; });
+    }
+    __syncwarp();
+    {  // [dO; dR], and dv, dR.v on the way
+        const int c0 = 32 * part;
+        uint32_t hi[16], lo[16];
+        if (!second) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (i < m && c0 < dv)
+                    v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.d_o) + ((row0 + i) * hv + h) * dv + c0 + 8 * e);
+                hi[4 * e] = v.x, hi[4 * e + 1] = v.y, hi[4 * e + 2] = v.z, hi[4 * e + 3] = v.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) lo[e] = 0u;
+        } else {
+            float x[32], dot = 0.f;
+            load_row(x, p.dR + (at_chunk * C + i) * dv, c0, dv);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) split2(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
+            if (i < m && c0 < dv) {
+                const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.f.v) + (row0 + i) * p.f.vs + (size_t)h * dv + c0;
+                float *to = p.dv + ((row0 + i) * hv + h) * dv + c0;
+                const float b = p.f.beta[(row0 + i) * hv + h];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float y[8];
+                    bf16_pairs(*reinterpret_cast<const uint4 *>(v + 8 * e), y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) dot = fmaf(x[8 * e + j], y[j], dot);
+                    *reinterpret_cast<float4 *>(to + 8 * e) = make_float4(b * x[8 * e], b * x[8 * e + 1], b * x[8 * e + 2], b * x[8 * e + 3]);
+                    *reinterpret_cast<float4 *>(to + 8 * e + 4) = make_float4(b * x[8 * e + 4], b * x[8 * e + 5], b * x[8 * e + 6], b * x[8 * e + 7]);
+                }
+            }
+            s.sums[part][4][i] = dot;
+        }
+        tmem_st(at + TG_A + 16 * part, hi);
+        tmem_st(at + TG_A + 64 + 16 * part, lo);
+    }
+    {  // U
+        const int r = tid >> 3, c0 = (tid & 7) * 16;
+        float x[16];
+        load_row(x, p.U + (at_chunk * C + r) * dv, c0, dv);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            store_operand(s.u_hi + (c0 >> 6) * 8192, s.u_lo + (c0 >> 6) * 8192, r, ((c0 & 63) >> 3) + e, x + 8 * e);
+    }
+    const float *S0 = p.S + at_chunk * dk * dv, *dS = p.dS + at_chunk * dk * dv;
+    state_operand<DK>(s, S0, nullptr, dk, dv);
+    ok = mbar_wait(&s.full, 0, kWaitNs);
+    if (m < C) {  // the rows behind the sequence are another one's
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        for (int e = tid; e < (C - m) * 8; e += kGradThreads)
+#pragma unroll
+            for (int a = 0; a < DK / 32; ++a) *reinterpret_cast<uint4 *>(&s.kq[a * 8192 + m * 128 + e * 16]) = zero;
+    }
+    tmem_st_wait();
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint64_t u_hi = sdesc_sw128(smem_u32(s.u_hi), 16u, 1024u), s_hi = sdesc_sw128(smem_u32(s.s_hi), 16u, 1024u);
+    constexpr uint64_t kULo = sizeof(s.u_hi) >> 4, kSLo = sizeof(s.s_hi) >> 4, kGLo = sizeof(s.g_hi) >> 4, kBLo = sizeof(s.bg_hi) >> 4;
+    if (warp == 0) {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)  // first x first, first x second, second x first
+#pragma unroll
+            for (int st = 0; st < 8; ++st)
+                mma_bf16_tmem_a_warp(tmem + TG_P, tmem + TG_A + (e == 2 ? 64 : 0) + 8 * st, u_hi + (e == 1 ? kULo : 0) + kstep(st, 8192u),
+                                     idesc_bf16(128, 64), e + st > 0);
+        mma_commit_warp(&s.b0);
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+#pragma unroll
+            for (int st = 0; st < 8; ++st)
+                mma_bf16_tmem_a_warp(tmem + TG_1, tmem + TG_A + (e == 2 ? 64 : 0) + 8 * st, s_hi + (e == 1 ? kSLo : 0) + kstep(st, 16384u),
+                                     idesc_bf16(128, DK), e + st > 0);
+        mma_commit_warp(&s.b1);
+    }
+    __syncwarp();
+    ok = mbar_wait(&s.b0, 0, kWaitNs) && ok;
+    tc_fence_after();
+    const float b_row = s.vec.b[i];
+    {  // Gp, Ga (without b) and b Ga
+        float x[16];
+        tmem_ld(at + TG_P + 16 * part, x);
+        tmem_ld_wait();
+        decay_block(x, s.a, s.pre, s.f, i, 16 * part, !second, second ? -1.f : 1.f);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) store_operand(s.g_hi, s.g_lo, L, 2 * part + e, x + 8 * e);
+        if (second) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] *= b_row;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) store_operand(s.bg_hi, s.bg_lo, i, 2 * part + e, x + 8 * e);
+        }
+    }
+    ok = mbar_wait(&s.b1, 0, kWaitNs) && ok;
+    tc_fence_after();
+    {
+        float x[W];
+        const float E = second ? -s.vec.E[i] : s.vec.E[i];
+        tmem_ld(at + TG_1 + W * part, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < W; ++e) x[e] *= E;
+        tmem_st(at + TG_1 + W * part, x);
+    }
+    float joined = state_operand<DK>(s, dS, S0, dk, dv);  // S0's operand is read: dS in its place
+    tmem_st_wait();
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t kq = smem_u32(s.kq);
+    const uint64_t k_n = sdesc_sw128(kq, 16384u, 1024u), q_n = sdesc_sw128(kq + 8192u, 16384u, 1024u);
+    if (warp == 0) {
+        const uint64_t g = sdesc_sw128(smem_u32(s.g_hi), 16u, 1024u);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int st = 0; st < C / 16; ++st)
+                mma_bf16_warp(tmem + TG_1, g + (e ? kGLo : 0) + kstep(st, 0u), k_n + kDescStepMN128 * st, idesc_bf16(128, DK) | kIdescBMajorMN, 1u);
+        mma_commit_warp(&s.b2);
+        // A: the 64 rows of U; what lies behind them fills lanes 64..127, which are not read.
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+#pragma unroll
+            for (int st = 0; st < 8; ++st)
+                mma_bf16_warp(tmem + TG_2, u_hi + (e == 2 ? kULo : 0) + kstep(st, 8192u), s_hi + (e == 1 ? kSLo : 0) + kstep(st, 16384u),
+                              idesc_bf16(128, DK), e + st > 0);
+        mma_commit_warp(&s.b3);
+    }
+    __syncwarp();
+    // Row i of K or Q, this thread's columns.
+    auto dot_row = [&](const float (&x)[W], uint32_t q) {
+        float sum = 0.f;
+        const int c0 = W * part;
+#pragma unroll
+        for (int e = 0; e < W / 8; ++e) {
+            const int cc = c0 + 8 * e;
+            float y[8];
+            bf16_pairs(*reinterpret_cast<const uint4 *>(&s.kq[(cc >> 6) * 16384 + q * 8192 + i * 128 + ((((cc & 63) >> 3) ^ (i & 7)) << 4)]), y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = fmaf(x[8 * e + j], y[j], sum);
+        }
+        return sum;
+    };
+    const bool stored = i < m && W * part < dk;
+    const size_t out = ((row0 + i) * hv + h) * (size_t)dk + W * part;
+    ok = mbar_wait(&s.b2, 0, kWaitNs) && ok;
+    tc_fence_after();
+    float x[W];
+    tmem_ld(at + TG_1 + W * part, x);
+    tmem_ld_wait();
+    s.sums[part][second ? 1 : 0][i] = dot_row(x, second ? 0u : 1u);
+    if (!second && stored)
+#pragma unroll
+        for (int e = 0; e < W; e += 4) *reinterpret_cast<float4 *>(p.dq + out + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+    ok = mbar_wait(&s.b3, 0, kWaitNs) && ok;
+    tc_fence_after();
+    float *rows = reinterpret_cast<float *>(s.s_hi);  // dS's operand is read: the rows of b row in its place
+    constexpr int kRow = DK + 4;
+    if (second) {
+#pragma unroll
+        for (int e = 0; e < W; e += 4)
+            *reinterpret_cast<float4 *>(rows + i * kRow + W * part + e) = make_float4(b_row * x[e], b_row * x[e + 1], b_row * x[e + 2], b_row * x[e + 3]);
+    } else {
+        const float F = s.vec.F[i];
+        tmem_ld(at + TG_2 + W * part, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < W; ++e) x[e] *= F;
+        s.sums[part][3][i] = dot_row(x, 0u);
+        tmem_st(at + TG_2 + W * part, x);
+        tmem_st_wait();
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) joined += __shfl_xor_sync(0xffffffffu, joined, d);
+    if (lane == 0) s.joined[warp] = joined;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) {
+        // A MN-major: the columns of Gp and of b Ga in lanes 0..63; the next 64 are not read.
+        const uint64_t g = sdesc_sw128(smem_u32(s.g_hi), 8192u, 1024u), bg = sdesc_sw128(smem_u32(s.bg_hi), 8192u, 1024u);
+        constexpr uint32_t kind = idesc_bf16(128, DK) | kIdescAMajorMN | kIdescBMajorMN;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int st = 0; st < C / 16; ++st) {
+                mma_bf16_warp(tmem + TG_2, g + (e ? kGLo : 0) + kDescStepMN128 * st, q_n + kDescStepMN128 * st, kind, 1u);
+                mma_bf16_warp(tmem + TG_2, bg + (e ? kBLo : 0) + kDescStepMN128 * st, k_n + kDescStepMN128 * st, kind, 1u);
+            }
+        mma_commit_warp(&s.b4);
+    }
+    __syncwarp();
+    ok = mbar_wait(&s.b4, 0, kWaitNs) && ok;
+    tc_fence_after();
+    if (!second) {
+        tmem_ld(at + TG_2 + W * part, x);
+        tmem_ld_wait();
+        s.sums[part][2][i] = dot_row(x, 0u);
+        if (stored)
+#pragma unroll
+            for (int e = 0; e < W; e += 4) {
+                const float4 r = *reinterpret_cast<const float4 *>(rows + i * kRow + W * part + e);
+                *reinterpret_cast<float4 *>(p.dk + out + e) = make_float4(x[e] + r.x, x[e + 1] + r.y, x[e + 2] + r.z, x[e + 3] + r.w);
+            }
+    }
+    if (!ok) atomicOr(p.f.err, kErrTimeout);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+    if (warp == 1) {
+        float dG[2], behind[2], inner = lane < kGradThreads / 32 ? s.joined[lane] : 0.f, krow[2], dRv[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int r = lane + 32 * half;
+            float v[5];
+#pragma unroll
+            for (int e = 0; e < 5; ++e) v[e] = (s.sums[0][e][r] + s.sums[1][e][r]) + (s.sums[2][e][r] + s.sums[3][e][r]);
+            dG[half] = v[0] + s.vec.b[r] * v[1] - v[2];
+            krow[half] = v[1];
+            behind[half] = v[3];
+            dRv[half] = v[4];
+        }
+        float through = behind[0] + behind[1];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            through += __shfl_xor_sync(0xffffffffu, through, d);
+            inner += __shfl_xor_sync(0xffffffffu, inner, d);
+        }
+        if (lane == 31) dG[1] += fmaf(s.vec.whole, inner, through);  // <S1, dS>
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2)  // dg_i = sum of dG_j, j >= i
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const float y = __shfl_down_sync(0xffffffffu, dG[half], d);
+                if (lane + d < 32) dG[half] += y;
+            }
+        dG[0] += __shfl_sync(0xffffffffu, dG[1], 0);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int r = lane + 32 * half;
+            if (r < m) {
+                p.dg[(row0 + r) * hv + h] = dG[half];
+                p.db[(row0 + r) * hv + h] = dRv[half] + krow[half];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------- launches ---
+
+long long chunk_slots(const DeltaParams &p) { return p.seqs.rows / C + p.seqs.n_seqs; }
+
+struct Parts {
+    DeltaKept kept;
+    float *dS, *dR;
+    size_t bytes;
+};
+Parts parts_of(const DeltaParams &p, void *ws) {
+    const size_t n = (size_t)chunk_slots(p) * p.hv, state = n * p.dk * p.dv * 4, rows = n * C * p.dv * 4;
+    uint8_t *at = static_cast<uint8_t *>(ws);
+    Parts r;
+    r.kept = DeltaKept{at, reinterpret_cast<float *>(at + n * kDeltaTpBytes), reinterpret_cast<float *>(at + n * kDeltaTpBytes + state)};
+    r.dS = reinterpret_cast<float *>(at + n * kDeltaTpBytes + state + rows);
+    r.dR = reinterpret_cast<float *>(at + n * kDeltaTpBytes + 2 * state + rows);
+    r.bytes = n * kDeltaTpBytes + 2 * state + 2 * rows;
+    return r;
+}
+
+template <typename F>
+cudaError_t more_shared(F *f, size_t bytes) {
+    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <int DK>
+cudaError_t launch(const DeltaParams &p, const DeltaGradients &g, const Parts &w, cudaStream_t s) {
+    ChainMaps maps;
+    GradMaps grad_maps;
+    if (!encode(&maps.q, p.q, p.seqs.rows, p.hk, p.dk, p.qs) || !encode(&maps.k, p.k, p.seqs.rows, p.hk, p.dk, p.ks) ||
+        !encode(&maps.d_o, g.d_o, p.seqs.rows, p.hv, p.dv, (long long)p.hv * p.dv))
+        return cudaErrorInvalidValue;
+    grad_maps.q = maps.q;
+    grad_maps.k = maps.k;
+    cudaError_t e = launch_delta_tc_kept(p, w.kept, s);
+    if (e != cudaSuccess) return e;
+    constexpr size_t chain_bytes = sizeof(ChainShared) + 1024, grad_bytes = sizeof(GradShared) + 1024;
+    static_assert(chain_bytes <= 227 * 1024 && grad_bytes <= 227 * 1024, "shared memory of a block");
+    if ((e = more_shared(&delta_chain_back_kernel<DK>, chain_bytes)) != cudaSuccess) return e;
+    const ChainParams cp{p, w.kept.tp, g.d_fin, w.dS, w.dR, g.d_init};
+    delta_chain_back_kernel<DK><<<(unsigned)((long long)p.seqs.n_seqs * p.hv), kThreads, chain_bytes, s>>>(maps, cp);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = more_shared(&delta_chunk_back_kernel<DK>, grad_bytes)) != cudaSuccess) return e;
+    const GradParams gp{p, g.d_o, w.kept.S, w.kept.U, w.dS, w.dR, g.dq, g.dk, g.dv, g.dg, g.db};
+    delta_chunk_back_kernel<DK><<<(unsigned)(chunk_slots(p) * p.hv), kGradThreads, grad_bytes, s>>>(grad_maps, gp);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t delta_tc_backward_bytes(const DeltaParams &p) { return parts_of(p, nullptr).bytes; }
+
+cudaError_t launch_delta_tc_backward(const DeltaParams &p, const DeltaGradients &g, void *ws, cudaStream_t s) {
+    const Parts w = parts_of(p, ws);
+    return p.dk == 128 ? launch<128>(p, g, w, s) : launch<64>(p, g, w, s);
+}
+
+}  // namespace kda
