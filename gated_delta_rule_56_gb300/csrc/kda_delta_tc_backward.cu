@@ -41,7 +41,7 @@ struct ChainShared {
     uint8_t d_o[kStages][16384];
     uint8_t tp[kStages][kDeltaTpBytes];
     Vec vec[kVecs];
-    uint64_t full[kStages], free[kStages], ready[kStages];
+    uint64_t full[kStages], free[kStages], ready;
     uint64_t ready_vec[kVecs], free_vec[kVecs];
     uint64_t s, o, pd, pd_read, kd, r, u, h, u2, ds, drain;
     uint32_t tmem;
@@ -67,7 +67,16 @@ __device__ __forceinline__ bool chain_issue(ChainShared &s, int chunks) {
         const uint32_t kq = smem_u32(s.kq[st]), tp = smem_u32(s.tp[st]);
         const uint64_t d_k = sdesc_sw128(kq, 16u, 1024u), d_kn = sdesc_sw128(kq, 16384u, 1024u), d_qn = sdesc_sw128(kq + 8192u, 16384u, 1024u);
         const uint64_t d_t = sdesc_sw128(tp, 8192u, 1024u), d_p = sdesc_sw128(tp + 16384u, 8192u, 1024u);  // MN-major: the column is the N index
-        if (!warp_wait(&s.ready[st], (uint32_t)(k / kStages) & 1u) || !warp_wait(&s.o, par)) return false;
+        // The last chunk's rows behind the sequence are cleared first; the others are there as soon as they are loaded.
+        if (!warp_wait(k == 0 ? &s.ready : &s.full[st], (uint32_t)(k / kStages) & 1u) || !warp_wait(&s.s, par)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < DK / 16; ++i)
+                mma_bf16_tmem_a_warp(tmem + TM_KD, tmem + TM_D + 64 * e + 8 * i, d_k + kstep(i, 16384u), idesc_bf16(128, 64), e + i > 0);
+        mma_commit_warp(&s.kd);
+        if (!warp_wait(&s.o, par)) return false;
         tc_fence_after();
 #pragma unroll
         for (int e = 0; e < 2; ++e)
@@ -76,14 +85,6 @@ __device__ __forceinline__ bool chain_issue(ChainShared &s, int chunks) {
                 mma_bf16_tmem_a_warp(tmem + TM_PD, tmem + TM_O + 8 * i, d_p + 512u * e + kDescStepMN128 * i, idesc_bf16(128, 64) | kIdescBMajorMN,
                                      e + i > 0);
         mma_commit_warp(&s.pd);
-        if (!warp_wait(&s.s, par)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int i = 0; i < DK / 16; ++i)
-                mma_bf16_tmem_a_warp(tmem + TM_KD, tmem + TM_D + 64 * e + 8 * i, d_k + kstep(i, 16384u), idesc_bf16(128, 64), e + i > 0);
-        mma_commit_warp(&s.kd);
         if (!warp_wait(&s.r, par)) return false;
         tc_fence_after();
 #pragma unroll
@@ -169,31 +170,32 @@ __device__ __forceinline__ bool chain(ChainShared &s, const ChainParams &p, int 
     const int keys = min(max(dk - part * H, 0), H);
     const uint32_t o_in = (uint32_t)(col >> 6) * 8192u + (uint32_t)(col & 7) * 2u + (uint32_t)t0 * 128u, piece = (uint32_t)(col & 63) >> 3;
     const long long chunk0 = first_chunk(begin, n, C);
-    auto scaled = [&](float (&S)[H], int k) -> bool {
+    auto scaled = [&](const float (&S)[H], int k) -> bool {
         if (!warp_wait(&s.ready_vec[k % kVecs], (uint32_t)(k / kVecs) & 1u)) return false;
         const float whole = s.vec[k % kVecs].whole;
+        float x[H];
 #pragma unroll
-        for (int e = 0; e < H; ++e) S[e] *= whole;
-        tmem_st(at + TM_DF + part * H, S);
+        for (int e = 0; e < H; ++e) x[e] = whole * S[e];
+        tmem_st(at + TM_DF + part * H, x);
         return true;
     };
-    auto store = [&](const float (&S)[H], float *to) {
+    float S[H];
+    auto store = [&](float *to) {
         if (live)
 #pragma unroll
             for (int e = 0; e < H; ++e)
                 if (e < keys) to[in + (size_t)e * dv] = S[e];
     };
     {
-        float S[H];
 #pragma unroll
         for (int e = 0; e < H; ++e) S[e] = p.d_fin && live && e < keys ? p.d_fin[(size_t)n * one + in + (size_t)e * dv] : 0.f;
         if (chunks == 0) {
-            if (p.d_init) store(S, p.d_init + (size_t)n * one);
+            if (p.d_init) store(p.d_init + (size_t)n * one);
             return true;
         }
         publish_state(S, at + TM_D + part * (H / 2));
         warp_arrive(&s.s);
-        store(S, p.dS + (size_t)(chunk0 + chunks - 1) * one);
+        store(p.dS + (size_t)(chunk0 + chunks - 1) * one);
         if (!scaled(S, 0)) return false;
     }
 #pragma unroll 1
@@ -209,7 +211,7 @@ __device__ __forceinline__ bool chain(ChainShared &s, const ChainParams &p, int 
                 for (int a = 0; a < DK / 32; ++a) *reinterpret_cast<uint4 *>(&s.kq[st][a * 8192 + m * 128 + e * 16]) = zero;
             fence_async_smem();
         }
-        warp_arrive(&s.ready[st]);
+        if (k == 0) warp_arrive(&s.ready);
         // dO^T: exact for P, with its decay for Q
         float d_o[16];
         {
@@ -293,16 +295,15 @@ __device__ __forceinline__ bool chain(ChainShared &s, const ChainParams &p, int 
         }
         if (!warp_wait(&s.ds, par)) return false;
         tc_fence_after();
-        float S[H];
         tmem_ld(at + TM_DF + part * H, S);
         tmem_ld_wait();
         if (k + 1 < chunks) {
             publish_state(S, at + TM_D + part * (H / 2));
             warp_arrive(&s.s);
-            store(S, p.dS + (size_t)(chunk0 + c - 1) * one);
+            store(p.dS + (size_t)(chunk0 + c - 1) * one);
             if (!scaled(S, k + 1)) return false;
         } else if (p.d_init) {
-            store(S, p.d_init + (size_t)n * one);
+            store(p.d_init + (size_t)n * one);
         }
     }
     return true;
@@ -325,8 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chain_back_kernel(const __g
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.free[i], 1);
-            mbar_init(&s.ready[i], kChainWarps);
         }
+        mbar_init(&s.ready, kChainWarps);
         for (int i = 0; i < kVecs; ++i) {
             mbar_init(&s.ready_vec[i], 1);
             mbar_init(&s.free_vec[i], 1);
@@ -372,7 +373,7 @@ constexpr uint32_t TG_A = 320;   // [dO; dR]: two times 64
 struct GradShared {
     uint8_t kq[32768];
     uint8_t u_hi[16384], u_lo[16384];    // U, per 64 value channels 64 rows
-    uint8_t s_hi[32768], s_lo[32768];    // S0, then dS, per 64 value channels 128 rows (key channels); then rows of b row
+    uint8_t s_hi[32768], s_lo[32768];    // S0, then dS, per 64 value channels 128 rows (key channels)
     uint8_t g_hi[16384], g_lo[16384];    // [Gp; Ga], 128 rows
     uint8_t bg_hi[8192], bg_lo[8192];    // b Ga
     Vec vec;
@@ -382,8 +383,6 @@ struct GradShared {
     uint64_t full, b0, b1, b2, b3, b4;
     uint32_t tmem;
 };
-static_assert(2 * 32768 >= C * (128 + 4) * 4, "b row in the state's place");
-
 struct GradMaps {
     CUtensorMap q, k;
 };
@@ -409,30 +408,44 @@ __device__ __forceinline__ void bf16_pairs(const uint4 &v, float (&x)[8]) {
     for (int e = 0; e < 4; ++e) x[2 * e] = __uint_as_float(w[e] << 16), x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
 }
 
-// A state [dk, dv] as the operand of s_hi, s_lo: thread = row and quarter of its columns. With `other`, also the products with that state.
-template <int DK>
-__device__ __forceinline__ float state_operand(GradShared &s, const float *S, const float *other, int dk, int dv) {
-    const int r = threadIdx.x >> 2, c0 = (threadIdx.x & 3) * 32;
-    float sum = 0.f;
-    if (r < DK) {
+// A state [dk, dv]: thread = half a line's 16-byte words, so a warp reads two lines; N = DK / 32 pieces of 8 values.
+template <int N>
+__device__ __forceinline__ void load_state(float (&x)[N][8], const float *S, int dk, int dv) {
+    const int c = (threadIdx.x & 15) * 8;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int c = c0 + 8 * e;
-            float x[8];
-            load_row(x, S + (size_t)r * dv, c, r < dk ? dv : 0);
-            if (other) {
-                float y[8];
-                load_row(y, other + (size_t)r * dv, c, r < dk ? dv : 0);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum = fmaf(x[j], y[j], sum);
-            }
-            store_operand(s.s_hi + (c >> 6) * 16384, s.s_lo + (c >> 6) * 16384, r, (c & 63) >> 3, x);
-        }
+    for (int e = 0; e < N; ++e) {
+        const int r = (threadIdx.x >> 4) + 32 * e;
+        load_row(x[e], S + (size_t)r * dv, c, r < dk ? dv : 0);
     }
-    return sum;
+}
+// The same as the operand of s_hi, s_lo.
+template <int N>
+__device__ __forceinline__ void state_operand(GradShared &s, const float (&x)[N][8]) {
+    const int c = (threadIdx.x & 15) * 8;
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        store_operand(s.s_hi + (c >> 6) * 16384, s.s_lo + (c >> 6) * 16384, (threadIdx.x >> 4) + 32 * e, (c & 63) >> 3, x[e]);
 }
 
-// D = A B^T over the value channels, A and B in two bf16 values each without the product of the rests; one warp.
+static_assert(2 * 16384 + 2 * 32768 >= 2 * C * 132 * 4 && 2 * 16384 + 2 * 8192 >= C * 132 * 4, "rows in the operands' places");
+
+// A chunk's fp32 outputs leave through shared memory: a thread holds a part of a row, and 32 lanes that write to 32 rows at a time take four
+// times as long.
+constexpr int kPitch = 132;  // floats between rows there
+template <int N>
+__device__ __forceinline__ void put_row(float *rows, int i, int c, const float (&x)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; e += 4) *reinterpret_cast<float4 *>(rows + i * kPitch + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+}
+// All threads, behind a barrier: rows 0 .. m - 1 of `width` values (a multiple of 32), `stride` apart in `to`.
+__device__ __forceinline__ void rows_out(float *to, size_t stride, const float *rows, int m, int width) {
+    const int c = (threadIdx.x & 31) * 4;
+    if (c < width)
+#pragma unroll
+        for (int r = threadIdx.x >> 5; r < C; r += kGradThreads / 32)
+            if (r < m) *reinterpret_cast<float4 *>(to + r * stride + c) = *reinterpret_cast<const float4 *>(rows + r * kPitch + c);
+}
+
 template <int DK>
 __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradParams p) {
     extern __shared__ uint8_t raw[];
@@ -453,6 +466,26 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
     const long long row0 = begin + c * C;
     const int m = (int)min((long long)C, end - row0);
     const size_t at_chunk = (size_t)slot * hv + h;
+    const int L = tid & 127, part = tid >> 7, i = L & 63;  // TMEM lane, quarter of the columns, row of the chunk
+    const bool second = L >= 64;                           // a row of dR
+    // The loads of the first products, all in flight together.
+    constexpr int N = DK / 32;
+    const float *S0 = p.S + at_chunk * dk * dv, *dS = p.dS + at_chunk * dk * dv;
+    float state[N][8], u_row[16], dR[32], beta_row = 0.f;
+    uint4 words[4];  // of dO's row, or v's
+    {
+        const bool there = i < m && 32 * part < dv;
+        const __nv_bfloat16 *from = second ? static_cast<const __nv_bfloat16 *>(p.f.v) + (row0 + i) * p.f.vs + (size_t)h * dv
+                                           : static_cast<const __nv_bfloat16 *>(p.d_o) + ((row0 + i) * hv + h) * dv;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) words[e] = there ? *reinterpret_cast<const uint4 *>(from + 32 * part + 8 * e) : make_uint4(0u, 0u, 0u, 0u);
+        if (second) {
+            load_row(dR, p.dR + (at_chunk * C + i) * dv, 32 * part, dv);
+            if (there) beta_row = p.f.beta[(row0 + i) * hv + h];
+        }
+    }
+    load_row(u_row, p.U + (at_chunk * C + (tid >> 3)) * dv, (tid & 7) * 16, dv);
+    load_state(state, S0, dk, dv);
 
     if (warp == 0) {
         tmem_alloc(&s.tmem, 512);
@@ -466,8 +499,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
-    const int L = tid & 127, part = tid >> 7, i = L & 63;  // TMEM lane, quarter of the columns, row of the chunk
-    const bool second = L >= 64;                           // a row of dR
     const uint32_t at = tmem + ((uint32_t)(L & 96) << 16);
     bool ok = true;
     if (tid == 0) {
@@ -493,48 +524,35 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
         uint32_t hi[16], lo[16];
         if (!second) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (i < m && c0 < dv)
-                    v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.d_o) + ((row0 + i) * hv + h) * dv + c0 + 8 * e);
-                hi[4 * e] = v.x, hi[4 * e + 1] = v.y, hi[4 * e + 2] = v.z, hi[4 * e + 3] = v.w;
-            }
+            for (int e = 0; e < 4; ++e) hi[4 * e] = words[e].x, hi[4 * e + 1] = words[e].y, hi[4 * e + 2] = words[e].z, hi[4 * e + 3] = words[e].w;
 #pragma unroll
             for (int e = 0; e < 16; ++e) lo[e] = 0u;
         } else {
-            float x[32], dot = 0.f;
-            load_row(x, p.dR + (at_chunk * C + i) * dv, c0, dv);
+            float dot = 0.f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) split2(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
-            if (i < m && c0 < dv) {
-                const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.f.v) + (row0 + i) * p.f.vs + (size_t)h * dv + c0;
-                float *to = p.dv + ((row0 + i) * hv + h) * dv + c0;
-                const float b = p.f.beta[(row0 + i) * hv + h];
+            for (int e = 0; e < 16; ++e) split2(dR[2 * e], dR[2 * e + 1], hi[e], lo[e]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float y[8];
-                    bf16_pairs(*reinterpret_cast<const uint4 *>(v + 8 * e), y);
+            for (int e = 0; e < 4; ++e) {
+                float y[8];
+                bf16_pairs(words[e], y);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) dot = fmaf(x[8 * e + j], y[j], dot);
-                    *reinterpret_cast<float4 *>(to + 8 * e) = make_float4(b * x[8 * e], b * x[8 * e + 1], b * x[8 * e + 2], b * x[8 * e + 3]);
-                    *reinterpret_cast<float4 *>(to + 8 * e + 4) = make_float4(b * x[8 * e + 4], b * x[8 * e + 5], b * x[8 * e + 6], b * x[8 * e + 7]);
-                }
+                for (int j = 0; j < 8; ++j) dot = fmaf(dR[8 * e + j], y[j], dot);
             }
             s.sums[part][4][i] = dot;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) dR[e] *= beta_row;
+            put_row(reinterpret_cast<float *>(s.g_hi), i, c0, dR);  // dv, in the place of Gp and Ga, which come later
         }
         tmem_st(at + TG_A + 16 * part, hi);
         tmem_st(at + TG_A + 64 + 16 * part, lo);
     }
-    {  // U
+    {
         const int r = tid >> 3, c0 = (tid & 7) * 16;
-        float x[16];
-        load_row(x, p.U + (at_chunk * C + r) * dv, c0, dv);
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-            store_operand(s.u_hi + (c0 >> 6) * 8192, s.u_lo + (c0 >> 6) * 8192, r, ((c0 & 63) >> 3) + e, x + 8 * e);
+            store_operand(s.u_hi + (c0 >> 6) * 8192, s.u_lo + (c0 >> 6) * 8192, r, ((c0 & 63) >> 3) + e, u_row + 8 * e);
     }
-    const float *S0 = p.S + at_chunk * dk * dv, *dS = p.dS + at_chunk * dk * dv;
-    state_operand<DK>(s, S0, nullptr, dk, dv);
+    state_operand(s, state);
     ok = mbar_wait(&s.full, 0, kWaitNs);
     if (m < C) {  // the rows behind the sequence are another one's
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -566,8 +584,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
         mma_commit_warp(&s.b1);
     }
     __syncwarp();
+    rows_out(p.dv + (row0 * hv + h) * dv, (size_t)hv * dv, reinterpret_cast<const float *>(s.g_hi), m, dv);
+    float joined = 0.f;  // <S0, dS>
+    {
+        float d[N][8];
+        load_state(d, dS, dk, dv);
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                joined = fmaf(state[e][j], d[e][j], joined);
+                state[e][j] = d[e][j];
+            }
+    }
     ok = mbar_wait(&s.b0, 0, kWaitNs) && ok;
     tc_fence_after();
+    __syncthreads();  // dv is out of the place
     const float b_row = s.vec.b[i];
     {  // Gp, Ga (without b) and b Ga
         float x[16];
@@ -594,7 +626,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
         for (int e = 0; e < W; ++e) x[e] *= E;
         tmem_st(at + TG_1 + W * part, x);
     }
-    float joined = state_operand<DK>(s, dS, S0, dk, dv);  // S0's operand is read: dS in its place
+    state_operand(s, state);  // S0's operand is read: dS in its place
     tmem_st_wait();
     fence_async_smem();
     tc_fence_before();
@@ -634,38 +666,20 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
         }
         return sum;
     };
-    const bool stored = i < m && W * part < dk;
-    const size_t out = ((row0 + i) * hv + h) * (size_t)dk + W * part;
-    ok = mbar_wait(&s.b2, 0, kWaitNs) && ok;
-    tc_fence_after();
+    const int kc = W * part;  // this thread's first key column
     float x[W];
-    tmem_ld(at + TG_1 + W * part, x);
-    tmem_ld_wait();
-    s.sums[part][second ? 1 : 0][i] = dot_row(x, second ? 0u : 1u);
-    if (!second && stored)
-#pragma unroll
-        for (int e = 0; e < W; e += 4) *reinterpret_cast<float4 *>(p.dq + out + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-    ok = mbar_wait(&s.b3, 0, kWaitNs) && ok;
+    ok = mbar_wait(&s.b3, 0, kWaitNs) && ok;  // also: U's and dS's operands are read
     tc_fence_after();
-    float *rows = reinterpret_cast<float *>(s.s_hi);  // dS's operand is read: the rows of b row in its place
-    constexpr int kRow = DK + 4;
-    if (second) {
-#pragma unroll
-        for (int e = 0; e < W; e += 4)
-            *reinterpret_cast<float4 *>(rows + i * kRow + W * part + e) = make_float4(b_row * x[e], b_row * x[e + 1], b_row * x[e + 2], b_row * x[e + 3]);
-    } else {
+    if (!second) {
         const float F = s.vec.F[i];
-        tmem_ld(at + TG_2 + W * part, x);
+        tmem_ld(at + TG_2 + kc, x);
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < W; ++e) x[e] *= F;
         s.sums[part][3][i] = dot_row(x, 0u);
-        tmem_st(at + TG_2 + W * part, x);
+        tmem_st(at + TG_2 + kc, x);
         tmem_st_wait();
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) joined += __shfl_xor_sync(0xffffffffu, joined, d);
-    if (lane == 0) s.joined[warp] = joined;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -683,24 +697,41 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
         mma_commit_warp(&s.b4);
     }
     __syncwarp();
+    // dq and b row in the place of the operands of U and dS
+    float *dq_rows = reinterpret_cast<float *>(s.u_hi), *row_rows = dq_rows + C * kPitch;
+    ok = mbar_wait(&s.b2, 0, kWaitNs) && ok;
+    tc_fence_after();
+    tmem_ld(at + TG_1 + kc, x);
+    tmem_ld_wait();
+    s.sums[part][second ? 1 : 0][i] = dot_row(x, second ? 0u : 1u);
+    if (second)
+#pragma unroll
+        for (int e = 0; e < W; ++e) x[e] *= b_row;
+    put_row(second ? row_rows : dq_rows, i, kc, x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) joined += __shfl_xor_sync(0xffffffffu, joined, d);
+    if (lane == 0) s.joined[warp] = joined;
+    __syncthreads();
+    rows_out(p.dq + (row0 * hv + h) * dk, (size_t)hv * dk, dq_rows, m, dk);
     ok = mbar_wait(&s.b4, 0, kWaitNs) && ok;
     tc_fence_after();
     if (!second) {
-        tmem_ld(at + TG_2 + W * part, x);
+        tmem_ld(at + TG_2 + kc, x);
         tmem_ld_wait();
         s.sums[part][2][i] = dot_row(x, 0u);
-        if (stored)
 #pragma unroll
-            for (int e = 0; e < W; e += 4) {
-                const float4 r = *reinterpret_cast<const float4 *>(rows + i * kRow + W * part + e);
-                *reinterpret_cast<float4 *>(p.dk + out + e) = make_float4(x[e] + r.x, x[e + 1] + r.y, x[e + 2] + r.z, x[e + 3] + r.w);
-            }
+        for (int e = 0; e < W; e += 4) {
+            const float4 r = *reinterpret_cast<const float4 *>(row_rows + i * kPitch + kc + e);
+            x[e] += r.x, x[e + 1] += r.y, x[e + 2] += r.z, x[e + 3] += r.w;
+        }
+        put_row(row_rows, i, kc, x);  // dk
     }
     if (!ok) atomicOr(p.f.err, kErrTimeout);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, 512);
+    rows_out(p.dk + (row0 * hv + h) * dk, (size_t)hv * dk, row_rows, m, dk);
     if (warp == 1) {
         float dG[2], behind[2], inner = lane < kGradThreads / 32 ? s.joined[lane] : 0.f, krow[2], dRv[2];
 #pragma unroll
