@@ -47,11 +47,10 @@ struct Shared {
     uint8_t kq[kKqStages][kKqBytes];  // per 64 key channels: 64 rows of K, 64 rows of Q
     uint8_t v[kVStages][kVBytes];     // per 64 value channels: 64 rows
     uint8_t tp[kTpStages][kTpBytes];  // T - I (two bf16 values), P (two)
-    float A[C][C + 4];
-    float Y[32][36];
+    float D[C][20];                   // A's blocks of 16 on the diagonal
     Vec vec[kVecs];
     float a[2][C], pre[2][C], f[2][C];  // decays: of a row; within its block of 16, up to the row; from the row to the block's end
-    uint64_t full_kq[kKqStages], free_kq[kKqStages], ready_kq[kKqStages];
+    uint64_t full_kq[kKqStages], free_kq[kKqStages], ready_kq;
     uint64_t full_v[kVStages], free_v[kVStages], ready_v[kVStages];
     uint64_t free_tp[kTpStages], ready_tp[kTpStages];
     uint64_t free_vec[kVecs], ready_decays[2];
@@ -80,46 +79,82 @@ __device__ __forceinline__ bool prep_all(bool ok) {
 }
 // ------------------------------------------------------------------------ prep -----------
 
-// acc += A (16 x K) B (K x 8), fp32 in shared memory, one warp: tf32 MMAs over two values per operand (2^-21 of a product is left).
-__device__ __forceinline__ void two_tf32(float x, uint32_t &hi, uint32_t &lo) {
-    hi = __float_as_uint(x) & 0xffffe000u;
-    lo = __float_as_uint(x - __uint_as_float(hi));
+// ---- the inverse of I + A, in place of A's operand. T = I + N with N strictly lower; blocks of 16, then
+//     X21 = -(I + N22) A21 (I + N11)
+// twice (16 -> 32 -> 64). All operands are two bf16 values in the operand's own 128-byte swizzled rows (the product of the rests is left out), and
+// the products are transposed: Y^T = A21^T + N11^T A21^T leaves its accumulators as the A operand of X21^T = -(Y^T + Y^T N22^T).
+
+__device__ __forceinline__ uint32_t element(uint32_t base, int r, int c) { return base + (uint32_t)r * 128u + (uint32_t)((((c >> 3) ^ (r & 7)) << 4)); }
+// 16 x 16 values from (r, c): as the A operand of rows r.., or the two B operands of columns n = row, k = column.
+__device__ __forceinline__ void load_tile(uint32_t (&f)[4], uint32_t base, int r, int c, int lane) {
+    const uint32_t at = element(base, r + (lane & 15), c + 8 * (lane >> 4));
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3]) : "r"(at) : "memory");
 }
-__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+// The transposed tile as an A operand, and back.
+__device__ __forceinline__ uint32_t turned(uint32_t base, int r, int c, int lane) {
+    return element(base, r + (lane & 7) + 8 * (lane >> 4), c + 8 * ((lane >> 3) & 1));
 }
-template <int K>
-__device__ __forceinline__ void warp_product(float (&acc)[4], const float *A, int as, const float *B, int bs, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    float more[2][4] = {};  // three chains of MMAs
+__device__ __forceinline__ void load_turned(uint32_t (&f)[4], uint32_t base, int r, int c, int lane) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+                 : "r"(turned(base, r, c, lane))
+                 : "memory");
+}
+__device__ __forceinline__ void store_turned(const uint32_t (&f)[4], uint32_t base, int r, int c, int lane) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(turned(base, r, c, lane)), "r"(f[0]), "r"(f[1]),
+                 "r"(f[2]), "r"(f[3])
+                 : "memory");
+}
+struct Tile {  // two bf16 values each
+    uint32_t hi[4], lo[4];
+};
+constexpr uint32_t kLo = 8192;  // from an operand's first values to its second
+__device__ __forceinline__ Tile tile(uint32_t T, int r, int c, int lane) {
+    Tile t;
+    load_tile(t.hi, T, r, c, lane);
+    load_tile(t.lo, T + kLo, r, c, lane);
+    return t;
+}
+__device__ __forceinline__ Tile tile_turned(uint32_t T, int r, int c, int lane) {
+    Tile t;
+    load_turned(t.hi, T, r, c, lane);
+    load_turned(t.lo, T + kLo, r, c, lane);
+    return t;
+}
+// Accumulators of 16 x 16 (two of 16 x 8) from and to such a tile.
+__device__ __forceinline__ void to_sums(float (&d)[2][4], const Tile &t) {
 #pragma unroll
-    for (int k = 0; k < K; k += 8) {
-        uint32_t ah[4], al[4], bh[2], bl[2];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) two_tf32(A[(g + 8 * (e & 1)) * as + k + t + 4 * (e >> 1)], ah[e], al[e]);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) two_tf32(B[(k + t + 4 * e) * bs + g], bh[e], bl[e]);
-        mma_tf32(acc, ah, bh);
-        mma_tf32(more[0], ah, bl);
-        mma_tf32(more[1], al, bh);
+    for (int e = 0; e < 4; ++e) {
+        d[e >> 1][2 * (e & 1)] = __uint_as_float(t.hi[e] << 16) + __uint_as_float(t.lo[e] << 16);
+        d[e >> 1][2 * (e & 1) + 1] = __uint_as_float(t.hi[e] & 0xffff0000u) + __uint_as_float(t.lo[e] & 0xffff0000u);
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] += more[0][e] + more[1][e];
 }
-__device__ __forceinline__ void warp_store(float *out, int os, const float (&acc)[4], float sign, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    *reinterpret_cast<float2 *>(out + g * os + 2 * t) = make_float2(sign * acc[0], sign * acc[1]);
-    *reinterpret_cast<float2 *>(out + (g + 8) * os + 2 * t) = make_float2(sign * acc[2], sign * acc[3]);
+__device__ __forceinline__ Tile from_sums(const float (&d)[2][4], float sign) {
+    Tile t;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2(sign * d[e >> 1][2 * (e & 1)], sign * d[e >> 1][2 * (e & 1) + 1], t.hi[e], t.lo[e]);
+    return t;
+}
+__device__ __forceinline__ void mma_16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// d += A B^T, 16 x 16 x 16.
+__device__ __forceinline__ void product(float (&d)[2][4], const Tile &a, const Tile &b) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) mma_16(d[n], a.hi, b.hi[n], b.hi[n + 2]);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) mma_16(d[n], a.hi, b.lo[n], b.lo[n + 2]);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) mma_16(d[n], a.lo, b.hi[n], b.hi[n + 2]);
 }
 
-// (I + A)^-1 in place of A (strictly lower; the blocks right of the diagonal ones are not read), 8 warps: 16 x 16 blocks by
-// substitution, then joined twice: the block below the diagonal is -X22 A21 X11.
-__device__ __forceinline__ void invert(Shared &s, int pt) {
-    constexpr int L = C + 4;
+// s.D: the 16 x 16 blocks on A's diagonal in fp32; T: the operand.
+__device__ __forceinline__ void invert(Shared &s, uint8_t *operand, int pt) {
     const int w = pt >> 5, lane = pt & 31;
-    if (w < 4) {
+    const uint32_t T = smem_u32(operand);
+    if (w < 4) {  // by substitution, lane = column
         const int j = lane & 15, o = 16 * w;
         float x[16];
 #pragma unroll
@@ -128,48 +163,70 @@ __device__ __forceinline__ void invert(Shared &s, int pt) {
         for (int m = 0; m < 16; m += 4) {  // four columns of A at a time
             float4 own[4];
 #pragma unroll
-            for (int i = 1; i < 4; ++i) own[i] = *reinterpret_cast<const float4 *>(&s.A[o + m + i][o + m]);
+            for (int i = 1; i < 4; ++i) own[i] = *reinterpret_cast<const float4 *>(&s.D[o + m + i][m]);
             x[m + 1] = fmaf(-own[1].x, x[m], x[m + 1]);
             x[m + 2] = fmaf(-own[2].y, x[m + 1], fmaf(-own[2].x, x[m], x[m + 2]));
             x[m + 3] = fmaf(-own[3].z, x[m + 2], fmaf(-own[3].y, x[m + 1], fmaf(-own[3].x, x[m], x[m + 3])));
 #pragma unroll
             for (int i = m + 4; i < 16; ++i) {
-                const float4 a = *reinterpret_cast<const float4 *>(&s.A[o + i][o + m]);
+                const float4 a = *reinterpret_cast<const float4 *>(&s.D[o + i][m]);
                 x[i] = fmaf(-a.w, x[m + 3], fmaf(-a.z, x[m + 2], fmaf(-a.y, x[m + 1], fmaf(-a.x, x[m], x[i]))));
             }
         }
-        __syncwarp();
         if (lane < 16)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s.A[o + i][o + j] = x[i];
+            for (int i = 0; i < 16; i += 2) {  // N: without the ones
+                uint32_t hi, lo;
+                split2(i > j ? x[i] : 0.f, i + 1 > j ? x[i + 1] : 0.f, hi, lo);
+                const uint32_t a0 = (uint32_t)(o + i) * 128u + (uint32_t)((((o + j) >> 3) ^ (i & 7)) << 4) + (uint32_t)(j & 7) * 2u;
+                const uint32_t a1 = (uint32_t)(o + i + 1) * 128u + (uint32_t)((((o + j) >> 3) ^ ((i + 1) & 7)) << 4) + (uint32_t)(j & 7) * 2u;
+                *reinterpret_cast<uint16_t *>(operand + a0) = (uint16_t)hi;
+                *reinterpret_cast<uint16_t *>(operand + kLo + a0) = (uint16_t)lo;
+                *reinterpret_cast<uint16_t *>(operand + a1) = (uint16_t)(hi >> 16);
+                *reinterpret_cast<uint16_t *>(operand + kLo + a1) = (uint16_t)(lo >> 16);
+            }
     }
     prep_sync();
-    {
-        const int o = 32 * (w >> 1), n = 8 * (w & 1);
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        if (w < 4) {
-            warp_product<16>(acc, &s.A[o + 16][o], L, &s.A[o][o + n], L, lane);
-            warp_store(&s.Y[o >> 1][n], 36, acc, 1.f, lane);
-        }
-        prep_sync();
-        if (w < 4) {
-            acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-            warp_product<16>(acc, &s.A[o + 16][o + 16], L, &s.Y[o >> 1][n], 36, lane);
-            warp_store(&s.A[o + 16][o + n], L, acc, -1.f, lane);
-        }
+    if (w < 2) {  // two pairs of blocks
+        const int o = 32 * w;
+        float y[2][4];
+        to_sums(y, tile_turned(T, o + 16, o, lane));
+        product(y, tile_turned(T, o, o, lane), tile(T, o + 16, o, lane));
+        const Tile Y = from_sums(y, 1.f);
+        product(y, Y, tile(T, o + 16, o + 16, lane));
+        const Tile X = from_sums(y, -1.f);
+        __syncwarp();
+        store_turned(X.hi, T, o + 16, o, lane);
+        store_turned(X.lo, T + kLo, o + 16, o, lane);
     }
     prep_sync();
-    {
-        const int o = 16 * (w & 1), n = 8 * (w >> 1);
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        warp_product<32>(acc, &s.A[32 + o][0], L, &s.A[0][n], L, lane);
-        warp_store(&s.Y[o][n], 36, acc, 1.f, lane);
-        prep_sync();
-        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-        warp_product<32>(acc, &s.A[32 + o][32], L, &s.Y[0][n], 36, lane);
-        warp_store(&s.A[32 + o][n], L, acc, -1.f, lane);
+    Tile X;
+    const int c = 16 * (w & 1), r = 32 + 16 * ((w >> 1) & 1);  // this warp's columns and rows of the last block
+    if (w < 4) {
+        float y[2][2][4];  // rows 32..47 and 48..63 of A21
+#pragma unroll
+        for (int e = 0; e < 2; ++e) to_sums(y[e], tile_turned(T, 32 + 16 * e, c, lane));
+#pragma unroll
+        for (int k = 0; k < 32; k += 16)
+            if (k >= c) {
+                const Tile n11 = tile_turned(T, k, c, lane);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) product(y[e], n11, tile(T, 32 + 16 * e, k, lane));
+            }
+        float x[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[n][e] = r == 32 ? y[0][n][e] : y[1][n][e];
+        product(x, from_sums(y[0], 1.f), tile(T, r, 32, lane));
+        if (r == 48) product(x, from_sums(y[1], 1.f), tile(T, r, 48, lane));
+        X = from_sums(x, -1.f);
     }
-    prep_sync();
+    prep_sync();  // A21 is read
+    if (w < 4) {
+        store_turned(X.hi, T, r, c, lane);
+        store_turned(X.lo, T + kLo, r, c, lane);
+    }
 }
 
 // The chunks' decays, by one warp, up to two chunks ahead of the chain.
@@ -199,7 +256,7 @@ __device__ __forceinline__ bool decays(Shared &s, const DeltaParams &p, int h, l
 
 template <int DK>
 __device__ __forceinline__ bool prep(Shared &s, const DeltaParams &p, int h, long long begin, long long end, int chunks, uint32_t tmem) {
-    const int pt = threadIdx.x - kChainWarps * 32, lane = pt & 31, w = pt >> 5;
+    const int pt = threadIdx.x - kChainWarps * 32, w = pt >> 5;
     // A warp's rows: quarter w % 4 of [K; Q], columns of half w / 4. Rows 0..31 have nothing in the second half.
     const int i = pt & 63, c0 = 32 * (w >> 2);
     const bool q_row = w & 2, live = (w & 1) || w < 4;
@@ -222,7 +279,7 @@ __device__ __forceinline__ bool prep(Shared &s, const DeltaParams &p, int h, lon
             }
             fence_async_smem();
         }
-        warp_arrive(&s.ready_kq[ks]);
+        if (c == chunks - 1) warp_arrive(&s.ready_kq);
         warp_arrive(&s.ready_v[vs]);
         if (c >= kTpStages) ok = ok && mbar_wait(&s.free_tp[ts], (uint32_t)(c / kTpStages - 1) & 1u, kWaitNs);
         if (!prep_all(ok && mbar_wait(&s.ready_decays[c & 1], (uint32_t)(c >> 1) & 1u, kWaitNs) && mbar_wait(&s.kk, (uint32_t)c & 1u, kWaitNs)))
@@ -238,36 +295,20 @@ __device__ __forceinline__ bool prep(Shared &s, const DeltaParams &p, int h, lon
             const float scale = q_row ? 1.f : s.vec[c % kVecs].b[i];
 #pragma unroll
             for (int b = 0; b < 2; ++b) decay_block(x + 16 * b, s.a[c & 1], s.pre[c & 1], s.f[c & 1], i, c0 + 16 * b, q_row, scale);
-            if (q_row) {
+            uint8_t *to = q_row ? tp + 16384 : tp;  // P, or A until it is inverted
 #pragma unroll
-                for (int e = 0; e < 4; ++e) store_operand(tp + 16384, tp + 24576, i, c0 / 8 + e, &x[8 * e]);
-            } else {
+            for (int e = 0; e < 4; ++e) store_operand(to, to + kLo, i, c0 / 8 + e, &x[8 * e]);
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<float4 *>(&s.A[i][c0 + e]) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-            }
+            for (int b = 0; b < 2; ++b)
+                if (!q_row && c0 + 16 * b == (i & 48))
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        *reinterpret_cast<float4 *>(&s.D[i][e]) = make_float4(x[16 * b + e], x[16 * b + e + 1], x[16 * b + e + 2], x[16 * b + e + 3]);
         }
         prep_sync();
-        invert(s, pt);
-        {
-            const int r = pt >> 2, e0 = (pt & 3) * 16;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int at0 = e0 + 8 * e;
-                if (at0 > (r | 15)) continue;
-                float y[8];
-#pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                    const float4 t = *reinterpret_cast<const float4 *>(&s.A[r][at0 + j]);
-                    y[j] = t.x, y[j + 1] = t.y, y[j + 2] = t.z, y[j + 3] = t.w;
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = at0 + j < r ? y[j] : 0.f;  // T - I
-                store_operand(tp, tp + 8192, r, at0 / 8, y);
-            }
-        }
+        invert(s, tp, pt);
         fence_async_smem();
-        warp_arrive(&s.ready_tp[ts]);  // A is read out: the next chunk's comes behind another prep_all
+        warp_arrive(&s.ready_tp[ts]);
     }
     return true;
 }
@@ -280,7 +321,8 @@ __device__ __forceinline__ bool issue(Shared &s, int chunks) {
     const uint32_t kq = smem_u32(s.kq[0]), tp = smem_u32(s.tp[0]);
     auto gram = [&](int c) -> bool {  // [K; Q] K^T
         const int ks = c % kKqStages;
-        if (!warp_wait(&s.ready_kq[ks], (uint32_t)(c / kKqStages) & 1u)) return false;
+        // The last chunk's rows behind the sequence are cleared first; the others are there as soon as they are loaded.
+        if (!warp_wait(c == chunks - 1 ? &s.ready_kq : &s.full_kq[ks], c == chunks - 1 ? 0u : (uint32_t)(c / kKqStages) & 1u)) return false;
         if (c > 0 && !warp_wait(&s.kk_free, (uint32_t)(c - 1) & 1u)) return false;
         tc_fence_after();
         const uint64_t d = sdesc_sw128(kq + ks * kKqBytes, 16u, 1024u);
@@ -415,11 +457,13 @@ __device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, const Del
     // Kept for the gradients: the state before chunk c.
     float *kept_S = KEEP ? kept.S + (size_t)first_chunk(begin, n, C) * one + in : nullptr;
     auto keep = [&](const float (&S)[H], int c) {
-        if constexpr (KEEP)
-            if (live)
+        if constexpr (KEEP) {
+            if (live) {
 #pragma unroll
                 for (int e = 0; e < H; ++e)
                     if (e < keys) kept_S[(size_t)c * one + (size_t)e * p.dv] = S[e];
+            }
+        }
     };
     auto finish = [&](const float (&S)[H]) {
         const long long to = p.fin ? state_slot(p.fin_idx, p.pool, n, p.err) : -1;
@@ -442,15 +486,10 @@ __device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, const Del
             finish(S);
         }
     }
-    const uint32_t o_step = (uint32_t)p.hv * p.dv * 2;  // bytes between rows of o
-    char *o = reinterpret_cast<char *>(static_cast<__nv_bfloat16 *>(p.o) + (begin * p.hv + h) * p.dv);
-#pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-        const uint32_t par = (uint32_t)c & 1u;
+    // A chunk's values, for R = b v - b E KS
+    float R[16];
+    auto values = [&](int c) -> bool {
         const int vs = c % kVStages;
-        const Vec &vec = s.vec[c % kVecs];  // there: the state was scaled by it
-        float R[16];
-        // R = b v - b E KS
         if (!warp_wait(&s.ready_v[vs], (uint32_t)(c / kVStages) & 1u)) return false;
         const uint8_t *v = s.v[vs] + v_in;
 #pragma unroll
@@ -459,6 +498,15 @@ __device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, const Del
             R[e] = __uint_as_float(x << 16);
         }
         warp_arrive(&s.free_v[vs]);
+        return true;
+    };
+    if (chunks > 0 && !values(0)) return false;
+    const uint32_t o_step = (uint32_t)p.hv * p.dv * 2;  // bytes between rows of o
+    char *o = reinterpret_cast<char *>(static_cast<__nv_bfloat16 *>(p.o) + (begin * p.hv + h) * p.dv);
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+        const uint32_t par = (uint32_t)c & 1u;
+        const Vec &vec = s.vec[c % kVecs];  // there: the state was scaled by it
         scale16(R, vec.b + t0);
         if (!warp_wait(&s.ks, par)) return false;
         tc_fence_after();
@@ -529,6 +577,7 @@ __device__ __forceinline__ bool chain(Shared &s, const DeltaParams &p, const Del
                 warp_arrive(&s.up);
             }
         }
+        if (c + 1 < chunks && !values(c + 1)) return false;  // beside the state's update
         if (!warp_wait(&s.ds, par)) return false;
         tc_fence_after();
         {
@@ -609,8 +658,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kKqStages; ++i) {
             mbar_init(&s.full_kq[i], 1);
             mbar_init(&s.free_kq[i], 1);
-            mbar_init(&s.ready_kq[i], kPrepWarps);
         }
+        mbar_init(&s.ready_kq, kPrepWarps);
         for (int i = 0; i < kVStages; ++i) {
             mbar_init(&s.full_v[i], 1);
             mbar_init(&s.free_v[i], kChainWarps);
@@ -637,15 +686,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     bool ok = true;
-    // 896 x 72 registers, the same for all: each role is held to them by itself (0 to 12 bytes spill; without the word 48 to 136 do).
+    // The block was launched with 896 x 72 registers: 512 x 72 + 256 x 80 + 128 x 56.
     if (warp < kChainWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         ok = chain<DK, KEEP>(s, p, kept, n, h, begin, end, chunks, tmem);
     } else if (warp < kChainWarps + kPrepWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
         ok = prep<DK>(s, p, h, begin, end, chunks, tmem);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kIssuer) {
             ok = issue<DK, KEEP>(s, chunks);
             if (!ok) {  // nothing may be in flight at the end

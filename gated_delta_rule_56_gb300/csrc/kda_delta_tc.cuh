@@ -140,11 +140,14 @@ __device__ __forceinline__ void store_operand(uint8_t *hi, uint8_t *lo, int i, i
 // The state's operands from its fp32 values, N of a thread.
 template <int N>
 __device__ __forceinline__ void publish_state(const float (&S)[N], uint32_t at) {
-    uint32_t hi[N / 2], lo[N / 2];
 #pragma unroll
-    for (int e = 0; e < N / 2; ++e) split2(S[2 * e], S[2 * e + 1], hi[e], lo[e]);
-    tmem_st(at, hi);
-    tmem_st(at + 64, lo);
+    for (int g = 0; g < N; g += 16) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) split2(S[g + 2 * e], S[g + 2 * e + 1], hi[e], lo[e]);
+        tmem_st(at + g / 2, hi);
+        tmem_st(at + 64 + g / 2, lo);
+    }
     tmem_st_wait();
     tc_fence_before();
 }
