@@ -338,12 +338,16 @@ cudaError_t launch_delta_decode(const kda_delta_args &a, float *state, void *o, 
     return a.dtype == KDA_BF16 ? by_size<__nv_bfloat16>(p, f) : by_size<float>(p, f);
 }
 
-size_t delta_prefill_workspace_bytes(const kda_delta_args &, int) { return 0; }
+size_t delta_prefill_workspace_bytes(const kda_delta_args &a, int) {
+    const DeltaParams p = delta_params(a, nullptr, nullptr, nullptr);
+    return delta_tc_supported(a.dtype, p) ? delta_tc_order_bytes(p) : 0;
+}
 
-cudaError_t launch_delta_prefill(const kda_delta_args &a, void *o, float *final_state, void *, int, unsigned *err, cudaStream_t s) {
-    const DeltaParams p = delta_params(a, o, final_state, err);
-    if (delta_tc_supported(a.dtype, p)) return launch_delta_tc(p, s);
-    return launch_delta_rows(a.dtype, p, nullptr, 0, s);
+cudaError_t launch_delta_prefill(const kda_delta_args &a, void *o, float *final_state, void *ws, int, unsigned *err, cudaStream_t s) {
+    DeltaParams p = delta_params(a, o, final_state, err);
+    if (!delta_tc_supported(a.dtype, p)) return launch_delta_rows(a.dtype, p, nullptr, 0, s);
+    const cudaError_t e = launch_delta_tc_order(p, ws, s);
+    return e != cudaSuccess ? e : launch_delta_tc(p, s);
 }
 
 }  // namespace kda

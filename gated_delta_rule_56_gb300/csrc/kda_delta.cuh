@@ -19,6 +19,7 @@ struct DeltaParams {
     void *o;
     float *fin;
     unsigned *err;
+    const int32_t *order;  // tensor-core kernels: null, or the sequences in the order in which their blocks start
 };
 
 // The rows of sequence n; false (and an error) if cu_seqlens makes no sense there. Called by whole blocks.

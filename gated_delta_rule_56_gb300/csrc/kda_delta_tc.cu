@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t raw[];
     Shared &s = *reinterpret_cast<Shared *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5;
-    const int h = blockIdx.x % p.hv, n = blockIdx.x / p.hv;
+    const int h = blockIdx.x % p.hv, n = p.order ? p.order[blockIdx.x / p.hv] : blockIdx.x / p.hv;
     long long begin, end;
     if (!rows_of(p, n, begin, end)) return;
     const int chunks = (int)((end - begin + C - 1) / C);
@@ -773,6 +773,17 @@ bool encode(CUtensorMap *map, const void *base, long long rows, int heads, int d
 bool delta_tc_supported(kda_dtype dtype, const DeltaParams &p) {
     auto ok = [](const void *x, long long stride) { return aligned16(x) && stride % 8 == 0; };
     return dtype == KDA_BF16 && p.seqs.rows > 0 && p.seqs.rows >= kFewestRows * p.seqs.n_seqs && ok(p.q, p.qs) && ok(p.k, p.ks) && ok(p.v, p.vs) && delta_tc::encoder();
+}
+
+// Packed sequences start longest first, so that no long one is left for the end.
+size_t delta_tc_order_bytes(const DeltaParams &p) {
+    return p.seqs.cu && p.seqs.n_seqs >= 2 && p.seqs.n_seqs <= kMaxOrderedSeqs ? ((size_t)p.seqs.n_seqs * 4 + 255) / 256 * 256 : 0;
+}
+cudaError_t launch_delta_tc_order(DeltaParams &p, void *ws, cudaStream_t s) {
+    if (!delta_tc_order_bytes(p)) return cudaSuccess;
+    int32_t *order = static_cast<int32_t *>(ws);
+    p.order = order;
+    return launch_order_by_length(p.seqs.cu, p.seqs.n_seqs, order, s);
 }
 
 cudaError_t launch_delta_tc(const DeltaParams &p, cudaStream_t s) { return launch_any<false>(p, DeltaKept{}, s); }

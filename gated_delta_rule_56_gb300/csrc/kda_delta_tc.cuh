@@ -23,7 +23,8 @@ struct Vec {
 
 // a, b as hi + lo, each a pair of bf16 values: 2^-16 at most is left.
 __device__ __forceinline__ void rest_of(float a, float b, uint32_t hi, float &c, float &d) {
-    unpair(add2(pair(a, b), pair(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xffff0000u))), c, d);
+    c = a - __uint_as_float(hi << 16);
+    d = b - __uint_as_float(hi & 0xffff0000u);
 }
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
     float c, d;

@@ -7,6 +7,9 @@ namespace kda {
 
 // bf16 rows that TMA can load (16-byte aligned), sequences long enough for chunks of 64 rows.
 bool delta_tc_supported(kda_dtype dtype, const DeltaParams &p);
+// The blocks' order of packed sequences: workspace bytes (0: none), and its making (into p.order).
+size_t delta_tc_order_bytes(const DeltaParams &p);
+cudaError_t launch_delta_tc_order(DeltaParams &p, void *ws, cudaStream_t s);
 cudaError_t launch_delta_tc(const DeltaParams &p, cudaStream_t s);
 
 // What the gradients keep of the forward pass, per chunk (number of first_chunk) and value head.

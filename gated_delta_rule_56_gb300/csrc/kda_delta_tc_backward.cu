@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chain_back_kernel(const __g
     extern __shared__ uint8_t raw[];
     ChainShared &s = *reinterpret_cast<ChainShared *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5;
-    const int h = blockIdx.x % p.f.hv, n = blockIdx.x / p.f.hv;
+    const int h = blockIdx.x % p.f.hv, n = p.f.order ? p.f.order[blockIdx.x / p.f.hv] : blockIdx.x / p.f.hv;
     long long begin, end;
     if (!rows_of(p.f, n, begin, end)) return;
     const int chunks = (int)((end - begin + C - 1) / C);
@@ -821,10 +821,13 @@ cudaError_t launch(const DeltaParams &p, const DeltaGradients &g, const Parts &w
 
 }  // namespace
 
-size_t delta_tc_backward_bytes(const DeltaParams &p) { return parts_of(p, nullptr).bytes; }
+size_t delta_tc_backward_bytes(const DeltaParams &p) { return parts_of(p, nullptr).bytes + delta_tc_order_bytes(p); }
 
-cudaError_t launch_delta_tc_backward(const DeltaParams &p, const DeltaGradients &g, void *ws, cudaStream_t s) {
+cudaError_t launch_delta_tc_backward(const DeltaParams &params, const DeltaGradients &g, void *ws, cudaStream_t s) {
+    DeltaParams p = params;
     const Parts w = parts_of(p, ws);
+    const cudaError_t e = launch_delta_tc_order(p, static_cast<uint8_t *>(ws) + w.bytes, s);
+    if (e != cudaSuccess) return e;
     return p.dk == 128 ? launch<128>(p, g, w, s) : launch<64>(p, g, w, s);
 }
 
