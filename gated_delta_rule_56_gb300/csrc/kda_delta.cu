@@ -18,7 +18,7 @@ namespace kda {
 namespace {
 
 constexpr int kCols = 16;       // columns of a warp
-constexpr int kStage = 8;       // tokens of a stage
+constexpr int kStage = 8;       // tokens of a stage (and lanes that hold their decays)
 constexpr int kStages = 4;
 
 __device__ __forceinline__ f32x2 dup(float a) { return pair(a, a); }
@@ -227,11 +227,13 @@ __global__ void __launch_bounds__(W * 32) delta_rows_kernel(DeltaParams p, float
         }
         const Stage<T, DK, W> &s = ring[i % kStages];
         const int m = tokens(i);
+        const float a8 = expf(log_decay(s.g[lane & 7])), b8 = s.b[lane & 7];  // of the stage's tokens, those behind its end unused
         for (int t = 0; t < m; ++t) {
             f32x2 k[R / 2], q[R / 2];
             load_pairs<T, R, true>(&s.k[t][rl * R], k);
             load_pairs<T, R, true>(&s.q[t][rl * R], q);
-            const float o = S.step(k, q, to_float(s.v[t][col]), expf(log_decay(s.g[t])), s.b[t], lane);
+            const float a = __shfl_sync(0xffffffffu, a8, t), b = __shfl_sync(0xffffffffu, b8, t);
+            const float o = S.step(k, q, to_float(s.v[t][col]), a, b, lane);
             if (p.o && lane >= 16)
                 static_cast<T *>(p.o)[((begin + (long long)i * kStage + t) * p.hv + h) * p.dv + c0 + col] = from_float<T>(o);
         }

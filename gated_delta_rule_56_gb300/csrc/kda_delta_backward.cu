@@ -76,16 +76,41 @@ __global__ void __launch_bounds__(kThreads) delta_back_kernel(BackParams p) {
         const int m = (int)min((long long)kC, end - row0);
         __syncthreads();
         const float *S0 = p.kept + ((size_t)(chunk0 + ch) * hv + h) * one;
-        for (int i = tid; i < (int)one; i += kThreads) s.S0[i / DV][i % DV] = S0[i];
-        for (int i = tid; i < kC * DK; i += kThreads) {
-            const int r = i / DK, c = i % DK;
-            s.k[r][c] = r < m ? to_float(kp[(row0 + r) * p.f.ks + hk * DK + c]) : 0.f;
-            s.q[r][c] = r < m ? to_float(qp[(row0 + r) * p.f.qs + hk * DK + c]) : 0.f;
-        }
-        for (int i = tid; i < kC * DV; i += kThreads) {
-            const int r = i / DV, c = i % DV;
-            s.v[r][c] = r < m ? to_float(vp[(row0 + r) * p.f.vs + (size_t)h * DV + c]) : 0.f;
-            s.d_o[r][c] = r < m ? to_float(dop[((row0 + r) * hv + h) * DV + c]) : 0.f;
+        {  // all of a chunk's loads in flight before the first store
+            constexpr int NS = DK * DV / 4 / kThreads, NK = kC * DK / kThreads, NV = kC * DV / kThreads;
+            float4 st[NS];
+            T k[NK], q[NK], v[NV], d[NV];
+#pragma unroll
+            for (int e = 0; e < NS; ++e) st[e] = reinterpret_cast<const float4 *>(S0)[tid + kThreads * e];
+#pragma unroll
+            for (int e = 0; e < NK; ++e) {
+                const int r = (tid + kThreads * e) / DK, c = (tid + kThreads * e) % DK;
+                k[e] = r < m ? kp[(row0 + r) * p.f.ks + hk * DK + c] : from_float<T>(0.f);
+                q[e] = r < m ? qp[(row0 + r) * p.f.qs + hk * DK + c] : from_float<T>(0.f);
+            }
+#pragma unroll
+            for (int e = 0; e < NV; ++e) {
+                const int r = (tid + kThreads * e) / DV, c = (tid + kThreads * e) % DV;
+                v[e] = r < m ? vp[(row0 + r) * p.f.vs + (size_t)h * DV + c] : from_float<T>(0.f);
+                d[e] = r < m ? dop[((row0 + r) * hv + h) * DV + c] : from_float<T>(0.f);
+            }
+#pragma unroll
+            for (int e = 0; e < NS; ++e) {
+                const int i = (tid + kThreads * e) * 4;
+                *reinterpret_cast<float4 *>(&s.S0[i / DV][i % DV]) = st[e];
+            }
+#pragma unroll
+            for (int e = 0; e < NK; ++e) {
+                const int r = (tid + kThreads * e) / DK, c = (tid + kThreads * e) % DK;
+                s.k[r][c] = to_float(k[e]);
+                s.q[r][c] = to_float(q[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < NV; ++e) {
+                const int r = (tid + kThreads * e) / DV, c = (tid + kThreads * e) % DV;
+                s.v[r][c] = to_float(v[e]);
+                s.d_o[r][c] = to_float(d[e]);
+            }
         }
         if (warp == 0) {
             const bool live = lane < m;
