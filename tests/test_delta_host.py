@@ -197,3 +197,20 @@ def test_the_binding_refuses_host_tensors_and_unknown_words():
         kda.delta_prefill(q.half(), q, v, g, g)
     with pytest.raises(TypeError, match="tensors"):
         kda.layer_norm(None)
+
+
+@pytest.mark.parametrize("cls", [layers.DeltaArgs, layers.DeltaGrads, layers.LayerNormArgs])
+def test_argument_structs_are_as_long_as_they_say(cls):
+    """The library reads struct_size bytes: the packed form has them all, and each field where the C struct has it."""
+    values = [7 + i for i in range(len(cls._fields_) - 1)]
+    packed = layers._packer(cls)(*values)
+    assert len(packed) == ctypes.sizeof(cls)
+    a = cls.from_buffer_copy(packed)
+    assert a.struct_size == ctypes.sizeof(cls)
+    assert [getattr(a, name) for name, _ in cls._fields_[1:]] == values
+
+
+def test_no_value_heads_give_zero_gradients_of_their_key_heads(lib):
+    a = _delta(v_heads=0, B=0)
+    assert lib.kda_delta_backward(ctypes.byref(a), ctypes.byref(_delta_grads()), None, 0, None) == 0  # no rows either: nothing to clear
+    assert lib.kda_delta_backward(ctypes.byref(_delta(v_heads=0)), ctypes.byref(_delta_grads(dq=None)), None, 0, None) == INVALID
