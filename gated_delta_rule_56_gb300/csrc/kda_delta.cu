@@ -8,8 +8,10 @@
 // Row pairs sit in register pairs, so decay, update and both products are two elements per instruction. The 8 partial sums of a lane (4
 // columns, k and q) meet in 7 shuffles that leave every lane one finished sum.
 //
-// Single token: bound by HBM, the fp32 state is read once and written once (16-byte accesses, all of a lane's loads in flight together).
-// Prompts: bound by a token's latency (the sums' shuffles between two dependent passes over the registers).
+// Single token: bound by HBM, the fp32 state is read once and written once (16-byte accesses, all of a lane's loads in flight together): 256
+// sequences x 32 heads of 128 x 128 take 158 us, 6.85 TB/s (what is above the copy rate of 6.7 comes out of L2); one sequence 4.8 us.
+// Prompts: bound by a token's latency (the sums' shuffles between two dependent passes over the registers, and some 180 instructions of a warp
+// that has its scheduler to itself): 0.35 us per token with heads of 64, 0.5 us with 128.
 #include "kda_delta.cuh"
 #include "kda_delta_tc.h"
 #include "kda_layers.h"
@@ -125,7 +127,7 @@ __device__ __forceinline__ void load_pairs(const T *p, f32x2 (&x)[R / 2]) {
 
 // One token of every sequence. A block: one value head of one sequence, or part of its columns.
 template <typename T, int DK, bool WIDE>
-__global__ void __launch_bounds__(256) delta_token_kernel(DeltaParams p) {
+__global__ void __launch_bounds__(64) delta_token_kernel(DeltaParams p) {
     constexpr int R = DK / 8;
     const int lane = threadIdx.x & 31, rl = lane >> 2;
     const int warps = p.dv / kCols;
@@ -245,8 +247,8 @@ __global__ void __launch_bounds__(W * 32) delta_rows_kernel(DeltaParams p, float
 template <typename T, int DK, bool WIDE>
 cudaError_t launch_token(const DeltaParams &p, cudaStream_t s) {
     const long long warps = (long long)p.seqs.n_seqs * p.hv * (p.dv / kCols);
-    const int per = warps < 4096 ? 2 : 8;  // few warps go to more SMs
-    delta_token_kernel<T, DK, WIDE><<<(unsigned)((warps + per - 1) / per), per * 32, 0, s>>>(p);
+    // Two warps per block: 256 sequences of 32 heads of 128 take 158 us (171 with eight), one takes 4.8 us (6.2).
+    delta_token_kernel<T, DK, WIDE><<<(unsigned)((warps + 1) / 2), 64, 0, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -340,14 +342,18 @@ cudaError_t launch_delta_decode(const kda_delta_args &a, float *state, void *o, 
     return a.dtype == KDA_BF16 ? by_size<__nv_bfloat16>(p, f) : by_size<float>(p, f);
 }
 
+// bf16 prompts of fewer rows than this on average go token by token: a chunk of 64 rows takes the tensor-core kernel the same time whatever it
+// holds. 32 heads of 128, sequences of 16 rows: 12.4 us here and 14.4 there for one, 131 and 160 for 64; of 32 rows: 20.6 and 14.4, 252 and 162.
+constexpr int kFewestRows = 20;
+
 size_t delta_prefill_workspace_bytes(const kda_delta_args &a, int) {
     const DeltaParams p = delta_params(a, nullptr, nullptr, nullptr);
-    return delta_tc_supported(a.dtype, p) ? delta_tc_order_bytes(p) : 0;
+    return delta_tc_supported(a.dtype, p, kFewestRows) ? delta_tc_order_bytes(p) : 0;
 }
 
 cudaError_t launch_delta_prefill(const kda_delta_args &a, void *o, float *final_state, void *ws, int, unsigned *err, cudaStream_t s) {
     DeltaParams p = delta_params(a, o, final_state, err);
-    if (!delta_tc_supported(a.dtype, p)) return launch_delta_rows(a.dtype, p, nullptr, 0, s);
+    if (!delta_tc_supported(a.dtype, p, kFewestRows)) return launch_delta_rows(a.dtype, p, nullptr, 0, s);
     const cudaError_t e = launch_delta_tc_order(p, ws, s);
     return e != cudaSuccess ? e : launch_delta_tc(p, s);
 }

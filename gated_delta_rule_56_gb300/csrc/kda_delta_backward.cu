@@ -15,7 +15,8 @@
 // recurrence before this kernel (kda_delta.cu).
 //
 // One block per (sequence, value head), the chunks from the last to the first with S0 and dS in shared memory. Bound by the
-// multiply-adds (6 products of 16 rows with a state) and their reads of shared memory; a path for few, small or fp32 calls.
+// latency of its phases (ten barriers per chunk; 6 products of 16 rows with a state, whose operands come out of shared memory), a path for fp32 and
+// for short sequences: 1501 rows in 9 sequences, 8 heads of 64, fp32: 282 us in a captured graph where the longest sequence has some 450 rows.
 #include "kda_delta.cuh"
 #include "kda_delta_tc.h"
 #include "kda_layers.h"
@@ -368,15 +369,19 @@ size_t head_floats(const kda_delta_args &a) {  // one of dq, dk per value head
 
 }  // namespace
 
+// bf16 sequences of fewer rows than this on average take this file's kernel. 32 heads of 128, sequences of 8 rows: 45 us here and 39 on the
+// tensor cores for one, 568 and 488 for 64; of 64 rows: 167 and 41, 2391 and 557. Shorter ones do not fill the chunks of 16 either.
+constexpr int kFewestRows = 8;
+
 size_t delta_backward_workspace_bytes(const kda_delta_args &a, int) {
     const DeltaParams p = delta_params(a, nullptr, nullptr, nullptr);
-    return (delta_tc_supported(a.dtype, p) ? delta_tc_backward_bytes(p) : kept_floats(a) * 4) + 2 * head_floats(a) * 4;
+    return (delta_tc_supported(a.dtype, p, kFewestRows) ? delta_tc_backward_bytes(p) : kept_floats(a) * 4) + 2 * head_floats(a) * 4;
 }
 
 cudaError_t launch_delta_backward(const kda_delta_args &a, const kda_delta_grads &g, void *ws, int, unsigned *err, cudaStream_t s) {
     const DeltaParams f = delta_params(a, nullptr, nullptr, err);
     if (f.seqs.n_seqs == 0) return cudaSuccess;
-    const bool apart = head_floats(a) > 0, tc = delta_tc_supported(a.dtype, f);
+    const bool apart = head_floats(a) > 0, tc = delta_tc_supported(a.dtype, f, kFewestRows);
     float *heads = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + (tc ? delta_tc_backward_bytes(f) : kept_floats(a) * 4));
     float *dq = apart ? heads : g.dq, *dk = apart ? heads + head_floats(a) : g.dk;
     cudaError_t e;

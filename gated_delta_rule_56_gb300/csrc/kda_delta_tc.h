@@ -5,8 +5,8 @@
 
 namespace kda {
 
-// bf16 rows that TMA can load (16-byte aligned), sequences long enough for chunks of 64 rows.
-bool delta_tc_supported(kda_dtype dtype, const DeltaParams &p);
+// bf16 rows that TMA can load (16-byte aligned), and at least `fewest` of them per sequence on average.
+bool delta_tc_supported(kda_dtype dtype, const DeltaParams &p, int fewest);
 // The blocks' order of packed sequences: workspace bytes (0: none), and its making (into p.order).
 size_t delta_tc_order_bytes(const DeltaParams &p);
 cudaError_t launch_delta_tc_order(DeltaParams &p, void *ws, cudaStream_t s);

@@ -14,7 +14,14 @@
 // Operands that are not exact in bf16 go in as two values (2^-17 of them is left, the products of both rests are left out), those that are
 // added to the gradient of the state as three; sums, states and outputs are fp32.
 //
-// Bound by latency: the chains have one block per SM and sequence and value head, the third kernel runs its phases one after the other.
+// Gradients are 2e-6 to 5e-6 off 64 bits in the 2-norm (the plain fp32 form 0.3e-6).
+//
+// Measured at 4 x 2048 rows, 32 value heads, 16 key heads of 128 (2 x 2048 in brackets: 616 us in all): the kept forward pass 197 us (the same: 64
+// of 128 chains), the chain 157 us (the same), the chunks 440 us (220), the sums over shared heads 57 us (29). The chains are bound by latency, as the
+// forward one (9 000 cycles per chunk, a quarter of them the stores of dS, which the chain's warps make themselves); the third kernel by its
+// phases, which load (280 KB per chunk and head: S0, dS, U, dR), compute and store one after the other with one block per SM: 3.5 TB/s. L2 prefetches
+// for a later block made it slower (480), bulk copies of single rows out of shared memory too (550); 32 lanes that write to 32 rows
+// took 470.
 #include "kda_delta_tc.cuh"
 
 namespace kda {

@@ -5,6 +5,9 @@
 // A line (`width` values) is held in registers by a group of lanes (8 to 32 of a warp, or a whole block), so every input is read once:
 // bound by HBM as long as the instructions fit, which they do in register pairs with the options known to the compiler. The mean is taken
 // first and the squares of the differences after it, both from registers: no cancellation. Weights stay in registers while a group goes over its lines.
+// Measured (bf16): 32768 tokens x 32 heads of 128 with a SiLU gate 151 us, 5.3 TB/s (79 % of the copy rate); 8192 rows of 4096 with residual and bias
+// 52 us, 5.2 TB/s (77 %); 16 rows 4.1 us in a captured graph, a launch. One element at a time with the options looked up per element it took 203
+// and 82 us; the next line's loads ahead of the work took registers and with them blocks: 269 to 404 us.
 #include "kda_layers.h"
 #include "kda_norm.cuh"
 
@@ -110,8 +113,9 @@ struct Forward {
 template <typename T>
 cudaError_t forward(const NormParams &p, int sms, cudaStream_t s) {
     const bool wide = wide_lines<T>(p);
-    if (p.res) return p.z ? by_width<T>(p.width, wide, Forward<T, true, true>{p, sms, s}) : by_width<T>(p.width, wide, Forward<T, true, false>{p, sms, s});
-    return p.z ? by_width<T>(p.width, wide, Forward<T, false, true>{p, sms, s}) : by_width<T>(p.width, wide, Forward<T, false, false>{p, sms, s});
+    constexpr int V = 16 / sizeof(T);
+    if (p.res) return p.z ? by_width<V>(p.width, wide, Forward<T, true, true>{p, sms, s}) : by_width<V>(p.width, wide, Forward<T, true, false>{p, sms, s});
+    return p.z ? by_width<V>(p.width, wide, Forward<T, false, true>{p, sms, s}) : by_width<V>(p.width, wide, Forward<T, false, false>{p, sms, s});
 }
 
 }  // namespace

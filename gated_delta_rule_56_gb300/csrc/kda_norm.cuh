@@ -129,11 +129,10 @@ bool wide_lines(const NormParams &p) {
            ok(p.y, 0) && ok(p.sum, 0) && ok(p.dy, 0) && ok(p.d_sum, 0) && ok(p.dx, 0) && ok(p.dz, 0);
 }
 
-// Calls f.run<V, K, GROUP>() for a width: up to half a warp's or a warp's lanes with one or two 16-byte words each, then blocks of up to
-// 1024 threads; single values where something is not aligned.
-template <typename T, typename F>
+// Calls f.run<V, K, GROUP>() for a width: up to a warp's lanes with one or two packs of V values each, then blocks of up to 1024 threads;
+// single values where something is not aligned.
+template <int V, typename F>
 cudaError_t by_width(int width, bool wide, const F &f) {
-    constexpr int V = 16 / sizeof(T);
     if (wide) {
         const int packs = width / V;
         if (packs <= 8) return f.template run<V, 1, 8>();
