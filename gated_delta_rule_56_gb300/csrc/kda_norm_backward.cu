@@ -7,8 +7,7 @@
 // A line is held in registers as in the forward pass: every input is read once, two rounds of sums (one for RMS): sum t and sum t h come with
 // the squares. A group keeps its sums of the weights' gradients in registers while it goes over its lines; a second kernel adds the
 // blocks' parts in a fixed order with their rounding errors (no atomics). Bound by the latency of the loads: 8 accumulators and 8 inputs per pair
-// leave two blocks of 256 threads per SM. Measured: 8192 tokens x 32 heads of 128 with a gate in bf16 108 us, 4.3 TB/s (65 % of the copy rate; 24 us of it
-// the parts' sums and the second launch); 4101 lines of 1531 in fp32, which take single values, 44 us, 2.3 TB/s.
+// leave two blocks of 256 threads per SM. Measured: 8192 tokens x 32 heads of 128 with a gate in bf16 108 us, 4.3 TB/s (65 % of the copy rate); 4101 lines of 1531 in fp32, which take single values, 44 us, 2.3 TB/s.
 #include "kda_layers.h"
 #include "kda_norm.cuh"
 
