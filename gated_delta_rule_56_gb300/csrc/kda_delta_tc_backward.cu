@@ -21,6 +21,8 @@
 // quarter of them the stores of dS, which the chain's warps make themselves); the third kernel by its phases, which load (280 KB per
 // chunk and head: S0, dS, U, dR), compute and store one after the other with one block per SM: 3.5 TB/s, 27 % of the issue slots. L2 prefetches for a
 // later block made it slower (480 for 440), bulk copies of single rows out of shared memory too (550); 32 lanes that write to 32 rows took 470.
+#include <cstddef>
+
 #include "kda_delta_tc.cuh"
 
 namespace kda {
@@ -376,12 +378,14 @@ constexpr uint32_t TG_2 = 128;   // U dS^T, scaled, then with Gp^T Q + (b Ga)^T 
 constexpr uint32_t TG_P = 256;   // [dO; dR] U^T
 constexpr uint32_t TG_A = 320;   // [dO; dR]: two times 64
 
+// The MMAs that take 64 rows (U) or 64 columns (Gp, b Ga) as 128 read what lies behind them as well, into lanes that nobody reads: the order here
+// keeps that inside the block's memory.
 struct GradShared {
     uint8_t kq[32768];
-    uint8_t u_hi[16384], u_lo[16384];    // U, per 64 value channels 64 rows
-    uint8_t s_hi[32768], s_lo[32768];    // S0, then dS, per 64 value channels 128 rows (key channels)
     uint8_t g_hi[16384], g_lo[16384];    // [Gp; Ga], 128 rows
     uint8_t bg_hi[8192], bg_lo[8192];    // b Ga
+    uint8_t u_hi[16384], u_lo[16384];    // U, per 64 value channels 64 rows
+    uint8_t s_hi[32768], s_lo[32768];    // S0, then dS, per 64 value channels 128 rows (key channels)
     Vec vec;
     float a[C], pre[C], f[C];
     float sums[4][5][C];                 // per quarter of the columns: q.dq, k.row, k.col, k.(the part of col from dS), dR.v
@@ -389,6 +393,8 @@ struct GradShared {
     uint64_t full, b0, b1, b2, b3, b4;
     uint32_t tmem;
 };
+static_assert(offsetof(GradShared, bg_lo) + 16384 <= offsetof(GradShared, vec) && offsetof(GradShared, u_lo) + 24576 <= offsetof(GradShared, vec),
+              "128 rows or columns from every operand of 64");
 struct GradMaps {
     CUtensorMap q, k;
 };
