@@ -1,5 +1,5 @@
-// kda_delta.cu -- the delta rule with one decay per value head, token by token on the CUDA cores: the step of a single
-// token, prompts in fp32 and short prompts.
+// kda_delta.cu -- the delta rule with one decay per value head in fp32 on the CUDA cores: the step of a single token, prompts in fp32 and short
+// prompts, row by row and (below) in chunks of 16 rows.
 //
 // Per value head and token, with a = exp(g): u = b (v - a S^T k), S <- a S + k u^T, o = a S^T q + (q.k) u, where S is the state before
 // the token: both products read the old state, so one pass over it serves them and the update follows in registers.
@@ -10,8 +10,8 @@
 //
 // Single token: bound by HBM, the fp32 state is read once and written once (16-byte accesses, all of a lane's loads in flight together): 256
 // sequences x 32 heads of 128 x 128 take 158 us, 6.85 TB/s (what is above the copy rate of 6.7 comes out of L2); one sequence 4.8 us.
-// Prompts: bound by a token's latency (the sums' shuffles between two dependent passes over the registers, and some 180 instructions of a warp
-// that has its scheduler to itself): 0.35 us per token with heads of 64, 0.5 us with 128.
+// Prompts row by row: bound by a token's latency where warps are few (the sums' shuffles between two dependent passes over the registers): 0.35 us
+// per token with heads of 64, 0.43 us with 128; with 4 warps per scheduler by the instructions.
 #include "kda_delta.cuh"
 #include "kda_delta_tc.h"
 #include "kda_layers.h"
@@ -19,9 +19,10 @@
 namespace kda {
 namespace {
 
-constexpr int kCols = 16;       // columns of a warp
-constexpr int kStage = 8;       // tokens of a stage (and lanes that hold their decays)
+constexpr int kCols = 16;   // columns of a warp
+constexpr int kStage = 8;   // tokens of a stage (and lanes that hold their decays)
 constexpr int kStages = 4;
+constexpr int kC = 16;      // rows of a chunk
 
 __device__ __forceinline__ f32x2 dup(float a) { return pair(a, a); }
 
@@ -165,7 +166,7 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Whole sequences. A block of W warps: one value head of one sequence, 16 W of its columns. The rows come through a ring of stages of 8
+// ---- whole sequences, row by row. A block of W warps: one value head of one sequence, 16 W of its columns. The rows come through a ring of stages of 8
 // tokens in shared memory, so a token's latency holds none of HBM's.
 template <typename T, int DK, int W>
 struct Stage {
@@ -192,9 +193,9 @@ __device__ __forceinline__ void fill(Stage<T, DK, W> &s, const DeltaParams &p, l
     }
 }
 
-// `kept` non-null: the state before every kept_rows-th row of a sequence goes there (kept_rows a multiple of a stage).
+// `kept` non-null: the state before every chunk of 16 rows goes there (number of first_chunk).
 template <typename T, int DK, int W, bool WIDE>
-__global__ void __launch_bounds__(W * 32) delta_rows_kernel(DeltaParams p, float *kept, int kept_rows) {
+__global__ void __launch_bounds__(W * 32) delta_rows_kernel(DeltaParams p, float *kept) {
     constexpr int R = DK / 8;
     extern __shared__ __align__(16) unsigned char raw[];
     Stage<T, DK, W> *ring = reinterpret_cast<Stage<T, DK, W> *>(raw);
@@ -223,10 +224,7 @@ __global__ void __launch_bounds__(W * 32) delta_rows_kernel(DeltaParams p, float
         const int ahead = i + kStages - 1;
         if (ahead < stages) fill<T, DK, W, WIDE>(ring[ahead % kStages], p, begin + (long long)ahead * kStage, tokens(ahead), h, c0);
         copies_commit();
-        if (kept && (i * kStage) % kept_rows == 0) {
-            const long long chunk = first_chunk(begin, n, kept_rows) + i * kStage / kept_rows;
-            S.store(kept + chunk * one + at, p.dv);
-        }
+        if (kept && i * kStage % kC == 0) S.store(kept + (first_chunk(begin, n, kC) + i * kStage / kC) * one + at, p.dv);
         const Stage<T, DK, W> &s = ring[i % kStages];
         const int m = tokens(i);
         const float a8 = expf(log_decay(s.g[lane & 7])), b8 = s.b[lane & 7];  // of the stage's tokens, those behind its end unused
@@ -244,6 +242,272 @@ __global__ void __launch_bounds__(W * 32) delta_rows_kernel(DeltaParams p, float
     if (to >= 0) S.store(p.fin + to * one + at, p.dv);
 }
 
+// ---- whole sequences, in chunks of 16 rows. With G the sum of the log-decays up to a row in the chunk, D_ij = exp(G_i - G_j), E_i = exp(G_i),
+// F_i = exp(G_C - G_i), S the state before the chunk and A_ij = b_i D_ij k_i.k_j (j < i), P_ij = D_ij q_i.k_j (j <= i):
+//     (I + A) U = b (V - E K S),   O = E Q S + P U,   S <- exp(G_C) S + (F K)^T U
+// A block: 32 columns of one (sequence, value head). Warps 0-3 hold the state, a lane 4 columns of a sixteenth of the rows, and solve for U by
+// substitution, lane = column, each warp for itself; warps 4-7 load the chunks and make the next one's A, P and decays. Bound by
+// latency, one warp per scheduler that goes from the products over sums and substitution to the update: 2.6 us per chunk with heads of 64, 3.5 us
+// with 128 (16 rows one by one: 5.6 and 6.9). With one column and a quarter of the rows per lane heads of 128 took 3.8 us.
+constexpr int kSlice = 32, kHalf = 128;
+
+template <int DK>
+struct ChunkShared {
+    float k[2][kC][DK + 4], q[2][kC][DK + 4], v[2][kC][kSlice];
+    float A[2][kC][kC];  // [j][i]: columns
+    float P[2][kC][kC];
+    float b[2][kC], E[2][kC], F[2][kC];
+    float G[kC], rest[kC];  // sums of the log-decays in two fp32 values
+    float part[2][4][kC][kSlice];
+    float fu[4][kC][kSlice];  // per warp: F U
+};
+
+__device__ __forceinline__ void half_sync(int which) { asm volatile("bar.sync %0, 128;" ::"r"(which + 1) : "memory"); }
+
+// A chunk's rows on their way, in the registers of 128 threads.
+template <typename T, int DK, bool WIDE>
+struct ChunkRows {
+    static constexpr int V = WIDE ? 16 / (int)sizeof(T) : 1, KP = kC * DK / V, VP = kC * kSlice / V;
+    static constexpr int KN = (KP + kHalf - 1) / kHalf, VN = (VP + kHalf - 1) / kHalf;
+    Pack<T, V> k[KN], q[KN], v[VN];
+    float g, b;
+
+    // Rows [row, row + m) of key head hk and of 32 value columns from `col` of a row; zeros behind them.
+    __device__ __forceinline__ void load(const DeltaParams &p, long long row, int m, int h, int c0, int t) {
+        const T *kp = static_cast<const T *>(p.k) + h / p.per * DK, *qp = static_cast<const T *>(p.q) + h / p.per * DK;
+        const T *vp = static_cast<const T *>(p.v) + (size_t)h * p.dv + c0;
+        Pack<T, V> zero;
+#pragma unroll
+        for (int j = 0; j < V; ++j) zero.e[j] = from_float<T>(0.f);
+#pragma unroll
+        for (int e = 0; e < KN; ++e) {
+            const int at = t + kHalf * e, r = at / (DK / V), x = at % (DK / V) * V;
+            const bool there = at < KP && r < m;
+            k[e] = there ? load_pack<T, V>(kp + (row + r) * p.ks + x) : zero;
+            q[e] = there ? load_pack<T, V>(qp + (row + r) * p.qs + x) : zero;
+        }
+#pragma unroll
+        for (int e = 0; e < VN; ++e) {
+            const int at = t + kHalf * e, r = at / (kSlice / V), x = at % (kSlice / V) * V;
+            v[e] = at < VP && r < m ? load_pack<T, V>(vp + (row + r) * p.vs + x) : zero;
+        }
+        g = t < m ? log_decay(p.g[(row + t) * p.hv + h]) : 0.f;  // m <= 16
+        b = t < m ? p.beta[(row + t) * p.hv + h] : 0.f;
+    }
+    __device__ __forceinline__ static void put(float *to, const Pack<T, V> &x) {
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = to_float(x.e[j]);
+        store_floats<V>(to, f);
+    }
+    __device__ __forceinline__ void store(ChunkShared<DK> &s, int buf, int t) const {
+#pragma unroll
+        for (int e = 0; e < KN; ++e) {
+            const int at = t + kHalf * e, r = at / (DK / V), x = at % (DK / V) * V;
+            if (at < KP) {
+                put(&s.k[buf][r][x], k[e]);
+                put(&s.q[buf][r][x], q[e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < VN; ++e) {
+            const int at = t + kHalf * e, r = at / (kSlice / V), x = at % (kSlice / V) * V;
+            if (at < VP) put(&s.v[buf][r][x], v[e]);
+        }
+        if (t < 32) {
+            // Sums of up to 16 decays in two fp32 values, so that differences of neighbours behind strong decays stay exact.
+            float G = g, r = 0.f;
+#pragma unroll
+            for (int d = 1; d < kC; d *= 2) {
+                const float x = __shfl_up_sync(0xffffffffu, G, d, kC), y = __shfl_up_sync(0xffffffffu, r, d, kC);
+                if ((t & 15) >= d) {
+                    const float sum = __fadd_rn(G, x), w = __fsub_rn(sum, G);
+                    r = __fadd_rn(__fadd_rn(r, y), __fadd_rn(__fsub_rn(G, __fsub_rn(sum, w)), __fsub_rn(x, w)));
+                    G = sum;
+                }
+            }
+            const float Gc = __shfl_sync(0xffffffffu, G, kC - 1, kC), rc = __shfl_sync(0xffffffffu, r, kC - 1, kC);
+            if (t < kC) {
+                s.G[t] = G;
+                s.rest[t] = r;
+                s.b[buf][t] = b;
+                s.E[buf][t] = expf(G + r);
+                s.F[buf][t] = expf(__fadd_rn(__fsub_rn(Gc, G), __fsub_rn(rc, r)));
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ float dot4(const float4 a, const float4 b, float c) {
+    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
+// A and P of the chunk in `buf`: thread (i, j), for j and j + 8.
+template <int DK>
+__device__ __forceinline__ void chunk_pairs(ChunkShared<DK> &s, int buf, int t) {
+    const int i = t >> 3, j = t & 7;
+    float kk[2] = {0.f, 0.f}, qk[2] = {0.f, 0.f};
+#pragma unroll 4
+    for (int x = 0; x < DK; x += 4) {
+        const float4 ki = *reinterpret_cast<const float4 *>(&s.k[buf][i][x]), qi = *reinterpret_cast<const float4 *>(&s.q[buf][i][x]);
+        const float4 kj = *reinterpret_cast<const float4 *>(&s.k[buf][j][x]);
+        kk[0] = dot4(ki, kj, kk[0]);
+        qk[0] = dot4(qi, kj, qk[0]);
+        if (i >= 8) {  // whole warps
+            const float4 kj8 = *reinterpret_cast<const float4 *>(&s.k[buf][j + 8][x]);
+            kk[1] = dot4(ki, kj8, kk[1]);
+            qk[1] = dot4(qi, kj8, qk[1]);
+        }
+    }
+    const float G = s.G[i], r = s.rest[i], b = s.b[buf][i];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int c = j + 8 * e;
+        const float D = c <= i ? expf(__fadd_rn(__fsub_rn(G, s.G[c]), __fsub_rn(r, s.rest[c]))) : 0.f;
+        s.A[buf][c][i] = c < i ? b * D * kk[e] : 0.f;
+        s.P[buf][i][c] = c <= i ? D * qk[e] : 0.f;
+    }
+}
+
+// KEEP: no outputs, but the state before every chunk goes to `kept` (number of first_chunk).
+template <typename T, int DK, bool WIDE, bool KEEP>
+__global__ void __launch_bounds__(2 * kHalf, 2) delta_chunks_kernel(DeltaParams p, float *kept) {
+    constexpr int R = DK / 16;  // rows of a lane
+    extern __shared__ __align__(16) unsigned char raw[];
+    auto &s = *reinterpret_cast<ChunkShared<DK> *>(raw);
+    const int slices = p.dv / kSlice;
+    const int slice = blockIdx.x % slices, h = (blockIdx.x / slices) % p.hv, n = blockIdx.x / slices / p.hv;
+    const int c0 = slice * kSlice;
+    long long begin, end;
+    if (!rows_of(p, n, begin, end)) return;
+    const int chunks = (int)((end - begin + kC - 1) / kC);
+    auto rows_in = [&](int c) { return (int)min((long long)kC, end - begin - (long long)c * kC); };
+    if (threadIdx.x >= kHalf) {
+        const int t = threadIdx.x - kHalf;
+        ChunkRows<T, DK, WIDE> next;
+        if (chunks > 0) next.load(p, begin, rows_in(0), h, c0, t);
+        for (int c = 0; c <= chunks; ++c) {  // makes chunk c beside the work on chunk c - 1
+            if (c < chunks) {
+                next.store(s, c & 1, t);
+                if (c + 1 < chunks) next.load(p, begin + (long long)(c + 1) * kC, rows_in(c + 1), h, c0, t);
+                half_sync(1);
+                chunk_pairs<DK>(s, c & 1, t);
+            }
+            __syncthreads();
+        }
+        return;
+    }
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane >> 3, c4 = (lane & 7) * 4, r0 = (4 * w + rg) * R;
+    const long long from = p.init ? state_slot(p.init_idx, p.pool, n, p.err) : -1;
+    const size_t at = ((size_t)h * DK + r0) * p.dv + c0 + c4, one = (size_t)p.hv * DK * p.dv;
+    Tile<R> S;
+    if (from >= 0) S.load(p.init + from * one + at, p.dv); else S.clear();
+    // This lane's rows of a row of K or Q.
+    auto row = [&](const float *from, f32x2 (&x)[R / 2]) {
+        if constexpr (R == 2) {
+            x[0] = *reinterpret_cast<const f32x2 *>(from + r0);
+        } else {
+#pragma unroll
+            for (int e = 0; e < R / 2; e += 2) {
+                const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(from + r0 + 2 * e);
+                x[e] = two.x;
+                x[e + 1] = two.y;
+            }
+        }
+    };
+    // Sums over the lanes' row groups of four rows of products, which leave row rg with this lane.
+    const bool up = lane & 16, odd = lane & 8;
+    auto join = [&](const float (&x)[4][4]) {
+        float y[2][4], z[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[e][j] = (up ? x[2 + e][j] : x[e][j]) + __shfl_xor_sync(0xffffffffu, up ? x[e][j] : x[2 + e][j], 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = (odd ? y[1][j] : y[0][j]) + __shfl_xor_sync(0xffffffffu, odd ? y[0][j] : y[1][j], 8);
+        return make_float4(z[0], z[1], z[2], z[3]);
+    };
+    __syncthreads();  // chunk 0 is made
+    for (int c = 0; c < chunks; ++c) {
+        const int buf = c & 1, m = rows_in(c);
+        if constexpr (KEEP) S.store(kept + (size_t)(first_chunk(begin, n, kC) + c) * one + at, p.dv);
+        // K S and Q S over this lane's rows of S, then over the warp's
+#pragma unroll
+        for (int r = 0; r < kC; r += 4) {
+#pragma unroll
+            for (int which = 0; which < (KEEP ? 1 : 2); ++which) {
+                float sums[4][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f32x2 x[R / 2];
+                    row(which ? s.q[buf][r + e] : s.k[buf][r + e], x);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        f32x2 sum = mul2(x[0], S.s[0][j]);
+#pragma unroll
+                        for (int i = 1; i < R / 2; ++i) sum = fma2(x[i], S.s[i][j], sum);
+                        float lo, hi;
+                        unpair(sum, lo, hi);
+                        sums[e][j] = lo + hi;
+                    }
+                }
+                *reinterpret_cast<float4 *>(&s.part[which][w][r + rg][c4]) = join(sums);
+            }
+        }
+        half_sync(0);
+        float u[kC];
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+            const float ks = (s.part[0][0][i][lane] + s.part[0][1][i][lane]) + (s.part[0][2][i][lane] + s.part[0][3][i][lane]);
+            u[i] = s.b[buf][i] * (s.v[buf][i][lane] - s.E[buf][i] * ks);
+        }
+#pragma unroll
+        for (int j = 0; j < kC - 1; ++j)
+#pragma unroll
+            for (int i4 = (j + 1) & ~3; i4 < kC; i4 += 4) {
+                const float4 a = *reinterpret_cast<const float4 *>(&s.A[buf][j][i4]);
+                const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (i4 + e > j) u[i4 + e] = fmaf(-av[e], u[j], u[i4 + e]);
+            }
+        if constexpr (!KEEP) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // rows w, w + 4, ...: about the same work in every warp
+                const int i = 4 * e + w;
+                const float qs = (s.part[1][0][i][lane] + s.part[1][1][i][lane]) + (s.part[1][2][i][lane] + s.part[1][3][i][lane]);
+                float o = s.E[buf][i] * qs;
+#pragma unroll
+                for (int j = 0; j < 4 * e + 4; ++j)
+                    if (j <= i) o = fmaf(s.P[buf][i][j], u[j], o);
+                if (i < m) static_cast<T *>(p.o)[((begin + (long long)c * kC + i) * p.hv + h) * p.dv + c0 + lane] = from_float<T>(o);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kC; ++j)  // rows behind the sequence leave even a state that is not finite as it is
+            s.fu[w][j][lane] = j < m ? s.F[buf][j] * u[j] : 0.f;
+        __syncwarp();
+        const f32x2 whole = dup(s.E[buf][kC - 1]);
+#pragma unroll
+        for (int i = 0; i < R / 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S.s[i][j] = mul2(whole, S.s[i][j]);
+#pragma unroll
+        for (int t = 0; t < kC; ++t) {
+            f32x2 k[R / 2];
+            row(s.k[buf][t], k);
+            const float4 f = *reinterpret_cast<const float4 *>(&s.fu[w][t][c4]);
+            const f32x2 fu[4] = {dup(f.x), dup(f.y), dup(f.z), dup(f.w)};
+#pragma unroll
+            for (int i = 0; i < R / 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) S.s[i][j] = fma2(k[i], fu[j], S.s[i][j]);
+        }
+        __syncthreads();  // chunk c + 1 is made, and everyone is done with chunk c
+    }
+    const long long to = p.fin ? state_slot(p.fin_idx, p.pool, n, p.err) : -1;
+    if (to >= 0) S.store(p.fin + to * one + at, p.dv);
+}
+
 template <typename T, int DK, bool WIDE>
 cudaError_t launch_token(const DeltaParams &p, cudaStream_t s) {
     const long long warps = (long long)p.seqs.n_seqs * p.hv * (p.dv / kCols);
@@ -252,22 +516,29 @@ cudaError_t launch_token(const DeltaParams &p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <typename T, int DK, int W, bool WIDE>
-cudaError_t launch_rows_with(const DeltaParams &p, float *kept, int kept_rows, cudaStream_t s) {
-    const unsigned blocks = (unsigned)((long long)p.seqs.n_seqs * p.hv * (p.dv / (W * kCols)));
-    const size_t bytes = sizeof(Stage<T, DK, W>) * kStages;
-    auto *f = &delta_rows_kernel<T, DK, W, WIDE>;
+// Blocks of `columns` columns.
+template <typename F>
+cudaError_t launch_sequences(F *f, const DeltaParams &p, float *kept, int columns, int threads, size_t bytes, cudaStream_t s) {
     if (bytes > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (e != cudaSuccess) return e;
     }
-    f<<<blocks, W * 32, bytes, s>>>(p, kept, kept_rows);
+    f<<<(unsigned)((long long)p.seqs.n_seqs * p.hv * (p.dv / columns)), threads, bytes, s>>>(p, kept);
     return cudaGetLastError();
 }
 
+// Chunks of 16 rows where their blocks are few and a token's latency is what counts, else row by row, whose many warps hide it. fp32, heads of 128 (of
+// 64), row by row and in chunks: 256 rows in 8 blocks 113 and 60 us (92 and 43), in 304 115 and 90 (92 and 66), in 608 162 and 174 (115 and 125), in
+// 2432 561 and 690; 16 rows in 304 blocks 12.3 and 12.3 (10.3 and 10.3), 32 rows 20.5 and 16.8, 8 rows 8.2 and 12.3.
+constexpr int kChunkBlocks = 2;  // per SM
+
 template <typename T, int DK, bool WIDE>
-cudaError_t launch_rows(const DeltaParams &p, float *kept, int kept_rows, cudaStream_t s) {
-    return launch_rows_with<T, DK, 2, WIDE>(p, kept, kept_rows, s);
+cudaError_t launch_rows(const DeltaParams &p, float *kept, int sms, cudaStream_t s) {
+    const long long blocks = (long long)p.seqs.n_seqs * p.hv * (p.dv / kSlice);
+    if (blocks > (long long)kChunkBlocks * sms || p.seqs.rows < (long long)kC * p.seqs.n_seqs)
+        return launch_sequences(&delta_rows_kernel<T, DK, 2, WIDE>, p, kept, 2 * kCols, 64, sizeof(Stage<T, DK, 2>) * kStages, s);
+    auto *f = kept ? &delta_chunks_kernel<T, DK, WIDE, true> : &delta_chunks_kernel<T, DK, WIDE, false>;
+    return launch_sequences(f, p, kept, kSlice, 2 * kHalf, sizeof(ChunkShared<DK>), s);
 }
 
 template <typename T>
@@ -296,10 +567,10 @@ struct Token {
 struct Rows {
     const DeltaParams &p;
     float *kept;
-    int kept_rows;
+    int sms;
     cudaStream_t s;
     template <typename T, int DK, bool WIDE>
-    cudaError_t operator()() const { return launch_rows<T, DK, WIDE>(p, kept, kept_rows, s); }
+    cudaError_t operator()() const { return launch_rows<T, DK, WIDE>(p, kept, sms, s); }
 };
 
 }  // namespace
@@ -330,8 +601,8 @@ DeltaParams delta_params(const kda_delta_args &a, void *o, float *final_state, u
     return p;
 }
 
-cudaError_t launch_delta_rows(kda_dtype dtype, const DeltaParams &p, float *kept, int kept_rows, cudaStream_t s) {
-    const Rows f{p, kept, kept_rows, s};
+cudaError_t launch_delta_rows(kda_dtype dtype, const DeltaParams &p, float *kept, int sms, cudaStream_t s) {
+    const Rows f{p, kept, sms, s};
     return dtype == KDA_BF16 ? by_size<__nv_bfloat16>(p, f) : by_size<float>(p, f);
 }
 
@@ -351,9 +622,9 @@ size_t delta_prefill_workspace_bytes(const kda_delta_args &a, int) {
     return delta_tc_supported(a.dtype, p, kFewestRows) ? delta_tc_order_bytes(p) : 0;
 }
 
-cudaError_t launch_delta_prefill(const kda_delta_args &a, void *o, float *final_state, void *ws, int, unsigned *err, cudaStream_t s) {
+cudaError_t launch_delta_prefill(const kda_delta_args &a, void *o, float *final_state, void *ws, int sms, unsigned *err, cudaStream_t s) {
     DeltaParams p = delta_params(a, o, final_state, err);
-    if (!delta_tc_supported(a.dtype, p, kFewestRows)) return launch_delta_rows(a.dtype, p, nullptr, 0, s);
+    if (!delta_tc_supported(a.dtype, p, kFewestRows)) return launch_delta_rows(a.dtype, p, nullptr, sms, s);
     const cudaError_t e = launch_delta_tc_order(p, ws, s);
     return e != cudaSuccess ? e : launch_delta_tc(p, s);
 }

@@ -120,3 +120,25 @@ def test_the_binding_refuses_what_does_not_fit():
         kda.layer_norm(x, gate=torch.zeros(4, 9, device=DEV))
     with pytest.raises(kda.KDAError, match="32768"):
         kda.layer_norm(torch.zeros(1, 32769, device=DEV))
+
+
+@pytest.mark.parametrize("shape", [(80, 33, 2, 4, 128, 128), (2, 33, 2, 4, 128, 128), (80, 17, 1, 2, 64, 64), (1, 17, 1, 2, 64, 64),
+                                   (160, 40, 1, 2, 32, 32), (160, 15, 1, 2, 32, 64), (3, 15, 1, 2, 128, 64)])
+def test_fp32_with_many_and_with_few_states(shape):
+    c = Case(FP32, *shape, seed=13)
+    c.check_prefill(*c.prefill())
+    c.check_backward(c.backward())
+    kda.check_status()
+
+
+@pytest.mark.parametrize("B", [2, 160])
+def test_a_value_that_is_not_a_number_stays_behind_the_rows_before_it(B):
+    c = Case(FP32, B, 40, 1, 2, 64, 64, seed=14)
+    q, k, v, g, b = c.inputs()
+    o, _ = c.prefill()
+    for x in (k, v, g, b):
+        y = x.clone()
+        y[:, 21] = float("nan")
+        got, _ = kda.delta_prefill(*(y if t is x else t for t in (q, k, v, g, b)), initial_state=c.state)
+        assert torch.equal(got[:, :21], o[:, :21]) and got[:, 22:].isnan().any()
+    kda.check_status()
