@@ -613,8 +613,8 @@ cudaError_t launch_delta_decode(const kda_delta_args &a, float *state, void *o, 
     return a.dtype == KDA_BF16 ? by_size<__nv_bfloat16>(p, f) : by_size<float>(p, f);
 }
 
-// bf16 prompts of fewer rows than this on average go token by token: a chunk of 64 rows takes the tensor-core kernel the same time whatever it
-// holds. 32 heads of 128, sequences of 16 rows: 12.4 us here and 14.4 there for one, 131 and 160 for 64; of 32 rows: 20.6 and 14.4, 252 and 162.
+// bf16 prompts of fewer rows than this on average are computed in fp32 here: a chunk of 64 rows takes the tensor-core kernel the same time whatever it
+// holds. 32 heads of 128, sequences of 16 rows: 10.3 us here and 14.4 there for one, 131 and 160 for 64; of 32 rows: 14.4 and 14.4, 252 and 162.
 constexpr int kFewestRows = 20;
 
 size_t delta_prefill_workspace_bytes(const kda_delta_args &a, int) {

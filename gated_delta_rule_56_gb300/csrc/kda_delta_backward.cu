@@ -370,7 +370,7 @@ size_t head_floats(const kda_delta_args &a) {  // one of dq, dk per value head
 }  // namespace
 
 // bf16 sequences of fewer rows than this on average take this file's kernel. 32 heads of 128, sequences of 8 rows: 45 us here and 39 on the
-// tensor cores for one, 568 and 488 for 64; of 64 rows: 167 and 41, 2391 and 557. Shorter ones do not fill the chunks of 16 either.
+// tensor cores for one, 568 and 488 for 64; 64 sequences of 64 rows: 2391 and 557. Shorter ones do not fill the chunks of 16 either.
 constexpr int kFewestRows = 8;
 
 size_t delta_backward_workspace_bytes(const kda_delta_args &a, int) {
