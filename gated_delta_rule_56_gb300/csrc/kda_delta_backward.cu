@@ -9,8 +9,11 @@
 //     dq = E dO S0^T + Gp K
 //     dk = b row + col,  row = Ga K - E dR S0^T (through k_i of the row itself),  col = F U dS^T + Gp^T Q + Ga^T (b K)
 //     db_i = dR_i.v_i + k_i.row_i
-//     dG_i = q_i.dq_i + b_i k_i.row_i - k_i.col_i, and for the last row <S1, dS> = exp(G_C) <S0, dS> + sum_j F_j k_j.(dS u_j)
+//     dg_t = sum over the pairs j < t <= i of (dO_i.u_j) P_ij - (dR_i.u_j) A_ij, + sum_{i >= t} E_i (q_i.(S0 dO_i) - b_i k_i.(S0 dR_i))
+//            + sum_{j < t} F_j k_j.(dS u_j) + exp(G_C) <S0, dS>
 //     dS <- exp(G_C) dS + sum_i E_i (q_i dO_i^T - b_i k_i dR_i^T)
+// dg_t is a sum of those terms alone whose decay has row t's in it, so behind a strong decay it is as small as they are. (As a sum of
+// q.dq + b k.row - k.col over the rows from t on it would be the rest of terms of size 1: at g = -12 a tenth of it lost in fp32, at -20 all.)
 // No division, so b = 0 and decays of 0 are ordinary values. All of it is fp32; the states before the chunks come from a run of the
 // recurrence before this kernel (kda_delta.cu).
 //
@@ -48,8 +51,9 @@ struct BackShared {
     float k[kC][DK + 4], q[kC][DK + 4];
     float v[kC][DV + 4], d_o[kC][DV + 4], u[kC][DV + 4], dr[kC][DV + 4];
     float A[kC][kC + 1], P[kC][kC + 1], Gp[kC][kC + 1], Ga[kC][kC + 1];
+    float cross[kC][kC + 1];  // [i][t]: row i's pairs with the rows before t
     float G[kC], E[kC], F[kC], b[kC], g[kC];
-    float sums[8][5][kC];
+    float sums[8][3][kC];
     float joined[8];
 };
 
@@ -220,6 +224,13 @@ __global__ void __launch_bounds__(kThreads) delta_back_kernel(BackParams p) {
                 }
             s.Gp[i][j] = j <= i ? D * gp : 0.f;
             s.Ga[i][j] = j < i ? -D * ga : 0.f;
+            float pairs = j < i ? fmaf(gp, s.P[i][j], -ga * s.A[i][j]) : 0.f;
+#pragma unroll
+            for (int d = 1; d < kC; d *= 2) {
+                const float y = __shfl_up_sync(0xffffffffu, pairs, d, kC);
+                if (j >= d) pairs += y;
+            }
+            if (j < i) s.cross[i][j + 1] = pairs;
             if (tid < kC) {
                 float x = 0.f;
 #pragma unroll 4
@@ -250,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) delta_back_kernel(BackParams p) {
                 const int i = k0 + r;
                 const float ki = s.k[i][kc];
                 float dq = s.E[i] * os[r], row = -s.E[i] * rs[r], col = s.F[i] * us[r];
-                const float through = ki * col;
+                const float from = fmaf(s.q[i][kc], dq, s.b[i] * ki * row), through = ki * col;
                 for (int j = 0; j < kC; ++j) {
                     const float kj = s.k[j][kc];
                     dq = fmaf(s.Gp[i][j], kj, dq);
@@ -263,9 +274,9 @@ __global__ void __launch_bounds__(kThreads) delta_back_kernel(BackParams p) {
                     p.dq[at] = dq;
                     p.dk[at] = fmaf(s.b[i], row, col);
                 }
-                float x[4] = {s.q[i][kc] * dq, ki * row, ki * col, through};
+                float x[3] = {from, through, ki * row};
 #pragma unroll
-                for (int a = 0; a < 4; ++a) {
+                for (int a = 0; a < 3; ++a) {
 #pragma unroll
                     for (int d = 16; d > 0; d >>= 1) x[a] += __shfl_xor_sync(0xffffffffu, x[a], d);
                     if (lane == 0) s.sums[warp][a][i] = x[a];
@@ -294,27 +305,29 @@ __global__ void __launch_bounds__(kThreads) delta_back_kernel(BackParams p) {
         }
         if (warp == 0) {  // the sums over the key columns: the warps that hold row i
             const int i = lane & 15, w0 = i / KR * (DK / 32);
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
+            float x[3] = {0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < DK / 32; ++w)
 #pragma unroll
-                for (int a = 0; a < 4; ++a) x[a] += s.sums[w0 + w][a][i];
-            float S1 = x[3];
-#pragma unroll
-            for (int d = 8; d > 0; d >>= 1) S1 += __shfl_xor_sync(0xffffffffu, S1, d);
+                for (int a = 0; a < 3; ++a) x[a] += s.sums[w0 + w][a][i];
             float inner = 0.f;
 #pragma unroll
             for (int w = 0; w < DK / 32; ++w) inner += s.joined[w];
-            float dG = x[0] + s.b[i] * x[1] - x[2];
-            if (i == kC - 1) dG += fmaf(whole, inner, S1);
+            float dg = whole * inner, before = __shfl_up_sync(0xffffffffu, x[1], 1, kC);
+            if (i == 0) before = 0.f;
 #pragma unroll
-            for (int d = 1; d < kC; d *= 2) {  // dg_i = sum of dG_j, j >= i
-                const float y = __shfl_down_sync(0xffffffffu, dG, d);
-                if (i + d < kC) dG += y;
+            for (int d = 1; d < kC; d *= 2) {  // sums over the rows from i on, and before i
+                const float y = __shfl_down_sync(0xffffffffu, x[0], d, kC), z = __shfl_up_sync(0xffffffffu, before, d, kC);
+                if (i + d < kC) x[0] += y;
+                if (i >= d) before += z;
             }
+            float across = 0.f;
+            for (int r = i; r < m; ++r)
+                if (i > 0) across += s.cross[r][i];
+            dg += across + (x[0] + before);
             if (lane < m) {
-                p.dg[(row0 + i) * hv + h] = dG;
-                p.db[(row0 + i) * hv + h] = s.g[i] + x[1];
+                p.dg[(row0 + i) * hv + h] = dg;
+                p.db[(row0 + i) * hv + h] = s.g[i] + x[2];
             }
         }
     }

@@ -9,6 +9,7 @@
 //      T - I, P, K and Q are the operands of the forward pass read with the other index as the long one. It keeps dS and dR per chunk;
 //   3. everything else, which needs no other chunk: one block per (chunk, value head), [dO; dR] as the 128 rows of the accumulators:
 //          [dO; dR] U^T -> Gp, Ga;   [dO; dR] S0^T, scaled by +-E, + [Gp; Ga] K = [dq; row];   F (U dS^T) + Gp^T Q + (b Ga)^T K = col.
+//      dg is made of the pairs' products with [Q; K] K^T and of the parts of dq, row and col that come from the states.
 // Where value heads share key heads, dq and dk go per value head to the workspace and are added up in a fixed order.
 //
 // Operands that are not exact in bf16 go in as two values (2^-17 of them is left, the products of both rests are left out), those that are
@@ -377,18 +378,21 @@ constexpr uint32_t TG_1 = 0;     // [dO; dR] S0^T, scaled, then with [Gp; Ga] K:
 constexpr uint32_t TG_2 = 128;   // U dS^T, scaled, then with Gp^T Q + (b Ga)^T K: col in lanes 0..63
 constexpr uint32_t TG_P = 256;   // [dO; dR] U^T
 constexpr uint32_t TG_A = 320;   // [dO; dR]: two times 64
+constexpr uint32_t TG_G = 448;   // [Q; K] K^T
 
 // The MMAs that take 64 rows (U) or 64 columns (Gp, b Ga) as 128 read what lies behind them as well, into lanes that nobody reads: the order here
 // keeps that inside the block's memory.
 struct GradShared {
-    uint8_t kq[32768];
+    uint8_t qk[32768];                   // per 64 key channels, 64 rows of Q, 64 rows of K
     uint8_t g_hi[16384], g_lo[16384];    // [Gp; Ga], 128 rows
     uint8_t bg_hi[8192], bg_lo[8192];    // b Ga
     uint8_t u_hi[16384], u_lo[16384];    // U, per 64 value channels 64 rows
     uint8_t s_hi[32768], s_lo[32768];    // S0, then dS, per 64 value channels 128 rows (key channels)
     Vec vec;
     float a[C], pre[C], f[C];
-    float sums[4][5][C];                 // per quarter of the columns: q.dq, k.row, k.col, k.(the part of col from dS), dR.v
+    float sums[4][5][C];                 // per quarter of the columns: q.(the part of dq from S0), k.row, k.(the part of row from S0),
+                                         // k.(the part of col from dS), dR.v
+    float cross[4][C], pairs[4][2 * C];  // dg_t from the pairs in t's quarter of the columns, per 32 lanes; a quarter's pairs of a lane
     float joined[kGradThreads / 32];
     uint64_t full, b0, b1, b2, b3, b4;
     uint32_t tmem;
@@ -516,8 +520,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
     if (tid == 0) {
         mbar_arrive_expect_tx(&s.full, DK / 64 * 16384);
         for (int a = 0; a < DK / 64; ++a) {
-            tma_load_3d(s.kq + a * 16384, &maps.k, &s.full, 64 * a, h / p.f.per, (int)row0);
-            tma_load_3d(s.kq + a * 16384 + 8192, &maps.q, &s.full, 64 * a, h / p.f.per, (int)row0);
+            tma_load_3d(s.qk + a * 16384, &maps.q, &s.full, 64 * a, h / p.f.per, (int)row0);
+            tma_load_3d(s.qk + a * 16384 + 8192, &maps.k, &s.full, 64 * a, h / p.f.per, (int)row0);
         }
     }
     if (warp == 1) {
@@ -570,7 +574,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         for (int e = tid; e < (C - m) * 8; e += kGradThreads)
 #pragma unroll
-            for (int a = 0; a < DK / 32; ++a) *reinterpret_cast<uint4 *>(&s.kq[a * 8192 + m * 128 + e * 16]) = zero;
+            for (int a = 0; a < DK / 32; ++a) *reinterpret_cast<uint4 *>(&s.qk[a * 8192 + m * 128 + e * 16]) = zero;
     }
     tmem_st_wait();
     fence_async_smem();
@@ -579,7 +583,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
     tc_fence_after();
     const uint64_t u_hi = sdesc_sw128(smem_u32(s.u_hi), 16u, 1024u), s_hi = sdesc_sw128(smem_u32(s.s_hi), 16u, 1024u);
     constexpr uint64_t kULo = sizeof(s.u_hi) >> 4, kSLo = sizeof(s.s_hi) >> 4, kGLo = sizeof(s.g_hi) >> 4, kBLo = sizeof(s.bg_hi) >> 4;
+    const uint32_t qk = smem_u32(s.qk);
     if (warp == 0) {
+        const uint64_t d_qk = sdesc_sw128(qk, 16u, 1024u), d_k = sdesc_sw128(qk + 8192u, 16u, 1024u);
+#pragma unroll
+        for (int st = 0; st < DK / 16; ++st)
+            mma_bf16_warp(tmem + TG_G, d_qk + kstep(st, 16384u), d_k + kstep(st, 16384u), idesc_bf16(128, 64), st > 0);
 #pragma unroll
         for (int e = 0; e < 3; ++e)  // first x first, first x second, second x first
 #pragma unroll
@@ -613,6 +622,20 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
     tc_fence_after();
     __syncthreads();  // dv is out of the place
     const float b_row = s.vec.b[i];
+    // Row i of Q (0) or K (1), this thread's columns.
+    auto dot_row = [&](const float (&x)[W], uint32_t k) {
+        float sum = 0.f;
+        const int c0 = W * part;
+#pragma unroll
+        for (int e = 0; e < W / 8; ++e) {
+            const int cc = c0 + 8 * e;
+            float y[8];
+            bf16_pairs(*reinterpret_cast<const uint4 *>(&s.qk[(cc >> 6) * 16384 + k * 8192 + i * 128 + ((((cc & 63) >> 3) ^ (i & 7)) << 4)]), y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = fmaf(x[8 * e + j], y[j], sum);
+        }
+        return sum;
+    };
     {  // Gp, Ga (without b) and b Ga
         float x[16];
         tmem_ld(at + TG_P + 16 * part, x);
@@ -626,6 +649,30 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
 #pragma unroll
             for (int e = 0; e < 2; ++e) store_operand(s.bg_hi, s.bg_lo, i, 2 * part + e, x + 8 * e);
         }
+        // dg_t has the pairs j < t <= i. For this quarter's t, from those j < t that are in the quarter: the lane's sums up to t, then the sum
+        // over the lanes i >= t, which leaves lane l with t = its quarter's l & 15. The earlier quarters' pairs come at the end.
+        float y[16], sum = 0.f;
+        tmem_ld(at + TG_G + 16 * part, y);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int t = 16 * part + e;
+            const float pair = t < i ? x[e] * y[e] : 0.f;
+            y[e] = t <= i ? sum : 0.f;
+            sum += pair;
+        }
+        s.pairs[part][L] = sum;
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) {
+            const bool up = lane & d;
+#pragma unroll
+            for (int e = 0; e < d; ++e) {
+                const float other = __shfl_xor_sync(0xffffffffu, up ? y[e] : y[e + d], d);
+                y[e] = (up ? y[e + d] : y[e]) + other;
+            }
+        }
+        y[0] += __shfl_xor_sync(0xffffffffu, y[0], 16);
+        if (lane < 16) s.cross[L >> 5][16 * part + lane] = y[0];
     }
     ok = mbar_wait(&s.b1, 0, kWaitNs) && ok;
     tc_fence_after();
@@ -637,6 +684,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
 #pragma unroll
         for (int e = 0; e < W; ++e) x[e] *= E;
         tmem_st(at + TG_1 + W * part, x);
+        s.sums[part][second ? 2 : 0][i] = dot_row(x, second ? 1u : 0u);
     }
     state_operand(s, state);  // S0's operand is read: dS in its place
     tmem_st_wait();
@@ -644,8 +692,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t kq = smem_u32(s.kq);
-    const uint64_t k_n = sdesc_sw128(kq, 16384u, 1024u), q_n = sdesc_sw128(kq + 8192u, 16384u, 1024u);
+    const uint64_t q_n = sdesc_sw128(qk, 16384u, 1024u), k_n = sdesc_sw128(qk + 8192u, 16384u, 1024u);
     if (warp == 0) {
         const uint64_t g = sdesc_sw128(smem_u32(s.g_hi), 16u, 1024u);
 #pragma unroll
@@ -664,20 +711,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
         mma_commit_warp(&s.b3);
     }
     __syncwarp();
-    // Row i of K or Q, this thread's columns.
-    auto dot_row = [&](const float (&x)[W], uint32_t q) {
-        float sum = 0.f;
-        const int c0 = W * part;
-#pragma unroll
-        for (int e = 0; e < W / 8; ++e) {
-            const int cc = c0 + 8 * e;
-            float y[8];
-            bf16_pairs(*reinterpret_cast<const uint4 *>(&s.kq[(cc >> 6) * 16384 + q * 8192 + i * 128 + ((((cc & 63) >> 3) ^ (i & 7)) << 4)]), y);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(x[8 * e + j], y[j], sum);
-        }
-        return sum;
-    };
     const int kc = W * part;  // this thread's first key column
     float x[W];
     ok = mbar_wait(&s.b3, 0, kWaitNs) && ok;  // also: U's and dS's operands are read
@@ -688,7 +721,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < W; ++e) x[e] *= F;
-        s.sums[part][3][i] = dot_row(x, 0u);
+        s.sums[part][3][i] = dot_row(x, 1u);
         tmem_st(at + TG_2 + kc, x);
         tmem_st_wait();
     }
@@ -715,10 +748,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
     tc_fence_after();
     tmem_ld(at + TG_1 + kc, x);
     tmem_ld_wait();
-    s.sums[part][second ? 1 : 0][i] = dot_row(x, second ? 0u : 1u);
-    if (second)
+    if (second) {
+        s.sums[part][1][i] = dot_row(x, 1u);
 #pragma unroll
         for (int e = 0; e < W; ++e) x[e] *= b_row;
+    }
     put_row(second ? row_rows : dq_rows, i, kc, x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) joined += __shfl_xor_sync(0xffffffffu, joined, d);
@@ -730,7 +764,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
     if (!second) {
         tmem_ld(at + TG_2 + kc, x);
         tmem_ld_wait();
-        s.sums[part][2][i] = dot_row(x, 0u);
 #pragma unroll
         for (int e = 0; e < W; e += 4) {
             const float4 r = *reinterpret_cast<const float4 *>(row_rows + i * kPitch + kc + e);
@@ -745,38 +778,67 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_chunk_back_kernel(const
     if (warp == 0) tmem_dealloc(tmem, 512);
     rows_out(p.dk + (row0 * hv + h) * dk, (size_t)hv * dk, row_rows, m, dk);
     if (warp == 1) {
-        float dG[2], behind[2], inner = lane < kGradThreads / 32 ? s.joined[lane] : 0.f, krow[2], dRv[2];
+        // dg_t: the pairs across t, the rows i >= t that read S0, the rows j < t whose values dS reads, and whole <S0, dS>. Only terms that t's
+        // own decay is in, so a strong one leaves no rest of terms of size 1.
+        float dg[2], from[2], before[2], krow[2], dRv[2], inner = lane < kGradThreads / 32 ? s.joined[lane] : 0.f;
+        float earlier[2][3];  // of row r: its pairs with the quarters before quarter 1, 2, 3
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int r = lane + 32 * half;
             float v[5];
 #pragma unroll
             for (int e = 0; e < 5; ++e) v[e] = (s.sums[0][e][r] + s.sums[1][e][r]) + (s.sums[2][e][r] + s.sums[3][e][r]);
-            dG[half] = v[0] + s.vec.b[r] * v[1] - v[2];
+            from[half] = fmaf(s.vec.b[r], v[2], v[0]);
+            before[half] = v[3];
             krow[half] = v[1];
-            behind[half] = v[3];
             dRv[half] = v[4];
-        }
-        float through = behind[0] + behind[1];
+            dg[half] = (s.cross[0][r] + s.cross[1][r]) + (s.cross[2][r] + s.cross[3][r]);
+            float sum = 0.f;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-            through += __shfl_xor_sync(0xffffffffu, through, d);
-            inner += __shfl_xor_sync(0xffffffffu, inner, d);
+            for (int e = 0; e < 3; ++e) earlier[half][e] = sum += s.pairs[e][r] + s.pairs[e][C + r];
         }
-        if (lane == 31) dG[1] += fmaf(s.vec.whole, inner, through);  // <S1, dS>
 #pragma unroll
-        for (int d = 1; d < 32; d *= 2)  // dg_i = sum of dG_j, j >= i
+        for (int d = 16; d > 0; d >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, d);
+        {  // the pairs of t with the quarters before its own: over the rows from t to its quarter's end, and the quarters behind it
+            const bool upper = lane & 16;
+            float own[2] = {upper ? earlier[0][0] : 0.f, upper ? earlier[1][2] : earlier[1][1]};
+#pragma unroll
+            for (int d = 1; d < 16; d *= 2)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float y = __shfl_down_sync(0xffffffffu, own[half], d, 16);
+                    if ((lane & 15) + d < 16) own[half] += y;
+                }
+            float first = earlier[1][0], second = upper ? earlier[1][1] : 0.f;  // rows 32..63 for quarter 1, 48..63 for quarter 2
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) {
+                first += __shfl_xor_sync(0xffffffffu, first, d);
+                second += __shfl_xor_sync(0xffffffffu, second, d);
+            }
+            dg[0] += upper ? own[0] + first : 0.f;
+            dg[1] += upper ? own[1] : own[1] + second;
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const float y = __shfl_down_sync(0xffffffffu, dG[half], d);
-                if (lane + d < 32) dG[half] += y;
+                const float y = __shfl_down_sync(0xffffffffu, from[half], d), z = __shfl_up_sync(0xffffffffu, before[half], d);
+                if (lane + d < 32) from[half] += y;
+                if (lane >= d) before[half] += z;
             }
-        dG[0] += __shfl_sync(0xffffffffu, dG[1], 0);
+        from[0] += __shfl_sync(0xffffffffu, from[1], 0);
+        const float lower = __shfl_sync(0xffffffffu, before[0], 31);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const float y = __shfl_up_sync(0xffffffffu, before[half], 1);
+            before[half] = (lane > 0 ? y : 0.f) + (half ? lower : 0.f);
+            dg[half] += (from[half] + before[half]) + s.vec.whole * inner;
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int r = lane + 32 * half;
             if (r < m) {
-                p.dg[(row0 + r) * hv + h] = dG[half];
+                p.dg[(row0 + r) * hv + h] = dg[half];
                 p.db[(row0 + r) * hv + h] = dRv[half] + krow[half];
             }
         }
