@@ -262,12 +262,18 @@ __global__ void __launch_bounds__(kThreads) delta_back_kernel(BackParams p) {
                 const float ki = s.k[i][kc];
                 float dq = s.E[i] * os[r], row = -s.E[i] * rs[r], col = s.F[i] * us[r];
                 const float from = fmaf(s.q[i][kc], dq, s.b[i] * ki * row), through = ki * col;
-                for (int j = 0; j < kC; ++j) {
+                // Pairs beyond the diagonal are left out, not multiplied by zero: a NaN or an infinity stays with the rows that it belongs to. i is
+                // the warp's.
+                for (int j = 0; j < i; ++j) {
                     const float kj = s.k[j][kc];
                     dq = fmaf(s.Gp[i][j], kj, dq);
                     row = fmaf(s.Ga[i][j], kj, row);
+                }
+                dq = fmaf(s.Gp[i][i], ki, dq);
+                col = fmaf(s.Gp[i][i], s.q[i][kc], col);
+                for (int j = i + 1; j < kC; ++j) {
                     col = fmaf(s.Gp[j][i], s.q[j][kc], col);
-                    col = fmaf(s.Ga[j][i] * s.b[j], kj, col);
+                    col = fmaf(s.Ga[j][i] * s.b[j], s.k[j][kc], col);
                 }
                 if (i < m) {
                     const size_t at = ((row0 + i) * hv + h) * DK + kc;

@@ -452,8 +452,8 @@ KDA_API size_t kda_qk_norm_rotary_backward_workspace_size(const kda_rotary_args 
  *     S' = a S_{t-1};   u = b (v_t - S'^T k_t);   S_t = S' + k_t u^T;   o_t = S_t^T q_t      (no scale is applied to q)
  * bf16 sequences of 20 rows and more on average (8 for the gradients) go in chunks of 64 rows on the tensor cores, with operands in two or
  * three bf16 values: final states are within 2e-6 and gradients within 6e-6 of an exact computation (2-norm) instead of about 4e-7, and a NaN or an infinity may
- * also reach the rows of its chunk before it. fp32 and shorter sequences are computed in fp32, row by row or in
- * chunks of 16 rows.
+ * also reach the other rows of its chunk, outputs and gradients. fp32 and shorter sequences are computed in fp32, row by row or in
+ * chunks of 16 rows, and only a NaN of g may reach other gradients of its chunk there.
  * g <= 0 is the log-decay (-inf clears the state; below -128 is computed as -128, whose exponential is 0 in fp32). The rows of k are taken
  * as unit rows (kda_qk_norm_rotary with norm 1) and b in [0, 1] (up to 2 is computed as well): with |k|^2 b > 2 the recurrence itself grows.
  */

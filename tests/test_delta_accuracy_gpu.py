@@ -58,3 +58,33 @@ def test_the_decays_gradients_behind_strong_decays(dtype, g, shape):
     worst = gradients_of_each(c, c.backward())
     kda.check_status()
     assert all(v <= GRADIENT[dtype] for v in worst.values()), worst
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("what", ["q", "k", "v", "beta", "d_o"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_what_is_not_finite_reaches_the_gradients_that_the_formulas_give_it_to(dtype, what, value):
+    """Gradients that do not depend on the bad value are those of a call without it, bit for bit (bf16: outside the value's chunk of 64)."""
+    T, row = 200, 101
+    c = Case(dtype, 1, T, 2, 2, 128, 128, seed=22)
+    clean = c.backward()
+    getattr(c, what)[(0, row, 1) if what == "beta" else (0, row, 1, 5)] = value
+    g = c.backward()
+    kda.check_status()
+    (s, do, df), = c.sequences()
+    s = list(s)
+    # What depends on it, by the definition in 64 bits: NaN there.
+    names = ("q", "k", "v", "g", "beta")
+    if what == "d_o":
+        do[row, 1, 5] = float("nan")
+    else:
+        s[names.index(what)][(row, 1) if what == "beta" else (row, 1, 5)] = float("nan")
+    finite = 0
+    for name, w in zip(GRADS, ref.delta_backward(*s, do, df)):
+        got, before = g[name].cpu(), clean[name].cpu()
+        free = torch.isfinite(w).reshape(got.shape)
+        if dtype == BF16 and name != "d_initial_state":
+            free[:, 64:128, 1] = False
+        finite += int(free.sum())
+        assert torch.equal(got[free], before[free]), name
+    assert finite > 0
