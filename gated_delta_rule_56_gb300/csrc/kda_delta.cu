@@ -619,7 +619,7 @@ constexpr int kFewestRows = 20;
 
 size_t delta_prefill_workspace_bytes(const kda_delta_args &a, int) {
     const DeltaParams p = delta_params(a, nullptr, nullptr, nullptr);
-    return delta_tc_supported(a.dtype, p, kFewestRows) ? delta_tc_order_bytes(p) : 0;
+    return delta_tc_shape(a.dtype, p, kFewestRows) ? delta_tc_order_bytes(p) : 0;
 }
 
 cudaError_t launch_delta_prefill(const kda_delta_args &a, void *o, float *final_state, void *ws, int sms, unsigned *err, cudaStream_t s) {

@@ -394,7 +394,9 @@ constexpr int kFewestRows = 8;
 
 size_t delta_backward_workspace_bytes(const kda_delta_args &a, int) {
     const DeltaParams p = delta_params(a, nullptr, nullptr, nullptr);
-    return (delta_tc_supported(a.dtype, p, kFewestRows) ? delta_tc_backward_bytes(p) : kept_floats(a) * 4) + 2 * head_floats(a) * 4;
+    // Rows that TMA cannot load take this file's kernel, which may need more or less.
+    const size_t rows = kept_floats(a) * 4, tc = delta_tc_shape(a.dtype, p, kFewestRows) ? delta_tc_backward_bytes(p) : 0;
+    return (tc > rows ? tc : rows) + 2 * head_floats(a) * 4;
 }
 
 cudaError_t launch_delta_backward(const kda_delta_args &a, const kda_delta_grads &g, void *ws, int sms, unsigned *err, cudaStream_t s) {

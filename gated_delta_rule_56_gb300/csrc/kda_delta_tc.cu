@@ -775,9 +775,12 @@ bool encode(CUtensorMap *map, const void *base, long long rows, int heads, int d
 
 }  // namespace delta_tc
 
+bool delta_tc_shape(kda_dtype dtype, const DeltaParams &p, int fewest) {
+    return dtype == KDA_BF16 && p.seqs.rows > 0 && p.seqs.rows >= (long long)fewest * p.seqs.n_seqs;
+}
 bool delta_tc_supported(kda_dtype dtype, const DeltaParams &p, int fewest) {
     auto ok = [](const void *x, long long stride) { return aligned16(x) && stride % 8 == 0; };
-    return dtype == KDA_BF16 && p.seqs.rows > 0 && p.seqs.rows >= (long long)fewest * p.seqs.n_seqs && ok(p.q, p.qs) && ok(p.k, p.ks) && ok(p.v, p.vs) && delta_tc::encoder();
+    return delta_tc_shape(dtype, p, fewest) && ok(p.q, p.qs) && ok(p.k, p.ks) && ok(p.v, p.vs) && delta_tc::encoder();
 }
 
 // Packed sequences start longest first, so that no long one is left for the end.

@@ -5,7 +5,9 @@
 
 namespace kda {
 
-// bf16 rows that TMA can load (16-byte aligned), and at least `fewest` of them per sequence on average.
+// bf16 rows, at least `fewest` of them per sequence on average. Workspaces are sized by this alone: where the rows lie is no part of a shape.
+bool delta_tc_shape(kda_dtype dtype, const DeltaParams &p, int fewest);
+// And TMA can load them (16-byte aligned).
 bool delta_tc_supported(kda_dtype dtype, const DeltaParams &p, int fewest);
 // The blocks' order of packed sequences: workspace bytes (0: none), and its making (into p.order).
 size_t delta_tc_order_bytes(const DeltaParams &p);

@@ -315,6 +315,8 @@ KDA_API kda_status kda_decode_step_gated(kda_dtype dtype, int N, int H, int dk, 
  * not a non-decreasing list from 0 to T sets KDA_ERR_INVALID_ARG in the error word and leaves the outputs
  * unspecified (nothing out of range is read or written), and rows without any sequence (n_seqs == 0) are refused.
  * Gradients are fp32, and the same bits every time (no atomics).
+ * A *_workspace_size call looks at the arguments as the call itself does, pointers included, and returns 0 for those that it would
+ * refuse. The size goes by shapes, types, the packing and which optional inputs are given, not by where rows lie: it serves every call of its shape.
  */
 
 /*
