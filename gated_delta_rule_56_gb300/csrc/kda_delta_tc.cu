@@ -28,6 +28,7 @@
 // a chunk takes 8 000 cycles, without the decays no less than with them). Kept out by measurement: 8 chain and 4 prep warps (1.02 ms: each waits
 // for its own latencies), the inverse with fp32 or tf32 products (0.67 to 0.80 ms), conversions by truncation or on register pairs (the same time),
 // waits that sleep longer (the same).
+#include <atomic>
 #include <mutex>
 
 #include "kda_delta_tc.cuh"
@@ -39,6 +40,17 @@ using namespace delta_tc;
 
 constexpr int kChainWarps = 16, kPrepWarps = 8, kIssuer = 24, kLoader = 25, kDecays = 26, kKeeper = 27;
 constexpr int kThreads = 28 * 32, kPrep = kPrepWarps * 32;
+
+// Registers of a thread: the preparing warps take what the last four give, the chain keeps what the block was launched with. More than that
+// in all waits forever, and a move in the wrong direction is an illegal instruction; the count is the compiler's (72 as built: 896 x 72 = 512 x
+// 72 + 256 x 80 + 128 x 56), so launch() asks for it first.
+constexpr int kPrepRegisters = 80, kOtherRegisters = 56;
+constexpr bool registers_suffice(int launched) {
+    return kOtherRegisters <= launched && launched <= kPrepRegisters &&
+           kPrep * (kPrepRegisters - launched) <= (kThreads - kPrep - kChainWarps * 32) * (launched - kOtherRegisters);
+}
+static_assert(registers_suffice(72) && registers_suffice(80) && !registers_suffice(64) && !registers_suffice(48) && !registers_suffice(88),
+              "enough to give, and moves in their directions");
 
 // TMEM columns
 constexpr uint32_t TM_S = 0;      // S^T: first bf16 values in 0..63, second in 64..127; then U with its decay, three times 32
@@ -694,15 +706,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     bool ok = true;
-    // The block was launched with 896 x 72 registers: 512 x 72 + 256 x 80 + 128 x 56.
     if (warp < kChainWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         ok = chain<DK, KEEP>(s, p, kept, n, h, begin, end, chunks, tmem);
     } else if (warp < kChainWarps + kPrepWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrepRegisters));
         ok = prep<DK>(s, p, h, begin, end, chunks, tmem);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
         if (warp == kIssuer) {
             ok = issue<DK, KEEP>(s, chunks);
             if (!ok) {  // nothing may be in flight at the end
@@ -731,8 +741,15 @@ constexpr size_t kSharedBytes = sizeof(Shared) + 1024;
 template <int DK, bool KEEP>
 cudaError_t launch(const Maps &maps, const DeltaParams &p, const DeltaKept &kept, cudaStream_t s) {
     auto *f = &delta_tc_kernel<DK, KEEP>;
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSharedBytes);
-    if (e != cudaSuccess) return e;
+    static std::atomic<int> registers{0};  // of a thread, in the units of 8 that they are given in
+    cudaError_t e;
+    if (registers == 0) {
+        cudaFuncAttributes compiled;
+        if ((e = cudaFuncGetAttributes(&compiled, f)) != cudaSuccess) return e;
+        registers = (compiled.numRegs + 7) / 8 * 8;
+    }
+    if (!registers_suffice(registers)) return cudaErrorLaunchOutOfResources;
+    if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSharedBytes)) != cudaSuccess) return e;
     f<<<(unsigned)((long long)p.seqs.n_seqs * p.hv), kThreads, kSharedBytes, s>>>(maps, p, kept);
     return cudaGetLastError();
 }
