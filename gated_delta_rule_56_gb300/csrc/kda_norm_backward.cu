@@ -14,6 +14,17 @@
 namespace kda {
 namespace {
 
+// sigmoid(z) and 1 - sigmoid(z) = sigmoid(-z), two at a time. With e = exp(-z) the second is e sigmoid(z) where the first is near 1: a
+// difference would leave 24 bits of 1, and behind z = 17 nothing (a sigmoid gate's gradient is their product).
+__device__ __forceinline__ void sigmoids2(f32x2 z, f32x2 &s, f32x2 &other) {
+    float z0, z1, t0, t1;
+    unpair(z, z0, z1);
+    unpair(mul2(z, both(-kLog2e)), t0, t1);
+    const float e0 = ex2(t0), e1 = ex2(t1), s0 = rcp(1.f + e0), s1 = rcp(1.f + e1);
+    s = pair(s0, s1);
+    other = pair(z0 < 0.f ? 1.f - s0 : e0 * s0, z1 < 0.f ? 1.f - s1 : e1 * s1);
+}
+
 template <typename T, int V, int K, int GROUP, bool GATE>
 __global__ void __launch_bounds__(kBlock<GROUP>) norm_back_kernel(NormParams p) {
     constexpr int LINES = kBlock<GROUP> / GROUP, P = (V + 1) / 2;
@@ -68,7 +79,9 @@ __global__ void __launch_bounds__(kBlock<GROUP>) norm_back_kernel(NormParams p) 
             for (int j = 0; j < P; ++j) {
                 f32x2 v = t[i][j];
                 if constexpr (GATE) {  // silu' = s (1 + z (1 - s)), sigmoid' = s (1 - s)
-                    const f32x2 s = sigmoid2(zi[j]), other = add2(both(1.f), minus(s)), vs = mul2(v, s);
+                    f32x2 s, other;
+                    sigmoids2(zi[j], s, other);
+                    const f32x2 vs = mul2(v, s);
                     g[i][j] = mul2(vs, p.silu ? fma2(zi[j], other, both(1.f)) : other);
                     v = p.silu ? mul2(vs, zi[j]) : vs;
                 }
