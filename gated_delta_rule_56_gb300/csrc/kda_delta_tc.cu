@@ -4,30 +4,32 @@
 //     A_ij = b_i exp(G_i - G_j) k_i.k_j (j < i),  P_ij = exp(G_i - G_j) q_i.k_j (j <= i),  T = (I + A)^-1
 //     R_i = b_i v_i - b_i exp(G_i) S^T k_i,  U = T R,  o_i = exp(G_i) S^T q_i + sum_j P_ij u_j
 //     S <- exp(G_C) S + sum_j k_j (exp(G_C - G_j) u_j)^T
-// With one decay per head every decay is a scalar of a row pair: exponents are differences (<= 0) and no product needs a decayed
-// operand, so K and Q go into every MMA as they are in memory, exact in bf16.
+// With one decay per head every decay is a scalar of a row pair, the exponential of the log-decays between the two rows (<= 0), and no product
+// needs a decayed operand, so K and Q go into every MMA as they are in memory, exact in bf16.
 //
 // Everything of the chain is transposed: TMEM lane = value column, so S^T, R^T, U^T are A operands in TMEM, K and Q (and T, P) are B operands
 // in shared memory, read K-major or MN-major from the same 128-byte swizzled tile, and all work between two MMAs is within a lane:
 //     KS = S^T K^T  ->  R  ->  (T - I) R  ->  U  ->  S^T += U^T K        (o: QS and P U, beside the chain)
 //
 // Precision. The state is accumulated in fp32, its final value is an fp32 output, and a bf16 operand has 8 bits. So what is not exact goes in
-// as several bf16 values: S, R, T and P as two (2^-17 of them is left; the products of both rests, 2^-18, are left out), U with its
-// decay as three in the state's update, where its rounding would be the state's. U = R + (T - I) R adds R itself in fp32. The final state of
-// 8192 rows is 1.9e-6 off 64 bits in the 2-norm (the plain fp32 form 0.2e-6); one bf16 value for S and U would leave 2e-3. The outputs are
+// as several bf16 values: S, R and P as two (2^-18 of them is left), T - I as three (of its products with R, those of 2^-25 and less are left
+// out), U with its decay as three in the state's update, where its rounding would be the state's. U = R + (T - I) R adds R itself in fp32. The inverse
+// is made in fp32 with joins of two tf32 values: an error there is multiplied by |A| |T|. The final state of 8192 rows is 1.7e-6 off 64
+// bits in the 2-norm (the plain fp32 form 0.2e-6); one bf16 value for S and U would leave 2e-3. With T - I and the joins in two bf16 values it was
+// 1.9e-6, but 2e-2 with equal keys and beta = 2, where it is 7e-4 now (fp32 row by row: 1e-4), and the prompt below took 661 us. The outputs are
 // as near as their one rounding.
 //
 // Roles (one block per SM): warps 0-15 the chain (four per lane quarter, a quarter of the rows and key channels each), 16-23 prepare the next
 // chunk: A and P from the K K^T and Q K^T accumulators (thread = TMEM lane = row), the inverse of I + A, T - I and P as operands; 24
 // issues the MMAs, 25 the TMA loads, 26 makes the decays, 27 hands T and P out for the gradients. Tiles of K and Q have three stages, V, T and
-// P two: 205 KB of shared memory, and all 512 columns of TMEM.
+// P two: 218 KB of shared memory, and all 512 columns of TMEM.
 //
-// Measured: 4 x 8192 rows, 32 value heads, 16 key heads of 128: 0.66 ms, 10 000 cycles per chunk on 128 of 152 SMs; 37 packed sequences of 20 011
-// rows, 16 heads: 0.23 ms. Bound by the latency of the chain (three dependent MMA groups and the conversions between them, some 7 000 cycles) and of
-// the preparation beside it (5 400 warp instructions per scheduler and chunk, issued in 54 % of the cycles: without the inverse
-// a chunk takes 8 000 cycles, without the decays no less than with them). Kept out by measurement: 8 chain and 4 prep warps (1.02 ms: each waits
-// for its own latencies), the inverse with fp32 or tf32 products (0.67 to 0.80 ms), conversions by truncation or on register pairs (the same time),
-// waits that sleep longer (the same).
+// Measured: 4 x 8192 rows, 32 value heads, 16 key heads of 128: 0.70 ms, 10 600 cycles per chunk on 128 of 152 SMs; 37 packed sequences of 20 011
+// rows, 16 heads: 0.24 ms. Bound by the latency of the chain (three dependent MMA groups and the conversions between them, some 7 000 cycles) and of
+// the preparation beside it, which sets the pace: substitution and joins have six barriers between them. Kept out by measurement: 8 chain and 4 prep
+// warps (1.02 ms: each waits for its own latencies), the joins' last block through shared memory (0.72 ms), substitution and first joins on
+// the four warps that hold K's rows while the others make P (0.77 ms: those four sit on two of the SM's schedulers), conversions by truncation or on
+// register pairs (the same time), waits that sleep longer (the same).
 #include <atomic>
 #include <mutex>
 
@@ -61,13 +63,12 @@ constexpr uint32_t TM_O = 384;    // QS, scaled, then with P U added
 constexpr uint32_t TM_KK = 448;   // [K; Q] K^T
 
 constexpr int kKqStages = 3, kVStages = 2, kTpStages = 2, kVecs = 3;
-constexpr uint32_t kKqBytes = 32768, kVBytes = 16384, kTpBytes = 32768;
+constexpr uint32_t kKqBytes = 32768, kVBytes = 16384, kTpBytes = kDeltaTpBytes;
 
 struct Shared {
     uint8_t kq[kKqStages][kKqBytes];  // per 64 key channels: 64 rows of K, 64 rows of Q
     uint8_t v[kVStages][kVBytes];     // per 64 value channels: 64 rows
-    uint8_t tp[kTpStages][kTpBytes];  // T - I (two bf16 values), P (two)
-    float D[C][20];                   // A's blocks of 16 on the diagonal
+    uint8_t tp[kTpStages][kTpBytes];  // T - I (three bf16 values; before that A and its inverse in fp32), P (two)
     Vec vec[kVecs];
     float a[2][C], pre[2][C], f[2][C];  // decays: of a row; within its block of 16, up to the row; from the row to the block's end
     uint64_t full_kq[kKqStages], free_kq[kKqStages], ready_kq;
@@ -99,81 +100,64 @@ __device__ __forceinline__ bool prep_all(bool ok) {
 }
 // ------------------------------------------------------------------------ prep -----------
 
-// ---- the inverse of I + A, in place of A's operand. T = I + N with N strictly lower; blocks of 16, then
-//     X21 = -(I + N22) A21 (I + N11)
-// twice (16 -> 32 -> 64). All operands are two bf16 values in the operand's own 128-byte swizzled rows (the product of the rests is left out), and
-// the products are transposed: Y^T = A21^T + N11^T A21^T leaves its accumulators as the A operand of X21^T = -(Y^T + Y^T N22^T).
-
-__device__ __forceinline__ uint32_t element(uint32_t base, int r, int c) { return base + (uint32_t)r * 128u + (uint32_t)((((c >> 3) ^ (r & 7)) << 4)); }
-// 16 x 16 values from (r, c): as the A operand of rows r.., or the two B operands of columns n = row, k = column.
-__device__ __forceinline__ void load_tile(uint32_t (&f)[4], uint32_t base, int r, int c, int lane) {
-    const uint32_t at = element(base, r + (lane & 15), c + 8 * (lane >> 4));
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3]) : "r"(at) : "memory");
+// ---- the inverse of I + A, in fp32 in A's place, which the operand takes afterwards. Right of the diagonal's blocks of 32 lies what the joins
+// hold in between. Blocks of 16 by substitution, then joined twice through X21 = -X22 (A21 X11). An error of A or of a
+// join is multiplied by |A| |(I + A)^-1|, a hundred where keys resemble one another and thousands with b near 2, so the joins' operands are
+// two tf32 values each, 2^-21 of a product is left (two bf16 values, 2^-17: final states 20 to 100 times as far off there).
+__device__ __forceinline__ void two_tf32(float x, uint32_t &hi, uint32_t &lo) {
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
 }
-// The transposed tile as an A operand, and back.
-__device__ __forceinline__ uint32_t turned(uint32_t base, int r, int c, int lane) {
-    return element(base, r + (lane & 7) + 8 * (lane >> 4), c + 8 * ((lane >> 3) & 1));
-}
-__device__ __forceinline__ void load_turned(uint32_t (&f)[4], uint32_t base, int r, int c, int lane) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
-                 : "r"(turned(base, r, c, lane))
-                 : "memory");
-}
-__device__ __forceinline__ void store_turned(const uint32_t (&f)[4], uint32_t base, int r, int c, int lane) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(turned(base, r, c, lane)), "r"(f[0]), "r"(f[1]),
-                 "r"(f[2]), "r"(f[3])
-                 : "memory");
-}
-struct Tile {  // two bf16 values each
-    uint32_t hi[4], lo[4];
-};
-constexpr uint32_t kLo = 8192;  // from an operand's first values to its second
-__device__ __forceinline__ Tile tile(uint32_t T, int r, int c, int lane) {
-    Tile t;
-    load_tile(t.hi, T, r, c, lane);
-    load_tile(t.lo, T + kLo, r, c, lane);
-    return t;
-}
-__device__ __forceinline__ Tile tile_turned(uint32_t T, int r, int c, int lane) {
-    Tile t;
-    load_turned(t.hi, T, r, c, lane);
-    load_turned(t.lo, T + kLo, r, c, lane);
-    return t;
-}
-// Accumulators of 16 x 16 (two of 16 x 8) from and to such a tile.
-__device__ __forceinline__ void to_sums(float (&d)[2][4], const Tile &t) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        d[e >> 1][2 * (e & 1)] = __uint_as_float(t.hi[e] << 16) + __uint_as_float(t.lo[e] << 16);
-        d[e >> 1][2 * (e & 1) + 1] = __uint_as_float(t.hi[e] & 0xffff0000u) + __uint_as_float(t.lo[e] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ Tile from_sums(const float (&d)[2][4], float sign) {
-    Tile t;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) split2(sign * d[e >> 1][2 * (e & 1)], sign * d[e >> 1][2 * (e & 1) + 1], t.hi[e], t.lo[e]);
-    return t;
-}
-__device__ __forceinline__ void mma_16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
-// d += A B^T, 16 x 16 x 16.
-__device__ __forceinline__ void product(float (&d)[2][4], const Tile &a, const Tile &b) {
+constexpr int kPitch = C + 4;  // floats between rows
+static_assert(C * kPitch * 4 == 16384 + 8 * 128, "in the place of T - I: its first and second values, and 8 rows of the third");
+// d = A (16 x K) B (K x 8), by one warp: lane 4 g + t has columns 2 t, 2 t + 1 of rows g and g + 8.
+template <int K>
+__device__ __forceinline__ void join(float (&d)[4], const float *A, const float *B, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    float more[2][4] = {};  // three chains of MMAs
 #pragma unroll
-    for (int n = 0; n < 2; ++n) mma_16(d[n], a.hi, b.hi[n], b.hi[n + 2]);
+    for (int e = 0; e < 4; ++e) d[e] = 0.f;
 #pragma unroll
-    for (int n = 0; n < 2; ++n) mma_16(d[n], a.hi, b.lo[n], b.lo[n + 2]);
+    for (int k = 0; k < K; k += 8) {
+        uint32_t ah[4], al[4], bh[2], bl[2];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) mma_16(d[n], a.lo, b.hi[n], b.hi[n + 2]);
+        for (int e = 0; e < 4; ++e) two_tf32(A[(g + 8 * (e & 1)) * kPitch + k + t + 4 * (e >> 1)], ah[e], al[e]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) two_tf32(B[(k + t + 4 * e) * kPitch + g], bh[e], bl[e]);
+        mma_tf32(d, ah, bh);
+        mma_tf32(more[0], ah, bl);
+        mma_tf32(more[1], al, bh);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] += more[0][e] + more[1][e];
+}
+__device__ __forceinline__ void put_join(float *to, float sign, const float (&d)[4], int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    *reinterpret_cast<float2 *>(to + g * kPitch + 2 * t) = make_float2(sign * d[0], sign * d[1]);
+    *reinterpret_cast<float2 *>(to + (g + 8) * kPitch + 2 * t) = make_float2(sign * d[2], sign * d[3]);
 }
 
-// s.D: the 16 x 16 blocks on A's diagonal in fp32; T: the operand.
-__device__ __forceinline__ void invert(Shared &s, uint8_t *operand, int pt) {
+// 8 values of row i as three bf16 operands of 64 x 64.
+__device__ __forceinline__ void store_operand3(uint8_t *to, int i, int chunk, const float *x) {
+    uint32_t h[4], m[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split3(x[2 * e], x[2 * e + 1], h[e], m[e], l[e]);
+    const uint32_t at = (uint32_t)i * 128u + (uint32_t)((chunk ^ (i & 7)) << 4);
+    *reinterpret_cast<uint4 *>(to + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4 *>(to + 8192 + at) = make_uint4(m[0], m[1], m[2], m[3]);
+    *reinterpret_cast<uint4 *>(to + 16384 + at) = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// A in the operand's place -> the operand.
+__device__ __forceinline__ void invert(uint8_t *tp, int pt) {
+    float *A = reinterpret_cast<float *>(tp);
+    auto at = [A](int r, int c) { return A + r * kPitch + c; };
     const int w = pt >> 5, lane = pt & 31;
-    const uint32_t T = smem_u32(operand);
     if (w < 4) {  // by substitution, lane = column
         const int j = lane & 15, o = 16 * w;
         float x[16];
@@ -183,70 +167,65 @@ __device__ __forceinline__ void invert(Shared &s, uint8_t *operand, int pt) {
         for (int m = 0; m < 16; m += 4) {  // four columns of A at a time
             float4 own[4];
 #pragma unroll
-            for (int i = 1; i < 4; ++i) own[i] = *reinterpret_cast<const float4 *>(&s.D[o + m + i][m]);
+            for (int i = 1; i < 4; ++i) own[i] = *reinterpret_cast<const float4 *>(at(o + m + i, o + m));
             x[m + 1] = fmaf(-own[1].x, x[m], x[m + 1]);
             x[m + 2] = fmaf(-own[2].y, x[m + 1], fmaf(-own[2].x, x[m], x[m + 2]));
             x[m + 3] = fmaf(-own[3].z, x[m + 2], fmaf(-own[3].y, x[m + 1], fmaf(-own[3].x, x[m], x[m + 3])));
 #pragma unroll
             for (int i = m + 4; i < 16; ++i) {
-                const float4 a = *reinterpret_cast<const float4 *>(&s.D[o + i][m]);
+                const float4 a = *reinterpret_cast<const float4 *>(at(o + i, o + m));
                 x[i] = fmaf(-a.w, x[m + 3], fmaf(-a.z, x[m + 2], fmaf(-a.y, x[m + 1], fmaf(-a.x, x[m], x[i]))));
             }
         }
+        __syncwarp();
         if (lane < 16)
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {  // N: without the ones
-                uint32_t hi, lo;
-                split2(i > j ? x[i] : 0.f, i + 1 > j ? x[i + 1] : 0.f, hi, lo);
-                const uint32_t a0 = (uint32_t)(o + i) * 128u + (uint32_t)((((o + j) >> 3) ^ (i & 7)) << 4) + (uint32_t)(j & 7) * 2u;
-                const uint32_t a1 = (uint32_t)(o + i + 1) * 128u + (uint32_t)((((o + j) >> 3) ^ ((i + 1) & 7)) << 4) + (uint32_t)(j & 7) * 2u;
-                *reinterpret_cast<uint16_t *>(operand + a0) = (uint16_t)hi;
-                *reinterpret_cast<uint16_t *>(operand + kLo + a0) = (uint16_t)lo;
-                *reinterpret_cast<uint16_t *>(operand + a1) = (uint16_t)(hi >> 16);
-                *reinterpret_cast<uint16_t *>(operand + kLo + a1) = (uint16_t)(lo >> 16);
-            }
+            for (int i = 0; i < 16; ++i) *at(o + i, o + j) = x[i];
     }
     prep_sync();
-    if (w < 2) {  // two pairs of blocks
-        const int o = 32 * w;
-        float y[2][4];
-        to_sums(y, tile_turned(T, o + 16, o, lane));
-        product(y, tile_turned(T, o, o, lane), tile(T, o + 16, o, lane));
-        const Tile Y = from_sums(y, 1.f);
-        product(y, Y, tile(T, o + 16, o + 16, lane));
-        const Tile X = from_sums(y, -1.f);
-        __syncwarp();
-        store_turned(X.hi, T, o + 16, o, lane);
-        store_turned(X.lo, T + kLo, o + 16, o, lane);
+    float d[4];
+    {  // two pairs of blocks
+        const int o = 32 * ((w >> 1) & 1), n = 8 * (w & 1);
+        if (w < 4) {
+            join<16>(d, at(o + 16, o), at(o, o + n), lane);
+            put_join(at(o >> 1, 32 + n), 1.f, d, lane);
+        }
+        prep_sync();
+        if (w < 4) {
+            join<16>(d, at(o + 16, o + 16), at(o >> 1, 32 + n), lane);
+            put_join(at(o + 16, o + n), -1.f, d, lane);
+        }
     }
     prep_sync();
-    Tile X;
-    const int c = 16 * (w & 1), r = 32 + 16 * ((w >> 1) & 1);  // this warp's columns and rows of the last block
-    if (w < 4) {
-        float y[2][2][4];  // rows 32..47 and 48..63 of A21
+    const int o = 16 * (w & 1), n = 8 * (w >> 1);
+    join<32>(d, at(32 + o, 0), at(0, n), lane);
+    put_join(at(o, 32 + n), 1.f, d, lane);
+    prep_sync();
+    join<32>(d, at(32 + o, 32), at(0, 32 + n), lane);
+    // T - I from here: the last join's block from the registers, the blocks of 32 on the diagonal, zeros behind them.
+    const int r = pt >> 2, c = (r & 32) + 8 * (pt & 3);
+    float y[8];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) to_sums(y[e], tile_turned(T, 32 + 16 * e, c, lane));
-#pragma unroll
-        for (int k = 0; k < 32; k += 16)
-            if (k >= c) {
-                const Tile n11 = tile_turned(T, k, c, lane);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) product(y[e], n11, tile(T, 32 + 16 * e, k, lane));
-            }
-        float x[2][4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[n][e] = r == 32 ? y[0][n][e] : y[1][n][e];
-        product(x, from_sums(y[0], 1.f), tile(T, r, 32, lane));
-        if (r == 48) product(x, from_sums(y[1], 1.f), tile(T, r, 48, lane));
-        X = from_sums(x, -1.f);
+    for (int j = 0; j < 8; j += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(at(r, c + j));
+        y[j] = x.x, y[j + 1] = x.y, y[j + 2] = x.z, y[j + 3] = x.w;
     }
-    prep_sync();  // A21 is read
-    if (w < 4) {
-        store_turned(X.hi, T, r, c, lane);
-        store_turned(X.lo, T + kLo, r, c, lane);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = c + j < r ? y[j] : 0.f;
+    prep_sync();  // everyone has read
+    store_operand3(tp, r, c >> 3, y);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int row = 32 + o + (lane >> 2) + 8 * half;
+        uint32_t v[3];
+        split3(-d[2 * half], -d[2 * half + 1], v[0], v[1], v[2]);
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            *reinterpret_cast<uint32_t *>(tp + 8192 * e + row * 128 + (((n >> 3) ^ (row & 7)) << 4) + (lane & 3) * 4) = v[e];
     }
+    const int zero = (pt >> 2 & 31) * 128 + (((4 + (pt & 3)) ^ (pt >> 2 & 7)) << 4);
+    *reinterpret_cast<uint4 *>(tp + 8192 * (pt >> 7) + zero) = make_uint4(0u, 0u, 0u, 0u);
+    if (pt < 32) *reinterpret_cast<uint4 *>(tp + 16384 + zero) = make_uint4(0u, 0u, 0u, 0u);  // A ends in its row 7
 }
 
 // The chunks' decays, by one warp, up to two chunks ahead of the chain.
@@ -306,6 +285,7 @@ __device__ __forceinline__ bool prep(Shared &s, const DeltaParams &p, int h, lon
             return false;
         tc_fence_after();
         uint8_t *tp = s.tp[ts];
+        float *A = reinterpret_cast<float *>(tp);
         if (live) {
             float x[32];
             tmem_ld32(tmem + tq + TM_KK + c0, x);
@@ -315,18 +295,17 @@ __device__ __forceinline__ bool prep(Shared &s, const DeltaParams &p, int h, lon
             const float scale = q_row ? 1.f : s.vec[c % kVecs].b[i];
 #pragma unroll
             for (int b = 0; b < 2; ++b) decay_block(x + 16 * b, s.a[c & 1], s.pre[c & 1], s.f[c & 1], i, c0 + 16 * b, q_row, scale);
-            uint8_t *to = q_row ? tp + 16384 : tp;  // P, or A until it is inverted
+            if (q_row) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) store_operand(to, to + kLo, i, c0 / 8 + e, &x[8 * e]);
+                for (int e = 0; e < 4; ++e) store_operand(tp + kDeltaP, tp + kDeltaP + 8192, i, c0 / 8 + e, &x[8 * e]);
+            } else {
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-                if (!q_row && c0 + 16 * b == (i & 48))
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        *reinterpret_cast<float4 *>(&s.D[i][e]) = make_float4(x[16 * b + e], x[16 * b + e + 1], x[16 * b + e + 2], x[16 * b + e + 3]);
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4 *>(A + i * kPitch + c0 + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            }
         }
         prep_sync();
-        invert(s, tp, pt);
+        invert(tp, pt);
         fence_async_smem();
         warp_arrive(&s.ready_tp[ts]);
     }
@@ -380,12 +359,12 @@ __device__ __forceinline__ bool issue(Shared &s, int chunks) {
         }
         if (!warp_wait(&s.ready_tp[c % kTpStages], (uint32_t)(c / kTpStages) & 1u) || !warp_wait(&s.r, par)) return false;
         tc_fence_after();
-        const uint64_t d_t = sdesc_sw128(tpc, 16u, 1024u), d_p = sdesc_sw128(tpc + 16384u, 16u, 1024u);
+        const uint64_t d_t = sdesc_sw128(tpc, 16u, 1024u), d_p = sdesc_sw128(tpc + kDeltaP, 16u, 1024u);
 #pragma unroll
-        for (int e = 0; e < 3; ++e)  // first x first, first x second, second x first
+        for (int e = 0; e < 5; ++e)  // R's first value by T's first, second and third, R's second by T's first and second
 #pragma unroll
             for (int st = 0; st < C / 16; ++st)
-                mma_bf16_tmem_a_warp(tmem + TM_KS, tmem + TM_R + (e == 2 ? 32 : 0) + 8 * st, d_t + (e == 1 ? 512u : 0u) + kstep(st, 0u),
+                mma_bf16_tmem_a_warp(tmem + TM_KS, tmem + TM_R + (e > 2 ? 32 : 0) + 8 * st, d_t + 512u * (e > 2 ? e - 3 : e) + kstep(st, 0u),
                                      idesc_bf16(128, 64), e + st > 0);
         mma_commit_warp(&s.u);
         if (!warp_wait(&s.u2, par)) return false;
@@ -737,6 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 constexpr size_t kSharedBytes = sizeof(Shared) + 1024;
+static_assert(kSharedBytes <= 227 * 1024, "shared memory of a block");
 
 template <int DK, bool KEEP>
 cudaError_t launch(const Maps &maps, const DeltaParams &p, const DeltaKept &kept, cudaStream_t s) {

@@ -16,11 +16,11 @@ cudaError_t launch_delta_tc(const DeltaParams &p, cudaStream_t s);
 
 // What the gradients keep of the forward pass, per chunk (number of first_chunk) and value head.
 struct DeltaKept {
-    uint8_t *tp;  // operands T - I and P, two bf16 values each: 32768 bytes
+    uint8_t *tp;  // operands T - I, three bf16 values, and P, two
     float *S;     // the state before the chunk [dk, dv]
     float *U;     // its written values [64, dv]
 };
-constexpr size_t kDeltaTpBytes = 32768;
+constexpr uint32_t kDeltaP = 24576, kDeltaTpBytes = 40960;  // where P is, and bytes in all
 cudaError_t launch_delta_tc_kept(const DeltaParams &p, const DeltaKept &kept, cudaStream_t s);
 
 // Gradients: workspace bytes, and the launches. dq, dk: per value head where value heads share a key head (p.per > 1).

@@ -75,7 +75,7 @@ __device__ __forceinline__ bool chain_issue(ChainShared &s, int chunks) {
         const int st = k % kStages;
         const uint32_t kq = smem_u32(s.kq[st]), tp = smem_u32(s.tp[st]);
         const uint64_t d_k = sdesc_sw128(kq, 16u, 1024u), d_kn = sdesc_sw128(kq, 16384u, 1024u), d_qn = sdesc_sw128(kq + 8192u, 16384u, 1024u);
-        const uint64_t d_t = sdesc_sw128(tp, 8192u, 1024u), d_p = sdesc_sw128(tp + 16384u, 8192u, 1024u);  // MN-major: the column is the N index
+        const uint64_t d_t = sdesc_sw128(tp, 8192u, 1024u), d_p = sdesc_sw128(tp + kDeltaP, 8192u, 1024u);  // MN-major: the column is the N index
         // The last chunk's rows behind the sequence are cleared first; the others are there as soon as they are loaded.
         if (!warp_wait(k == 0 ? &s.ready : &s.full[st], (uint32_t)(k / kStages) & 1u) || !warp_wait(&s.s, par)) return false;
         tc_fence_after();
@@ -97,10 +97,10 @@ __device__ __forceinline__ bool chain_issue(ChainShared &s, int chunks) {
         if (!warp_wait(&s.r, par)) return false;
         tc_fence_after();
 #pragma unroll
-        for (int e = 0; e < 3; ++e)
+        for (int e = 0; e < 5; ++e)  // dU's first value by T's first, second and third, dU's second by T's first and second
 #pragma unroll
             for (int i = 0; i < C / 16; ++i)
-                mma_bf16_tmem_a_warp(tmem + TM_KD, tmem + TM_U + (e == 2 ? 32 : 0) + 8 * i, d_t + (e == 1 ? 512u : 0u) + kDescStepMN128 * i,
+                mma_bf16_tmem_a_warp(tmem + TM_KD, tmem + TM_U + (e > 2 ? 32 : 0) + 8 * i, d_t + 512u * (e > 2 ? e - 3 : e) + kDescStepMN128 * i,
                                      idesc_bf16(128, 64) | kIdescBMajorMN, e + i > 0);
         mma_commit_warp(&s.u);
         if (!warp_wait(&s.h, par)) return false;
@@ -133,13 +133,13 @@ __device__ __forceinline__ bool chain_load(ChainShared &s, const ChainMaps &maps
         const int st = k % kStages, c = chunks - 1 - k, row = (int)(begin + (long long)c * C);
         if (k >= kStages && !(ok = warp_wait(&s.free[st], (uint32_t)(k / kStages - 1) & 1u))) break;
         if (elect_one()) {
-            mbar_arrive_expect_tx(&s.full[st], DK / 64 * 16384 + vtiles * 8192 + (uint32_t)kDeltaTpBytes);
+            mbar_arrive_expect_tx(&s.full[st], DK / 64 * 16384 + vtiles * 8192 + kDeltaTpBytes);
             for (int a = 0; a < DK / 64; ++a) {
                 tma_load_3d(s.kq[st] + a * 16384, &maps.k, &s.full[st], 64 * a, hk, row);
                 tma_load_3d(s.kq[st] + a * 16384 + 8192, &maps.q, &s.full[st], 64 * a, hk, row);
             }
             for (int a = 0; a < vtiles; ++a) tma_load_3d(s.d_o[st] + a * 8192, &maps.d_o, &s.full[st], 64 * a, h, row);
-            bulk_load(s.tp[st], p.tp + ((size_t)(first_chunk(begin, n, C) + c) * p.f.hv + h) * kDeltaTpBytes, (uint32_t)kDeltaTpBytes, &s.full[st]);
+            bulk_load(s.tp[st], p.tp + ((size_t)(first_chunk(begin, n, C) + c) * p.f.hv + h) * kDeltaTpBytes, kDeltaTpBytes, &s.full[st]);
         }
         __syncwarp();
     }
