@@ -50,3 +50,41 @@ def test_a_workspace_serves_every_call_of_its_shape(dtype, dk, dv, lengths):
                 assert lib.kda_delta_backward(ctypes.byref(_args(x)), ctypes.byref(grads), ws.data_ptr(), sizes[0], stream) == 0
                 x.check_backward(g)
     kda.check_status()
+
+
+def _filled(*shape, dtype=FP32, scale=1.0, seed=0):
+    return torch.empty(*shape, dtype=dtype, device=DEV).normal_(0, scale, generator=torch.Generator(device=DEV).manual_seed(seed))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_gradients_of_more_than_2_to_the_31_values(dtype):
+    """Outputs, kept states and operands past 2^31 elements: the last head is that of a call with it alone, and so is a head in the middle."""
+    T, H = 1400, 12288
+    q, k = (_filled(1, T, H, 128, dtype=dtype, scale=128 ** -0.5, seed=s) for s in (31, 32))
+    v, do = (_filled(1, T, H, 128, dtype=dtype, seed=s) for s in (33, 34))
+    g, beta = -0.1 * torch.rand(1, T, H, device=DEV), 0.9 * torch.rand(1, T, H, device=DEV)
+    assert v.numel() > 2 ** 31
+    grads = kda.delta_backward(q, k, v, g, beta, do)
+    for h in (H - 1, H // 2):
+        one = kda.delta_backward(*(t[:, :, h:h + 1].contiguous() for t in (q, k, v, g, beta, do)))
+        for name in GRADS:
+            got, want = (grads[name][:, h:h + 1] if name == "d_initial_state" else grads[name][:, :, h:h + 1]), one[name]
+            if dtype == BF16:
+                assert torch.equal(got, want), (name, h)
+            else:  # few heads keep their states in chunks, many row by row: each within the header's bound of the exact one
+                off = ((got - want).double().norm() / want.double().norm()).item()
+                assert off <= 2 * 4e-6, (name, h, off)
+    kda.check_status()
+    del grads, q, k, v, do, g, beta, one, got, want
+    torch.cuda.empty_cache()
+
+
+def test_norm_gradients_of_more_than_2_to_the_31_values():
+    x, dy, z = (_filled(70000, 256, 128, dtype=BF16, seed=s) for s in (35, 36, 37))
+    assert x.numel() > 2 ** 31
+    g = kda.layer_norm_backward(x, None, dy, gate=z, norm="rms")
+    for rows in (slice(-3, None), slice(40000, 40002)):
+        one = kda.layer_norm_backward(*(t[rows].contiguous() if t is not None else None for t in (x, None, dy)), gate=z[rows].contiguous(), norm="rms")
+        assert torch.equal(g["dx"][rows], one["dx"]) and torch.equal(g["dgate"][rows], one["dgate"])
+    del x, dy, z, g, one
+    torch.cuda.empty_cache()
