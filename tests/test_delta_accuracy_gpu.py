@@ -124,7 +124,8 @@ def test_states_and_gradients_of_many_chunks(dtype, shape):
 @pytest.mark.parametrize("decay", [0.0, 0.3])
 def test_keys_that_are_alike_and_large_beta(dtype, cosine, beta, decay):
     """What the header promises; and in bf16 the state as the model of its roundings has it: errors of 16 000 values scatter little, so a half
-    more than the model's, and the sums' share in fp32, half a step per operand of a product times what it meets."""
+    more than the model's, and the sums' share in fp32: four half steps (R, U, the state's product and sum), and of A's and T's own an eighth,
+    as errors of 64 rows of random signs, of what the largest could meet. One operand with a value less than the model's is beyond it."""
     c = Case(dtype, 1, 832, 2, 2, 128, 128, seed=24, decay=decay)
     alike(c, cosine, 25)
     c.beta[:] = beta
@@ -140,5 +141,5 @@ def test_keys_that_are_alike_and_large_beta(dtype, cosine, beta, decay):
         assert far <= (STATE[dtype] if cosine == 0 and beta <= 1 else state), far
         if dtype == BF16:
             expected = off(model.final_state(k, v, g, b, S), want[h])
-            assert far <= 1.5 * expected + ULP32 * (32 + model.growth(k, g, b)), (far, expected)
+            assert far <= 1.5 * expected + ULP32 * (4 + model.growth(k, g, b) / 8), (far, expected)
     assert all(v <= (GRADIENT[dtype] if cosine == 0 and beta <= 1 else gradient) for v in worst.values()), worst
