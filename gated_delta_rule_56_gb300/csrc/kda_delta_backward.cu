@@ -19,7 +19,8 @@
 //
 // One block per (sequence, value head), the chunks from the last to the first with S0 and dS in shared memory. Bound by the
 // latency of its phases (ten barriers per chunk; 6 products of 16 rows with a state, whose operands come out of shared memory), a path for fp32 and
-// for short sequences: 1501 rows in 9 sequences, 8 heads of 64, fp32: 230 us in a captured graph where the longest sequence has some 450 rows.
+// for short sequences: 1501 rows in 9 sequences, 8 heads of 64, fp32: 253 us in a captured graph where the longest
+// sequence has 252 rows, 468 us where it has 490 (15 us per chunk of it, a sixth of that for the states before the chunks).
 #include "kda_delta.cuh"
 #include "kda_delta_tc.h"
 #include "kda_layers.h"

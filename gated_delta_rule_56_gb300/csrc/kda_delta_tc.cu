@@ -14,7 +14,7 @@
 // Precision. The state is accumulated in fp32, its final value is an fp32 output, and a bf16 operand has 8 bits. So what is not exact goes in
 // as several bf16 values: S, R and P as two (2^-18 of them is left), T - I as three (of its products with R, those of 2^-25 and less are left
 // out), U with its decay as three in the state's update, where its rounding would be the state's. U = R + (T - I) R adds R itself in fp32. The inverse
-// is made in fp32 with joins of two tf32 values: an error there is multiplied by |A| |T|. The final state of 8192 rows is 1.7e-6 off 64
+// is made in fp32 with joins of two tf32 values: an error there is multiplied by |A| |T|. The final state of 8192 rows is 1.3e-6 off 64
 // bits in the 2-norm (the plain fp32 form 0.2e-6); one bf16 value for S and U would leave 2e-3. With T - I and the joins in two bf16 values it was
 // 1.9e-6, but 2e-2 with equal keys and beta = 2, where it is 7e-4 now (fp32 row by row: 1e-4), and the prompt below took 661 us. The outputs are
 // as near as their one rounding.

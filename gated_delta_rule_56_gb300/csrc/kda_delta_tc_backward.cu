@@ -15,10 +15,10 @@
 // Operands that are not exact in bf16 go in as two values (2^-17 of them is left, the products of both rests are left out), those that are
 // added to the gradient of the state as three; sums, states and outputs are fp32.
 //
-// Gradients are 2e-6 to 5e-6 off 64 bits in the 2-norm (the plain fp32 form 0.3e-6).
+// Gradients are 2e-6 to 6e-6 off 64 bits in the 2-norm (the plain fp32 form 0.3e-6).
 //
-// Measured at 2 x 2048 rows, 32 value heads, 16 key heads of 128 (616 us in all): the kept forward pass 202 us, the chain 156, the chunks 217, the sums
-// over shared heads 30; with 4 x 2048 rows 197, 157, 440 and 57. The chains are bound by latency, as the forward one (9 000 cycles per chunk, a
+// Measured at 2 x 2048 rows, 32 value heads, 16 key heads of 128 (642 us in all): the kept forward pass 215 us, the chain 160, the chunks 229, the sums
+// over shared heads 29; with 4 x 2048 rows 227, 162, 442 and 58. The chains are bound by latency, as the forward one (9 000 cycles per chunk, a
 // quarter of them the stores of dS, which the chain's warps make themselves); the third kernel by its phases, which load (280 KB per
 // chunk and head: S0, dS, U, dR), compute and store one after the other with one block per SM: 3.5 TB/s, 27 % of the issue slots. L2 prefetches for a
 // later block made it slower (480 for 440), bulk copies of single rows out of shared memory too (550); 32 lanes that write to 32 rows took 470.

@@ -4,10 +4,13 @@
 //     dx = r (t - mean(t) - h r^2 mean(t h)) + d_sum   (without mean(t) for RMS);   dz = dy (h r w + b) act'(z)
 //     dweight = sum d h r,  dbias = sum d   over all lines
 //
-// A line is held in registers as in the forward pass: every input is read once, two rounds of sums (one for RMS): sum t and sum t h come with
+// A line is held in registers as in the forward pass (above 4096 values, 2048 that are not aligned, part of it spills): every
+// input is read from HBM once, two rounds of sums (one for RMS): sum t and sum t h come with
 // the squares. A group keeps its sums of the weights' gradients in registers while it goes over its lines; a second kernel adds the
 // blocks' parts in a fixed order with their rounding errors (no atomics). Bound by the latency of the loads: 8 accumulators and 8 inputs per pair
-// leave two blocks of 256 threads per SM. Measured: 8192 tokens x 32 heads of 128 with a gate in bf16 108 us, 4.3 TB/s (65 % of the copy rate); 4101 lines of 1531 in fp32, which take single values, 44 us, 2.3 TB/s.
+// leave two blocks of 256 threads per SM. Measured: 8192 tokens x 32 heads of 128 with a gate in bf16 109 us, 4.3 TB/s (64 % of the copy rate);
+// 4101 lines of 1531 in fp32, which take single values, 44 us, 2.3 TB/s. 2^28 values with weight and bias: width 4096 933 us, 8192 771 us, 16384 1.0 ms,
+// 32768 2.3 ms, 32767 6.4 ms; 2^27 in fp32 483, 382, 534 us, 1.1 and 2.4 ms.
 #include "kda_layers.h"
 #include "kda_norm.cuh"
 

@@ -454,7 +454,8 @@ KDA_API size_t kda_qk_norm_rotary_backward_workspace_size(const kda_rotary_args 
  *     S' = a S_{t-1};   u = b (v_t - S'^T k_t);   S_t = S' + k_t u^T;   o_t = S_t^T q_t      (no scale is applied to q)
  * bf16 sequences of 20 rows and more on average (8 for the gradients) go in chunks of 64 rows on the tensor cores, with operands in two or
  * three bf16 values; a NaN or an infinity may also reach the other rows of its chunk there, outputs and gradients. fp32 and shorter sequences
- * are computed in fp32, row by row or in chunks of 16 rows, where only a NaN of g may reach other gradients of its chunk.
+ * are computed in fp32, row by row or in chunks of 16 rows, where only a NaN of g may reach other gradients of its chunk. A call takes one of the
+ * two for all its sequences: a prompt packed with many single tokens is faster in a call of its own.
  * Accuracy, as the 2-norm of the error of a head's final state (of a gradient) in a sequence. Keys that have little to do with one another
  * and b <= 1: in bf16 6e-6 (1.5e-5), in fp32 2e-6 (4e-6). An error inside a chunk is multiplied by up to |A| |(I + A)^-1|, where A_ij = b_i
  * exp(g_(j+1) + .. + g_i) k_i.k_j, j < i: 1 there, up to 100 for b <= 1 with keys that are all alike, up to 7000 for b near 2, such keys and no
