@@ -459,8 +459,8 @@ KDA_API size_t kda_qk_norm_rotary_backward_workspace_size(const kda_rotary_args 
  * Accuracy, as the 2-norm of the error of a head's final state (of a gradient) in a sequence. Keys that have little to do with one another
  * and b <= 1: in bf16 6e-6 (1.5e-5), in fp32 2e-6 (4e-6). An error inside a chunk is multiplied by up to |A| |(I + A)^-1|, where A_ij = b_i
  * exp(g_(j+1) + .. + g_i) k_i.k_j, j < i: 1 there, up to 100 for b <= 1 with keys that are all alike, up to 7000 for b near 2, such keys and no
- * decays. Over all keys and decays: b <= 1 in bf16 4e-5 (2e-4), in fp32 2e-6 (1e-5); b <= 2 in bf16 1e-3 (1e-3), in fp32 3e-4 (3e-4). Outputs
- * in bf16 add their rounding, 2^-8 of a value at most.
+ * decays. Over all keys and decays, up to 8192 rows: b <= 1 in bf16 6e-5 (2e-4), in fp32 4e-6 (1e-5); b <= 2 in bf16 1e-3 (1e-3), in fp32
+ * 3e-4 (3e-4). Outputs in bf16 add their rounding, 2^-8 of a value at most.
  * g <= 0 is the log-decay (-inf clears the state; below -128 is computed as -128, whose exponential is 0 in fp32). The rows of k are taken
  * as unit rows (kda_qk_norm_rotary with norm 1) and b in [0, 2]: with |k|^2 b > 2 the recurrence itself grows.
  */
