@@ -12,8 +12,8 @@
 //      dg is made of the pairs' products with [Q; K] K^T and of the parts of dq, row and col that come from the states.
 // Where value heads share key heads, dq and dk go per value head to the workspace and are added up in a fixed order.
 //
-// Operands that are not exact in bf16 go in as two values (2^-17 of them is left, the products of both rests are left out), those that are
-// added to the gradient of the state as three; sums, states and outputs are fp32.
+// Operands that are not exact in bf16 go in as two values (2^-18 of them is left, the products of both rests are left out), T - I and those that
+// are added to the gradient of the state as three; sums, states and outputs are fp32.
 //
 // Gradients are 2e-6 to 6e-6 off 64 bits in the 2-norm (the plain fp32 form 0.3e-6).
 //
